@@ -451,6 +451,47 @@ sbp_status sbp_clip_scale(double total_sq, float max_norm, float scale,
                           float* clipped_scale, double* coef);
 
 /* ------------------------------------------------------------------------
+ * The momentum-orthogonalising step for weight matrices, in three calls.
+ * ("Parallelisms", ZeRO-1: a rank updates the shard it owns with its local
+ * optimizer state.)  A weight matrix's update direction is its momentum with
+ * every singular value moved towards 1; norms, biases and embeddings stay
+ * with sbp_adamw_shard.  A rank that owns whole matrices (its own plan with
+ * world_n = 1) runs
+ *   sbp_momentum_shard -> sbp_newton_schulz on the matrices inside u_out,
+ *   in place -> sbp_update_shard;
+ * with row shards (sbp_bucket_plan_per_tensor) the direction is gathered
+ * before and cut again after:
+ *   sbp_momentum_shard -> all-gather, sbp_unpack_shards ->
+ *   sbp_newton_schulz -> sbp_pack_grads, sbp_shard_of -> sbp_update_shard.
+ *
+ * sbp_momentum_shard: per element, with G as in sbp_adamw_shard (acc + S, S,
+ *   or acc when R == 0):
+ *     g  = fl(G * scale)
+ *     m' = mu*m + (1-mu)*g
+ *     u  = (1-mu)*g + mu*m'   (nesterov != 0)      u = m'   (nesterov == 0)
+ *     m[i] = m', u_out[i] = bf16_rne(u)
+ *   with 1-mu formed in float64 and rounded once.
+ *   m          device fp32[n], updated in place (zeros before the first step)
+ *   u_out      device bf16[n]
+ *   mu         in [0, 1)
+ *   Other arguments, alignment and errors as in sbp_adamw_shard.
+ *
+ * sbp_update_shard: th' = th*decay - lr*u, master[i] = th', param_out[i] =
+ *   bf16_rne(th'), decay = 1 - lr*weight_decay formed in float64 and rounded
+ *   once.  u: device bf16[n]; master: device fp32[n], in place; param_out:
+ *   device bf16[n]; 16-byte aligned, pairwise disjoint; lr and weight_decay
+ *   finite and >= 0.  Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE
+ *   (n > SBP_MAX_SHARD_NUMEL), SBP_EHIP.
+ * ---------------------------------------------------------------------- */
+sbp_status sbp_momentum_shard(const void* const* peers, int32_t R,
+                              const float* acc, float scale, float* m,
+                              void* u_out, int64_t n, float mu,
+                              int32_t nesterov, hipStream_t stream);
+sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
+                            int64_t n, float lr, float weight_decay,
+                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Spread arena: device memory for a rank's shard state and receive buffers
  * ("Parallelisms", ZeRO-1 and ZeRO-3: each rank keeps its shard's fp32
  * master copy, first and second moments and parameter shard, and receives

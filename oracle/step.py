@@ -316,3 +316,28 @@ def shard_step(peers, acc, scale, theta, m, v, hp, t):
     sc = adamw_scalars(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, t)
     theta1, m1, v1 = adamw(theta, m, v, g, sc)
     return theta1, m1, v1, f32_to_bf16(theta1)
+
+
+# ---- the momentum-orthogonalising step ------------------------------------------
+
+def momentum_step(G, scale, m, mu, nesterov):
+    """(m', u bits): g = fl(G*scale), m' = mu*m + (1-mu)*g, the direction u is m'
+    or the look-ahead (1-mu)*g + mu*m', rounded to bf16.
+
+    The optimizer state lives on the owned shard ("Parallelisms", section
+    ZeRO-1).  Reading taken for the momentum: the exponential average, in the
+    same form as AdamW's first moment.
+    """
+    mu32 = F32(mu)
+    omm = F32(1.0 - float(mu32))
+    og = omm * (np.asarray(G, F32) * F32(scale))
+    m1 = mu32 * np.asarray(m, F32) + og
+    return m1, f32_to_bf16(og + mu32 * m1 if nesterov else m1)
+
+
+def update_step(u, master, lr, weight_decay):
+    """(th', param bits): th' = th*decay - lr*u, decay = 1 - lr*weight_decay."""
+    lr32 = F32(lr)
+    decay = F32(1.0 - float(lr32) * float(F32(weight_decay)))
+    th = np.asarray(master, F32) * decay - lr32 * bf16_to_f32(u)
+    return th, f32_to_bf16(th)

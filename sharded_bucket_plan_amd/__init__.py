@@ -44,6 +44,7 @@ EXPORTS = (
     "sbp_unpack_params", "sbp_shard_of", "sbp_gather_shards", "sbp_bucket_plan_per_tensor",
     "sbp_group_runs", "sbp_adamw_shard_grouped", "sbp_unpack_shards",
     "sbp_grad_sq_norm_noalloc", "sbp_arena_create", "sbp_arena_info", "sbp_arena_free",
+    "sbp_momentum_shard", "sbp_update_shard",
 )
 
 MAX_GROUPS = 8
@@ -128,6 +129,11 @@ def lib():
         "sbp_grad_sq_norm_noalloc": ([_vpp, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float,
                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_void_p], st),
+        "sbp_momentum_shard": ([_vpp, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float,
+                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_float,
+                                ctypes.c_int32, ctypes.c_void_p], st),
+        "sbp_update_shard": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                              ctypes.c_float, ctypes.c_float, ctypes.c_void_p], st),
         "sbp_arena_create": ([_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                               ctypes.c_uint64, _vpp, ctypes.POINTER(ctypes.c_void_p)], st),
         "sbp_arena_info": ([ctypes.c_void_p, _i64p, _i64p, _i64p], st),
@@ -609,6 +615,35 @@ def clip_scale(total_sq, max_norm, scale):
     _check(lib().sbp_clip_scale(float(total_sq), float(max_norm), float(scale),
                                 ctypes.byref(out), ctypes.byref(coef)))
     return out.value, coef.value
+
+
+# ---- the momentum-orthogonalising step -----------------------------------------
+
+def momentum_shard(peers, acc, scale, m, u_out, mu, nesterov=True, stream=None):
+    """sbp_momentum_shard: reduce (+acc) -> *scale -> momentum (fp32, in place)
+    -> the bf16 update direction in u_out."""
+    n = m.numel()
+    if u_out.numel() != n:
+        raise ValueError("momentum_shard: u_out has the wrong size")
+    if any(p.numel() != n for p in peers) or (acc is not None and acc.numel() != n):
+        raise ValueError("momentum_shard: peers/acc differ in size")
+    _check(lib().sbp_momentum_shard(
+        _ptrs(peers, "momentum_shard peers"), len(peers),
+        None if acc is None else _f32(acc, "momentum_shard acc"), float(scale),
+        _f32(m, "momentum_shard m"), _dev(u_out, 2, "momentum_shard u_out"), n, float(mu),
+        1 if nesterov else 0, _stream(stream, m)))
+
+
+def update_shard(u, master, param_out, lr, weight_decay=0.0, stream=None):
+    """sbp_update_shard: master = master*(1 - lr*weight_decay) - lr*u, and the
+    bf16 parameters in param_out."""
+    n = master.numel()
+    if u.numel() != n or param_out.numel() != n:
+        raise ValueError("update_shard: u, master and param_out differ in size")
+    _check(lib().sbp_update_shard(
+        _dev(u, 2, "update_shard u"), _f32(master, "update_shard master"),
+        _dev(param_out, 2, "update_shard param_out"), n, float(lr), float(weight_decay),
+        _stream(stream, master)))
 
 
 def unpack_params(plan, flat, params, bucket=-1, stream=None):

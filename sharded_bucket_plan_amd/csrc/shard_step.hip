@@ -55,6 +55,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "bf16.h"
 #include "internal.h"
 
 #pragma clang fp contract(off)
@@ -134,19 +135,10 @@ struct GroupArgs {
   float decay[SBP_MAX_GROUPS];
 };
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ float bf16_one(uint16_t h) {
-  return __uint_as_float(static_cast<uint32_t>(h) << 16);
-}
-
-// binary32 -> bf16 bits: nearest, ties to even; NaN kept (quiet bit set).
-__device__ __forceinline__ uint32_t bf16_rne(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t rounded = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-  const uint32_t quiet = (u >> 16) | 0x40u;
-  return __builtin_isnan(x) ? quiet : rounded;  // a select, not a branch
-}
+using sbp::bf16_hi;
+using sbp::bf16_lo;
+using sbp::bf16_one;
+using sbp::bf16_rne;
 
 __device__ __forceinline__ void adamw_one(float g, float& th, float& m, float& v,
                                           const Scalars& s) {
@@ -498,6 +490,113 @@ fused_adamw_kernel(Peers P, const float* __restrict__ acc, float scale,
       master[i] = th;
       mom1[i] = m;
       mom2[i] = v;
+      pout[i] = static_cast<uint16_t>(bf16_rne(th));
+    }
+  }
+}
+
+// ---- momentum: G = [acc +] S, g = G*scale, m' = mu*m + (1-mu)*g, bf16 direction --
+// One pass like the fused step with one state array in place of three: per
+// element 2R + 4 (+ 4) bytes read and 6 written, a handful of flops, so HBM
+// bounds it.  Lane map and tile order as the fused step's 8 consecutive
+// elements per lane.
+template <int R, bool ACC>
+__global__ void __launch_bounds__(kBlock)
+momentum_kernel(Peers P, const float* __restrict__ acc, float scale, float* __restrict__ mom,
+                uint16_t* __restrict__ uout, int64_t n, float mu, float omm, bool nesterov) {
+  static_assert(R > 0 || ACC, "R == 0 needs the accumulator");
+  // (1-mu)*g is shared by the momentum and the look-ahead direction
+  auto one = [&](float G, float& m) -> uint32_t {
+    const float og = omm * (G * scale);
+    m = mu * m + og;
+    return bf16_rne(nesterov ? og + mu * m : m);
+  };
+  const int64_t groups = n >> 3;
+  const int64_t gi = my_group<SBP_FUSED_XCD_CHUNK>();
+  if (gi < groups) {
+    u32x4 w[R > 0 ? R : 1];
+    if constexpr (R > 0) load_peers<R>(P, gi, w);
+    float A[8], m[8], G[8];
+    if (ACC) load8(acc, gi, A);
+    load8(mom, gi, m);
+    if constexpr (R > 0) {
+      peer_sum8<R>(w, G);
+      if (ACC) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) G[j] = A[j] + G[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) G[j] = A[j];
+    }
+    uint32_t ub[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ub[j] = one(G[j], m[j]);
+    store8(mom, gi, m);
+    stg(reinterpret_cast<u32x4*>(uout) + gi,
+        u32x4{ub[0] | (ub[1] << 16), ub[2] | (ub[3] << 16), ub[4] | (ub[5] << 16),
+              ub[6] | (ub[7] << 16)});
+  }
+  if (blockIdx.x == 0) {  // the n % 8 tail, element by element
+    const int64_t i = (groups << 3) + threadIdx.x;
+    if (i < n) {
+      float G;
+      if constexpr (R > 0) {
+        G = peer_sum1<R>(P, i);
+        if (ACC) G = acc[i] + G;
+      } else {
+        G = acc[i];
+      }
+      float m = mom[i];
+      uout[i] = static_cast<uint16_t>(one(G, m));
+      mom[i] = m;
+    }
+  }
+}
+
+// ---- update: th' = th*decay - lr*u, bf16 emit --------------------------------
+// Reads 6 and writes 6 bytes per element: bound by HBM.  The fused step's
+// split lane map (two runs of 4 elements per lane), so each 16-byte fp32
+// access of a wave covers one contiguous kilobyte.
+__global__ void __launch_bounds__(kBlock)
+update_kernel(const uint16_t* __restrict__ u, float* __restrict__ master,
+              uint16_t* __restrict__ pout, int64_t n, float decay, float lr) {
+  const int64_t full = (n >> 3) << 3;
+  const int wv = threadIdx.x >> 6, ln = threadIdx.x & 63;
+  const int64_t tile0 = static_cast<int64_t>(my_tile<SBP_FUSED_XCD_CHUNK>()) * (kBlock * 8);
+  const int64_t e[2] = {tile0 + wv * 512 + ln * 4, tile0 + wv * 512 + 256 + ln * 4};
+  // a run of 4 lies wholly inside or outside [0, full): full is a multiple of 8
+  const bool ok[2] = {e[0] < full, e[1] < full};
+  u32x2 w[2];
+  f32x4 T[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if (ok[c]) {
+      w[c] = ldg(reinterpret_cast<const u32x2*>(u + e[c]));
+      T[c] = ldg(reinterpret_cast<const f32x4*>(master + e[c]));
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    if (ok[c]) {
+      float x[4], th[4];
+      uint32_t pb[4];
+      bf16x4(w[c], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        th[j] = T[c][j] * decay - lr * x[j];
+        pb[j] = bf16_rne(th[j]);
+      }
+      stg(reinterpret_cast<f32x4*>(master + e[c]), f32x4{th[0], th[1], th[2], th[3]});
+      stg(reinterpret_cast<u32x2*>(pout + e[c]),
+          u32x2{pb[0] | (pb[1] << 16), pb[2] | (pb[3] << 16)});
+    }
+  }
+  if (blockIdx.x == 0) {  // the n % 8 tail, element by element
+    const int64_t i = full + threadIdx.x;
+    if (i < n) {
+      const float th = master[i] * decay - lr * bf16_one(u[i]);
+      master[i] = th;
       pout[i] = static_cast<uint16_t>(bf16_rne(th));
     }
   }
@@ -1030,6 +1129,80 @@ sbp_status sbp_adamw_shard_grouped(const void* const* peers, int32_t R, const fl
     ga.decay[k] = sk.decay;
   }
   return launch_fused<true>(who, P, R, acc, scale, master, m, v, param_out, n, s, ga, stream);
+}
+
+sbp_status sbp_momentum_shard(const void* const* peers, int32_t R, const float* acc, float scale,
+                              float* m, void* u_out, int64_t n, float mu, int32_t nesterov,
+                              hipStream_t stream) {
+  const char* who = "sbp_momentum_shard";
+  const std::string w(who);
+  if (R < 0 || R > SBP_MAX_PEERS) return sbp::fail(SBP_EINVAL, w + ": R must be in 0..16");
+  if (n < 0) return sbp::fail(SBP_EINVAL, w + ": n < 0");
+  if (!(mu >= 0.0f && mu < 1.0f)) return sbp::fail(SBP_EINVAL, w + ": mu must be in [0, 1)");
+  if (n == 0) return sbp::ok();  // nothing is read or written
+  Peers P;
+  sbp_status st = collect_peers(who, peers, R, P);
+  if (st != SBP_OK) return st;
+  if (R == 0 && acc == nullptr)
+    return sbp::fail(SBP_EINVAL, w + ": R == 0 needs an accumulator");
+  if (m == nullptr || u_out == nullptr)
+    return sbp::fail(SBP_EINVAL, w + ": null momentum or output pointer");
+  if ((acc && !sbp::aligned(acc, 16)) || !sbp::aligned(m, 16) || !sbp::aligned(u_out, 16))
+    return sbp::fail(SBP_EALIGN, w + ": device pointers must be 16-byte aligned");
+  if (n > SBP_MAX_SHARD_NUMEL) return sbp::fail(SBP_ERANGE, w + ": n above SBP_MAX_SHARD_NUMEL");
+  // pairwise disjoint: m, u_out, acc and the peers
+  const void* ptr[3 + SBP_MAX_PEERS];
+  int64_t len[3 + SBP_MAX_PEERS];
+  int k = 0;
+  ptr[k] = m; len[k++] = 4 * n;
+  ptr[k] = u_out; len[k++] = 2 * n;
+  ptr[k] = acc; len[k++] = acc ? 4 * n : 0;
+  for (int32_t r = 0; r < R; ++r) { ptr[k] = peers[r]; len[k++] = 2 * n; }
+  for (int a = 0; a < 2; ++a)  // the two outputs against everything else
+    for (int b = a + 1; b < k; ++b)
+      if (sbp::overlaps(ptr[a], len[a], ptr[b], len[b]))
+        return sbp::fail(SBP_EINVAL, w + ": buffers overlap");
+  const float omm = static_cast<float>(1.0 - static_cast<double>(mu));
+  uint16_t* uo = static_cast<uint16_t*>(u_out);
+  const int lane_bytes = 16 * R + 32 + (acc ? 32 : 0);
+  (void)hipGetLastError();
+  return dispatch_r(R, [&](auto rc) -> sbp_status {
+    constexpr int RR = decltype(rc)::value;
+    auto go = [&](auto kernel) {
+      return launch(who, kernel, n, lane_bytes, stream, P, acc, scale, m, uo, n, mu, omm,
+                    nesterov != 0);
+    };
+    if constexpr (RR == 0) {
+      return go(momentum_kernel<0, true>);
+    } else if (acc) {
+      return go(momentum_kernel<RR, true>);
+    } else {
+      return go(momentum_kernel<RR, false>);
+    }
+  });
+}
+
+sbp_status sbp_update_shard(const void* u, float* master, void* param_out, int64_t n, float lr,
+                            float weight_decay, hipStream_t stream) {
+  const char* who = "sbp_update_shard";
+  if (n < 0) return sbp::fail(SBP_EINVAL, "sbp_update_shard: n < 0");
+  if (!valid_lr_wd(lr, weight_decay))
+    return sbp::fail(SBP_EINVAL, "sbp_update_shard: lr and weight_decay must be finite and >= 0");
+  if (n == 0) return sbp::ok();  // nothing is read or written
+  if (u == nullptr || master == nullptr || param_out == nullptr)
+    return sbp::fail(SBP_EINVAL, "sbp_update_shard: null pointer");
+  if (!sbp::aligned(u, 16) || !sbp::aligned(master, 16) || !sbp::aligned(param_out, 16))
+    return sbp::fail(SBP_EALIGN, "sbp_update_shard: device pointers must be 16-byte aligned");
+  if (n > SBP_MAX_SHARD_NUMEL)
+    return sbp::fail(SBP_ERANGE, "sbp_update_shard: n above SBP_MAX_SHARD_NUMEL");
+  if (sbp::overlaps(u, 2 * n, master, 4 * n) || sbp::overlaps(u, 2 * n, param_out, 2 * n) ||
+      sbp::overlaps(master, 4 * n, param_out, 2 * n))
+    return sbp::fail(SBP_EINVAL, "sbp_update_shard: buffers overlap");
+  const float decay =
+      static_cast<float>(1.0 - static_cast<double>(lr) * static_cast<double>(weight_decay));
+  (void)hipGetLastError();
+  return launch(who, update_kernel, n, 48, stream, static_cast<const uint16_t*>(u), master,
+                static_cast<uint16_t*>(param_out), n, decay, lr);
 }
 
 // Groups of 8 per lane of the squared-norm pass for `lane_bytes` of loads per
