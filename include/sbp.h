@@ -482,7 +482,7 @@ sbp_status sbp_clip_scale(double total_sq, float max_norm, float scale,
  *   device bf16[n]; 16-byte aligned, pairwise disjoint; lr and weight_decay
  *   finite and >= 0.  Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE
  *   (n > SBP_MAX_SHARD_NUMEL), SBP_EHIP.
- * ---------------------------------------------------------------------- */
+ */
 sbp_status sbp_momentum_shard(const void* const* peers, int32_t R,
                               const float* acc, float scale, float* m,
                               void* u_out, int64_t n, float mu,
@@ -490,6 +490,72 @@ sbp_status sbp_momentum_shard(const void* const* peers, int32_t R,
 sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
                             int64_t n, float lr, float weight_decay,
                             hipStream_t stream);
+
+/*
+ * sbp_newton_schulz: orthogonalises weight-matrix updates.  For each matrix U
+ *   (rows x cols), in exact arithmetic:
+ *     X = U / max(|U|_F, eps)
+ *     steps times:  A = X X',  X = a X + (b A + c A A) X
+ *     out = bf16_rne(out_scale * X)
+ *   (for rows > cols the same with X' X on the short side: both give the same
+ *   X).  An odd polynomial of X, it moves every singular value towards 1 and
+ *   keeps the singular vectors.  The usual coefficients are (3.4445, -4.7750,
+ *   2.0315) with 5 steps; each step has its own triple.
+ *   Products run on fp16 matrix instructions with binary32 accumulation; the
+ *   entries of X, A and b A + c A A must stay below 16, 16 and 64 (a and b, c
+ *   of the size above do; larger ones give infinities, then NaN).  Relative
+ *   error in the 2-norm against exact arithmetic, the output's rounding to
+ *   bf16 included: about 2e-3.  Results are the same from run to run, and do
+ *   not depend on the other matrices of the call or on the tile sizes beyond
+ *   that error.  A matrix of zeros gives zeros; one with a NaN or an infinity
+ *   gives NaN throughout, and leaves the others alone.
+ *
+ *   groups      host array of n_groups groups of equal matrices:
+ *     in, out     first matrix of the group, device bf16, row-major, 2-byte
+ *                 aligned (16-byte rows take the vector path); out may be in
+ *                 itself (the same pointer and distances), else no output
+ *                 overlaps an input or another output; column blocks of one
+ *                 buffer (a common row distance, disjoint columns) are disjoint
+ *     in_ld, out_ld          elements from one row to the next, >= cols
+ *     in_stride, out_stride  elements from one matrix to the next, >= 0
+ *                            (read if count > 1)
+ *     rows, cols, count      >= 0; a group with a zero is skipped
+ *     out_scale              finite; multiplies the result
+ *   hp          steps in 1..SBP_NS_MAX_STEPS; eps finite and >= 0; coefs:
+ *               a, b, c of each step, magnitudes up to SBP_NS_MAX_COEF
+ *   workspace   device memory, 256-byte aligned, workspace_bytes >=
+ *               sbp_newton_schulz_workspace(groups, n_groups); written before
+ *               read, so it needs no clearing; calls that may overlap in time
+ *               need one each
+ *   Large calls run in parts that use the workspace one after the other.
+ *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE, SBP_EHIP.
+ * sbp_newton_schulz_workspace (host): bytes for these groups (their pointers
+ *   and distances are not read), or -1 if their sizes are refused.
+ * ---------------------------------------------------------------------- */
+#define SBP_NS_MAX_STEPS 16
+#define SBP_NS_MAX_DIM 1048576        /* rows, cols, count                   */
+#define SBP_NS_MAX_NUMEL 4294967296LL /* elements of one matrix              */
+#define SBP_NS_MAX_LD 1099511627776LL /* elements between rows               */
+#define SBP_NS_MAX_COEF 64
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t rows, cols, count;
+  int64_t in_ld, out_ld;
+  int64_t in_stride, out_stride;
+  float out_scale;
+} sbp_matrices;
+typedef struct {
+  int32_t steps;
+  float eps;
+  float coefs[3 * SBP_NS_MAX_STEPS];
+} sbp_ns_hparams;
+
+int64_t sbp_newton_schulz_workspace(const sbp_matrices* groups,
+                                    int32_t n_groups);
+sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
+                             const sbp_ns_hparams* hp, void* workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Spread arena: device memory for a rank's shard state and receive buffers

@@ -341,3 +341,50 @@ def update_step(u, master, lr, weight_decay):
     decay = F32(1.0 - float(lr32) * float(F32(weight_decay)))
     th = np.asarray(master, F32) * decay - lr32 * bf16_to_f32(u)
     return th, f32_to_bf16(th)
+
+
+def newton_schulz(U, steps, coefs, eps=1e-7, out_scale=1.0):
+    """The Newton-Schulz iteration in float64, before the output's rounding.
+
+    X = U / max(|U|_F, eps); per step A = X X', X = a X + (b A + c A A) X, for
+    any shape (the iteration commutes with transposition).  coefs: one (a, b,
+    c), or one per step.  U: float64 matrix.
+    """
+    X = np.asarray(U, np.float64)
+    if X.shape[0] > X.shape[1]:
+        return newton_schulz(X.T, steps, coefs, eps, out_scale).T
+    coefs = [coefs] * steps if np.ndim(coefs[0]) == 0 else coefs
+    with np.errstate(all="ignore"):
+        norm = np.sqrt(np.sum(X * X))
+        X = X / (norm if not norm < F32(eps) else float(F32(eps)))  # a NaN norm stays
+        for a, b, c in [[float(F32(x)) for x in t] for t in coefs]:
+            A = X @ X.T
+            X = a * X + (b * A + c * (A @ A)) @ X
+        return float(F32(out_scale)) * X
+
+
+def newton_schulz_rounded(U, steps, coefs, eps=1e-7):
+    """The same with X, A and b A + c A A kept in binary16 as the device keeps
+    them (scaled by 2^12, 2^12 and 2^10; X's remainder next to it while three
+    steps remain), all other arithmetic in float64: how far those roundings by
+    themselves move the result."""
+    X = np.asarray(U, np.float64)
+    if X.shape[0] > X.shape[1]:
+        return newton_schulz_rounded(X.T, steps, coefs, eps).T
+    coefs = [coefs] * steps if np.ndim(coefs[0]) == 0 else coefs
+
+    def kept(x, scale):
+        return (x * scale).astype(np.float16).astype(np.float64) / scale
+
+    norm = max(np.sqrt(np.sum(X * X)), float(F32(eps)))
+    X = X / norm
+    whole = X  # the first step's X is exact: bf16 values times a power of two
+    for s, (a, b, c) in enumerate([[float(F32(x)) for x in t] for t in coefs]):
+        A = kept(X @ X.T, 4096.0)
+        new = a * whole + kept(b * A + c * (A @ A), 1024.0) @ X
+        if s == steps - 1:
+            return new
+        X = kept(new, 4096.0)
+        rest = kept(new - X, 4096.0 * 2048.0) if steps - 1 - s >= 3 else 0.0
+        whole = X + rest
+    return X

@@ -44,13 +44,16 @@ EXPORTS = (
     "sbp_unpack_params", "sbp_shard_of", "sbp_gather_shards", "sbp_bucket_plan_per_tensor",
     "sbp_group_runs", "sbp_adamw_shard_grouped", "sbp_unpack_shards",
     "sbp_grad_sq_norm_noalloc", "sbp_arena_create", "sbp_arena_info", "sbp_arena_free",
-    "sbp_momentum_shard", "sbp_update_shard",
+    "sbp_momentum_shard", "sbp_update_shard", "sbp_newton_schulz_workspace",
+    "sbp_newton_schulz",
 )
 
 MAX_GROUPS = 8
 NOALLOC_SCRATCH_DOUBLES = 1 << 20  # SBP_NOALLOC_SCRATCH_DOUBLES
 NOALLOC_MAX_NUMEL = 2146435079  # SBP_NOALLOC_MAX_NUMEL
 ARENA_MAX_ARRAYS = 64  # SBP_ARENA_MAX_ARRAYS
+NS_MAX_STEPS = 16  # SBP_NS_MAX_STEPS
+NS_COEFS = (3.4445, -4.7750, 2.0315)  # the usual quintic's a, b, c
 
 
 class SbpError(RuntimeError):
@@ -77,6 +80,34 @@ class AdamWHParams(ctypes.Structure):
 
 class GroupHParams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class Matrices(ctypes.Structure):
+    """A group of equal matrices (sbp_matrices)."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("count", ctypes.c_int64),
+                ("in_ld", ctypes.c_int64), ("out_ld", ctypes.c_int64),
+                ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("out_scale", ctypes.c_float)]
+
+
+class NsHParams(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("coefs", ctypes.c_float * (3 * NS_MAX_STEPS))]
+
+    @classmethod
+    def of(cls, steps, coefs, eps, what):
+        """steps and one (a, b, c) for all of them, or one per step."""
+        steps = int(steps)
+        if not 1 <= steps <= NS_MAX_STEPS:
+            raise ValueError(f"{what}: steps must be in 1..{NS_MAX_STEPS}")
+        rows = [tuple(c) for c in coefs] if hasattr(coefs[0], "__len__") else [tuple(coefs)] * steps
+        if len(rows) != steps or any(len(r) != 3 for r in rows):
+            raise ValueError(f"{what}: coefs must be (a, b, c), or one such triple per step")
+        h = cls(steps, float(eps))
+        for i, r in enumerate(rows):
+            h.coefs[3 * i:3 * i + 3] = [float(x) for x in r]
+        return h
 
 
 _lib = None
@@ -134,6 +165,11 @@ def lib():
                                 ctypes.c_int32, ctypes.c_void_p], st),
         "sbp_update_shard": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                               ctypes.c_float, ctypes.c_float, ctypes.c_void_p], st),
+        "sbp_newton_schulz_workspace": ([ctypes.POINTER(Matrices), ctypes.c_int32],
+                                        ctypes.c_int64),
+        "sbp_newton_schulz": ([ctypes.POINTER(Matrices), ctypes.c_int32,
+                               ctypes.POINTER(NsHParams), ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_void_p], st),
         "sbp_arena_create": ([_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                               ctypes.c_uint64, _vpp, ctypes.POINTER(ctypes.c_void_p)], st),
         "sbp_arena_info": ([ctypes.c_void_p, _i64p, _i64p, _i64p], st),
@@ -644,6 +680,101 @@ def update_shard(u, master, param_out, lr, weight_decay=0.0, stream=None):
         _dev(u, 2, "update_shard u"), _f32(master, "update_shard master"),
         _dev(param_out, 2, "update_shard param_out"), n, float(lr), float(weight_decay),
         _stream(stream, master)))
+
+
+def _matrix_groups(mats, outs, out_scales, what):
+    """sbp_matrices of a list of 2-D or 3-D bf16 device tensors."""
+    import torch
+    if len(outs) != len(mats):
+        raise ValueError(f"{what}: one output per input")
+    scales = list(out_scales) if hasattr(out_scales, "__len__") else [out_scales] * len(mats)
+    if len(scales) != len(mats):
+        raise ValueError(f"{what}: one out_scale, or one per input")
+    arr = (Matrices * max(len(mats), 1))()
+    for g, x, o, sc in zip(arr, mats, outs, scales):
+        if x.shape != o.shape or x.dim() not in (2, 3):
+            raise ValueError(f"{what}: matrices are 2-D, or 3-D for equal ones; outputs match")
+        if x.device != mats[0].device or o.device != mats[0].device:
+            raise ValueError(f"{what}: tensors on different devices")
+        for t in (x, o):
+            if not t.is_cuda:
+                raise ValueError(f"{what}: expected a device tensor")
+            if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+                raise ValueError(f"{what}: expected bf16 (or its 16-bit storage), got {t.dtype}")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{what}: the elements of a row must be consecutive")
+        rows, cols = x.shape[-2:]
+        g.in_, g.out = x.data_ptr(), o.data_ptr()
+        g.rows, g.cols, g.count = rows, cols, x.shape[0] if x.dim() == 3 else 1
+        # torch leaves the distance of a dimension of one element open
+        g.in_ld = x.stride(-2) if rows > 1 else max(cols, 1)
+        g.out_ld = o.stride(-2) if rows > 1 else max(cols, 1)
+        if g.count > 1:
+            g.in_stride, g.out_stride = x.stride(0), o.stride(0)
+        g.out_scale = float(sc)
+    return arr
+
+
+def newton_schulz_workspace(mats):
+    """Bytes of workspace sbp_newton_schulz needs for these 2-D or 3-D tensors."""
+    arr = (Matrices * max(len(mats), 1))()
+    for g, x in zip(arr, mats):
+        g.rows, g.cols = x.shape[-2:]
+        g.count = x.shape[0] if x.dim() == 3 else 1
+    return _ns_workspace_bytes(arr, len(mats))
+
+
+def _ns_workspace_bytes(arr, n):
+    need = lib().sbp_newton_schulz_workspace(arr, n)
+    if need < 0:
+        raise SbpError(SBP_EINVAL, lib().sbp_last_error().decode())
+    return int(need)
+
+
+def newton_schulz(mats, out=None, steps=5, coefs=NS_COEFS, eps=1e-7, out_scales=1.0,
+                  workspace=None, stream=None):
+    """sbp_newton_schulz: each matrix orthogonalised (see include/sbp.h).
+
+    mats: list of bf16 device tensors, 2-D, or 3-D for equal matrices; rows may
+    be further apart than they are long.  out: tensors of the same shapes, or
+    the inputs themselves (in place); new contiguous ones when not given.
+    out_scales: one factor, or one per list entry.  coefs: one (a, b, c), or
+    one per step.  workspace: a device tensor of at least
+    newton_schulz_workspace(mats) bytes; allocated with torch when not given.
+    Returns the outputs.
+    """
+    import torch
+    what = "newton_schulz"
+    mats = list(mats)
+    h = NsHParams.of(steps, coefs, eps, what)
+    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in mats] \
+        if out is None else list(out)
+    arr = _matrix_groups(mats, outs, out_scales, what)
+    if not mats:
+        return outs
+    need = _ns_workspace_bytes(arr, len(mats))
+    s = _stream(stream, mats[0])
+    dev = mats[0].device
+    if stream is not None:
+        # the caching allocator reuses memory in the order of the stream it was
+        # taken on: take the workspace on the call's, and tell it of the outputs
+        on = torch.cuda.ExternalStream(s.value, device=dev) if s.value else \
+            torch.cuda.default_stream(dev)
+        if out is None:
+            for o in outs:
+                o.record_stream(on)
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(on):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or \
+            workspace.device != dev:
+        raise ValueError(f"{what}: workspace must be a contiguous tensor on the matrices' device")
+    _check(lib().sbp_newton_schulz(arr, len(mats), ctypes.byref(h), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), s))
+    return outs
 
 
 def unpack_params(plan, flat, params, bucket=-1, stream=None):

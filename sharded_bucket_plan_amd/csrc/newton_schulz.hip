@@ -1,0 +1,882 @@
+// Newton-Schulz orthogonalisation of weight-matrix updates on CDNA4 (gfx950).
+//
+// Per matrix U (rows x cols), with X on its short side (m <= n; X = U, or U'
+// where rows > cols):
+//   X_0 = U / max(|U|_F, eps)
+//   A = X X',  B = b A + c A^2,  X <- a X + B X      (steps times)
+//   out = bf16(out_scale * X)
+//
+// Three products per step, all of the one form C = P Q' with both operands'
+// k index contiguous: X is kept twice, as X (m x n) and as Y = X' (n x m), so
+//   gram   A  = X X'          lower-triangle tiles only, mirrored on the way out
+//   poly   B  = b A + c A A'  (A is symmetric) likewise
+//   apply  Y' = a Y + Y B'    written as Y' and, transposed, as X
+// and one kernel core serves the three, with the additions, scalings and the
+// transposed copy in its epilogue.  A second copy of X costs 2 bytes per
+// element and step; reading X against its storage order instead would cost
+// transposing LDS reads in the inner loop of a third of the flops.
+//
+// Numbers.  The products run on fp16 MFMA with binary32 accumulation: fp16
+// keeps 11 significand bits where bf16 keeps 8, at the same rate, and every
+// operand has a known range that a power of two places inside fp16's:
+//   X_0     U * 2^k with the Frobenius norm in [2^13, 2^14): exact for bf16
+//           U down to 2^-28 of the norm; the rest of the normalisation, rho =
+//           1 / (max(norm, eps) 2^k), multiplies the accumulators of step 1
+//   X, Y    * 2^12 (entries up to 16); a matrix whose norm lies below eps
+//           gets a further power of two that its iterates cannot outgrow
+//   A       * 2^12,  B * 2^10
+// The step's amplification of small singular values (a^steps ~ 485) would
+// amplify X's rounding noise as well.  The noise that matters reaches them
+// only through the term a X, since B's share of it is multiplied by B, small
+// on exactly those directions; so while at least three steps remain, X's
+// rounding remainder is kept next to it (fp16, * 2^11) and a X is formed from
+// both parts.  Against the iteration in 64 bits, for 5 steps on spectra from
+// flat to rank 16 plus noise of 0.003: relative error 2e-4 .. 1.6e-3 before
+// the output's rounding (1.7e-3 by itself); without the remainder up to
+// 2.6e-2, with bf16 products 7e-3 .. 2e-1.
+// The squared norm is summed in float64 in a fixed order, so results are the
+// same from run to run.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+#include <vector>
+
+#include "bf16.h"
+#include "internal.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBlock = 256;
+constexpr int kXcds = 8;
+constexpr int kPad = 64;        // both padded sides are multiples of this
+constexpr int kBK = 64;         // k elements per staged slice: 128 bytes a row
+constexpr int kMaxGroups = 16;  // groups of equal matrices per launch
+constexpr int kMaxNormBlocks = 256;
+constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 1024.0f, kScaleLo = 2048.0f;
+
+// Per-matrix scalars, written by the prologue.
+// Stored X_0 = X_0 / rho, stored X_k = X_k * sx for k >= 1.
+struct Scal {
+  float gram_first, gram;  // accumulator -> stored A: rho^2 * 2^12, 2^12 / sx^2
+  float apply_first;       // step 1's accumulator -> stored X_1: rho * sx
+  float inv_sx;
+};
+
+// One group: `count` matrices of one shape, at equal distances.
+struct Group {
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t in_ld, out_ld, in_stride, out_stride;
+  _Float16* base;    // X, Y, Y2, L (count*m*n each), A, B (count*m*m each)
+  double* partial;   // count * norm_blocks
+  Scal* scal;        // count
+  int32_t rows, cols, count;
+  int32_t m, n;      // padded short and long side
+  int32_t norm_blocks;
+  float out_scale;
+  int32_t in_vec, out_vec;  // 16-byte rows
+  uint32_t t_norm, t_pro, t_gram, t_apply;  // first block of the group in each launch
+
+  __host__ __device__ bool tall() const { return rows > cols; }
+  __device__ int64_t mn() const { return static_cast<int64_t>(m) * n; }
+  __device__ _Float16* X(int item) const { return base + item * mn(); }
+  __device__ _Float16* Y(int which, int item) const {
+    return base + (static_cast<int64_t>(1 + which) * count + item) * mn();
+  }
+  __device__ _Float16* L(int item) const {
+    return base + (static_cast<int64_t>(3) * count + item) * mn();
+  }
+  __device__ _Float16* A(int which, int item) const {
+    return base + static_cast<int64_t>(4) * count * mn() +
+           (static_cast<int64_t>(which) * count + item) * m * m;
+  }
+};
+
+struct Groups {
+  Group g[kMaxGroups];
+  int32_t n;
+};
+
+struct Step {
+  float a, b, c, eps;
+  int32_t grow;   // the iterates of a matrix grow by less than 2^grow in all
+  int32_t first, last, lo_in, lo_out;
+  int32_t yin;    // which of the two Y copies this step reads
+};
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = x + __shfl_xor(x, off, 64);
+  return x;
+}
+
+// Sum over the block in a fixed order, in every thread.
+__device__ __forceinline__ double block_sum_all(double x) {
+  __shared__ double per_wave[kBlock / 64];
+  x = wave_sum(x);
+  if ((threadIdx.x & 63) == 0) per_wave[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < kBlock / 64; ++w) t = t + per_wave[w];
+  return t;
+}
+
+// Up to 8 consecutive bf16 values of a row, zeros from `left` on.
+__device__ __forceinline__ u32x4 load_row8(const uint16_t* p, int left, bool vec) {
+  if (vec && left >= 8) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 w{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+  return w;
+}
+
+// ---- squared norms: one float64 partial per block ----------------------------
+// A wave takes one row's 512 columns at a time; block b of a matrix's
+// norm_blocks takes units b*4 + wave, then every norm_blocks*4 further on.
+__global__ void __launch_bounds__(kBlock) ns_norm_kernel(Groups gs) {
+  int gi = 0;
+  while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_norm) ++gi;
+  const Group& g = gs.g[gi];
+  const int local = blockIdx.x - g.t_norm;
+  const int item = local / g.norm_blocks, nb = local % g.norm_blocks;
+  const uint16_t* in = g.in + item * g.in_stride;
+  const int segs = (g.cols + 511) / 512;
+  const int64_t units = static_cast<int64_t>(g.rows) * segs;
+  const int lane = threadIdx.x & 63;
+  double sum = 0.0;
+  for (int64_t u = nb * 4 + (threadIdx.x >> 6); u < units; u += g.norm_blocks * 4) {
+    const int64_t row = u / segs;
+    const int col = static_cast<int>(u % segs) * 512 + lane * 8;
+    if (col < g.cols) {
+      const u32x4 w = load_row8(in + row * g.in_ld + col, g.cols - col, g.in_vec);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const double x = sbp::bf16_lo(w[q]), y = sbp::bf16_hi(w[q]);
+        sum = sum + x * x;
+        sum = sum + y * y;
+      }
+    }
+  }
+  sum = block_sum_all(sum);
+  if (threadIdx.x == 0) g.partial[local] = sum;
+}
+
+// ---- prologue: X_0 and Y_0 in fp16, zero-padded ---------------------------------
+// One block per 64 x 64 tile of the padded input, transposed through LDS.
+__global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float eps, int grow) {
+  int gi = 0;
+  while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_pro) ++gi;
+  const Group& g = gs.g[gi];
+  const int pr = g.tall() ? g.n : g.m, pc = g.tall() ? g.m : g.n;  // padded rows, cols
+  const int tc = pc / 64, per = (pr / 64) * tc;
+  const int local = blockIdx.x - g.t_pro;
+  const int item = local / per, t = local % per;
+  const int r0 = t / tc * 64, c0 = t % tc * 64;
+
+  double sq = 0.0;
+  for (int i = threadIdx.x; i < g.norm_blocks; i += kBlock)
+    sq = sq + g.partial[item * g.norm_blocks + i];
+  const double norm = sqrt(block_sum_all(sq));
+  // norm * 2^k in [2^13, 2^14); 0 for a zero, infinite or NaN norm
+  const bool plain = norm > 0.0 && norm < __builtin_huge_val();
+  const int k = plain ? 13 - ilogb(norm) : 0;
+  const double floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
+  if (t == 0 && threadIdx.x == 0) {
+    int below = plain && norm < eps ? ilogb(static_cast<double>(eps)) - ilogb(norm) : 0;
+    below = below > grow + 2 ? below - grow - 2 : 0;
+    below = below < 100 ? below : 100;
+    const double rho = 1.0 / (floor_norm * ldexp(1.0, k));
+    const double sx = ldexp(static_cast<double>(kScaleX), below);
+    g.scal[item] = Scal{static_cast<float>(rho * rho * kScaleA),
+                        static_cast<float>(kScaleA / (sx * sx)), static_cast<float>(rho * sx),
+                        static_cast<float>(1.0 / sx)};
+  }
+
+  __shared__ _Float16 tile[64][64 + 8];
+  _Float16* direct = g.tall() ? g.Y(0, item) : g.X(item);
+  _Float16* across = g.tall() ? g.X(item) : g.Y(0, item);
+  const uint16_t* in = g.in + item * g.in_stride;
+  const int cg = (threadIdx.x & 7) * 8;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int r = p * 32 + (threadIdx.x >> 3), row = r0 + r, col = c0 + cg;
+    u32x4 w{0, 0, 0, 0};
+    if (row < g.rows && col < g.cols)
+      w = load_row8(in + row * g.in_ld + col, g.cols - col, g.in_vec);
+    f16x8 h;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      h[2 * q] = static_cast<_Float16>(ldexpf(sbp::bf16_lo(w[q]), k));
+      h[2 * q + 1] = static_cast<_Float16>(ldexpf(sbp::bf16_hi(w[q]), k));
+    }
+    *reinterpret_cast<f16x8*>(direct + static_cast<int64_t>(row) * pc + col) = h;
+    *reinterpret_cast<f16x8*>(&tile[r][cg]) = h;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int c = p * 32 + (threadIdx.x >> 3);
+    f16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = tile[cg + j][c];
+    *reinterpret_cast<f16x8*>(across + static_cast<int64_t>(c0 + c) * pr + r0 + cg) = h;
+  }
+}
+
+// ---- the product ------------------------------------------------------------------
+
+enum Mode { kGram, kPoly, kApply };
+
+// One T x T tile of C = P Q' per block of 4 waves (2 x 2, each T/2 square, in
+// 32 x 32 MFMA tiles).  Slices of 64 k elements go straight from memory to
+// one of two LDS buffers while the other is multiplied; a row's eight 16-byte
+// pieces are stored rotated by row (piece ^ row mod 8), which the lanes'
+// global addresses bring about, so that reads of one piece of many rows
+// spread over the banks.
+template <int T>
+struct Tile {
+  static constexpr int kRowBytes = kBK * 2;
+  static constexpr int kBuf = 2 * T * kRowBytes;  // P rows, then Q rows
+  static constexpr int kSub = T / 64;             // 32 x 32 tiles per wave and side
+  static constexpr int kRounds = T / 32;          // staging rounds per operand
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const _Float16* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(p), 0,
+                                           static_cast<int>(bytes), 0x00027000);
+}
+
+template <int T>
+__device__ __forceinline__ void stage(char* buf, __amdgpu_buffer_rsrc_t P,
+                                      __amdgpu_buffer_rsrc_t Q, int wave, int voff,
+                                      int round_bytes, int koff) {
+#pragma unroll
+  for (int r = 0; r < Tile<T>::kRounds; ++r)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        P, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16, voff,
+        r * round_bytes + koff, 0, 0);
+#pragma unroll
+  for (int r = 0; r < Tile<T>::kRounds; ++r)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        Q,
+        (__attribute__((address_space(3))) void*)(buf + Tile<T>::kBuf / 2 + (r * 4 + wave) * 1024),
+        16, voff, r * round_bytes + koff, 0, 0);
+}
+
+// Everything this wave has asked of memory and LDS is done, then everyone's.
+__device__ __forceinline__ void slice_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int T>
+struct Frags {
+  f16x8 p[Tile<T>::kSub], q[Tile<T>::kSub];
+};
+
+template <int T>
+__device__ __forceinline__ void read_frags(const char* buf, int pbase, int qbase, int piece,
+                                           Frags<T>& f) {
+#pragma unroll
+  for (int i = 0; i < Tile<T>::kSub; ++i) {
+    f.p[i] = *reinterpret_cast<const f16x8*>(buf + pbase + piece + i * 32 * Tile<T>::kRowBytes);
+    f.q[i] = *reinterpret_cast<const f16x8*>(buf + qbase + piece + i * 32 * Tile<T>::kRowBytes);
+  }
+}
+
+template <int T>
+using Acc = f32x16[Tile<T>::kSub][Tile<T>::kSub];
+
+template <int T>
+__device__ __forceinline__ void multiply(const Frags<T>& f, Acc<T>& acc) {
+#pragma unroll
+  for (int i = 0; i < Tile<T>::kSub; ++i)
+#pragma unroll
+    for (int j = 0; j < Tile<T>::kSub; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+}
+
+// Column of the fp32 slab in LDS where (row, col) is kept: groups of 8 columns
+// are rotated by the row's 8-row group, so that both a row's 8 columns and a
+// column's 8 rows are read without bank conflicts.
+__device__ __forceinline__ int slab_col(int row, int col) {
+  return col ^ (((row >> 3) & 7) << 3);
+}
+
+template <int T, Mode M>
+__global__ void __launch_bounds__(kBlock, 2)
+ns_product_kernel(Groups gs, Step st, unsigned total) {
+  __shared__ __align__(16) char buf0[Tile<T>::kBuf];
+  __shared__ __align__(16) char buf1[Tile<T>::kBuf];
+  constexpr int W = T / 2;  // a wave's side
+
+  // neighbouring tiles to one XCD: its L2 then holds the rows they share
+  unsigned b = blockIdx.x;
+  const unsigned per_xcd = total / kXcds;
+  if (b < per_xcd * kXcds) b = (b % kXcds) * per_xcd + b / kXcds;
+  int gi = 0;
+  while (gi + 1 < gs.n && b >= (M == kApply ? gs.g[gi + 1].t_apply : gs.g[gi + 1].t_gram)) ++gi;
+  const Group& g = gs.g[gi];
+  const int m = g.m, n = g.n;
+  const int tm = (m + T - 1) / T;
+  int item, ti, tj;  // tile row (of P) and column (rows of Q)
+  if constexpr (M == kApply) {
+    const int tn = (n + T - 1) / T;
+    const int local = b - g.t_apply;
+    item = local / (tn * tm);
+    const int t = local % (tn * tm);
+    // strips of 8 tile rows, column by column
+    constexpr int kStrip = 8;
+    const int strip = t / (kStrip * tm), left = tn - strip * kStrip;
+    const int high = left < kStrip ? left : kStrip;
+    const int s = t - strip * kStrip * tm;
+    ti = strip * kStrip + s % high;
+    tj = s / high;
+  } else {
+    const int per = tm * (tm + 1) / 2;
+    const int local = b - g.t_gram;
+    item = local / per;
+    const int t = local % per;
+    ti = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (ti * (ti + 1) / 2 > t) --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+    tj = t - ti * (ti + 1) / 2;
+  }
+
+  const int k = M == kGram ? n : m;  // contracted length = both row lengths
+  const _Float16* Pm = M == kGram ? g.X(item) : M == kPoly ? g.A(0, item) : g.Y(st.yin, item);
+  const _Float16* Qm = M == kGram ? Pm : M == kPoly ? Pm : g.A(1, item);
+  const int prows = M == kApply ? n : m;
+  const int r0 = ti * T, c0 = tj * T;
+  const int pr = prows - r0 < T ? prows - r0 : T, qr = m - c0 < T ? m - c0 : T;
+  const __amdgpu_buffer_rsrc_t P =
+      rows_of(Pm + static_cast<int64_t>(r0) * k, static_cast<int64_t>(pr) * k * 2);
+  const __amdgpu_buffer_rsrc_t Q =
+      rows_of(Qm + static_cast<int64_t>(c0) * k, static_cast<int64_t>(qr) * k * 2);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wr = wave >> 1, wc = wave & 1;
+  const int voff = (wave * 8 + (lane >> 3)) * k * 2 + (((lane & 7) ^ (lane >> 3)) * 16);
+  const int round_bytes = 32 * k * 2;
+  const int pbase = (wr * W + (lane & 31)) * Tile<T>::kRowBytes;
+  const int qbase = Tile<T>::kBuf / 2 + (wc * W + (lane & 31)) * Tile<T>::kRowBytes;
+  int piece[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) piece[s] = ((s * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+
+  Acc<T> acc = {};
+  Frags<T> f[2];
+  const int slices = k / kBK;
+  stage<T>(buf0, P, Q, wave, voff, round_bytes, 0);
+  slice_barrier();
+  read_frags<T>(buf0, pbase, qbase, piece[0], f[0]);
+  // Slice s is in `cur`, its first fragments in f[0].  The barrier sits before
+  // the last multiply, whose time hides the first read of the next slice.
+  auto slice = [&](const char* cur, char* nxt, int s) {
+    const bool more = s + 1 < slices;
+    if (more) stage<T>(nxt, P, Q, wave, voff, round_bytes, (s + 1) * (kBK * 2));
+    read_frags<T>(cur, pbase, qbase, piece[1], f[1]);
+    multiply<T>(f[0], acc);
+    read_frags<T>(cur, pbase, qbase, piece[2], f[0]);
+    multiply<T>(f[1], acc);
+    read_frags<T>(cur, pbase, qbase, piece[3], f[1]);
+    multiply<T>(f[0], acc);
+    __builtin_amdgcn_sched_barrier(0);
+    slice_barrier();
+    if (more) read_frags<T>(nxt, pbase, qbase, piece[0], f[0]);
+    multiply<T>(f[1], acc);
+  };
+  for (int s = 0; s < slices; s += 2) {
+    slice(buf0, buf1, s);
+    if (s + 1 < slices) slice(buf1, buf0, s + 1);
+  }
+  __syncthreads();
+
+  // Epilogue, 64 rows at a time: accumulators to LDS as binary32, then row by
+  // row (8 columns a thread) the additions and the direct store, then the
+  // transposed store.
+  float* slab = reinterpret_cast<float*>(buf0);
+  static_assert(64 * T * 4 <= Tile<T>::kBuf, "the slab fits one buffer");
+  const Scal sc = g.scal[item];
+  const bool cross = M == kApply ? (!st.last || !g.tall()) : ti != tj;
+  constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow;
+#pragma unroll
+  for (int sl = 0; sl < T / 64; ++sl) {
+#pragma unroll
+    for (int i = 0; i < Tile<T>::kSub; ++i) {
+      const int rb = wr * Tile<T>::kSub + i;  // 32-row block of the tile
+      if (rb / 2 == sl) {
+#pragma unroll
+        for (int j = 0; j < Tile<T>::kSub; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int row = (rb & 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            const int col = wc * W + j * 32 + (lane & 31);
+            slab[row * T + slab_col(row, col)] = acc[i][j][e];
+          }
+      }
+    }
+    __syncthreads();
+    for (int p = 0; p < 64 / kRowsAtOnce; ++p) {
+      const int row = p * kRowsAtOnce + threadIdx.x / kPerRow;
+      const int col = (threadIdx.x % kPerRow) * 8;
+      const int gr = r0 + sl * 64 + row, gc = c0 + col;
+      if (gr >= prows || gc >= m) continue;
+      float* at = slab + row * T + slab_col(row, col);
+      float v[8];
+      {
+        const f32x4 lo = *reinterpret_cast<f32x4*>(at), hi = *reinterpret_cast<f32x4*>(at + 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = lo[q];
+          v[4 + q] = hi[q];
+        }
+      }
+      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
+      f16x8 h;
+      if constexpr (M == kGram) {
+        const float alpha = st.first ? sc.gram_first : sc.gram;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] = v[q] * alpha;
+          h[q] = static_cast<_Float16>(v[q]);
+        }
+        *reinterpret_cast<f16x8*>(g.A(0, item) + idx) = h;
+      } else if constexpr (M == kPoly) {
+        const f16x8 A = *reinterpret_cast<const f16x8*>(g.A(0, item) + idx);
+        const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] = fb * static_cast<float>(A[q]) + fc * v[q];
+          h[q] = static_cast<_Float16>(v[q]);
+        }
+        *reinterpret_cast<f16x8*>(g.A(1, item) + idx) = h;
+      } else {
+        const f16x8 y = *reinterpret_cast<const f16x8*>(g.Y(st.yin, item) + idx);
+        f16x8 rem{};
+        if (st.lo_in) rem = *reinterpret_cast<const f16x8*>(g.L(item) + idx);
+        const float to = st.last ? g.out_scale * sc.inv_sx : 1.0f;
+        const float f = st.first ? sc.apply_first : 1.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float x = static_cast<float>(y[q]) + static_cast<float>(rem[q]) * (1.0f / kScaleLo);
+          v[q] = (st.a * x + v[q] * (1.0f / kScaleB)) * f;
+          h[q] = static_cast<_Float16>(v[q]);
+        }
+        if (!st.last) {
+          *reinterpret_cast<f16x8*>(g.Y(st.yin ^ 1, item) + idx) = h;
+          if (st.lo_out) {
+            f16x8 l;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              l[q] = static_cast<_Float16>((v[q] - static_cast<float>(h[q])) * kScaleLo);
+            *reinterpret_cast<f16x8*>(g.L(item) + idx) = l;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = v[q] * to;
+          if (g.tall()) {
+            if (gr < g.rows) {
+              uint16_t* o = g.out + item * g.out_stride + gr * g.out_ld + gc;
+              if (g.out_vec && gc + 8 <= g.cols) {
+                u32x4 w;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
+                *reinterpret_cast<u32x4*>(o) = w;
+              } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  if (gc + q < g.cols) o[q] = static_cast<uint16_t>(sbp::bf16_rne(v[q]));
+              }
+            }
+          }
+        }
+      }
+      if (cross) {
+        *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      }
+    }
+    __syncthreads();
+    if (cross) {
+      // 8 threads take the 64 rows of one column, 8 rows each
+      for (int p = 0; p < T / 32; ++p) {
+        const int col = p * 32 + (threadIdx.x >> 3), row = (threadIdx.x & 7) * 8;
+        const int gr = r0 + sl * 64 + row, gc = c0 + col;
+        if (gr >= prows || gc >= m) continue;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = slab[(row + q) * T + slab_col(row + q, col)];
+        if (M == kApply && st.last) {
+          if (gc < g.rows) {  // X is rows x cols here: its row gc, columns gr ..
+            uint16_t* o = g.out + item * g.out_stride + gc * g.out_ld + gr;
+            if (g.out_vec && gr + 8 <= g.cols) {
+              u32x4 w;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
+              *reinterpret_cast<u32x4*>(o) = w;
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (gr + q < g.cols) o[q] = static_cast<uint16_t>(sbp::bf16_rne(v[q]));
+            }
+          }
+        } else {
+          f16x8 h;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
+          _Float16* to = M == kApply ? g.X(item) : g.A(M == kGram ? 0 : 1, item);
+          *reinterpret_cast<f16x8*>(to + static_cast<int64_t>(gc) * prows + gr) = h;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Matrices run in chunks that share one workspace: at most this many padded
+// elements (and kMaxGroups groups), or a single matrix.
+constexpr int64_t kChunkElems = int64_t{1} << 28;
+
+struct Piece {
+  int32_t group;  // caller's group
+  int64_t first, count;
+};
+
+struct Chunk {
+  std::vector<Piece> pieces;
+  int64_t bytes = 0;
+};
+
+struct Shape {
+  int64_t m, n;  // padded short and long side
+  int64_t norm_blocks;
+};
+
+Shape shape_of(const sbp_matrices& g) {
+  Shape s;
+  s.m = up(std::min(g.rows, g.cols), kPad);
+  s.n = up(std::max(g.rows, g.cols), kPad);
+  const int64_t units = g.rows * ((g.cols + 511) / 512);
+  s.norm_blocks = std::max<int64_t>(1, std::min<int64_t>(kMaxNormBlocks, (units + 31) / 32));
+  return s;
+}
+
+// Bytes one piece takes: fp16 arrays, norm partials, scalars (each 256-B aligned).
+int64_t half_bytes(const Shape& s, int64_t count) {
+  return up(2 * count * (4 * s.m * s.n + 2 * s.m * s.m), 256);
+}
+int64_t partial_bytes(const Shape& s, int64_t count) { return up(8 * count * s.norm_blocks, 256); }
+int64_t scal_bytes(int64_t count) { return up(static_cast<int64_t>(sizeof(Scal)) * count, 256); }
+
+std::vector<Chunk> chunks_of(const sbp_matrices* groups, int32_t n_groups) {
+  std::vector<Chunk> out;
+  int64_t room = 0;
+  for (int32_t i = 0; i < n_groups; ++i) {
+    const sbp_matrices& g = groups[i];
+    if (g.rows == 0 || g.cols == 0) continue;
+    const Shape s = shape_of(g);
+    const int64_t elems = s.m * s.n;
+    for (int64_t first = 0; first < g.count;) {
+      if (out.empty() || room < elems ||
+          static_cast<int>(out.back().pieces.size()) == kMaxGroups) {
+        out.emplace_back();
+        room = std::max(kChunkElems, elems);
+      }
+      const int64_t take = std::min(g.count - first, room / elems);
+      out.back().pieces.push_back(Piece{i, first, take});
+      out.back().bytes += half_bytes(s, take) + partial_bytes(s, take) + scal_bytes(take);
+      room -= take * elems;
+      first += take;
+    }
+  }
+  return out;
+}
+
+// Argument checks of the groups alone (no pointers): shared with the size query.
+sbp_status check_shapes(const std::string& w, const sbp_matrices* groups, int32_t n_groups) {
+  if (n_groups < 0) return sbp::fail(SBP_EINVAL, w + ": n_groups < 0");
+  if (n_groups > 0 && groups == nullptr) return sbp::fail(SBP_EINVAL, w + ": groups is null");
+  for (int32_t i = 0; i < n_groups; ++i) {
+    const sbp_matrices& g = groups[i];
+    if (g.rows < 0 || g.cols < 0 || g.count < 0)
+      return sbp::fail(SBP_EINVAL, w + ": negative rows, cols or count");
+    if (g.rows > SBP_NS_MAX_DIM || g.cols > SBP_NS_MAX_DIM || g.count > SBP_NS_MAX_DIM)
+      return sbp::fail(SBP_ERANGE, w + ": rows, cols or count above SBP_NS_MAX_DIM");
+    if (g.rows * g.cols > SBP_NS_MAX_NUMEL)
+      return sbp::fail(SBP_ERANGE, w + ": a matrix above SBP_NS_MAX_NUMEL elements");
+  }
+  return SBP_OK;
+}
+
+// A group's elements as a byte range, and the lattice they lie on.
+struct Span {
+  uintptr_t lo, hi;  // bytes
+  int64_t ld, stride, cols, count;
+  int32_t group;
+  bool out;
+  // columns a row of `ld` holds, and whether every matrix starts in the same one
+  int64_t width;
+  bool aligned_rows;
+};
+
+Span span_of(const void* p, const sbp_matrices& g, int64_t ld, int64_t stride, int32_t group,
+             bool out) {
+  const int64_t between = g.count > 1 ? stride : 0;
+  const int64_t all = (g.rows - 1) * ld + g.cols + (g.count - 1) * between;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  Span s{lo, lo + 2 * static_cast<uintptr_t>(all), ld, between, g.cols, g.count, group, out,
+         g.cols, between % ld == 0};
+  const int64_t beside = (g.count - 1) * between + g.cols;  // matrices next to each other
+  if (beside <= ld) {
+    s.width = beside;
+    s.aligned_rows = true;
+  }
+  return s;
+}
+
+// Whether two groups' elements are disjoint although their ranges overlap:
+// column blocks of one buffer with a common row distance.
+bool disjoint_columns(const Span& a, const Span& b) {
+  if (a.ld != b.ld || !a.aligned_rows || !b.aligned_rows) return false;
+  const int64_t ld = a.ld;
+  const int64_t bytes = static_cast<int64_t>(b.lo - a.lo);  // a.lo <= b.lo
+  if (bytes % 2) return false;
+  const int64_t d = (bytes / 2) % ld;  // b's first column relative to a's
+  return a.width <= d && d + b.width <= ld;
+}
+
+bool same_place(const Span& a, const Span& b) {
+  return a.lo == b.lo && a.ld == b.ld && a.stride == b.stride;
+}
+
+sbp_status check_overlap(const std::string& w, std::vector<Span>& spans) {
+  std::sort(spans.begin(), spans.end(),
+            [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  std::vector<const Span*> open;
+  for (const Span& s : spans) {
+    open.erase(std::remove_if(open.begin(), open.end(),
+                              [&](const Span* o) { return o->hi <= s.lo; }),
+               open.end());
+    for (const Span* o : open) {
+      if (!o->out && !s.out) continue;  // two inputs may share memory
+      if (o->group == s.group && o->out != s.out && same_place(*o, s)) continue;  // in place
+      if (disjoint_columns(*o, s)) continue;
+      return sbp::fail(SBP_EINVAL, w + ": an output overlaps another matrix");
+    }
+    open.push_back(&s);
+  }
+  return SBP_OK;
+}
+
+sbp_status launched(const char* who) {
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess)
+    return sbp::fail(SBP_EHIP, std::string(who) + ": launch failed: " + hipGetErrorString(e));
+  return SBP_OK;
+}
+
+struct Tiles {
+  uint32_t gram = 0, apply = 0;
+};
+
+// First blocks of every group for tiles of side T; the launches' sizes.
+Tiles lay_tiles(Groups& gs, int T) {
+  Tiles t;
+  for (int i = 0; i < gs.n; ++i) {
+    Group& g = gs.g[i];
+    const uint32_t tm = (g.m + T - 1) / T, tn = (g.n + T - 1) / T;
+    g.t_gram = t.gram;
+    g.t_apply = t.apply;
+    t.gram += g.count * (tm * (tm + 1) / 2);
+    t.apply += g.count * tm * tn;
+  }
+  return t;
+}
+
+template <int T>
+sbp_status run_step(const char* who, const Groups& gs, const Tiles& t, const Step& st,
+                    hipStream_t stream) {
+  hipLaunchKernelGGL((ns_product_kernel<T, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
+                     t.gram);
+  hipLaunchKernelGGL((ns_product_kernel<T, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
+                     t.gram);
+  hipLaunchKernelGGL((ns_product_kernel<T, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
+                     st, t.apply);
+  return launched(who);
+}
+
+sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c,
+                     const sbp_ns_hparams& hp, char* ws, hipStream_t stream) {
+  Groups gs{};
+  gs.n = static_cast<int32_t>(c.pieces.size());
+  uint32_t norm = 0, pro = 0;
+  for (int i = 0; i < gs.n; ++i) {
+    const Piece& p = c.pieces[i];
+    const sbp_matrices& src = groups[p.group];
+    const Shape s = shape_of(src);
+    Group& g = gs.g[i];
+    g.in = static_cast<const uint16_t*>(src.in) + p.first * src.in_stride;
+    g.out = static_cast<uint16_t*>(src.out) + p.first * src.out_stride;
+    g.in_ld = src.in_ld;
+    g.out_ld = src.out_ld;
+    g.in_stride = src.in_stride;
+    g.out_stride = src.out_stride;
+    g.rows = static_cast<int32_t>(src.rows);
+    g.cols = static_cast<int32_t>(src.cols);
+    g.count = static_cast<int32_t>(p.count);
+    g.m = static_cast<int32_t>(s.m);
+    g.n = static_cast<int32_t>(s.n);
+    g.norm_blocks = static_cast<int32_t>(s.norm_blocks);
+    g.out_scale = src.out_scale;
+    const bool many = p.count > 1;
+    g.in_vec = sbp::aligned(g.in, 16) && src.in_ld % 8 == 0 && (!many || src.in_stride % 8 == 0);
+    g.out_vec =
+        sbp::aligned(g.out, 16) && src.out_ld % 8 == 0 && (!many || src.out_stride % 8 == 0);
+    g.base = reinterpret_cast<_Float16*>(ws);
+    ws += half_bytes(s, p.count);
+    g.partial = reinterpret_cast<double*>(ws);
+    ws += partial_bytes(s, p.count);
+    g.scal = reinterpret_cast<Scal*>(ws);
+    ws += scal_bytes(p.count);
+    g.t_norm = norm;
+    g.t_pro = pro;
+    norm += g.count * g.norm_blocks;
+    pro += g.count * (g.m / 64) * (g.n / 64);
+  }
+  // |x| grows by at most a factor sum |coefficients| per step while small
+  double grow = 0.0;
+  for (int s = 0; s < hp.steps; ++s)
+    grow += std::log2(std::max(1.0, std::fabs(static_cast<double>(hp.coefs[3 * s]))));
+  const int igrow = static_cast<int>(std::min(200.0, std::ceil(grow)));
+
+  hipLaunchKernelGGL(ns_norm_kernel, dim3(norm), dim3(kBlock), 0, stream, gs);
+  hipLaunchKernelGGL(ns_prologue_kernel, dim3(pro), dim3(kBlock), 0, stream, gs, hp.eps, igrow);
+  sbp_status rc = launched(who);
+  if (rc != SBP_OK) return rc;
+
+  // the largest tile that still gives every CU one: fewer bytes read per flop
+  int T = 128;
+  Tiles t = lay_tiles(gs, T);
+  while (T > 64 && t.apply < 256) {
+    T /= 2;
+    t = lay_tiles(gs, T);
+  }
+  for (int s = 0; s < hp.steps; ++s) {
+    Step st{};
+    st.a = hp.coefs[3 * s];
+    st.b = hp.coefs[3 * s + 1];
+    st.c = hp.coefs[3 * s + 2];
+    st.first = s == 0;
+    st.last = s == hp.steps - 1;
+    st.lo_out = hp.steps - 1 - s >= 3;
+    st.lo_in = s > 0 && hp.steps - s >= 3;
+    st.yin = s & 1;
+    rc = T == 128 ? run_step<128>(who, gs, t, st, stream)
+                  : run_step<64>(who, gs, t, st, stream);
+    if (rc != SBP_OK) return rc;
+  }
+  return SBP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sbp_newton_schulz_workspace(const sbp_matrices* groups, int32_t n_groups) {
+  if (check_shapes("sbp_newton_schulz_workspace", groups, n_groups) != SBP_OK) return -1;
+  (void)sbp::ok();
+  int64_t most = 0;
+  for (const Chunk& c : chunks_of(groups, n_groups)) most = std::max(most, c.bytes);
+  return most;
+}
+
+sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
+                             const sbp_ns_hparams* hp, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream) {
+  const char* who = "sbp_newton_schulz";
+  const std::string w(who);
+  sbp_status st = check_shapes(w, groups, n_groups);
+  if (st != SBP_OK) return st;
+  if (hp == nullptr) return sbp::fail(SBP_EINVAL, w + ": hp is null");
+  if (hp->steps < 1 || hp->steps > SBP_NS_MAX_STEPS)
+    return sbp::fail(SBP_EINVAL, w + ": steps must be in 1..SBP_NS_MAX_STEPS");
+  if (!(hp->eps >= 0.0f) || !std::isfinite(hp->eps))
+    return sbp::fail(SBP_EINVAL, w + ": eps must be finite and >= 0");
+  for (int i = 0; i < 3 * hp->steps; ++i)
+    if (!(std::fabs(hp->coefs[i]) <= SBP_NS_MAX_COEF))
+      return sbp::fail(SBP_EINVAL, w + ": a coefficient beyond SBP_NS_MAX_COEF");
+  std::vector<Span> spans;
+  for (int32_t i = 0; i < n_groups; ++i) {
+    const sbp_matrices& g = groups[i];
+    if (!std::isfinite(g.out_scale))
+      return sbp::fail(SBP_EINVAL, w + ": out_scale must be finite");
+    if (g.rows == 0 || g.cols == 0 || g.count == 0) continue;
+    if (g.in == nullptr || g.out == nullptr)
+      return sbp::fail(SBP_EINVAL, w + ": null matrix pointer");
+    if (!sbp::aligned(g.in, 2) || !sbp::aligned(g.out, 2))
+      return sbp::fail(SBP_EALIGN, w + ": matrices must be 2-byte aligned");
+    if (g.in_ld < g.cols || g.out_ld < g.cols)
+      return sbp::fail(SBP_EINVAL, w + ": a row distance below cols");
+    if (g.in_ld > SBP_NS_MAX_LD || g.out_ld > SBP_NS_MAX_LD)
+      return sbp::fail(SBP_ERANGE, w + ": a row distance above SBP_NS_MAX_LD");
+    const int64_t out_one = (g.rows - 1) * g.out_ld + g.cols;
+    if (g.count > 1) {
+      const int64_t most = INT64_MAX / 8 / g.count;
+      if (g.in_stride < 0 || g.out_stride < 0)
+        return sbp::fail(SBP_EINVAL, w + ": a negative matrix distance");
+      if (g.in_stride > most || g.out_stride > most)
+        return sbp::fail(SBP_ERANGE, w + ": a matrix distance too large");
+      // a group's outputs: one after the other, or side by side in the rows
+      const bool apart = g.out_stride >= out_one;
+      const bool beside = g.out_stride >= g.cols &&
+                          (g.count - 1) * g.out_stride + g.cols <= g.out_ld;
+      if (!apart && !beside)
+        return sbp::fail(SBP_EINVAL, w + ": a group's outputs overlap each other");
+    }
+    spans.push_back(span_of(g.in, g, g.in_ld, g.in_stride, i, false));
+    spans.push_back(span_of(g.out, g, g.out_ld, g.out_stride, i, true));
+  }
+  if (spans.empty()) return sbp::ok();  // nothing is read or written
+  st = check_overlap(w, spans);
+  if (st != SBP_OK) return st;
+  const std::vector<Chunk> chunks = chunks_of(groups, n_groups);
+  int64_t need = 0;
+  for (const Chunk& c : chunks) need = std::max(need, c.bytes);
+  if (workspace == nullptr) return sbp::fail(SBP_EINVAL, w + ": workspace is null");
+  if (!sbp::aligned(workspace, 256))
+    return sbp::fail(SBP_EALIGN, w + ": workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return sbp::fail(SBP_EINVAL, w + ": workspace too small (see sbp_newton_schulz_workspace)");
+  const uintptr_t wlo = reinterpret_cast<uintptr_t>(workspace);
+  for (const Span& s : spans)
+    if (s.lo < wlo + static_cast<uintptr_t>(need) && wlo < s.hi)
+      return sbp::fail(SBP_EINVAL, w + ": the workspace overlaps a matrix");
+  (void)hipGetLastError();
+  for (const Chunk& c : chunks) {
+    st = run_chunk(who, groups, c, *hp, static_cast<char*>(workspace), stream);
+    if (st != SBP_OK) return st;
+  }
+  return sbp::ok();
+}
+
+}  // extern "C"

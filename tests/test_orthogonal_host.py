@@ -111,3 +111,168 @@ def test_update_refusals(kw, status):
 
 def test_update_empty_reads_nothing():
     assert _update(n=0, u=None, master=None, p=None) == sbp.SBP_OK
+
+
+# ---- Newton-Schulz -----------------------------------------------------------------
+
+COEFS = sbp.NS_COEFS
+
+
+def _poly(x, steps, coefs=COEFS):
+    for _ in range(steps):
+        x = coefs[0] * x + coefs[1] * x ** 3 + coefs[2] * x ** 5
+    return x
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 9), (6, 1), (5, 5), (4, 7), (9, 3)])
+def test_oracle_newton_schulz_acts_on_singular_values(shape):
+    """The result has U's singular vectors and the polynomial of its singular
+    values: the definition by decomposition."""
+    rng = np.random.default_rng(5)
+    U = rng.standard_normal(shape)
+    P, s, Q = np.linalg.svd(U, full_matrices=False)
+    f32 = [float(F32(c)) for c in COEFS]
+    want = (P * _poly(s / np.sqrt(np.sum(s * s)), 5, f32)) @ Q
+    got = OS.newton_schulz(U, 5, COEFS)
+    assert np.allclose(got, want, rtol=0, atol=1e-11)
+    # every singular value that was not tiny ends inside the quintic's band
+    assert np.all(np.linalg.svd(got, compute_uv=False)[s > 0.05 * s[0]] < 1.25)
+
+
+def test_oracle_newton_schulz_edges():
+    assert np.array_equal(OS.newton_schulz(np.zeros((3, 4)), 5, COEFS), np.zeros((3, 4)))
+    U = np.ones((2, 3))
+    U[0, 1] = np.nan
+    assert np.isnan(OS.newton_schulz(U, 1, COEFS)).all()
+    U[0, 1] = np.inf
+    assert np.isnan(OS.newton_schulz(U, 1, COEFS)).all()
+    # below eps the matrix is divided by eps: a power of the polynomial's slope
+    U = np.full((1, 1), 1e-12)
+    slope = float(F32(COEFS[0])) ** 3
+    assert np.allclose(OS.newton_schulz(U, 3, COEFS, eps=1e-7), 1e-12 / float(F32(1e-7)) * slope,
+                       rtol=1e-6)
+    a = OS.newton_schulz(np.eye(3), 2, [(1.5, -0.5, 0.0), (2.0, -1.5, 0.5)], out_scale=0.5)
+    x = 1 / np.sqrt(3.0)
+    x = 1.5 * x - 0.5 * x ** 3
+    x = 2 * x - 1.5 * x ** 3 + 0.5 * x ** 5
+    assert np.allclose(a, 0.5 * x * np.eye(3), atol=1e-14)
+
+
+def test_oracle_rounded_formats_cost_little():
+    """Flat and steep spectra: the kept formats move the result by less than
+    half a bf16 step, 2^-8 of it (each entry is within 2^-11, fp16's half
+    step, and the remainder keeps the early steps' noise from growing)."""
+    rng = np.random.default_rng(6)
+    for m, n in ((40, 60), (96, 96)):
+        flat = rng.standard_normal((m, n))
+        steep = rng.standard_normal((m, 4)) @ rng.standard_normal((4, n)) + 0.03 * flat
+        for U in (flat, steep):
+            U = OS.bf16_to_f32(OS.f32_to_bf16(U.astype(F32))).astype(np.float64)
+            e = OS.newton_schulz(U, 5, COEFS)
+            r = OS.newton_schulz_rounded(U, 5, COEFS)
+            assert np.linalg.norm(r - e) < 2.0 ** -8 * np.linalg.norm(e)
+
+
+def _mats(**kw):
+    a = dict(in_=0x1000000, out=0x2000000, rows=64, cols=64, count=1, in_ld=64, out_ld=64,
+             in_stride=0, out_stride=0, out_scale=1.0)
+    a.update(kw)
+    return sbp.Matrices(*[a[k] for k, _ in sbp.Matrices._fields_])
+
+
+def _ns(groups, hp=None, ws=0x8000000, ws_bytes=1 << 40, n=None):
+    arr = (sbp.Matrices * max(len(groups), 1))(*groups)
+    hp = hp if hp is not None else sbp.NsHParams.of(5, COEFS, 1e-7, "test")
+    return sbp.lib().sbp_newton_schulz(arr, len(groups) if n is None else n,
+                                       ctypes.byref(hp) if hp else None, V(ws), ws_bytes, None)
+
+
+def _hp(steps=5, eps=1e-7, **coefs):
+    h = sbp.NsHParams.of(5, COEFS, eps, "test")
+    h.steps = steps
+    for k, v in coefs.items():
+        h.coefs[int(k[1:])] = v
+    return h
+
+
+@pytest.mark.parametrize("groups,kw,status", [
+    ([_mats()], dict(n=-1), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=False), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(steps=0)), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(steps=17)), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(eps=-1.0)), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(eps=float("nan"))), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(c4=65.0)), sbp.SBP_EINVAL),
+    ([_mats()], dict(hp=_hp(c14=float("nan"))), sbp.SBP_EINVAL),
+    ([_mats(rows=-1)], {}, sbp.SBP_EINVAL),
+    ([_mats(count=-1)], {}, sbp.SBP_EINVAL),
+    ([_mats(rows=(1 << 20) + 1)], {}, sbp.SBP_ERANGE),
+    ([_mats(rows=1 << 17, cols=1 << 17, in_ld=1 << 17, out_ld=1 << 17)], {}, sbp.SBP_ERANGE),
+    ([_mats(in_=None)], {}, sbp.SBP_EINVAL),
+    ([_mats(out=None)], {}, sbp.SBP_EINVAL),
+    ([_mats(in_=0x1000001)], {}, sbp.SBP_EALIGN),
+    ([_mats(out=0x2000001)], {}, sbp.SBP_EALIGN),
+    ([_mats(in_ld=63)], {}, sbp.SBP_EINVAL),
+    ([_mats(out_ld=63)], {}, sbp.SBP_EINVAL),
+    ([_mats(in_ld=(1 << 40) + 1)], {}, sbp.SBP_ERANGE),
+    ([_mats(out_scale=float("inf"))], {}, sbp.SBP_EINVAL),
+    ([_mats(count=2, in_stride=-4096, out_stride=4096)], {}, sbp.SBP_EINVAL),
+    ([_mats(count=2, in_stride=1 << 62, out_stride=4096)], {}, sbp.SBP_ERANGE),
+    ([_mats(count=2, in_stride=4096, out_stride=4095)], {}, sbp.SBP_EINVAL),
+    ([_mats(count=2, in_stride=4096, out_stride=0)], {}, sbp.SBP_EINVAL),
+    # side by side in rows of 150: three of 64 do not fit
+    ([_mats(count=3, in_stride=4096, out_stride=64, out_ld=150)], {}, sbp.SBP_EINVAL),
+    ([_mats(out=0x1000000 + 64)], {}, sbp.SBP_EINVAL),  # shifted over its input
+    ([_mats(out=0x1000000, out_ld=65)], {}, sbp.SBP_EINVAL),  # same start, other distances
+    ([_mats(), _mats(in_=0x3000000)], {}, sbp.SBP_EINVAL),  # two outputs in one place
+    ([_mats(), _mats(in_=0x2000000, out=0x3000000)], {}, sbp.SBP_EINVAL),  # reads the first's
+    ([_mats(in_ld=200, out_ld=200, in_=0x1000000, out=0x1000000),
+      _mats(in_ld=200, out_ld=200, in_=0x1000000 + 2 * 32, out=0x1000000 + 2 * 32)], {},
+     sbp.SBP_EINVAL),  # column blocks that share columns
+    ([_mats(in_ld=200, out_ld=200, in_=0x1000000, out=0x1000000),
+      _mats(in_ld=201, out_ld=201, in_=0x1000000 + 2 * 64, out=0x1000000 + 2 * 64)], {},
+     sbp.SBP_EINVAL),  # column blocks of two row distances
+    ([_mats()], dict(ws=None), sbp.SBP_EINVAL),
+    ([_mats()], dict(ws=0x8000080), sbp.SBP_EALIGN),
+    ([_mats()], dict(ws_bytes=1000), sbp.SBP_EINVAL),
+    ([_mats()], dict(ws=0x1000000), sbp.SBP_EINVAL),
+    ([_mats()], dict(ws=0x2000000 - 4096), sbp.SBP_EINVAL),
+])
+def test_newton_schulz_refusals(groups, kw, status):
+    assert _ns(groups, **kw) == status
+    assert b"sbp_newton_schulz" in sbp.lib().sbp_last_error()
+
+
+def test_newton_schulz_nothing_to_do():
+    for g in ([], [_mats(rows=0)], [_mats(cols=0, in_=None)], [_mats(count=0, out=None)]):
+        assert _ns(g, ws=None, ws_bytes=0) == sbp.SBP_OK
+    assert sbp.lib().sbp_newton_schulz(None, 0, ctypes.byref(_hp()), None, 0, None) == sbp.SBP_OK
+
+
+def test_newton_schulz_workspace_size():
+    q = sbp.lib().sbp_newton_schulz_workspace
+    one = q((sbp.Matrices * 1)(_mats()), 1)
+    assert one >= 2 * 6 * 64 * 64  # X, its transpose twice, the remainder, A and B
+    assert q((sbp.Matrices * 1)(_mats(rows=1, cols=1)), 1) == one  # padded alike
+    assert q((sbp.Matrices * 1)(_mats(count=3)), 1) > 2 * one
+    assert q((sbp.Matrices * 1)(_mats(rows=0)), 1) == 0
+    assert q((sbp.Matrices * 1)(_mats(rows=-1)), 1) == -1
+    assert q((sbp.Matrices * 1)(_mats(cols=(1 << 20) + 1)), 1) == -1
+    assert q(None, 1) == -1
+    # a long list runs in parts: the workspace stays bounded
+    many = (sbp.Matrices * 40)(*[_mats(rows=4096, cols=14336)] * 40)
+    assert q(many, 40) < 8 * q(many, 1)
+
+
+def test_newton_schulz_python_arguments():
+    with pytest.raises(ValueError):
+        sbp.NsHParams.of(0, COEFS, 1e-7, "t")
+    with pytest.raises(ValueError):
+        sbp.NsHParams.of(2, [COEFS] * 3, 1e-7, "t")
+    with pytest.raises(ValueError):
+        sbp.NsHParams.of(2, (1.0, 2.0), 1e-7, "t")
+    import torch
+    x = torch.zeros(4, 4, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        sbp.newton_schulz([x])  # not a device tensor
+    assert sbp.newton_schulz([]) == []
