@@ -364,10 +364,10 @@ def newton_schulz(U, steps, coefs, eps=1e-7, out_scale=1.0):
 
 
 def newton_schulz_rounded(U, steps, coefs, eps=1e-7):
-    """The same with X, A and b A + c A A kept in binary16 as the device keeps
-    them (scaled by 2^12, 2^12 and 2^10; X's remainder next to it while three
-    steps remain), all other arithmetic in float64: how far those roundings by
-    themselves move the result."""
+    """The same with X, A and B = b A + c A A kept in binary16 as the device
+    keeps them (scaled by 2^12, 2^12 and 2^10; the remainders of both diagonals
+    kept, and X's next to it while three steps remain), all other arithmetic in
+    float64: how far those roundings by themselves move the result."""
     X = np.asarray(U, np.float64)
     if X.shape[0] > X.shape[1]:
         return newton_schulz_rounded(X.T, steps, coefs, eps).T
@@ -380,8 +380,12 @@ def newton_schulz_rounded(U, steps, coefs, eps=1e-7):
     X = X / norm
     whole = X  # the first step's X is exact: bf16 values times a power of two
     for s, (a, b, c) in enumerate([[float(F32(x)) for x in t] for t in coefs]):
-        A = kept(X @ X.T, 4096.0)
-        new = a * whole + kept(b * A + c * (A @ A), 1024.0) @ X
+        exact = X @ X.T
+        A = kept(exact, 4096.0)
+        d = np.diag(exact) - np.diag(A)
+        exact = b * (A + np.diag(d)) + c * (A @ A + (d[:, None] + d) * A + np.diag(d * d))
+        B = kept(exact, 1024.0)
+        new = (a + np.diag(exact) - np.diag(B))[:, None] * whole + B @ X
         if s == steps - 1:
             return new
         X = kept(new, 4096.0)

@@ -25,15 +25,20 @@
 //   X, Y    * 2^12 (entries up to 16); a matrix whose norm lies below eps
 //           gets a further power of two that its iterates cannot outgrow
 //   A       * 2^12,  B * 2^10
-// The step's amplification of small singular values (a^steps ~ 485) would
-// amplify X's rounding noise as well.  The noise that matters reaches them
-// only through the term a X, since B's share of it is multiplied by B, small
-// on exactly those directions; so while at least three steps remain, X's
-// rounding remainder is kept next to it (fp16, * 2^11) and a X is formed from
-// both parts.  Against the iteration in 64 bits, for 5 steps on spectra from
-// flat to rank 16 plus noise of 0.003: relative error 2e-4 .. 1.6e-3 before
-// the output's rounding (1.7e-3 by itself); without the remainder up to
-// 2.6e-2, with bf16 products 7e-3 .. 2e-1.
+// Two roundings would stand out, and their remainders are kept:
+//   - A and B end near multiples of the identity, so the rounding of their
+//     diagonals dominates theirs; the diagonals' remainders (binary32, m of
+//     each) enter B's epilogue as (A + D)^2 and apply's as (a + D) X;
+//   - the step's amplification of small singular values (a^steps ~ 485)
+//     amplifies X's rounding noise as well.  It reaches them only through the
+//     term a X, since B's share of it is multiplied by B, small on exactly
+//     those directions; so while at least three steps remain, X's remainder
+//     is kept (fp16, * 2^11) and a X is formed from both parts.
+// Relative error against the iteration in 64 bits, 5 steps, before the
+// output's rounding (1.7e-3 by itself), on spectra from flat to rank 16 plus
+// 0.03 of noise: 4e-4 .. 1.0e-3 (rank 16 plus 0.003: 2.3e-3); without the
+// diagonals' remainders up to 2.2e-3, without either up to 2.6e-2, with bf16
+// products 7e-3 .. 2e-1.
 // The squared norm is summed in float64 in a fixed order, so results are the
 // same from run to run.
 #include <hip/hip_runtime.h>
@@ -81,6 +86,7 @@ struct Group {
   _Float16* base;    // X, Y, Y2, L (count*m*n each), A, B (count*m*m each)
   double* partial;   // count * norm_blocks
   Scal* scal;        // count
+  float* diag;       // m each: count for A, count for B (rounding remainders)
   int32_t rows, cols, count;
   int32_t m, n;      // padded short and long side
   int32_t norm_blocks;
@@ -96,6 +102,9 @@ struct Group {
   }
   __device__ _Float16* L(int item) const {
     return base + (static_cast<int64_t>(3) * count + item) * mn();
+  }
+  __device__ float* D(int which, int item) const {
+    return diag + (static_cast<int64_t>(which) * count + item) * m;
   }
   __device__ _Float16* A(int which, int item) const {
     return base + static_cast<int64_t>(4) * count * mn() +
@@ -131,6 +140,15 @@ __device__ __forceinline__ double block_sum_all(double x) {
 #pragma unroll
   for (int w = 0; w < kBlock / 64; ++w) t = t + per_wave[w];
   return t;
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    x[q] = lo[q];
+    x[4 + q] = hi[q];
+  }
 }
 
 // Up to 8 consecutive bf16 values of a row, zeros from `left` on.
@@ -437,14 +455,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
       if (gr >= prows || gc >= m) continue;
       float* at = slab + row * T + slab_col(row, col);
       float v[8];
-      {
-        const f32x4 lo = *reinterpret_cast<f32x4*>(at), hi = *reinterpret_cast<f32x4*>(at + 4);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] = lo[q];
-          v[4 + q] = hi[q];
-        }
-      }
+      load8(at, v);
       const int64_t idx = static_cast<int64_t>(gr) * m + gc;
       f16x8 h;
       if constexpr (M == kGram) {
@@ -453,15 +464,24 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
         for (int q = 0; q < 8; ++q) {
           v[q] = v[q] * alpha;
           h[q] = static_cast<_Float16>(v[q]);
+          if (gr == gc + q) g.D(0, item)[gr] = v[q] - static_cast<float>(h[q]);
         }
         *reinterpret_cast<f16x8*>(g.A(0, item) + idx) = h;
       } else if constexpr (M == kPoly) {
         const f16x8 A = *reinterpret_cast<const f16x8*>(g.A(0, item) + idx);
         const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
+        const float* d = g.D(0, item);
+        const float dr = d[gr];
+        float dc[8];
+        load8(d + gc, dc);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          v[q] = fb * static_cast<float>(A[q]) + fc * v[q];
+          // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
+          const float a = static_cast<float>(A[q]);
+          v[q] = fb * a + fc * (v[q] + (dr + dc[q]) * a);
+          if (gr == gc + q) v[q] = v[q] + (fb * dr + fc * (dr * dr));
           h[q] = static_cast<_Float16>(v[q]);
+          if (gr == gc + q) g.D(1, item)[gr] = v[q] - static_cast<float>(h[q]);
         }
         *reinterpret_cast<f16x8*>(g.A(1, item) + idx) = h;
       } else {
@@ -470,10 +490,12 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
         if (st.lo_in) rem = *reinterpret_cast<const f16x8*>(g.L(item) + idx);
         const float to = st.last ? g.out_scale * sc.inv_sx : 1.0f;
         const float f = st.first ? sc.apply_first : 1.0f;
+        float dc[8];
+        load8(g.D(1, item) + gc, dc);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float x = static_cast<float>(y[q]) + static_cast<float>(rem[q]) * (1.0f / kScaleLo);
-          v[q] = (st.a * x + v[q] * (1.0f / kScaleB)) * f;
+          v[q] = ((st.a + dc[q] * (1.0f / kScaleB)) * x + v[q] * (1.0f / kScaleB)) * f;
           h[q] = static_cast<_Float16>(v[q]);
         }
         if (!st.last) {
@@ -586,6 +608,7 @@ int64_t half_bytes(const Shape& s, int64_t count) {
   return up(2 * count * (4 * s.m * s.n + 2 * s.m * s.m), 256);
 }
 int64_t partial_bytes(const Shape& s, int64_t count) { return up(8 * count * s.norm_blocks, 256); }
+int64_t diag_bytes(const Shape& s, int64_t count) { return up(8 * count * s.m, 256); }
 int64_t scal_bytes(int64_t count) { return up(static_cast<int64_t>(sizeof(Scal)) * count, 256); }
 
 std::vector<Chunk> chunks_of(const sbp_matrices* groups, int32_t n_groups) {
@@ -604,7 +627,8 @@ std::vector<Chunk> chunks_of(const sbp_matrices* groups, int32_t n_groups) {
       }
       const int64_t take = std::min(g.count - first, room / elems);
       out.back().pieces.push_back(Piece{i, first, take});
-      out.back().bytes += half_bytes(s, take) + partial_bytes(s, take) + scal_bytes(take);
+      out.back().bytes += half_bytes(s, take) + partial_bytes(s, take) +
+                          diag_bytes(s, take) + scal_bytes(take);
       room -= take * elems;
       first += take;
     }
@@ -756,6 +780,8 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     ws += half_bytes(s, p.count);
     g.partial = reinterpret_cast<double*>(ws);
     ws += partial_bytes(s, p.count);
+    g.diag = reinterpret_cast<float*>(ws);
+    ws += diag_bytes(s, p.count);
     g.scal = reinterpret_cast<Scal*>(ws);
     ws += scal_bytes(p.count);
     g.t_norm = norm;
