@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "bf16.h"
@@ -65,7 +66,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBlock = 256;
 constexpr int kXcds = 8;
 constexpr int kPad = 64;        // both padded sides are multiples of this
-constexpr int kBK = 64;         // k elements per staged slice: 128 bytes a row
+constexpr int kBK = 32;         // k elements per staged slice: 64 bytes a row
 constexpr int kMaxGroups = 16;  // groups of equal matrices per launch
 constexpr int kMaxNormBlocks = 256;
 constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 1024.0f, kScaleLo = 2048.0f;
@@ -256,20 +257,20 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
 
 // ---- the product ------------------------------------------------------------------
 
-enum Mode { kGram, kPoly, kApply };
+enum Mode { kGram, kPoly, kApply, kLast };  // kLast: apply, to the caller's matrices
 
 // One T x T tile of C = P Q' per block of 4 waves (2 x 2, each T/2 square, in
-// 32 x 32 MFMA tiles).  Slices of 64 k elements go straight from memory to
-// one of two LDS buffers while the other is multiplied; a row's eight 16-byte
-// pieces are stored rotated by row (piece ^ row mod 8), which the lanes'
-// global addresses bring about, so that reads of one piece of many rows
-// spread over the banks.
+// 32 x 32 MFMA tiles).  Slices of 32 k elements go straight from memory to
+// one of four LDS buffers, three slices ahead of the one being multiplied.  A
+// row's four 16-byte pieces are stored rotated (piece ^ (row / 4) mod 4),
+// which the lanes' global addresses bring about, so that reads of one piece
+// of many rows spread over the banks.
 template <int T>
 struct Tile {
   static constexpr int kRowBytes = kBK * 2;
   static constexpr int kBuf = 2 * T * kRowBytes;  // P rows, then Q rows
   static constexpr int kSub = T / 64;             // 32 x 32 tiles per wave and side
-  static constexpr int kRounds = T / 32;          // staging rounds per operand
+  static constexpr int kRounds = T / 64;          // loads per operand, slice and lane
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const _Float16* p, int64_t bytes) {
@@ -277,27 +278,58 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const _Float16* p, int
                                            static_cast<int>(bytes), 0x00027000);
 }
 
+// One operand's rows of a slice, this wave's share.
 template <int T>
-__device__ __forceinline__ void stage(char* buf, __amdgpu_buffer_rsrc_t P,
-                                      __amdgpu_buffer_rsrc_t Q, int wave, int voff,
+__device__ __forceinline__ void stage(char* buf, __amdgpu_buffer_rsrc_t rows, int wave, int voff,
                                       int round_bytes, int koff) {
 #pragma unroll
   for (int r = 0; r < Tile<T>::kRounds; ++r)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        P, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16, voff,
+        rows, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16, voff,
         r * round_bytes + koff, 0, 0);
-#pragma unroll
-  for (int r = 0; r < Tile<T>::kRounds; ++r)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        Q,
-        (__attribute__((address_space(3))) void*)(buf + Tile<T>::kBuf / 2 + (r * 4 + wave) * 1024),
-        16, voff, r * round_bytes + koff, 0, 0);
 }
 
-// Everything this wave has asked of memory and LDS is done, then everyone's.
-__device__ __forceinline__ void slice_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// Order of a phase's instructions: one MFMA, one LDS read and one load to LDS
+// in turn, so that both kinds of memory work run under the MFMAs.
+template <int T, int LOADS>
+__device__ __forceinline__ void interleave() {
+  constexpr int mfmas = Tile<T>::kSub * Tile<T>::kSub, reads = 2 * Tile<T>::kSub;
+  constexpr int r1 = (reads + mfmas - 1) / mfmas, l1 = (LOADS + mfmas - 1) / mfmas;
+#pragma unroll
+  for (int i = 0; i < mfmas; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i * r1 < reads) __builtin_amdgcn_sched_group_barrier(0x100, r1, 0);
+    if (i * l1 < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, l1, 0);
+  }
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// All of this wave's loads but the newest LEFT are done, and its LDS reads;
+// then everyone's.
+template <int LEFT>
+__device__ __forceinline__ void slice_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// This wave's LDS work is done, then everyone's; loads and stores run on.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Up to 8 consecutive bf16 values of a row of the caller's output.
+__device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
+  uint32_t b[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) b[q] = sbp::bf16_rne(v[q]);
+  if (vec && left >= 8) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{b[0] | (b[1] << 16), b[2] | (b[3] << 16),
+                                         b[4] | (b[5] << 16), b[6] | (b[7] << 16)};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < left) p[q] = static_cast<uint16_t>(b[q]);
+  }
 }
 
 template <int T>
@@ -327,31 +359,38 @@ __device__ __forceinline__ void multiply(const Frags<T>& f, Acc<T>& acc) {
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
 }
 
-// Column of the fp32 slab in LDS where (row, col) is kept: groups of 8 columns
-// are rotated by the row's 8-row group, so that both a row's 8 columns and a
-// column's 8 rows are read without bank conflicts.
-__device__ __forceinline__ int slab_col(int row, int col) {
-  return col ^ (((row >> 3) & 7) << 3);
+// Where (row, col) of the epilogue's binary32 slab is kept: 32 rows in each of
+// two buffers; groups of 8 columns are rotated by the row's 8-row group, so
+// that both a row's 8 columns and a column's 8 rows are read without bank
+// conflicts.
+template <int T>
+__device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) {
+  float* half = reinterpret_cast<float*>(row & 32 ? hi : lo);
+  return half + (row & 31) * T + (col ^ (((row >> 3) & 7) << 3));
 }
 
 template <int T, Mode M>
-__global__ void __launch_bounds__(kBlock, 2)
+__global__ void __launch_bounds__(kBlock, T == 256 ? 1 : 2)
 ns_product_kernel(Groups gs, Step st, unsigned total) {
+  // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[Tile<T>::kBuf];
   __shared__ __align__(16) char buf1[Tile<T>::kBuf];
+  __shared__ __align__(16) char buf2[Tile<T>::kBuf];
+  __shared__ __align__(16) char buf3[Tile<T>::kBuf];
   constexpr int W = T / 2;  // a wave's side
+  constexpr bool kApplies = M == kApply || M == kLast;
 
   // neighbouring tiles to one XCD: its L2 then holds the rows they share
   unsigned b = blockIdx.x;
   const unsigned per_xcd = total / kXcds;
   if (b < per_xcd * kXcds) b = (b % kXcds) * per_xcd + b / kXcds;
   int gi = 0;
-  while (gi + 1 < gs.n && b >= (M == kApply ? gs.g[gi + 1].t_apply : gs.g[gi + 1].t_gram)) ++gi;
+  while (gi + 1 < gs.n && b >= (kApplies ? gs.g[gi + 1].t_apply : gs.g[gi + 1].t_gram)) ++gi;
   const Group& g = gs.g[gi];
   const int m = g.m, n = g.n;
   const int tm = (m + T - 1) / T;
   int item, ti, tj;  // tile row (of P) and column (rows of Q)
-  if constexpr (M == kApply) {
+  if constexpr (kApplies) {
     const int tn = (n + T - 1) / T;
     const int local = b - g.t_apply;
     item = local / (tn * tm);
@@ -377,7 +416,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
   const int k = M == kGram ? n : m;  // contracted length = both row lengths
   const _Float16* Pm = M == kGram ? g.X(item) : M == kPoly ? g.A(0, item) : g.Y(st.yin, item);
   const _Float16* Qm = M == kGram ? Pm : M == kPoly ? Pm : g.A(1, item);
-  const int prows = M == kApply ? n : m;
+  const int prows = kApplies ? n : m;
   const int r0 = ti * T, c0 = tj * T;
   const int pr = prows - r0 < T ? prows - r0 : T, qr = m - c0 < T ? m - c0 : T;
   const __amdgpu_buffer_rsrc_t P =
@@ -387,52 +426,130 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = wave >> 1, wc = wave & 1;
-  const int voff = (wave * 8 + (lane >> 3)) * k * 2 + (((lane & 7) ^ (lane >> 3)) * 16);
-  const int round_bytes = 32 * k * 2;
+  const int voff = (wave * 16 + (lane >> 2)) * k * 2 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  const int round_bytes = 64 * k * 2;
   const int pbase = (wr * W + (lane & 31)) * Tile<T>::kRowBytes;
   const int qbase = Tile<T>::kBuf / 2 + (wc * W + (lane & 31)) * Tile<T>::kRowBytes;
-  int piece[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) piece[s] = ((s * 2 + (lane >> 5)) ^ (lane & 7)) * 16;
+  const int rot = (lane >> 2) & 3;
+  const int piece[2] = {((lane >> 5) ^ rot) * 16, ((2 + (lane >> 5)) ^ rot) * 16};
 
   Acc<T> acc = {};
   Frags<T> f[2];
-  const int slices = k / kBK;
-  stage<T>(buf0, P, Q, wave, voff, round_bytes, 0);
-  slice_barrier();
-  read_frags<T>(buf0, pbase, qbase, piece[0], f[0]);
-  // Slice s is in `cur`, its first fragments in f[0].  The barrier sits before
-  // the last multiply, whose time hides the first read of the next slice.
-  auto slice = [&](const char* cur, char* nxt, int s) {
-    const bool more = s + 1 < slices;
-    if (more) stage<T>(nxt, P, Q, wave, voff, round_bytes, (s + 1) * (kBK * 2));
+  constexpr int kHalf = Tile<T>::kBuf / 2, L = Tile<T>::kRounds;
+  int koff = 0;  // of the next slice to load
+  auto load = [&](char* to) {
+    stage<T>(to, P, wave, voff, round_bytes, koff);
+    stage<T>(to + kHalf, Q, wave, voff, round_bytes, koff);
+    koff += kBK * 2;
+  };
+  // One slice: it is in `cur`, its first fragments in f[0].  The barrier sits
+  // between the two multiplies, so that each hides the reads for the next.
+  // LOAD: the slice three further on is loaded into `to`; LEFT: loads that may
+  // still be under way when the next slice has to be there (-1: no next one).
+  auto slice = [&](const char* cur, const char* nxt, char* to, auto load_c, auto left_c) {
+    constexpr bool kLoad = decltype(load_c)::value;
+    constexpr int kLeft = decltype(left_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kLoad) stage<T>(to, P, wave, voff, round_bytes, koff);
     read_frags<T>(cur, pbase, qbase, piece[1], f[1]);
     multiply<T>(f[0], acc);
-    read_frags<T>(cur, pbase, qbase, piece[2], f[0]);
+    interleave<T, kLoad ? L : 0>();
+    if constexpr (kLeft >= 0) {
+      slice_barrier<kLeft>();
+      if constexpr (kLoad) stage<T>(to + kHalf, Q, wave, voff, round_bytes, koff);
+      read_frags<T>(nxt, pbase, qbase, piece[0], f[0]);
+    }
     multiply<T>(f[1], acc);
-    read_frags<T>(cur, pbase, qbase, piece[3], f[1]);
-    multiply<T>(f[0], acc);
-    __builtin_amdgcn_sched_barrier(0);
-    slice_barrier();
-    if (more) read_frags<T>(nxt, pbase, qbase, piece[0], f[0]);
-    multiply<T>(f[1], acc);
+    interleave<T, kLoad ? L : 0>();
+    if constexpr (kLoad) koff += kBK * 2;
   };
-  for (int s = 0; s < slices; s += 2) {
-    slice(buf0, buf1, s);
-    if (s + 1 < slices) slice(buf1, buf0, s + 1);
+  constexpr std::true_type kYes{};
+  constexpr std::false_type kNo{};
+  // two slices under way, and the first half of a third
+  constexpr std::integral_constant<int, 3 * L> kSteady{};
+  constexpr std::integral_constant<int, 2 * L> kOne{};
+  constexpr std::integral_constant<int, 0> kNone{};
+  constexpr std::integral_constant<int, -1> kEnd{};
+  const int slices = k / kBK;  // even; the last is in buf3
+  if (slices & 2) {
+    load(buf2);
+    load(buf3);
+    if (slices == 2) {
+      slice_barrier<2 * L>();
+      read_frags<T>(buf2, pbase, qbase, piece[0], f[0]);
+      slice(buf2, buf3, nullptr, kNo, kNone);
+    } else {
+      load(buf0);
+      slice_barrier<4 * L>();
+      read_frags<T>(buf2, pbase, qbase, piece[0], f[0]);
+      slice(buf2, buf3, buf1, kYes, kSteady);
+      slice(buf3, buf0, buf2, kYes, kSteady);
+    }
+  } else {
+    load(buf0);
+    load(buf1);
+    load(buf2);
+    slice_barrier<4 * L>();
+    read_frags<T>(buf0, pbase, qbase, piece[0], f[0]);
   }
-  __syncthreads();
+  if (slices > 2) {
+    for (int s = slices >> 2; s > 1; --s) {
+      slice(buf0, buf1, buf3, kYes, kSteady);
+      slice(buf1, buf2, buf0, kYes, kSteady);
+      slice(buf2, buf3, buf1, kYes, kSteady);
+      slice(buf3, buf0, buf2, kYes, kSteady);
+    }
+    slice(buf0, buf1, buf3, kYes, kSteady);
+    slice(buf1, buf2, nullptr, kNo, kOne);
+    slice(buf2, buf3, nullptr, kNo, kNone);
+  }
+  slice(buf3, nullptr, nullptr, kNo, kEnd);
 
   // Epilogue, 64 rows at a time: accumulators to LDS as binary32, then row by
   // row (8 columns a thread) the additions and the direct store, then the
-  // transposed store.
-  float* slab = reinterpret_cast<float*>(buf0);
-  static_assert(64 * T * 4 <= Tile<T>::kBuf, "the slab fits one buffer");
+  // transposed store.  What the additions read is asked for ahead of the
+  // barriers, which wait for LDS alone: a block has one wave per SIMD, so
+  // nothing else would hide the latency (waiting for memory at each barrier
+  // and pass took as long as the products at k = 4096).
+  static_assert(32 * T * 4 <= Tile<T>::kBuf, "half the slab fits one buffer");
   const Scal sc = g.scal[item];
-  const bool cross = M == kApply ? (!st.last || !g.tall()) : ti != tj;
-  constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow;
+  const bool cross = M == kApply ? true : M == kLast ? !g.tall() : ti != tj;
+  constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow, kPasses = 64 / kRowsAtOnce;
+  const int prow = threadIdx.x / kPerRow, pcol = (threadIdx.x % kPerRow) * 8;
+  const int gc = c0 + pcol;
+  const bool col_in = gc < m;
+  // the matrix added and the remainders of the product's diagonal, per column
+  const _Float16* add = M == kPoly ? g.A(0, item) : kApplies ? g.Y(st.yin, item) : nullptr;
+  const _Float16* rem = kApplies && st.lo_in ? g.L(item) : nullptr;
+  const float* diag = M == kPoly ? g.D(0, item) : kApplies ? g.D(1, item) : nullptr;
+  float dc[8] = {};
+  if constexpr (M != kGram) {
+    if (col_in) load8(diag + gc, dc);
+  }
+  const float alpha = st.first ? sc.gram_first : sc.gram;
+  const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
+  const float fx = (st.first ? sc.apply_first : 1.0f) * (M == kLast ? g.out_scale * sc.inv_sx : 1.0f);
+  if constexpr (kApplies) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dc[q] = st.a + dc[q] * (1.0f / kScaleB);
+  }
+  lds_barrier();  // the last slice is read
 #pragma unroll
   for (int sl = 0; sl < T / 64; ++sl) {
+    f16x8 ad[kPasses], re[kPasses];
+    float dr[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int gr = r0 + sl * 64 + p * kRowsAtOnce + prow;
+      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
+      ad[p] = re[p] = f16x8{};
+      dr[p] = 0.0f;
+      if (gr < prows && col_in) {
+        if constexpr (M != kGram) ad[p] = *reinterpret_cast<const f16x8*>(add + idx);
+        if constexpr (M == kPoly) dr[p] = diag[gr];
+        if (kApplies && rem != nullptr) re[p] = *reinterpret_cast<const f16x8*>(rem + idx);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < Tile<T>::kSub; ++i) {
       const int rb = wr * Tile<T>::kSub + i;  // 32-row block of the tile
@@ -443,23 +560,22 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
           for (int e = 0; e < 16; ++e) {
             const int row = (rb & 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
             const int col = wc * W + j * 32 + (lane & 31);
-            slab[row * T + slab_col(row, col)] = acc[i][j][e];
+            *slab_at<T>(buf0, buf1, row, col) = acc[i][j][e];
           }
       }
     }
-    __syncthreads();
-    for (int p = 0; p < 64 / kRowsAtOnce; ++p) {
-      const int row = p * kRowsAtOnce + threadIdx.x / kPerRow;
-      const int col = (threadIdx.x % kPerRow) * 8;
-      const int gr = r0 + sl * 64 + row, gc = c0 + col;
-      if (gr >= prows || gc >= m) continue;
-      float* at = slab + row * T + slab_col(row, col);
+    lds_barrier();
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int row = p * kRowsAtOnce + prow;
+      const int gr = r0 + sl * 64 + row;
+      if (gr >= prows || !col_in) continue;
+      float* at = slab_at<T>(buf0, buf1, row, pcol);
+      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
       float v[8];
       load8(at, v);
-      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
       f16x8 h;
       if constexpr (M == kGram) {
-        const float alpha = st.first ? sc.gram_first : sc.gram;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           v[q] = v[q] * alpha;
@@ -468,37 +584,26 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
         }
         *reinterpret_cast<f16x8*>(g.A(0, item) + idx) = h;
       } else if constexpr (M == kPoly) {
-        const f16x8 A = *reinterpret_cast<const f16x8*>(g.A(0, item) + idx);
-        const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
-        const float* d = g.D(0, item);
-        const float dr = d[gr];
-        float dc[8];
-        load8(d + gc, dc);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
-          const float a = static_cast<float>(A[q]);
-          v[q] = fb * a + fc * (v[q] + (dr + dc[q]) * a);
-          if (gr == gc + q) v[q] = v[q] + (fb * dr + fc * (dr * dr));
+          const float x = static_cast<float>(ad[p][q]);
+          v[q] = fb * x + fc * (v[q] + (dr[p] + dc[q]) * x);
+          if (gr == gc + q) v[q] = v[q] + (fb * dr[p] + fc * (dr[p] * dr[p]));
           h[q] = static_cast<_Float16>(v[q]);
           if (gr == gc + q) g.D(1, item)[gr] = v[q] - static_cast<float>(h[q]);
         }
         *reinterpret_cast<f16x8*>(g.A(1, item) + idx) = h;
       } else {
-        const f16x8 y = *reinterpret_cast<const f16x8*>(g.Y(st.yin, item) + idx);
-        f16x8 rem{};
-        if (st.lo_in) rem = *reinterpret_cast<const f16x8*>(g.L(item) + idx);
-        const float to = st.last ? g.out_scale * sc.inv_sx : 1.0f;
-        const float f = st.first ? sc.apply_first : 1.0f;
-        float dc[8];
-        load8(g.D(1, item) + gc, dc);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float x = static_cast<float>(y[q]) + static_cast<float>(rem[q]) * (1.0f / kScaleLo);
-          v[q] = ((st.a + dc[q] * (1.0f / kScaleB)) * x + v[q] * (1.0f / kScaleB)) * f;
-          h[q] = static_cast<_Float16>(v[q]);
+          const float x =
+              static_cast<float>(ad[p][q]) + static_cast<float>(re[p][q]) * (1.0f / kScaleLo);
+          v[q] = (dc[q] * x + v[q] * (1.0f / kScaleB)) * fx;
         }
-        if (!st.last) {
+        if constexpr (M == kApply) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
           *reinterpret_cast<f16x8*>(g.Y(st.yin ^ 1, item) + idx) = h;
           if (st.lo_out) {
             f16x8 l;
@@ -507,25 +612,8 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
               l[q] = static_cast<_Float16>((v[q] - static_cast<float>(h[q])) * kScaleLo);
             *reinterpret_cast<f16x8*>(g.L(item) + idx) = l;
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = v[q] * to;
-          if (g.tall()) {
-            if (gr < g.rows) {
-              uint16_t* o = g.out + item * g.out_stride + gr * g.out_ld + gc;
-              if (g.out_vec && gc + 8 <= g.cols) {
-                u32x4 w;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
-                *reinterpret_cast<u32x4*>(o) = w;
-              } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  if (gc + q < g.cols) o[q] = static_cast<uint16_t>(sbp::bf16_rne(v[q]));
-              }
-            }
-          }
+        } else if (!cross && gr < g.rows) {
+          store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v);
         }
       }
       if (cross) {
@@ -533,40 +621,30 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
         *reinterpret_cast<f32x4*>(at + 4) = f32x4{v[4], v[5], v[6], v[7]};
       }
     }
-    __syncthreads();
+    lds_barrier();
     if (cross) {
       // 8 threads take the 64 rows of one column, 8 rows each
+#pragma unroll
       for (int p = 0; p < T / 32; ++p) {
         const int col = p * 32 + (threadIdx.x >> 3), row = (threadIdx.x & 7) * 8;
-        const int gr = r0 + sl * 64 + row, gc = c0 + col;
-        if (gr >= prows || gc >= m) continue;
+        const int gr = r0 + sl * 64 + row, xr = c0 + col;
+        if (gr >= prows || xr >= m) continue;
         float v[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = slab[(row + q) * T + slab_col(row + q, col)];
-        if (M == kApply && st.last) {
-          if (gc < g.rows) {  // X is rows x cols here: its row gc, columns gr ..
-            uint16_t* o = g.out + item * g.out_stride + gc * g.out_ld + gr;
-            if (g.out_vec && gr + 8 <= g.cols) {
-              u32x4 w;
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
-              *reinterpret_cast<u32x4*>(o) = w;
-            } else {
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                if (gr + q < g.cols) o[q] = static_cast<uint16_t>(sbp::bf16_rne(v[q]));
-            }
-          }
+        for (int q = 0; q < 8; ++q) v[q] = *slab_at<T>(buf0, buf1, row + q, col);
+        if constexpr (M == kLast) {
+          // X is rows x cols here: its row xr, columns gr ..
+          if (xr < g.rows)
+            store_out8(g.out + item * g.out_stride + xr * g.out_ld + gr, g.cols - gr, g.out_vec, v);
         } else {
           f16x8 h;
 #pragma unroll
           for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
           _Float16* to = M == kApply ? g.X(item) : g.A(M == kGram ? 0 : 1, item);
-          *reinterpret_cast<f16x8*>(to + static_cast<int64_t>(gc) * prows + gr) = h;
+          *reinterpret_cast<f16x8*>(to + static_cast<int64_t>(xr) * prows + gr) = h;
         }
       }
-      __syncthreads();
+      lds_barrier();
     }
   }
 }
@@ -744,8 +822,12 @@ sbp_status run_step(const char* who, const Groups& gs, const Tiles& t, const Ste
                      t.gram);
   hipLaunchKernelGGL((ns_product_kernel<T, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
                      t.gram);
-  hipLaunchKernelGGL((ns_product_kernel<T, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
-                     st, t.apply);
+  if (st.last)
+    hipLaunchKernelGGL((ns_product_kernel<T, kLast>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
+                       st, t.apply);
+  else
+    hipLaunchKernelGGL((ns_product_kernel<T, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
+                       st, t.apply);
   return launched(who);
 }
 
@@ -801,7 +883,7 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
   if (rc != SBP_OK) return rc;
 
   // the largest tile that still gives every CU one: fewer bytes read per flop
-  int T = 128;
+  int T = 256;
   Tiles t = lay_tiles(gs, T);
   while (T > 64 && t.apply < 256) {
     T /= 2;
@@ -817,8 +899,9 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     st.lo_out = hp.steps - 1 - s >= 3;
     st.lo_in = s > 0 && hp.steps - s >= 3;
     st.yin = s & 1;
-    rc = T == 128 ? run_step<128>(who, gs, t, st, stream)
-                  : run_step<64>(who, gs, t, st, stream);
+    rc = T == 256   ? run_step<256>(who, gs, t, st, stream)
+         : T == 128 ? run_step<128>(who, gs, t, st, stream)
+                    : run_step<64>(who, gs, t, st, stream);
     if (rc != SBP_OK) return rc;
   }
   return SBP_OK;
