@@ -6,15 +6,17 @@
 //   A = X X',  B = b A + c A^2,  X <- a X + B X      (steps times)
 //   out = bf16(out_scale * X)
 //
-// Three products per step, all of the one form C = P Q' with both operands'
-// k index contiguous: X is kept twice, as X (m x n) and as Y = X' (n x m), so
+// The iterate stays in its matrix's own orientation, S (rows x cols): S = X
+// where rows <= cols (wide), S = X' otherwise (tall).  Three products per step,
+// one kernel core:
 //   gram   A  = X X'          lower-triangle tiles only, mirrored on the way out
 //   poly   B  = b A + c A A'  (A is symmetric) likewise
-//   apply  Y' = a Y + Y B'    written as Y' and, transposed, as X
-// and one kernel core serves the three, with the additions, scalings and the
-// transposed copy in its epilogue.  A second copy of X costs 2 bytes per
-// element and step; reading X against its storage order instead would cost
-// transposing LDS reads in the inner loop of a third of the flops.
+//   apply  S' = a S + B S  (wide)  or  a S + S B  (tall)
+// C = P Q' wants rows of P and Q with the contracted index along the row.  A,
+// B, wide gram and tall apply have that; wide apply's and tall gram's S runs
+// across, and is read from LDS with the transposing reads of gfx950.  (Keeping
+// X in both orientations instead, written twice by every apply, took 45% of
+// apply's time in its epilogue at 14336 x 4096.)
 //
 // Numbers.  The products run on fp16 MFMA with binary32 accumulation: fp16
 // keeps 11 significand bits where bf16 keeps 8, at the same rate, and every
@@ -22,7 +24,7 @@
 //   X_0     U * 2^k with the Frobenius norm in [2^13, 2^14): exact for bf16
 //           U down to 2^-28 of the norm; the rest of the normalisation, rho =
 //           1 / (max(norm, eps) 2^k), multiplies the accumulators of step 1
-//   X, Y    * 2^12 (entries up to 16); a matrix whose norm lies below eps
+//   X       * 2^12 (entries up to 16); a matrix whose norm lies below eps
 //           gets a further power of two that its iterates cannot outgrow
 //   A       * 2^12,  B * 2^10
 // Two roundings would stand out, and their remainders are kept:
@@ -66,7 +68,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBlock = 256;
 constexpr int kXcds = 8;
 constexpr int kPad = 64;        // both padded sides are multiples of this
-constexpr int kBK = 32;         // k elements per staged slice: 64 bytes a row
 constexpr int kMaxGroups = 16;  // groups of equal matrices per launch
 constexpr int kMaxNormBlocks = 256;
 constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 1024.0f, kScaleLo = 2048.0f;
@@ -84,12 +85,13 @@ struct Group {
   const uint16_t* in;
   uint16_t* out;
   int64_t in_ld, out_ld, in_stride, out_stride;
-  _Float16* base;    // X, Y, Y2, L (count*m*n each), A, B (count*m*m each)
+  _Float16* base;    // S, S2, L (count*m*n each), A, B (count*m*m each)
   double* partial;   // count * norm_blocks
   Scal* scal;        // count
   float* diag;       // m each: count for A, count for B (rounding remainders)
   int32_t rows, cols, count;
-  int32_t m, n;      // padded short and long side
+  int32_t rp, cp;    // rows and cols padded
+  int32_t m, n;      // the smaller and the larger of rp and cp
   int32_t norm_blocks;
   float out_scale;
   int32_t in_vec, out_vec;  // 16-byte rows
@@ -97,18 +99,17 @@ struct Group {
 
   __host__ __device__ bool tall() const { return rows > cols; }
   __device__ int64_t mn() const { return static_cast<int64_t>(m) * n; }
-  __device__ _Float16* X(int item) const { return base + item * mn(); }
-  __device__ _Float16* Y(int which, int item) const {
-    return base + (static_cast<int64_t>(1 + which) * count + item) * mn();
+  __device__ _Float16* S(int which, int item) const {
+    return base + (static_cast<int64_t>(which) * count + item) * mn();
   }
   __device__ _Float16* L(int item) const {
-    return base + (static_cast<int64_t>(3) * count + item) * mn();
+    return base + (static_cast<int64_t>(2) * count + item) * mn();
   }
   __device__ float* D(int which, int item) const {
     return diag + (static_cast<int64_t>(which) * count + item) * m;
   }
   __device__ _Float16* A(int which, int item) const {
-    return base + static_cast<int64_t>(4) * count * mn() +
+    return base + static_cast<int64_t>(3) * count * mn() +
            (static_cast<int64_t>(which) * count + item) * m * m;
   }
 };
@@ -122,7 +123,7 @@ struct Step {
   float a, b, c, eps;
   int32_t grow;   // the iterates of a matrix grow by less than 2^grow in all
   int32_t first, last, lo_in, lo_out;
-  int32_t yin;    // which of the two Y copies this step reads
+  int32_t in;     // which of the two copies of S this step reads
 };
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -193,17 +194,19 @@ __global__ void __launch_bounds__(kBlock) ns_norm_kernel(Groups gs) {
   if (threadIdx.x == 0) g.partial[local] = sum;
 }
 
-// ---- prologue: X_0 and Y_0 in fp16, zero-padded ---------------------------------
-// One block per 64 x 64 tile of the padded input, transposed through LDS.
+// ---- prologue: S_0 in fp16, zero-padded ----------------------------------------
+// A block takes 32 rows of 64 columns of the padded matrix.
 __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float eps, int grow) {
   int gi = 0;
   while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_pro) ++gi;
   const Group& g = gs.g[gi];
-  const int pr = g.tall() ? g.n : g.m, pc = g.tall() ? g.m : g.n;  // padded rows, cols
-  const int tc = pc / 64, per = (pr / 64) * tc;
+  const int tc = g.cp / 64, per = (g.rp / 32) * tc;
   const int local = blockIdx.x - g.t_pro;
   const int item = local / per, t = local % per;
-  const int r0 = t / tc * 64, c0 = t % tc * 64;
+  const int row = t / tc * 32 + (threadIdx.x >> 3), col = t % tc * 64 + (threadIdx.x & 7) * 8;
+  u32x4 w{0, 0, 0, 0};
+  if (row < g.rows && col < g.cols)
+    w = load_row8(g.in + item * g.in_stride + row * g.in_ld + col, g.cols - col, g.in_vec);
 
   double sq = 0.0;
   for (int i = threadIdx.x; i < g.norm_blocks; i += kBlock)
@@ -212,8 +215,8 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
   // norm * 2^k in [2^13, 2^14); 0 for a zero, infinite or NaN norm
   const bool plain = norm > 0.0 && norm < __builtin_huge_val();
   const int k = plain ? 13 - ilogb(norm) : 0;
-  const double floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
   if (t == 0 && threadIdx.x == 0) {
+    const double floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
     int below = plain && norm < eps ? ilogb(static_cast<double>(eps)) - ilogb(norm) : 0;
     below = below > grow + 2 ? below - grow - 2 : 0;
     below = below < 100 ? below : 100;
@@ -223,36 +226,13 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
                         static_cast<float>(kScaleA / (sx * sx)), static_cast<float>(rho * sx),
                         static_cast<float>(1.0 / sx)};
   }
-
-  __shared__ _Float16 tile[64][64 + 8];
-  _Float16* direct = g.tall() ? g.Y(0, item) : g.X(item);
-  _Float16* across = g.tall() ? g.X(item) : g.Y(0, item);
-  const uint16_t* in = g.in + item * g.in_stride;
-  const int cg = (threadIdx.x & 7) * 8;
+  f16x8 h;
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int r = p * 32 + (threadIdx.x >> 3), row = r0 + r, col = c0 + cg;
-    u32x4 w{0, 0, 0, 0};
-    if (row < g.rows && col < g.cols)
-      w = load_row8(in + row * g.in_ld + col, g.cols - col, g.in_vec);
-    f16x8 h;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      h[2 * q] = static_cast<_Float16>(ldexpf(sbp::bf16_lo(w[q]), k));
-      h[2 * q + 1] = static_cast<_Float16>(ldexpf(sbp::bf16_hi(w[q]), k));
-    }
-    *reinterpret_cast<f16x8*>(direct + static_cast<int64_t>(row) * pc + col) = h;
-    *reinterpret_cast<f16x8*>(&tile[r][cg]) = h;
+  for (int q = 0; q < 4; ++q) {
+    h[2 * q] = static_cast<_Float16>(ldexpf(sbp::bf16_lo(w[q]), k));
+    h[2 * q + 1] = static_cast<_Float16>(ldexpf(sbp::bf16_hi(w[q]), k));
   }
-  __syncthreads();
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int c = p * 32 + (threadIdx.x >> 3);
-    f16x8 h;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = tile[cg + j][c];
-    *reinterpret_cast<f16x8*>(across + static_cast<int64_t>(c0 + c) * pr + r0 + cg) = h;
-  }
+  *reinterpret_cast<f16x8*>(g.S(0, item) + static_cast<int64_t>(row) * g.cp + col) = h;
 }
 
 // ---- the product ------------------------------------------------------------------
@@ -260,45 +240,128 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
 enum Mode { kGram, kPoly, kApply, kLast };  // kLast: apply, to the caller's matrices
 
 // One T x T tile of C = P Q' per block of 4 waves (2 x 2, each T/2 square, in
-// 32 x 32 MFMA tiles).  Slices of 32 k elements go straight from memory to
-// one of four LDS buffers, three slices ahead of the one being multiplied.  A
-// row's four 16-byte pieces are stored rotated (piece ^ (row / 4) mod 4),
-// which the lanes' global addresses bring about, so that reads of one piece
-// of many rows spread over the banks.
-template <int T>
+// 32 x 32 MFMA tiles).  Slices of BK k elements go straight from memory to one
+// of four LDS buffers, three slices ahead of the one being multiplied.
+template <int T, int BK>
 struct Tile {
-  static constexpr int kRowBytes = kBK * 2;
-  static constexpr int kBuf = 2 * T * kRowBytes;  // P rows, then Q rows
-  static constexpr int kSub = T / 64;             // 32 x 32 tiles per wave and side
-  static constexpr int kRounds = T / 64;          // loads per operand, slice and lane
+  static constexpr int kHalf = T * BK * 2;  // one operand's slice, bytes
+  static constexpr int kBuf = 2 * kHalf;
+  static constexpr int kSub = T / 64;                // 32 x 32 tiles per wave and side
+  static constexpr int kLoads = kHalf / (4 * 1024);  // per operand, slice and lane
+  static constexpr int kPhases = BK / 16;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const _Float16* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(p), 0,
-                                           static_cast<int>(bytes), 0x00027000);
-}
-
-// One operand's rows of a slice, this wave's share.
-template <int T>
-__device__ __forceinline__ void stage(char* buf, __amdgpu_buffer_rsrc_t rows, int wave, int voff,
-                                      int round_bytes, int koff) {
+// This wave's share of one operand's slice, `bytes` from `from`.
+template <int T, int BK>
+__device__ __forceinline__ void stage(char* buf, const char* from, int bytes, int wave, int voff,
+                                      int round_bytes) {
+  const __amdgpu_buffer_rsrc_t rows =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, bytes, 0x00027000);
 #pragma unroll
-  for (int r = 0; r < Tile<T>::kRounds; ++r)
+  for (int r = 0; r < Tile<T, BK>::kLoads; ++r)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rows, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16, voff,
-        r * round_bytes + koff, 0, 0);
+        r * round_bytes, 0, 0);
 }
 
-// Order of a phase's instructions: one MFMA, one LDS read and one load to LDS
-// in turn, so that both kinds of memory work run under the MFMAs.
-template <int T, int LOADS>
+// One operand of a tile.  Along: the matrix's rows r0 .. are the operand's
+// rows, and a slice is BK consecutive elements of each; LDS keeps a row's
+// 16-byte pieces rotated by row.  Across: the matrix's columns r0 .. are the
+// operand's rows, and a slice is BK rows of T elements; LDS keeps a row's
+// 64-byte pieces rotated by row, and the reads transpose.  Both rotations come
+// from the lanes' global addresses and spread the reads over the banks.
+// Rows past the matrix read as zero or as a neighbour: they only reach
+// results that are not stored.
+template <int T, int BK, bool ACROSS>
+struct Operand {
+  using TL = Tile<T, BK>;
+  const char* from;  // next slice to load
+  int64_t step;
+  int bytes, voff, round_bytes;
+  int at;                            // LDS offset of this lane's first fragment
+  int off[ACROSS ? TL::kSub : TL::kPhases];  // further offset by sub-tile or phase
+
+  __device__ __forceinline__ void init(const _Float16* mat, int rows, int ld, int r0, int wave,
+                                       int lane, int wrow) {
+    if constexpr (ACROSS) {
+      constexpr int kLanes = T / 8;  // lanes per row
+      from = reinterpret_cast<const char*>(mat + r0);
+      step = static_cast<int64_t>(BK) * ld * 2;
+      bytes = (BK * ld - r0) * 2;
+      const int row = wave * (64 / kLanes) + lane / kLanes;
+      const int piece = lane % kLanes;
+      voff = row * ld * 2 + ((((piece >> 2) ^ turn(row)) << 2) | (piece & 3)) * 16;
+      round_bytes = 4 * (64 / kLanes) * ld * 2;
+      const int k = (lane >> 5) * 8 + ((lane >> 2) & 3);  // of this lane's address
+      at = k * (T * 2) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < TL::kSub; ++i) off[i] = ((wrow / 32 + i) ^ turn(k)) * 64;
+    } else {
+      constexpr int kLanes = BK / 8;
+      from = reinterpret_cast<const char*>(mat + static_cast<int64_t>(r0) * ld);
+      step = BK * 2;
+      const int have = rows - r0 < T ? rows - r0 : T;
+      bytes = have * ld * 2;
+      const int row = wave * (64 / kLanes) + lane / kLanes;
+      voff = row * ld * 2 + ((lane % kLanes) ^ turn(row)) * 16;
+      round_bytes = 4 * (64 / kLanes) * ld * 2;
+      at = (wrow + (lane & 31)) * (BK * 2);
+#pragma unroll
+      for (int p = 0; p < TL::kPhases; ++p) off[p] = ((p * 2 + (lane >> 5)) ^ turn(lane)) * 16;
+    }
+  }
+  // The rotation of a row; rows that differ by 32 (along) or 4 (across) agree.
+  static __device__ __forceinline__ int turn(int row) {
+    if constexpr (ACROSS) return T >= 128 ? row & 3 : (row >> 1) & 1;
+    else return BK == 32 ? (row >> 2) & 3 : row & 7;
+  }
+  // Along, the last rows' slices end before `bytes` does by what is consumed.
+  __device__ __forceinline__ void load(char* buf, int wave) {
+    stage<T, BK>(buf, from, bytes, wave, voff, round_bytes);
+    from += step;
+    if constexpr (!ACROSS) bytes -= BK * 2;
+  }
+  __device__ __forceinline__ f16x8 read(const char* buf, int phase, int i) const {
+    if constexpr (ACROSS) {
+      typedef __fp16 h4 __attribute__((__vector_size__(8)));
+      typedef __attribute__((address_space(3))) h4* lds_h4;
+      const char* p = buf + at + off[i] + phase * 16 * (T * 2);
+      const h4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)p);
+      const h4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + 4 * (T * 2)));
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const f16x8*>(buf + at + off[phase] + i * 32 * (BK * 2));
+    }
+  }
+};
+
+template <int T>
+struct Frags {
+  f16x8 p[T / 64], q[T / 64];
+};
+
+template <int T>
+using Acc = f32x16[T / 64][T / 64];
+
+template <int T>
+__device__ __forceinline__ void multiply(const Frags<T>& f, Acc<T>& acc) {
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i)
+#pragma unroll
+    for (int j = 0; j < T / 64; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+}
+
+// Order of a phase's instructions: MFMAs, LDS reads and loads to LDS in turn,
+// so that both kinds of memory work run under the MFMAs.
+template <int T, int READS, int LOADS>
 __device__ __forceinline__ void interleave() {
-  constexpr int mfmas = Tile<T>::kSub * Tile<T>::kSub, reads = 2 * Tile<T>::kSub;
-  constexpr int r1 = (reads + mfmas - 1) / mfmas, l1 = (LOADS + mfmas - 1) / mfmas;
+  constexpr int mfmas = (T / 64) * (T / 64);
+  constexpr int r1 = (READS + mfmas - 1) / mfmas, l1 = (LOADS + mfmas - 1) / mfmas;
 #pragma unroll
   for (int i = 0; i < mfmas; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i * r1 < reads) __builtin_amdgcn_sched_group_barrier(0x100, r1, 0);
+    if (i * r1 < READS) __builtin_amdgcn_sched_group_barrier(0x100, r1, 0);
     if (i * l1 < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, l1, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -317,6 +380,121 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// acc = P Q' over `slices` slices.
+template <int T, int BK, bool PX, bool QX>
+__device__ __forceinline__ void product(char* buf0, char* buf1, char* buf2, char* buf3,
+                                        Operand<T, BK, PX>& P, Operand<T, BK, QX>& Q, int slices,
+                                        int wave, Acc<T>& acc) {
+  using TL = Tile<T, BK>;
+  constexpr int L = TL::kLoads, H = TL::kHalf, N = TL::kPhases;
+  constexpr int kReads = TL::kSub * ((PX ? 2 : 1) + (QX ? 2 : 1));
+  Frags<T> f[2];
+  auto load = [&](char* to) {
+    P.load(to, wave);
+    Q.load(to + H, wave);
+  };
+  auto read = [&](const char* buf, int phase, Frags<T>& to) {
+#pragma unroll
+    for (int i = 0; i < TL::kSub; ++i) {
+      to.p[i] = P.read(buf, phase, i);
+      to.q[i] = Q.read(buf + H, phase, i);
+    }
+  };
+  // One slice: it is in `cur`, its first fragments in f[0].  The barrier sits
+  // before the last multiply, so that each multiply hides the next one's reads.
+  // LOAD: the slice three further on is loaded into `to`; LEFT: loads that may
+  // still be under way when the next slice has to be there (-1: no next one).
+  auto slice = [&](const char* cur, const char* nxt, char* to, auto load_c, auto left_c) {
+    constexpr bool kLoad = decltype(load_c)::value;
+    constexpr int kLeft = decltype(left_c)::value;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int ph = 0; ph < N - 1; ++ph) {
+      if (kLoad && ph == 0) P.load(to, wave);
+      read(cur, ph + 1, f[(ph + 1) & 1]);
+      multiply<T>(f[ph & 1], acc);
+      if (kLoad && ph == 0) interleave<T, kReads, L>();
+      else interleave<T, kReads, 0>();
+    }
+    if constexpr (kLeft >= 0) {
+      slice_barrier<kLeft>();
+      if constexpr (kLoad) Q.load(to + H, wave);
+      read(nxt, 0, f[0]);
+    }
+    multiply<T>(f[1], acc);
+    interleave<T, kLeft >= 0 ? kReads : 0, kLoad ? L : 0>();
+  };
+  constexpr std::true_type kYes{};
+  constexpr std::false_type kNo{};
+  // two slices under way, and the first half of a third
+  constexpr std::integral_constant<int, 3 * L> kSteady{};
+  constexpr std::integral_constant<int, 2 * L> kOne{};
+  constexpr std::integral_constant<int, 0> kNone{};
+  constexpr std::integral_constant<int, -1> kEnd{};
+  // The last slice is in buf3, so that there is one way into the loop's rounds
+  // of four and one way out; a number that is no multiple of four starts
+  // further on, and drains its loads once (known to the compiler, whose own
+  // waits in the loop would else provide for the other way in).  With BK = 32
+  // the number is even.
+  constexpr bool kOdd = BK != 32;
+  const int rest = slices & 3;
+  if (slices < 4) {
+    if (kOdd && rest == 3) load(buf1);
+    if (!kOdd || rest >= 2) load(buf2);
+    load(buf3);
+    slice_barrier<0>();
+    read(kOdd && rest == 3 ? buf1 : !kOdd || rest == 2 ? buf2 : buf3, 0, f[0]);
+    if (kOdd && rest == 3) slice(buf1, buf2, nullptr, kNo, kNone);
+    if (!kOdd || rest >= 2) slice(buf2, buf3, nullptr, kNo, kNone);
+  } else {
+    if (rest == 0) {
+      load(buf0);
+      load(buf1);
+      load(buf2);
+      slice_barrier<4 * L>();
+      read(buf0, 0, f[0]);
+    } else {
+      if (kOdd && rest == 3) {
+        load(buf1);
+        load(buf2);
+        load(buf3);
+        slice_barrier<4 * L>();
+        read(buf1, 0, f[0]);
+        slice(buf1, buf2, buf0, kYes, kSteady);
+      }
+      if (rest >= 2) {
+        if (!kOdd || rest == 2) {
+          load(buf2);
+          load(buf3);
+          load(buf0);
+          slice_barrier<4 * L>();
+          read(buf2, 0, f[0]);
+        }
+        slice(buf2, buf3, buf1, kYes, kSteady);
+      }
+      if (kOdd && rest == 1) {
+        load(buf3);
+        load(buf0);
+        load(buf1);
+        slice_barrier<4 * L>();
+        read(buf3, 0, f[0]);
+      }
+      slice(buf3, buf0, buf2, kYes, kSteady);
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    }
+    for (int s = slices >> 2; s > 1; --s) {
+      slice(buf0, buf1, buf3, kYes, kSteady);
+      slice(buf1, buf2, buf0, kYes, kSteady);
+      slice(buf2, buf3, buf1, kYes, kSteady);
+      slice(buf3, buf0, buf2, kYes, kSteady);
+    }
+    slice(buf0, buf1, buf3, kYes, kSteady);
+    slice(buf1, buf2, nullptr, kNo, kOne);
+    slice(buf2, buf3, nullptr, kNo, kNone);
+  }
+  slice(buf3, nullptr, nullptr, kNo, kEnd);
+}
+
 // Up to 8 consecutive bf16 values of a row of the caller's output.
 __device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
   uint32_t b[8];
@@ -332,33 +510,6 @@ __device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, cons
   }
 }
 
-template <int T>
-struct Frags {
-  f16x8 p[Tile<T>::kSub], q[Tile<T>::kSub];
-};
-
-template <int T>
-__device__ __forceinline__ void read_frags(const char* buf, int pbase, int qbase, int piece,
-                                           Frags<T>& f) {
-#pragma unroll
-  for (int i = 0; i < Tile<T>::kSub; ++i) {
-    f.p[i] = *reinterpret_cast<const f16x8*>(buf + pbase + piece + i * 32 * Tile<T>::kRowBytes);
-    f.q[i] = *reinterpret_cast<const f16x8*>(buf + qbase + piece + i * 32 * Tile<T>::kRowBytes);
-  }
-}
-
-template <int T>
-using Acc = f32x16[Tile<T>::kSub][Tile<T>::kSub];
-
-template <int T>
-__device__ __forceinline__ void multiply(const Frags<T>& f, Acc<T>& acc) {
-#pragma unroll
-  for (int i = 0; i < Tile<T>::kSub; ++i)
-#pragma unroll
-    for (int j = 0; j < Tile<T>::kSub; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
-}
-
 // Where (row, col) of the epilogue's binary32 slab is kept: 32 rows in each of
 // two buffers; groups of 8 columns are rotated by the row's 8-row group, so
 // that both a row's 8 columns and a column's 8 rows are read without bank
@@ -369,14 +520,15 @@ __device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) 
   return half + (row & 31) * T + (col ^ (((row >> 3) & 7) << 3));
 }
 
-template <int T, Mode M>
+template <int T, int BK, Mode M>
 __global__ void __launch_bounds__(kBlock, T == 256 ? 1 : 2)
 ns_product_kernel(Groups gs, Step st, unsigned total) {
+  using TL = Tile<T, BK>;
   // separate arrays: reads of one do not wait for loads into another
-  __shared__ __align__(16) char buf0[Tile<T>::kBuf];
-  __shared__ __align__(16) char buf1[Tile<T>::kBuf];
-  __shared__ __align__(16) char buf2[Tile<T>::kBuf];
-  __shared__ __align__(16) char buf3[Tile<T>::kBuf];
+  __shared__ __align__(16) char buf0[TL::kBuf];
+  __shared__ __align__(16) char buf1[TL::kBuf];
+  __shared__ __align__(16) char buf2[TL::kBuf];
+  __shared__ __align__(16) char buf3[TL::kBuf];
   constexpr int W = T / 2;  // a wave's side
   constexpr bool kApplies = M == kApply || M == kLast;
 
@@ -387,23 +539,24 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
   int gi = 0;
   while (gi + 1 < gs.n && b >= (kApplies ? gs.g[gi + 1].t_apply : gs.g[gi + 1].t_gram)) ++gi;
   const Group& g = gs.g[gi];
-  const int m = g.m, n = g.n;
-  const int tm = (m + T - 1) / T;
-  int item, ti, tj;  // tile row (of P) and column (rows of Q)
+  const bool tall = g.tall();
+  const int m = g.m;
+  const int crows = kApplies ? g.rp : m, ccols = kApplies ? g.cp : m;  // of C
+  int item, ti, tj;
   if constexpr (kApplies) {
-    const int tn = (n + T - 1) / T;
+    const int tr = (crows + T - 1) / T, tc = (ccols + T - 1) / T;
     const int local = b - g.t_apply;
-    item = local / (tn * tm);
-    const int t = local % (tn * tm);
+    item = local / (tr * tc);
+    const int t = local % (tr * tc);
     // strips of 8 tile rows, column by column
     constexpr int kStrip = 8;
-    const int strip = t / (kStrip * tm), left = tn - strip * kStrip;
+    const int strip = t / (kStrip * tc), left = tr - strip * kStrip;
     const int high = left < kStrip ? left : kStrip;
-    const int s = t - strip * kStrip * tm;
+    const int s = t - strip * kStrip * tc;
     ti = strip * kStrip + s % high;
     tj = s / high;
   } else {
-    const int per = tm * (tm + 1) / 2;
+    const int tm = (m + T - 1) / T, per = tm * (tm + 1) / 2;
     const int local = b - g.t_gram;
     item = local / per;
     const int t = local % per;
@@ -412,156 +565,95 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
     tj = t - ti * (ti + 1) / 2;
   }
-
-  const int k = M == kGram ? n : m;  // contracted length = both row lengths
-  const _Float16* Pm = M == kGram ? g.X(item) : M == kPoly ? g.A(0, item) : g.Y(st.yin, item);
-  const _Float16* Qm = M == kGram ? Pm : M == kPoly ? Pm : g.A(1, item);
-  const int prows = kApplies ? n : m;
   const int r0 = ti * T, c0 = tj * T;
-  const int pr = prows - r0 < T ? prows - r0 : T, qr = m - c0 < T ? m - c0 : T;
-  const __amdgpu_buffer_rsrc_t P =
-      rows_of(Pm + static_cast<int64_t>(r0) * k, static_cast<int64_t>(pr) * k * 2);
-  const __amdgpu_buffer_rsrc_t Q =
-      rows_of(Qm + static_cast<int64_t>(c0) * k, static_cast<int64_t>(qr) * k * 2);
-
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = wave >> 1, wc = wave & 1;
-  const int voff = (wave * 16 + (lane >> 2)) * k * 2 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
-  const int round_bytes = 64 * k * 2;
-  const int pbase = (wr * W + (lane & 31)) * Tile<T>::kRowBytes;
-  const int qbase = Tile<T>::kBuf / 2 + (wc * W + (lane & 31)) * Tile<T>::kRowBytes;
-  const int rot = (lane >> 2) & 3;
-  const int piece[2] = {((lane >> 5) ^ rot) * 16, ((2 + (lane >> 5)) ^ rot) * 16};
 
   Acc<T> acc = {};
-  Frags<T> f[2];
-  constexpr int kHalf = Tile<T>::kBuf / 2, L = Tile<T>::kRounds;
-  int koff = 0;  // of the next slice to load
-  auto load = [&](char* to) {
-    stage<T>(to, P, wave, voff, round_bytes, koff);
-    stage<T>(to + kHalf, Q, wave, voff, round_bytes, koff);
-    koff += kBK * 2;
+  auto along = [&](const _Float16* Pm, const _Float16* Qm, int k) {
+    Operand<T, BK, false> P, Q;
+    P.init(Pm, crows, k, r0, wave, lane, wr * W);
+    Q.init(Qm, ccols, k, c0, wave, lane, wc * W);
+    product<T, BK>(buf0, buf1, buf2, buf3, P, Q, k / BK, wave, acc);
   };
-  // One slice: it is in `cur`, its first fragments in f[0].  The barrier sits
-  // between the two multiplies, so that each hides the reads for the next.
-  // LOAD: the slice three further on is loaded into `to`; LEFT: loads that may
-  // still be under way when the next slice has to be there (-1: no next one).
-  auto slice = [&](const char* cur, const char* nxt, char* to, auto load_c, auto left_c) {
-    constexpr bool kLoad = decltype(load_c)::value;
-    constexpr int kLeft = decltype(left_c)::value;
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (kLoad) stage<T>(to, P, wave, voff, round_bytes, koff);
-    read_frags<T>(cur, pbase, qbase, piece[1], f[1]);
-    multiply<T>(f[0], acc);
-    interleave<T, kLoad ? L : 0>();
-    if constexpr (kLeft >= 0) {
-      slice_barrier<kLeft>();
-      if constexpr (kLoad) stage<T>(to + kHalf, Q, wave, voff, round_bytes, koff);
-      read_frags<T>(nxt, pbase, qbase, piece[0], f[0]);
-    }
-    multiply<T>(f[1], acc);
-    interleave<T, kLoad ? L : 0>();
-    if constexpr (kLoad) koff += kBK * 2;
-  };
-  constexpr std::true_type kYes{};
-  constexpr std::false_type kNo{};
-  // two slices under way, and the first half of a third
-  constexpr std::integral_constant<int, 3 * L> kSteady{};
-  constexpr std::integral_constant<int, 2 * L> kOne{};
-  constexpr std::integral_constant<int, 0> kNone{};
-  constexpr std::integral_constant<int, -1> kEnd{};
-  const int slices = k / kBK;  // even; the last is in buf3
-  if (slices & 2) {
-    load(buf2);
-    load(buf3);
-    if (slices == 2) {
-      slice_barrier<2 * L>();
-      read_frags<T>(buf2, pbase, qbase, piece[0], f[0]);
-      slice(buf2, buf3, nullptr, kNo, kNone);
+  const _Float16* S = g.S(st.in, item);
+  if constexpr (M == kPoly) {
+    along(g.A(0, item), g.A(0, item), m);
+  } else if constexpr (M == kGram) {
+    if (tall) {
+      Operand<T, BK, true> P, Q;
+      P.init(S, m, m, r0, wave, lane, wr * W);
+      Q.init(S, m, m, c0, wave, lane, wc * W);
+      product<T, BK>(buf0, buf1, buf2, buf3, P, Q, g.n / BK, wave, acc);
     } else {
-      load(buf0);
-      slice_barrier<4 * L>();
-      read_frags<T>(buf2, pbase, qbase, piece[0], f[0]);
-      slice(buf2, buf3, buf1, kYes, kSteady);
-      slice(buf3, buf0, buf2, kYes, kSteady);
+      along(S, S, g.n);
     }
   } else {
-    load(buf0);
-    load(buf1);
-    load(buf2);
-    slice_barrier<4 * L>();
-    read_frags<T>(buf0, pbase, qbase, piece[0], f[0]);
-  }
-  if (slices > 2) {
-    for (int s = slices >> 2; s > 1; --s) {
-      slice(buf0, buf1, buf3, kYes, kSteady);
-      slice(buf1, buf2, buf0, kYes, kSteady);
-      slice(buf2, buf3, buf1, kYes, kSteady);
-      slice(buf3, buf0, buf2, kYes, kSteady);
+    if (tall) {
+      along(S, g.A(1, item), m);
+    } else {
+      Operand<T, BK, false> P;
+      Operand<T, BK, true> Q;
+      P.init(g.A(1, item), m, m, r0, wave, lane, wr * W);
+      Q.init(S, ccols, ccols, c0, wave, lane, wc * W);
+      product<T, BK>(buf0, buf1, buf2, buf3, P, Q, m / BK, wave, acc);
     }
-    slice(buf0, buf1, buf3, kYes, kSteady);
-    slice(buf1, buf2, nullptr, kNo, kOne);
-    slice(buf2, buf3, nullptr, kNo, kNone);
   }
-  slice(buf3, nullptr, nullptr, kNo, kEnd);
 
   // Epilogue, 64 rows at a time: accumulators to LDS as binary32, then row by
-  // row (8 columns a thread) the additions and the direct store, then the
-  // transposed store.  What the additions read is asked for ahead of the
-  // barriers, which wait for LDS alone: a block has one wave per SIMD, so
-  // nothing else would hide the latency (waiting for memory at each barrier
-  // and pass took as long as the products at k = 4096).
-  static_assert(32 * T * 4 <= Tile<T>::kBuf, "half the slab fits one buffer");
+  // row (8 columns a thread) the additions and the store; gram and poly store
+  // the mirrored tile as well.  What the additions read is asked for ahead of
+  // the barriers, which wait for LDS alone: nothing else would hide that
+  // latency where a block has one wave per SIMD.
+  static_assert(32 * T * 4 <= TL::kBuf, "half the slab fits one buffer");
   const Scal sc = g.scal[item];
-  const bool cross = M == kApply ? true : M == kLast ? !g.tall() : ti != tj;
+  const bool cross = !kApplies && ti != tj;
   constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow, kPasses = 64 / kRowsAtOnce;
   const int prow = threadIdx.x / kPerRow, pcol = (threadIdx.x % kPerRow) * 8;
   const int gc = c0 + pcol;
-  const bool col_in = gc < m;
-  // the matrix added and the remainders of the product's diagonal, per column
-  const _Float16* add = M == kPoly ? g.A(0, item) : kApplies ? g.Y(st.yin, item) : nullptr;
+  const bool col_in = gc < ccols;
+  // the matrix added and the remainders of the product's diagonal
+  const _Float16* add = M == kPoly ? g.A(0, item) : S;
   const _Float16* rem = kApplies && st.lo_in ? g.L(item) : nullptr;
-  const float* diag = M == kPoly ? g.D(0, item) : kApplies ? g.D(1, item) : nullptr;
-  float dc[8] = {};
-  if constexpr (M != kGram) {
-    if (col_in) load8(diag + gc, dc);
-  }
+  const float* diag = M == kPoly ? g.D(0, item) : g.D(1, item);
   const float alpha = st.first ? sc.gram_first : sc.gram;
   const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
   const float fx = (st.first ? sc.apply_first : 1.0f) * (M == kLast ? g.out_scale * sc.inv_sx : 1.0f);
-  if constexpr (kApplies) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) dc[q] = st.a + dc[q] * (1.0f / kScaleB);
-  }
+  float dc[8] = {};
+  if (M != kGram && col_in && (M == kPoly || tall)) load8(diag + gc, dc);
   lds_barrier();  // the last slice is read
-#pragma unroll
+#pragma unroll 1
   for (int sl = 0; sl < T / 64; ++sl) {
     f16x8 ad[kPasses], re[kPasses];
     float dr[kPasses];
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       const int gr = r0 + sl * 64 + p * kRowsAtOnce + prow;
-      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
+      const int64_t idx = static_cast<int64_t>(gr) * ccols + gc;
       ad[p] = re[p] = f16x8{};
       dr[p] = 0.0f;
-      if (gr < prows && col_in) {
+      if (gr < crows && col_in) {
         if constexpr (M != kGram) ad[p] = *reinterpret_cast<const f16x8*>(add + idx);
-        if constexpr (M == kPoly) dr[p] = diag[gr];
+        if (M == kPoly || (kApplies && !tall)) dr[p] = diag[gr];
         if (kApplies && rem != nullptr) re[p] = *reinterpret_cast<const f16x8*>(rem + idx);
       }
     }
 #pragma unroll
-    for (int i = 0; i < Tile<T>::kSub; ++i) {
-      const int rb = wr * Tile<T>::kSub + i;  // 32-row block of the tile
-      if (rb / 2 == sl) {
+    for (int part = 0; part < T / 64; ++part) {
+      if (part != sl) continue;
 #pragma unroll
-        for (int j = 0; j < Tile<T>::kSub; ++j)
+      for (int i = 0; i < TL::kSub; ++i) {
+        const int rb = wr * TL::kSub + i;  // 32-row block of the tile
+        if (rb / 2 == part) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int row = (rb & 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-            const int col = wc * W + j * 32 + (lane & 31);
-            *slab_at<T>(buf0, buf1, row, col) = acc[i][j][e];
-          }
+          for (int j = 0; j < TL::kSub; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int row = (rb & 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+              const int col = wc * W + j * 32 + (lane & 31);
+              *slab_at<T>(buf0, buf1, row, col) = acc[i][j][e];
+            }
+        }
       }
     }
     lds_barrier();
@@ -569,9 +661,9 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     for (int p = 0; p < kPasses; ++p) {
       const int row = p * kRowsAtOnce + prow;
       const int gr = r0 + sl * 64 + row;
-      if (gr >= prows || !col_in) continue;
+      if (gr >= crows || !col_in) continue;
       float* at = slab_at<T>(buf0, buf1, row, pcol);
-      const int64_t idx = static_cast<int64_t>(gr) * m + gc;
+      const int64_t idx = static_cast<int64_t>(gr) * ccols + gc;
       float v[8];
       load8(at, v);
       f16x8 h;
@@ -597,14 +689,16 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
+          // the diagonal's remainder multiplies S's row (wide) or column (tall)
+          const float a = st.a + (dr[p] + dc[q]) * (1.0f / kScaleB);
           const float x =
               static_cast<float>(ad[p][q]) + static_cast<float>(re[p][q]) * (1.0f / kScaleLo);
-          v[q] = (dc[q] * x + v[q] * (1.0f / kScaleB)) * fx;
+          v[q] = (a * x + v[q] * (1.0f / kScaleB)) * fx;
         }
         if constexpr (M == kApply) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
-          *reinterpret_cast<f16x8*>(g.Y(st.yin ^ 1, item) + idx) = h;
+          *reinterpret_cast<f16x8*>(g.S(st.in ^ 1, item) + idx) = h;
           if (st.lo_out) {
             f16x8 l;
 #pragma unroll
@@ -612,7 +706,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
               l[q] = static_cast<_Float16>((v[q] - static_cast<float>(h[q])) * kScaleLo);
             *reinterpret_cast<f16x8*>(g.L(item) + idx) = l;
           }
-        } else if (!cross && gr < g.rows) {
+        } else if (gr < g.rows) {
           store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v);
         }
       }
@@ -628,21 +722,13 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
       for (int p = 0; p < T / 32; ++p) {
         const int col = p * 32 + (threadIdx.x >> 3), row = (threadIdx.x & 7) * 8;
         const int gr = r0 + sl * 64 + row, xr = c0 + col;
-        if (gr >= prows || xr >= m) continue;
-        float v[8];
+        if (gr >= m || xr >= m) continue;
+        f16x8 h;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = *slab_at<T>(buf0, buf1, row + q, col);
-        if constexpr (M == kLast) {
-          // X is rows x cols here: its row xr, columns gr ..
-          if (xr < g.rows)
-            store_out8(g.out + item * g.out_stride + xr * g.out_ld + gr, g.cols - gr, g.out_vec, v);
-        } else {
-          f16x8 h;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
-          _Float16* to = M == kApply ? g.X(item) : g.A(M == kGram ? 0 : 1, item);
-          *reinterpret_cast<f16x8*>(to + static_cast<int64_t>(xr) * prows + gr) = h;
-        }
+        for (int q = 0; q < 8; ++q)
+          h[q] = static_cast<_Float16>(*slab_at<T>(buf0, buf1, row + q, col));
+        *reinterpret_cast<f16x8*>(g.A(M == kGram ? 0 : 1, item) + static_cast<int64_t>(xr) * m +
+                                  gr) = h;
       }
       lds_barrier();
     }
@@ -683,7 +769,7 @@ Shape shape_of(const sbp_matrices& g) {
 
 // Bytes one piece takes: fp16 arrays, norm partials, scalars (each 256-B aligned).
 int64_t half_bytes(const Shape& s, int64_t count) {
-  return up(2 * count * (4 * s.m * s.n + 2 * s.m * s.m), 256);
+  return up(2 * count * (3 * s.m * s.n + 2 * s.m * s.m), 256);
 }
 int64_t partial_bytes(const Shape& s, int64_t count) { return up(8 * count * s.norm_blocks, 256); }
 int64_t diag_bytes(const Shape& s, int64_t count) { return up(8 * count * s.m, 256); }
@@ -815,18 +901,18 @@ Tiles lay_tiles(Groups& gs, int T) {
   return t;
 }
 
-template <int T>
+template <int T, int BK>
 sbp_status run_step(const char* who, const Groups& gs, const Tiles& t, const Step& st,
                     hipStream_t stream) {
-  hipLaunchKernelGGL((ns_product_kernel<T, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
+  hipLaunchKernelGGL((ns_product_kernel<T, BK, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
                      t.gram);
-  hipLaunchKernelGGL((ns_product_kernel<T, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
+  hipLaunchKernelGGL((ns_product_kernel<T, BK, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
                      t.gram);
   if (st.last)
-    hipLaunchKernelGGL((ns_product_kernel<T, kLast>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
+    hipLaunchKernelGGL((ns_product_kernel<T, BK, kLast>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
                        st, t.apply);
   else
-    hipLaunchKernelGGL((ns_product_kernel<T, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
+    hipLaunchKernelGGL((ns_product_kernel<T, BK, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
                        st, t.apply);
   return launched(who);
 }
@@ -850,6 +936,8 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     g.rows = static_cast<int32_t>(src.rows);
     g.cols = static_cast<int32_t>(src.cols);
     g.count = static_cast<int32_t>(p.count);
+    g.rp = static_cast<int32_t>(up(src.rows, kPad));
+    g.cp = static_cast<int32_t>(up(src.cols, kPad));
     g.m = static_cast<int32_t>(s.m);
     g.n = static_cast<int32_t>(s.n);
     g.norm_blocks = static_cast<int32_t>(s.norm_blocks);
@@ -869,7 +957,7 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     g.t_norm = norm;
     g.t_pro = pro;
     norm += g.count * g.norm_blocks;
-    pro += g.count * (g.m / 64) * (g.n / 64);
+    pro += g.count * (g.rp / 32) * (g.cp / 64);
   }
   // |x| grows by at most a factor sum |coefficients| per step while small
   double grow = 0.0;
@@ -898,10 +986,10 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     st.last = s == hp.steps - 1;
     st.lo_out = hp.steps - 1 - s >= 3;
     st.lo_in = s > 0 && hp.steps - s >= 3;
-    st.yin = s & 1;
-    rc = T == 256   ? run_step<256>(who, gs, t, st, stream)
-         : T == 128 ? run_step<128>(who, gs, t, st, stream)
-                    : run_step<64>(who, gs, t, st, stream);
+    st.in = s & 1;
+    rc = T == 256   ? run_step<256, 32>(who, gs, t, st, stream)
+         : T == 128 ? run_step<128, 32>(who, gs, t, st, stream)
+                    : run_step<64, 64>(who, gs, t, st, stream);
     if (rc != SBP_OK) return rc;
   }
   return SBP_OK;
