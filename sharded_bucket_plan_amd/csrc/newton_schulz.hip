@@ -45,6 +45,7 @@
 // same from run to run.
 #include <hip/hip_runtime.h>
 #include <math.h>
+#include <stdlib.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -61,6 +62,7 @@
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -85,7 +87,8 @@ struct Group {
   const uint16_t* in;
   uint16_t* out;
   int64_t in_ld, out_ld, in_stride, out_stride;
-  _Float16* base;    // S, S2, L (count*m*n each), A, B (count*m*m each)
+  _Float16* base;    // S, S2, L (count*m*n each), A, B (count*m*m each);
+                     // short side of at most 128: S, L
   double* partial;   // count * norm_blocks
   Scal* scal;        // count
   float* diag;       // m each: count for A, count for B (rounding remainders)
@@ -96,6 +99,11 @@ struct Group {
   float out_scale;
   int32_t in_vec, out_vec;  // 16-byte rows
   uint32_t t_norm, t_pro, t_gram, t_apply;  // first block of the group in each launch
+  // short side of at most 128 only: blocks per matrix; their partial Gram
+  // matrices (twice, for steps in turn) and the powers of two of the first
+  int32_t splits;
+  float* parts;
+  int32_t* part_ks;
 
   __host__ __device__ bool tall() const { return rows > cols; }
   __device__ int64_t mn() const { return static_cast<int64_t>(m) * n; }
@@ -103,10 +111,16 @@ struct Group {
     return base + (static_cast<int64_t>(which) * count + item) * mn();
   }
   __device__ _Float16* L(int item) const {
-    return base + (static_cast<int64_t>(2) * count + item) * mn();
+    return base + (static_cast<int64_t>(splits > 0 ? 1 : 2) * count + item) * mn();
   }
   __device__ float* D(int which, int item) const {
     return diag + (static_cast<int64_t>(which) * count + item) * m;
+  }
+  __device__ float* part(int which, int item, int split) const {
+    return parts + ((static_cast<int64_t>(which) * count + item) * splits + split) * m * m;
+  }
+  __device__ int32_t* part_k(int item, int split) const {
+    return part_ks + static_cast<int64_t>(item) * splits + split;
   }
   __device__ _Float16* A(int which, int item) const {
     return base + static_cast<int64_t>(3) * count * mn() +
@@ -156,11 +170,19 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
 // Up to 8 consecutive bf16 values of a row, zeros from `left` on.
 __device__ __forceinline__ u32x4 load_row8(const uint16_t* p, int left, bool vec) {
   if (vec && left >= 8) return *reinterpret_cast<const u32x4*>(p);
-  u32x4 w{0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < left) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
-  return w;
+  auto one = [&](int j) -> uint32_t {  // element 0 exists: no branches
+    const uint32_t x = p[j < left ? j : 0];
+    return j < left ? x : 0u;
+  };
+  return u32x4{one(0) | one(1) << 16, one(2) | one(3) << 16, one(4) | one(5) << 16,
+               one(6) | one(7) << 16};
+}
+
+// 8 bf16 values times 2^k in fp16.
+__device__ __forceinline__ f16x8 half8(u32x4 w, int k) {
+  auto lo = [&](uint32_t x) { return static_cast<_Float16>(ldexpf(sbp::bf16_lo(x), k)); };
+  auto hi = [&](uint32_t x) { return static_cast<_Float16>(ldexpf(sbp::bf16_hi(x), k)); };
+  return f16x8{lo(w.x), hi(w.x), lo(w.y), hi(w.y), lo(w.z), hi(w.z), lo(w.w), hi(w.w)};
 }
 
 // ---- squared norms: one float64 partial per block ----------------------------
@@ -194,6 +216,26 @@ __global__ void __launch_bounds__(kBlock) ns_norm_kernel(Groups gs) {
   if (threadIdx.x == 0) g.partial[local] = sum;
 }
 
+// How a matrix of this norm is stored: X_0 = U * 2^k with the norm in [2^13,
+// 2^14) (k = 0 for a zero, infinite or NaN norm), X_0 = stored * rho, later
+// X = stored / sx.
+struct Norm {
+  int k;
+  double floor_norm, rho, sx;
+};
+__device__ __forceinline__ Norm norm_of(double norm, float eps, int grow) {
+  Norm r;
+  const bool plain = norm > 0.0 && norm < __builtin_huge_val();
+  r.k = plain ? 13 - ilogb(norm) : 0;
+  r.floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
+  int below = plain && norm < eps ? ilogb(static_cast<double>(eps)) - ilogb(norm) : 0;
+  below = below > grow + 2 ? below - grow - 2 : 0;
+  below = below < 100 ? below : 100;
+  r.rho = 1.0 / (r.floor_norm * ldexp(1.0, r.k));
+  r.sx = ldexp(static_cast<double>(kScaleX), below);
+  return r;
+}
+
 // ---- prologue: S_0 in fp16, zero-padded ----------------------------------------
 // A block takes 32 rows of 64 columns of the padded matrix.
 __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float eps, int grow) {
@@ -211,57 +253,67 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
   double sq = 0.0;
   for (int i = threadIdx.x; i < g.norm_blocks; i += kBlock)
     sq = sq + g.partial[item * g.norm_blocks + i];
-  const double norm = sqrt(block_sum_all(sq));
-  // norm * 2^k in [2^13, 2^14); 0 for a zero, infinite or NaN norm
-  const bool plain = norm > 0.0 && norm < __builtin_huge_val();
-  const int k = plain ? 13 - ilogb(norm) : 0;
-  if (t == 0 && threadIdx.x == 0) {
-    const double floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
-    int below = plain && norm < eps ? ilogb(static_cast<double>(eps)) - ilogb(norm) : 0;
-    below = below > grow + 2 ? below - grow - 2 : 0;
-    below = below < 100 ? below : 100;
-    const double rho = 1.0 / (floor_norm * ldexp(1.0, k));
-    const double sx = ldexp(static_cast<double>(kScaleX), below);
-    g.scal[item] = Scal{static_cast<float>(rho * rho * kScaleA),
-                        static_cast<float>(kScaleA / (sx * sx)), static_cast<float>(rho * sx),
-                        static_cast<float>(1.0 / sx)};
-  }
-  f16x8 h;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    h[2 * q] = static_cast<_Float16>(ldexpf(sbp::bf16_lo(w[q]), k));
-    h[2 * q + 1] = static_cast<_Float16>(ldexpf(sbp::bf16_hi(w[q]), k));
-  }
+  const Norm nm = norm_of(sqrt(block_sum_all(sq)), eps, grow);
+  if (t == 0 && threadIdx.x == 0)
+    g.scal[item] = Scal{static_cast<float>(nm.rho * nm.rho * kScaleA),
+                        static_cast<float>(kScaleA / (nm.sx * nm.sx)),
+                        static_cast<float>(nm.rho * nm.sx), static_cast<float>(1.0 / nm.sx)};
+  const f16x8 h = half8(w, nm.k);
   *reinterpret_cast<f16x8*>(g.S(0, item) + static_cast<int64_t>(row) * g.cp + col) = h;
 }
 
 // ---- the product ------------------------------------------------------------------
 
+// Tiles of the lower triangle of an m x m matrix.
+template <typename TL>
+__host__ __device__ __forceinline__ int lower_tiles(int m) {
+  const int side = (m + TL::T - 1) / TL::T;
+  return side * (side + 1) / 2;
+}
+
 enum Mode { kGram, kPoly, kApply, kLast };  // kLast: apply, to the caller's matrices
 
-// One T x T tile of C = P Q' per block of 4 waves (2 x 2, each T/2 square, in
+// One T x T tile of C = P Q' per block of 4 waves (2 x 2, each a quarter, in
 // 32 x 32 MFMA tiles).  Slices of BK k elements go straight from memory to one
 // of four LDS buffers, three slices ahead of the one being multiplied.
-template <int T, int BK>
+template <int T_, int BK_>
 struct Tile {
+  static constexpr int T = T_, BK = BK_;
+  static constexpr int NB = 4;
   static constexpr int kHalf = T * BK * 2;  // one operand's slice, bytes
-  static constexpr int kBuf = 2 * kHalf;
-  static constexpr int kSub = T / 64;                // 32 x 32 tiles per wave and side
-  static constexpr int kLoads = kHalf / (4 * 1024);  // per operand, slice and lane
+  static constexpr int kBuf = 2 * kHalf;    // P, then Q
+  static constexpr int kSub = T / 64;       // 32 x 32 tiles per wave and side
   static constexpr int kPhases = BK / 16;
+  static constexpr int kLoads = kHalf / 4096;  // per operand, slice and lane
+  static_assert(32 * T * 4 <= kBuf, "half the epilogue's slab fits one buffer");
 };
 
+// `bytes` from p on as a buffer; loads from beyond them give zeros, stores do
+// nothing.  An access is held to `bytes - scalar offset`, unsigned, so a scalar
+// offset past the end would lift the bound: whole offsets go into the vector
+// one, and the scalar one stays 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+template <typename V>
+__device__ __forceinline__ V load16(__amdgpu_buffer_rsrc_t from, int off) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(from, off, 0, 0));
+}
+template <typename V>
+__device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t to, V v, int off) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, off, 0, 0);
+}
+
 // This wave's share of one operand's slice, `bytes` from `from`.
-template <int T, int BK>
+template <int LOADS>
 __device__ __forceinline__ void stage(char* buf, const char* from, int bytes, int wave, int voff,
                                       int round_bytes) {
-  const __amdgpu_buffer_rsrc_t rows =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, bytes, 0x00027000);
+  const __amdgpu_buffer_rsrc_t rows = buffer(from, bytes);
 #pragma unroll
-  for (int r = 0; r < Tile<T, BK>::kLoads; ++r)
+  for (int r = 0; r < LOADS; ++r)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rows, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16, voff,
-        r * round_bytes, 0, 0);
+        rows, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16,
+        voff + r * round_bytes, 0, 0, 0);
 }
 
 // One operand of a tile.  Along: the matrix's rows r0 .. are the operand's
@@ -274,12 +326,12 @@ __device__ __forceinline__ void stage(char* buf, const char* from, int bytes, in
 // results that are not stored.
 template <int T, int BK, bool ACROSS>
 struct Operand {
-  using TL = Tile<T, BK>;
+  static constexpr int kSub = T / 64, kPhases = BK / 16;
   const char* from;  // next slice to load
   int64_t step;
   int bytes, voff, round_bytes;
   int at;                            // LDS offset of this lane's first fragment
-  int off[ACROSS ? TL::kSub : TL::kPhases];  // further offset by sub-tile or phase
+  int off[ACROSS ? kSub : kPhases];  // further offset by sub-tile or phase
 
   __device__ __forceinline__ void init(const _Float16* mat, int rows, int ld, int r0, int wave,
                                        int lane, int wrow) {
@@ -295,7 +347,7 @@ struct Operand {
       const int k = (lane >> 5) * 8 + ((lane >> 2) & 3);  // of this lane's address
       at = k * (T * 2) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-      for (int i = 0; i < TL::kSub; ++i) off[i] = ((wrow / 32 + i) ^ turn(k)) * 64;
+      for (int i = 0; i < kSub; ++i) off[i] = ((wrow / 32 + i) ^ turn(k)) * 64;
     } else {
       constexpr int kLanes = BK / 8;
       from = reinterpret_cast<const char*>(mat + static_cast<int64_t>(r0) * ld);
@@ -307,7 +359,7 @@ struct Operand {
       round_bytes = 4 * (64 / kLanes) * ld * 2;
       at = (wrow + (lane & 31)) * (BK * 2);
 #pragma unroll
-      for (int p = 0; p < TL::kPhases; ++p) off[p] = ((p * 2 + (lane >> 5)) ^ turn(lane)) * 16;
+      for (int p = 0; p < kPhases; ++p) off[p] = ((p * 2 + (lane >> 5)) ^ turn(lane)) * 16;
     }
   }
   // The rotation of a row; rows that differ by 32 (along) or 4 (across) agree.
@@ -317,7 +369,7 @@ struct Operand {
   }
   // Along, the last rows' slices end before `bytes` does by what is consumed.
   __device__ __forceinline__ void load(char* buf, int wave) {
-    stage<T, BK>(buf, from, bytes, wave, voff, round_bytes);
+    stage<T * BK * 2 / 4096>(buf, from, bytes, wave, voff, round_bytes);
     from += step;
     if constexpr (!ACROSS) bytes -= BK * 2;
   }
@@ -335,28 +387,28 @@ struct Operand {
   }
 };
 
-template <int T>
+template <typename TL>
 struct Frags {
-  f16x8 p[T / 64], q[T / 64];
+  f16x8 p[TL::kSub], q[TL::kSub];
 };
 
-template <int T>
-using Acc = f32x16[T / 64][T / 64];
+template <typename TL>
+using Acc = f32x16[TL::kSub][TL::kSub];
 
-template <int T>
-__device__ __forceinline__ void multiply(const Frags<T>& f, Acc<T>& acc) {
+template <typename TL>
+__device__ __forceinline__ void multiply(const Frags<TL>& f, Acc<TL>& acc) {
 #pragma unroll
-  for (int i = 0; i < T / 64; ++i)
+  for (int i = 0; i < TL::kSub; ++i)
 #pragma unroll
-    for (int j = 0; j < T / 64; ++j)
+    for (int j = 0; j < TL::kSub; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
 }
 
 // Order of a phase's instructions: MFMAs, LDS reads and loads to LDS in turn,
 // so that both kinds of memory work run under the MFMAs.
-template <int T, int READS, int LOADS>
+template <typename TL, int READS, int LOADS>
 __device__ __forceinline__ void interleave() {
-  constexpr int mfmas = (T / 64) * (T / 64);
+  constexpr int mfmas = TL::kSub * TL::kSub;
   constexpr int r1 = (READS + mfmas - 1) / mfmas, l1 = (LOADS + mfmas - 1) / mfmas;
 #pragma unroll
   for (int i = 0; i < mfmas; ++i) {
@@ -371,7 +423,9 @@ __device__ __forceinline__ void interleave() {
 // then everyone's.
 template <int LEFT>
 __device__ __forceinline__ void slice_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | 0x70);
+  asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -380,29 +434,29 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// acc = P Q' over `slices` slices.
-template <int T, int BK, bool PX, bool QX>
-__device__ __forceinline__ void product(char* buf0, char* buf1, char* buf2, char* buf3,
-                                        Operand<T, BK, PX>& P, Operand<T, BK, QX>& Q, int slices,
-                                        int wave, Acc<T>& acc) {
-  using TL = Tile<T, BK>;
-  constexpr int L = TL::kLoads, H = TL::kHalf, N = TL::kPhases;
+// acc = P Q' over `slices` slices.  early() issues EARLY loads of the
+// epilogue's, once all slices are loaded or under way.
+template <typename TL, int EARLY, bool PX, bool QX, typename F>
+__device__ __forceinline__ void product(char* const (&buf)[TL::NB],
+                                        Operand<TL::T, TL::BK, PX>& P,
+                                        Operand<TL::T, TL::BK, QX>& Q, int slices, int wave,
+                                        Acc<TL>& acc, F&& early) {
+  constexpr int NB = TL::NB, N = TL::kPhases, L = TL::kLoads;
   constexpr int kReads = TL::kSub * ((PX ? 2 : 1) + (QX ? 2 : 1));
-  Frags<T> f[2];
+  Frags<TL> f[2];
   auto load = [&](char* to) {
     P.load(to, wave);
-    Q.load(to + H, wave);
+    Q.load(to + TL::kHalf, wave);
   };
-  auto read = [&](const char* buf, int phase, Frags<T>& to) {
+  auto read = [&](const char* from, int phase, Frags<TL>& to) {
 #pragma unroll
-    for (int i = 0; i < TL::kSub; ++i) {
-      to.p[i] = P.read(buf, phase, i);
-      to.q[i] = Q.read(buf + H, phase, i);
-    }
+    for (int i = 0; i < TL::kSub; ++i) to.p[i] = P.read(from, phase, i);
+#pragma unroll
+    for (int j = 0; j < TL::kSub; ++j) to.q[j] = Q.read(from + TL::kHalf, phase, j);
   };
   // One slice: it is in `cur`, its first fragments in f[0].  The barrier sits
   // before the last multiply, so that each multiply hides the next one's reads.
-  // LOAD: the slice three further on is loaded into `to`; LEFT: loads that may
+  // LOAD: the slice NB - 1 further on is loaded into `to`; LEFT: loads that may
   // still be under way when the next slice has to be there (-1: no next one).
   auto slice = [&](const char* cur, const char* nxt, char* to, auto load_c, auto left_c) {
     constexpr bool kLoad = decltype(load_c)::value;
@@ -412,124 +466,120 @@ __device__ __forceinline__ void product(char* buf0, char* buf1, char* buf2, char
     for (int ph = 0; ph < N - 1; ++ph) {
       if (kLoad && ph == 0) P.load(to, wave);
       read(cur, ph + 1, f[(ph + 1) & 1]);
-      multiply<T>(f[ph & 1], acc);
-      if (kLoad && ph == 0) interleave<T, kReads, L>();
-      else interleave<T, kReads, 0>();
+      multiply<TL>(f[ph & 1], acc);
+      if (kLoad && ph == 0) interleave<TL, kReads, TL::kLoads>();
+      else interleave<TL, kReads, 0>();
     }
     if constexpr (kLeft >= 0) {
       slice_barrier<kLeft>();
-      if constexpr (kLoad) Q.load(to + H, wave);
+      if constexpr (kLoad) Q.load(to + TL::kHalf, wave);
       read(nxt, 0, f[0]);
     }
-    multiply<T>(f[1], acc);
-    interleave<T, kLeft >= 0 ? kReads : 0, kLoad ? L : 0>();
+    multiply<TL>(f[1], acc);
+    interleave<TL, kLeft >= 0 ? kReads : 0, kLoad ? TL::kLoads : 0>();
   };
   constexpr std::true_type kYes{};
   constexpr std::false_type kNo{};
   // two slices under way, and the first half of a third
   constexpr std::integral_constant<int, 3 * L> kSteady{};
-  constexpr std::integral_constant<int, 2 * L> kOne{};
-  constexpr std::integral_constant<int, 0> kNone{};
+  constexpr std::integral_constant<int, 2 * L + EARLY> kOne{};
+  constexpr std::integral_constant<int, EARLY> kNone{};
+  constexpr std::integral_constant<int, 0> kDrain{};
+  static_assert(4 * L < 64 && 2 * L + EARLY < 64, "what vmcnt can count");
   constexpr std::integral_constant<int, -1> kEnd{};
-  // The last slice is in buf3, so that there is one way into the loop's rounds
-  // of four and one way out; a number that is no multiple of four starts
-  // further on, and drains its loads once (known to the compiler, whose own
-  // waits in the loop would else provide for the other way in).  With BK = 32
-  // the number is even.
-  constexpr bool kOdd = BK != 32;
-  const int rest = slices & 3;
-  if (slices < 4) {
-    if (kOdd && rest == 3) load(buf1);
-    if (!kOdd || rest >= 2) load(buf2);
-    load(buf3);
-    slice_barrier<0>();
-    read(kOdd && rest == 3 ? buf1 : !kOdd || rest == 2 ? buf2 : buf3, 0, f[0]);
-    if (kOdd && rest == 3) slice(buf1, buf2, nullptr, kNo, kNone);
-    if (!kOdd || rest >= 2) slice(buf2, buf3, nullptr, kNo, kNone);
+  // The last slice is in the last buffer, so that there is one way into the
+  // loop's rounds of NB slices and one way out; a number that is no multiple of
+  // NB starts further on, and drains its loads once (known to the compiler,
+  // whose own waits in the loop would else provide for the other way in).
+  constexpr bool kEven = TL::BK == 32;  // both padded sides are multiples of 64
+  const int rest = static_cast<unsigned>(slices) % NB;
+  if (slices < NB) {
+#pragma unroll
+    for (int r = kEven ? 2 : 1; r < NB; ++r) {  // r slices
+      if (slices != r) continue;
+#pragma unroll
+      for (int i = NB - r; i < NB; ++i) load(buf[i]);
+      slice_barrier<0>();
+      read(buf[NB - r], 0, f[0]);
+#pragma unroll
+      for (int i = NB - r; i < NB - 1; ++i) slice(buf[i], buf[i + 1], nullptr, kNo, kDrain);
+    }
+    early();
   } else {
     if (rest == 0) {
-      load(buf0);
-      load(buf1);
-      load(buf2);
+#pragma unroll
+      for (int i = 0; i < NB - 1; ++i) load(buf[i]);
       slice_barrier<4 * L>();
-      read(buf0, 0, f[0]);
+      read(buf[0], 0, f[0]);
     } else {
-      if (kOdd && rest == 3) {
-        load(buf1);
-        load(buf2);
-        load(buf3);
+#pragma unroll
+      for (int r = kEven ? 2 : 1; r < NB; ++r) {  // r slices before the rounds
+        if (kEven ? r != 2 : rest != r) continue;
+#pragma unroll
+        for (int i = 0; i < NB - 1; ++i) load(buf[(NB - r + i) % NB]);
         slice_barrier<4 * L>();
-        read(buf1, 0, f[0]);
-        slice(buf1, buf2, buf0, kYes, kSteady);
+        read(buf[NB - r], 0, f[0]);
+#pragma unroll
+        for (int i = NB - r; i < NB; ++i)
+          slice(buf[i], buf[(i + 1) % NB], buf[(i + NB - 1) % NB], kYes, kSteady);
       }
-      if (rest >= 2) {
-        if (!kOdd || rest == 2) {
-          load(buf2);
-          load(buf3);
-          load(buf0);
-          slice_barrier<4 * L>();
-          read(buf2, 0, f[0]);
-        }
-        slice(buf2, buf3, buf1, kYes, kSteady);
-      }
-      if (kOdd && rest == 1) {
-        load(buf3);
-        load(buf0);
-        load(buf1);
-        slice_barrier<4 * L>();
-        read(buf3, 0, f[0]);
-      }
-      slice(buf3, buf0, buf2, kYes, kSteady);
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     }
-    for (int s = slices >> 2; s > 1; --s) {
-      slice(buf0, buf1, buf3, kYes, kSteady);
-      slice(buf1, buf2, buf0, kYes, kSteady);
-      slice(buf2, buf3, buf1, kYes, kSteady);
-      slice(buf3, buf0, buf2, kYes, kSteady);
+    for (int s = slices / NB; s > 1; --s) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        slice(buf[i], buf[(i + 1) % NB], buf[(i + NB - 1) % NB], kYes, kSteady);
     }
-    slice(buf0, buf1, buf3, kYes, kSteady);
-    slice(buf1, buf2, nullptr, kNo, kOne);
-    slice(buf2, buf3, nullptr, kNo, kNone);
+    slice(buf[0], buf[1], buf[NB - 1], kYes, kSteady);
+    early();
+    slice(buf[1], buf[2], nullptr, kNo, kOne);
+    slice(buf[2], buf[3], nullptr, kNo, kNone);
   }
-  slice(buf3, nullptr, nullptr, kNo, kEnd);
+  slice(buf[3], nullptr, nullptr, kNo, kEnd);
 }
 
 // Up to 8 consecutive bf16 values of a row of the caller's output.
-__device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
-  uint32_t b[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) b[q] = sbp::bf16_rne(v[q]);
+__device__ __forceinline__ void store_bits8(uint16_t* p, int left, bool vec, u32x4 w) {
   if (vec && left >= 8) {
-    *reinterpret_cast<u32x4*>(p) = u32x4{b[0] | (b[1] << 16), b[2] | (b[3] << 16),
-                                         b[4] | (b[5] << 16), b[6] | (b[7] << 16)};
+    *reinterpret_cast<u32x4*>(p) = w;
   } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < left) p[q] = static_cast<uint16_t>(b[q]);
+    auto one = [&](int j, uint32_t x) {
+      if (j < left) p[j] = static_cast<uint16_t>(x);
+    };
+    one(0, w.x), one(1, w.x >> 16), one(2, w.y), one(3, w.y >> 16);
+    one(4, w.z), one(5, w.z >> 16), one(6, w.w), one(7, w.w >> 16);
   }
 }
-
-// Where (row, col) of the epilogue's binary32 slab is kept: 32 rows in each of
-// two buffers; groups of 8 columns are rotated by the row's 8-row group, so
-// that both a row's 8 columns and a column's 8 rows are read without bank
-// conflicts.
-template <int T>
-__device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) {
-  float* half = reinterpret_cast<float*>(row & 32 ? hi : lo);
-  return half + (row & 31) * T + (col ^ (((row >> 3) & 7) << 3));
+__device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
+  store_bits8(p, left, vec, w);
 }
 
-template <int T, int BK, Mode M>
-__global__ void __launch_bounds__(kBlock, T == 256 ? 1 : 2)
+// Where (row, col) of the epilogue's binary32 slab is kept: 32 rows in
+// each of two buffers; groups of 8 columns are rotated by the row's 8-row
+// group, so that both a row's 8 columns and a column's 8 rows are read without
+// bank conflicts, and halves of 64 by its 4-row group, whose rows one
+// instruction writes two of.
+template <typename TL>
+__device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) {
+  float* half = reinterpret_cast<float*>(row & 32 ? hi : lo);
+  const int turned = col ^ (((row >> 3) & 7) << 3) ^ (((row >> 2) & 1) << 5);
+  return half + (row & 31) * TL::T + turned;
+}
+
+template <typename TL, Mode M>
+__global__ void __launch_bounds__(kBlock, TL::T == 256 ? 1 : 2)
 ns_product_kernel(Groups gs, Step st, unsigned total) {
-  using TL = Tile<T, BK>;
+  constexpr int T = TL::T, BK = TL::BK;
   // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[TL::kBuf];
   __shared__ __align__(16) char buf1[TL::kBuf];
   __shared__ __align__(16) char buf2[TL::kBuf];
   __shared__ __align__(16) char buf3[TL::kBuf];
-  constexpr int W = T / 2;  // a wave's side
+  char* const buf[TL::NB] = {buf0, buf1, buf2, buf3};
   constexpr bool kApplies = M == kApply || M == kLast;
 
   // neighbouring tiles to one XCD: its L2 then holds the rows they share
@@ -556,7 +606,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     ti = strip * kStrip + s % high;
     tj = s / high;
   } else {
-    const int tm = (m + T - 1) / T, per = tm * (tm + 1) / 2;
+    const int per = lower_tiles<TL>(m);
     const int local = b - g.t_gram;
     item = local / per;
     const int t = local % per;
@@ -565,26 +615,92 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
     tj = t - ti * (ti + 1) / 2;
   }
-  const int r0 = ti * T, c0 = tj * T;
+  const int r0 = ti * T, c0 = tj * T;  // inside C: both tile counts are rounded up
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = wave >> 1, wc = wave & 1;
 
-  Acc<T> acc = {};
-  auto along = [&](const _Float16* Pm, const _Float16* Qm, int k) {
-    Operand<T, BK, false> P, Q;
-    P.init(Pm, crows, k, r0, wave, lane, wr * W);
-    Q.init(Qm, ccols, k, c0, wave, lane, wc * W);
-    product<T, BK>(buf0, buf1, buf2, buf3, P, Q, k / BK, wave, acc);
-  };
+  // The epilogue goes by a slab of rows at a time: accumulators to LDS as
+  // binary32, then row by row (8 columns a thread) the additions and the store;
+  // gram and poly store the mirrored tile as well.  Its barriers wait for LDS
+  // alone, what the additions read is asked for a slab ahead, and for the first
+  // slab under the last products: a block has one wave per SIMD at the large
+  // tile, so nothing else would hide that latency.
+  constexpr int kSlab = 64;
+  constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow, kPasses = kSlab / kRowsAtOnce;
+  const int prow = threadIdx.x / kPerRow, pcol = (threadIdx.x % kPerRow) * 8;
+  const int gc = c0 + pcol;
+  const bool cross = !kApplies && ti != tj;
   const _Float16* S = g.S(st.in, item);
+  // C's rows r0 .. as buffers: rows and columns past the matrix are not
+  // touched (columns by an offset of the buffers' end)
+  const int have = crows - r0 < T ? crows - r0 : T;  // 1 .. T
+  const int64_t tile_at = static_cast<int64_t>(r0) * ccols;
+  const int tile_bytes = have * ccols * 2;
+  const int row_off = gc < ccols ? (prow * ccols + gc) * 2 : tile_bytes;
+  const auto add = buffer(M == kPoly ? g.A(0, item) + tile_at : S + tile_at, tile_bytes);
+  const auto rem = buffer(g.L(item) + tile_at, kApplies && st.lo_in ? tile_bytes : 0);
+  const auto rem_out = buffer(g.L(item) + tile_at, M == kApply && st.lo_out ? tile_bytes : 0);
+  const auto out = buffer((M == kGram   ? g.A(0, item)
+                           : M == kPoly ? g.A(1, item)
+                                        : g.S(st.in ^ 1, item)) + tile_at, tile_bytes);
+  // the remainders of the product's diagonal: by row, by column, or (poly) both
+  const float* diag = M == kPoly ? g.D(0, item) : g.D(1, item);
+  const bool by_row = M == kPoly || !tall, by_col = M == kPoly || tall;
+  const auto diag_row = buffer(diag + r0, by_row ? have * 4 : 0);
+  const auto diag_col = buffer(diag, by_col ? m * 4 : 0);
+  f16x8 ad[kPasses], re[kPasses];
+  float dr[kPasses], dc[8];
+  auto ask = [&](int sl, int p) {
+    const int row = sl * kSlab + p * kRowsAtOnce;
+    if constexpr (M != kGram) {
+      ad[p] = load16<f16x8>(add, row_off + row * ccols * 2);
+      dr[p] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(diag_row, (prow + row) * 4, 0, 0));
+    }
+  };
+  auto ask_rem = [&](int sl, int p) {
+    if constexpr (kApplies)
+      re[p] = load16<f16x8>(rem, row_off + (sl * kSlab + p * kRowsAtOnce) * ccols * 2);
+  };
+  // (the large tile has no registers left for it)
+  constexpr bool kAhead = M != kGram && T < 256;
+  constexpr int kEarly = kAhead ? 2 + kPasses * 2 : 0;
+  auto ask_first = [&] {
+    if constexpr (M != kGram) {
+      const int at = gc < ccols ? gc * 4 : m * 4;
+      const f32x4 lo = load16<f32x4>(diag_col, at), hi = load16<f32x4>(diag_col, at + 16);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        dc[q] = lo[q];
+        dc[4 + q] = hi[q];
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) ask(0, p);
+  };
+  auto early = [&] {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kAhead) ask_first();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  Acc<TL> acc = {};
+  auto along = [&](const _Float16* Pm, const _Float16* Qm, int k) {
+    Operand<T, BK, false> P;
+    Operand<T, BK, false> Q;
+    P.init(Pm, crows, k, r0, wave, lane, wr * (T / 2));
+    Q.init(Qm, ccols, k, c0, wave, lane, wc * (T / 2));
+    product<TL, kEarly>(buf, P, Q, k / BK, wave, acc, early);
+  };
   if constexpr (M == kPoly) {
     along(g.A(0, item), g.A(0, item), m);
   } else if constexpr (M == kGram) {
     if (tall) {
-      Operand<T, BK, true> P, Q;
-      P.init(S, m, m, r0, wave, lane, wr * W);
-      Q.init(S, m, m, c0, wave, lane, wc * W);
-      product<T, BK>(buf0, buf1, buf2, buf3, P, Q, g.n / BK, wave, acc);
+      Operand<T, BK, true> P;
+      Operand<T, BK, true> Q;
+      P.init(S, m, m, r0, wave, lane, wr * (T / 2));
+      Q.init(S, m, m, c0, wave, lane, wc * (T / 2));
+      product<TL, kEarly>(buf, P, Q, g.n / BK, wave, acc, early);
     } else {
       along(S, S, g.n);
     }
@@ -594,64 +710,42 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     } else {
       Operand<T, BK, false> P;
       Operand<T, BK, true> Q;
-      P.init(g.A(1, item), m, m, r0, wave, lane, wr * W);
-      Q.init(S, ccols, ccols, c0, wave, lane, wc * W);
-      product<T, BK>(buf0, buf1, buf2, buf3, P, Q, m / BK, wave, acc);
+      P.init(g.A(1, item), m, m, r0, wave, lane, wr * (T / 2));
+      Q.init(S, ccols, ccols, c0, wave, lane, wc * (T / 2));
+      product<TL, kEarly>(buf, P, Q, m / BK, wave, acc, early);
     }
   }
 
-  // Epilogue, 64 rows at a time: accumulators to LDS as binary32, then row by
-  // row (8 columns a thread) the additions and the store; gram and poly store
-  // the mirrored tile as well.  What the additions read is asked for ahead of
-  // the barriers, which wait for LDS alone: nothing else would hide that
-  // latency where a block has one wave per SIMD.
-  static_assert(32 * T * 4 <= TL::kBuf, "half the slab fits one buffer");
   const Scal sc = g.scal[item];
-  const bool cross = !kApplies && ti != tj;
-  constexpr int kPerRow = T / 8, kRowsAtOnce = kBlock / kPerRow, kPasses = 64 / kRowsAtOnce;
-  const int prow = threadIdx.x / kPerRow, pcol = (threadIdx.x % kPerRow) * 8;
-  const int gc = c0 + pcol;
-  const bool col_in = gc < ccols;
-  // the matrix added and the remainders of the product's diagonal
-  const _Float16* add = M == kPoly ? g.A(0, item) : S;
-  const _Float16* rem = kApplies && st.lo_in ? g.L(item) : nullptr;
-  const float* diag = M == kPoly ? g.D(0, item) : g.D(1, item);
   const float alpha = st.first ? sc.gram_first : sc.gram;
   const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
+  // apply: a x + acc / 2^10, scaled; the factors carry the scale
   const float fx = (st.first ? sc.apply_first : 1.0f) * (M == kLast ? g.out_scale * sc.inv_sx : 1.0f);
-  float dc[8] = {};
-  if (M != kGram && col_in && (M == kPoly || tall)) load8(diag + gc, dc);
+  const float fd = fx * (1.0f / kScaleB), fa = fx * st.a;
+  if constexpr (!kAhead) ask_first();
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) ask_rem(0, p);
   lds_barrier();  // the last slice is read
+  if constexpr (kApplies) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dc[q] = fmaf(dc[q], fd, fa);
+  }
 #pragma unroll 1
-  for (int sl = 0; sl < T / 64; ++sl) {
-    f16x8 ad[kPasses], re[kPasses];
-    float dr[kPasses];
+  for (int sl = 0; sl < T / kSlab; ++sl) {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int gr = r0 + sl * 64 + p * kRowsAtOnce + prow;
-      const int64_t idx = static_cast<int64_t>(gr) * ccols + gc;
-      ad[p] = re[p] = f16x8{};
-      dr[p] = 0.0f;
-      if (gr < crows && col_in) {
-        if constexpr (M != kGram) ad[p] = *reinterpret_cast<const f16x8*>(add + idx);
-        if (M == kPoly || (kApplies && !tall)) dr[p] = diag[gr];
-        if (kApplies && rem != nullptr) re[p] = *reinterpret_cast<const f16x8*>(rem + idx);
-      }
-    }
-#pragma unroll
-    for (int part = 0; part < T / 64; ++part) {
+    for (int part = 0; part < T / kSlab; ++part) {
       if (part != sl) continue;
 #pragma unroll
       for (int i = 0; i < TL::kSub; ++i) {
         const int rb = wr * TL::kSub + i;  // 32-row block of the tile
-        if (rb / 2 == part) {
+        if (rb / (kSlab / 32) == part) {
 #pragma unroll
           for (int j = 0; j < TL::kSub; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int row = (rb & 1) * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-              const int col = wc * W + j * 32 + (lane & 31);
-              *slab_at<T>(buf0, buf1, row, col) = acc[i][j][e];
+              const int row = rb * 32 % kSlab + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+              const int col = wc * (T / 2) + j * 32 + (lane & 31);
+              *slab_at<TL>(buf0, buf1, row, col) = acc[i][j][e];
             }
         }
       }
@@ -660,54 +754,60 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
       const int row = p * kRowsAtOnce + prow;
-      const int gr = r0 + sl * 64 + row;
-      if (gr >= crows || !col_in) continue;
-      float* at = slab_at<T>(buf0, buf1, row, pcol);
-      const int64_t idx = static_cast<int64_t>(gr) * ccols + gc;
+      const int gr = r0 + sl * kSlab + row;
+      const int off = (sl * kSlab + p * kRowsAtOnce) * ccols * 2;
+      float* at = slab_at<TL>(buf0, buf1, row, pcol);
       float v[8];
       load8(at, v);
       f16x8 h;
       if constexpr (M == kGram) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          v[q] = v[q] * alpha;
-          h[q] = static_cast<_Float16>(v[q]);
-          if (gr == gc + q) g.D(0, item)[gr] = v[q] - static_cast<float>(h[q]);
-        }
-        *reinterpret_cast<f16x8*>(g.A(0, item) + idx) = h;
+        for (int q = 0; q < 8; ++q) v[q] = v[q] * alpha;
       } else if constexpr (M == kPoly) {
+        // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
           const float x = static_cast<float>(ad[p][q]);
-          v[q] = fb * x + fc * (v[q] + (dr[p] + dc[q]) * x);
-          if (gr == gc + q) v[q] = v[q] + (fb * dr[p] + fc * (dr[p] * dr[p]));
-          h[q] = static_cast<_Float16>(v[q]);
-          if (gr == gc + q) g.D(1, item)[gr] = v[q] - static_cast<float>(h[q]);
+          v[q] = fmaf(fc, fmaf(dr[p] + dc[q], x, v[q]), fb * x);
         }
-        *reinterpret_cast<f16x8*>(g.A(1, item) + idx) = h;
+        if (!cross) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (gr == gc + q) v[q] = v[q] + (fb * dr[p] + fc * (dr[p] * dr[p]));
+        }
+      } else {
+        // the diagonal's remainder multiplies S's row (wide) or column (tall)
+        const float d = dr[p] * fd;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float x = static_cast<float>(ad[p][q]);
+          if (st.lo_in) x = fmaf(static_cast<float>(re[p][q]), 1.0f / kScaleLo, x);
+          v[q] = fmaf(dc[q] + d, x, v[q] * fd);
+        }
+      }
+      if (sl + 1 < T / kSlab) {
+        ask(sl + 1, p);
+        ask_rem(sl + 1, p);
+      }
+      if constexpr (M == kLast) {
+        if (gr < g.rows && gc < g.cols)
+          store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v);
       } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          // the diagonal's remainder multiplies S's row (wide) or column (tall)
-          const float a = st.a + (dr[p] + dc[q]) * (1.0f / kScaleB);
-          const float x =
-              static_cast<float>(ad[p][q]) + static_cast<float>(re[p][q]) * (1.0f / kScaleLo);
-          v[q] = (a * x + v[q] * (1.0f / kScaleB)) * fx;
+        for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
+        store16(out, h, row_off + off);
+        if (M == kApply && st.lo_out) {
+          f16x8 l;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            l[q] = static_cast<_Float16>((v[q] - static_cast<float>(h[q])) * kScaleLo);
+          store16(rem_out, l, row_off + off);
         }
-        if constexpr (M == kApply) {
+        if (!kApplies && !cross && gr < m) {
+          float* d = g.D(M == kGram ? 0 : 1, item);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
-          *reinterpret_cast<f16x8*>(g.S(st.in ^ 1, item) + idx) = h;
-          if (st.lo_out) {
-            f16x8 l;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              l[q] = static_cast<_Float16>((v[q] - static_cast<float>(h[q])) * kScaleLo);
-            *reinterpret_cast<f16x8*>(g.L(item) + idx) = l;
-          }
-        } else if (gr < g.rows) {
-          store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v);
+          for (int q = 0; q < 8; ++q)
+            if (gr == gc + q) d[gr] = v[q] - static_cast<float>(h[q]);
         }
       }
       if (cross) {
@@ -717,22 +817,439 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     }
     lds_barrier();
     if (cross) {
-      // 8 threads take the 64 rows of one column, 8 rows each
+      // kSlab / 8 threads take the rows of one column, 8 rows each
+      constexpr int kPerCol = kSlab / 8, kColsAtOnce = kBlock / kPerCol;
 #pragma unroll
-      for (int p = 0; p < T / 32; ++p) {
-        const int col = p * 32 + (threadIdx.x >> 3), row = (threadIdx.x & 7) * 8;
-        const int gr = r0 + sl * 64 + row, xr = c0 + col;
+      for (int p = 0; p < T / kColsAtOnce; ++p) {
+        const int col = p * kColsAtOnce + threadIdx.x / kPerCol;
+        const int row = threadIdx.x % kPerCol * 8;
+        const int gr = r0 + sl * kSlab + row, xr = c0 + col;
         if (gr >= m || xr >= m) continue;
         f16x8 h;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          h[q] = static_cast<_Float16>(*slab_at<T>(buf0, buf1, row + q, col));
+          h[q] = static_cast<_Float16>(*slab_at<TL>(buf0, buf1, row + q, col));
         *reinterpret_cast<f16x8*>(g.A(M == kGram ? 0 : 1, item) + static_cast<int64_t>(xr) * m +
                                   gr) = h;
       }
       lds_barrier();
     }
   }
+}
+
+// ---- matrices with a short side of at most 128 ----------------------------------
+// Here A and B fit a block's LDS, and a launch per product would be all latency.
+// One kernel per step instead: every block of a matrix sums the partial Gram
+// matrices of the step before, forms B from them for itself, multiplies its own
+// columns of X (of 64 at a time) by it, and adds their products into its partial
+// of the next Gram matrix while they are in LDS.  A matrix that one block
+// handles alone goes through all its steps in one launch, with the Gram matrix
+// staying in registers.  The first Gram matrix comes from the input as it is,
+// by a power of two that each block keeps for itself, and its trace is the
+// squared norm, so there is no prologue.
+//   MP    the padded short side, 64 or 128
+//   LDS   B (A before it); 64 columns of X and their remainder
+// 16-byte pieces of LDS rows are rotated by row against bank conflicts.
+
+template <int MP>
+struct Flat {
+  static constexpr int kSub = MP / 64;          // 32 x 32 tiles per wave and side of MP
+  static constexpr int kPasses = MP / 32;       // 16-byte pieces of 64 columns per thread
+  static constexpr int kB = MP * MP * 2, kX = MP * 64 * 2;
+};
+
+// Byte of piece `piece` (8 elements) of a row of COLS elements.
+template <int COLS>
+__device__ __forceinline__ int flat_at(int row, int piece) {
+  constexpr int kMask = (COLS / 8 < 16 ? COLS / 8 : 16) - 1;
+  return row * (COLS * 2) + (piece ^ (row & kMask)) * 16;
+}
+
+// MFMA operand fragments of phase ph (16 k): 32 rows from `row`, k along them;
+// or 32 columns from `col`, k running over the rows.
+template <int COLS>
+__device__ __forceinline__ f16x8 flat_along(const char* mat, int row, int ph, int lane) {
+  return *reinterpret_cast<const f16x8*>(mat +
+                                         flat_at<COLS>(row + (lane & 31), ph * 2 + (lane >> 5)));
+}
+template <int COLS>
+__device__ __forceinline__ f16x8 flat_across(const char* mat, int col, int ph, int lane) {
+  typedef __fp16 h4 __attribute__((__vector_size__(8)));
+  typedef __attribute__((address_space(3))) h4* lds_h4;
+  const int k = ph * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
+  const int piece = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+  const char* p = mat + (lane & 1) * 8;
+  const h4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + flat_at<COLS>(k, piece)));
+  const h4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + flat_at<COLS>(k + 4, piece)));
+  return __builtin_bit_cast(f16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+struct FlatStep {
+  float a, b, c;
+  int32_t last, lo_in, lo_out;
+};
+struct FlatSteps {
+  FlatStep s[SBP_NS_MAX_STEPS];
+  float eps;
+  int32_t grow;
+};
+
+// Stages first .. end-1: stage 0 is the input's Gram matrix, stage s step s.
+// TALL: X lies across (rows of 64 columns' groups hold MP elements).
+template <int MP, bool TALL>
+__device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs, int item,
+                                            int split, int first, int end, char* LB, char* LX,
+                                            char* LL, float* dA, float* dB, float* red) {
+  using F = Flat<MP>;
+  constexpr int kSub = F::kSub, H = MP / 2;
+  constexpr int XC = TALL ? MP : 64;  // elements of a row of LX and LL
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int lane = threadIdx.x & 63;
+  const int wr = wave >> 1, wc = wave & 1;
+  const int chunks = g.n / 64;
+  // this block's 64-column chunks
+  const int c_lo = static_cast<int>(static_cast<int64_t>(chunks) * split / g.splits);
+  const int c_hi = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / g.splits);
+  f32x16 G[kSub][kSub];
+  int kx = 0;          // stage 0: G is of the input * 2^kx
+  float inv_sx = 0.0f, gram = 0.0f, apply_first = 0.0f;
+  int k_in = 0;
+  if (first > 1) {
+    const Scal sc = g.scal[item];
+    inv_sx = sc.inv_sx;
+    gram = sc.gram;
+  }
+#pragma unroll 1
+  for (int stage = first; stage < end; ++stage) {
+    FlatStep st{};
+    // offsets are worked out again each stage: kept, they would not fit the registers
+    asm volatile("" : "+v"(lane));
+    if (stage > 0) {
+      st = fs.s[stage - 1];
+      // -- the Gram matrix of the stage before
+      if (g.splits > 1) {
+        const float* part = g.part(stage & 1, item, 0);
+        const int32_t* pk = g.part_k(item, 0);
+        kx = INT32_MAX;
+        if (stage == 1)
+          for (int s = 0; s < g.splits; ++s) kx = pk[s] < kx ? pk[s] : kx;
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) G[i][j] = f32x16{};
+#pragma unroll 1
+        for (int s = 0; s < g.splits; ++s) {
+          const float by = stage == 1 ? ldexpf(1.0f, 2 * (kx - pk[s] < -70 ? -70 : kx - pk[s])) : 1.0f;
+          const float* p = part + static_cast<int64_t>(s) * (MP * MP) + wave * (H * H) + lane * 4;
+#pragma unroll
+          for (int i = 0; i < kSub; ++i)
+#pragma unroll
+            for (int j = 0; j < kSub; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(p + ((i * kSub + j) * 4 + q) * 256);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) G[i][j][q * 4 + e] = fmaf(v[e], by, G[i][j][q * 4 + e]);
+              }
+        }
+      }
+      if (stage == 1) {
+        double tr = 0.0;
+        if (wr == wc) {
+#pragma unroll
+          for (int i = 0; i < kSub; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) == (lane & 31)) tr = tr + G[i][i][e];
+        }
+        const double norm = sqrt(block_sum_all(tr)) * ldexp(1.0, -kx);
+        const Norm nm = norm_of(norm, fs.eps, fs.grow);
+        k_in = nm.k;
+        inv_sx = static_cast<float>(1.0 / nm.sx);
+        apply_first = static_cast<float>(nm.rho * nm.sx);
+        gram = static_cast<float>(kScaleA * ldexp(1.0, -2 * kx) / (nm.floor_norm * nm.floor_norm));
+        if (split == 0 && threadIdx.x == 0)
+          g.scal[item] = Scal{0.0f, static_cast<float>(kScaleA / (nm.sx * nm.sx)), 0.0f, inv_sx};
+      }
+      // -- A in LDS (symmetric: a lane's 4 rows of a column go into the column's row)
+      auto put = [&](const f32x16 (&v)[kSub][kSub], float* d) {
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) {
+            const int col = wc * H + j * 32 + (lane & 31);
+            float rest = 0.0f;  // of this lane's diagonal element, if it has one
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row = wr * H + i * 32 + q * 8 + 4 * (lane >> 5);
+              f16x4 h;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                h[e] = static_cast<_Float16>(v[i][j][q * 4 + e]);
+                if (i == j)
+                  rest = row + e == col ? v[i][j][q * 4 + e] - static_cast<float>(h[e]) : rest;
+              }
+              *reinterpret_cast<f16x4*>(LB + flat_at<MP>(col, row >> 3) + (lane >> 5) * 8) = h;
+            }
+            if (i == j && wr == wc && ((lane >> 2) & 1) == lane >> 5) d[col] = rest;
+          }
+      };
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) G[i][j] = G[i][j] * gram;
+      put(G, dA);
+      __syncthreads();
+      f32x16 sq[kSub][kSub] = {};
+#pragma unroll 2
+      for (int ph = 0; ph < MP / 16; ++ph) {
+        f16x8 p[kSub], q[kSub];
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) {
+          p[i] = flat_along<MP>(LB, wr * H + i * 32, ph, lane);
+          q[i] = flat_along<MP>(LB, wc * H + i * 32, ph, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) sq[i][j] = mfma(p[i], q[j], sq[i][j]);
+      }
+      const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
+          const int col = wc * H + j * 32 + (lane & 31);
+          const float dc = dA[col];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int row = wr * H + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
+            const float a = G[i][j][e], x = static_cast<float>(static_cast<_Float16>(a));
+            float s = fmaf(dA[row] + dc, x, sq[i][j][e]);
+            if (row == col) s = fmaf(dc, dc, s);
+            sq[i][j][e] = fmaf(fc, s, fb * a);
+          }
+        }
+      __syncthreads();  // A is read
+      put(sq, dB);
+      __syncthreads();
+    }
+    const bool make_gram = stage == 0 || !st.last;
+#pragma unroll
+    for (int i = 0; i < kSub; ++i)
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) G[i][j] = f32x16{};
+    if (stage == 0) kx = 200;
+    const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_scale * inv_sx : 1.0f);
+    const float fd = fx * (1.0f / kScaleB), fa = fx * st.a;
+
+    // -- this block's columns
+    u32x4 next[F::kPasses], next_lo[F::kPasses];
+    auto fetch_one = [&](int c, int p) {
+      const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), col = at % (XC / 8) * 8;
+      const int gr = TALL ? c * 64 + row : row, gc = TALL ? col : c * 64 + col;
+      if (stage > 1)
+        return *reinterpret_cast<const u32x4*>(g.S(0, item) + static_cast<int64_t>(gr) * g.cp + gc);
+      if (gr < g.rows && gc < g.cols)
+        return load_row8(g.in + item * g.in_stride + gr * g.in_ld + gc, g.cols - gc, g.in_vec);
+      return u32x4{0, 0, 0, 0};
+    };
+    auto fetch_lo = [&](int c, int p) {
+      const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), col = at % (XC / 8) * 8;
+      const int gr = TALL ? c * 64 + row : row, gc = TALL ? col : c * 64 + col;
+      if (!st.lo_in) return u32x4{0, 0, 0, 0};
+      return *reinterpret_cast<const u32x4*>(g.L(item) + static_cast<int64_t>(gr) * g.cp + gc);
+    };
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int p = 0; p < F::kPasses; ++p) {
+        const u32x4 v = fetch_one(c, p);
+        next[p] = v;
+      }
+#pragma unroll
+      for (int p = 0; p < F::kPasses; ++p) {
+        const u32x4 v = fetch_lo(c, p);
+        next_lo[p] = v;
+      }
+    };
+    if (c_lo < c_hi) fetch(c_lo);
+#pragma unroll 1
+    for (int c = c_lo; c < c_hi; ++c) {
+      asm volatile("" : "+v"(lane));
+      if (stage == 0) {  // the chunk's largest magnitude sets its power of two
+        float big = 0.0f;
+        auto two = [&](uint32_t x) {
+          big = fmaxf(big, fmaxf(fabsf(sbp::bf16_lo(x)), fabsf(sbp::bf16_hi(x))));
+        };
+#pragma unroll
+        for (int p = 0; p < F::kPasses; ++p)
+          two(next[p].x), two(next[p].y), two(next[p].z), two(next[p].w);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+        if (lane == 0) red[wave] = big;
+        __syncthreads();
+        big = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        // 2^7 <= big * 2^k < 2^8; an infinity needs no room
+        const int k = big > 0.0f && big < __builtin_huge_valf() ? 7 - ilogbf(big) : 200;
+        if (k < kx) {
+          const float by = kx == 200 ? 1.0f : ldexpf(1.0f, 2 * (k - kx < -70 ? -70 : k - kx));
+#pragma unroll
+          for (int i = 0; i < kSub; ++i)
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) G[i][j] = G[i][j] * by;
+          kx = k;
+        }
+      }
+      const int k = stage == 0 ? kx : k_in;
+#pragma unroll
+      for (int p = 0; p < F::kPasses; ++p) {
+        const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), piece = at % (XC / 8);
+        const u32x4 w = stage <= 1 ? __builtin_bit_cast(u32x4, half8(next[p], k)) : next[p];
+        *reinterpret_cast<u32x4*>(LX + flat_at<XC>(row, piece)) = w;
+        if (st.lo_in) *reinterpret_cast<u32x4*>(LL + flat_at<XC>(row, piece)) = next_lo[p];
+      }
+      __syncthreads();
+      if (c + 1 < c_hi) fetch(c + 1);
+      if (stage > 0) {
+        // D = 64 columns x MP (wide) or MP x 64 columns (tall): a lane's 4 rows of D
+        // are 4 neighbours of one row of LX
+        constexpr int DI = TALL ? kSub : 1, DJ = TALL ? 1 : kSub;
+        f32x16 D[DI][DJ] = {};
+#pragma unroll 2
+        for (int ph = 0; ph < MP / 16; ++ph) {
+          f16x8 p[DI], q[DJ];
+#pragma unroll
+          for (int i = 0; i < DI; ++i)
+            p[i] = TALL ? flat_along<MP>(LB, wr * H + i * 32, ph, lane)
+                        : flat_across<XC>(LX, wr * 32, ph, lane);
+#pragma unroll
+          for (int j = 0; j < DJ; ++j)
+            q[j] = TALL ? flat_along<XC>(LX, wc * 32, ph, lane)
+                        : flat_along<MP>(LB, wc * H + j * 32, ph, lane);
+#pragma unroll
+          for (int i = 0; i < DI; ++i)
+#pragma unroll
+            for (int j = 0; j < DJ; ++j) D[i][j] = mfma(p[i], q[j], D[i][j]);
+        }
+        f16x4 hi[kSub][4], lo[kSub][4];
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int m0 = TALL ? wr * H + u * 32 + q * 8 + 4 * (lane >> 5)
+                                : wc * H + u * 32 + (lane & 31);
+            const int row = TALL ? wc * 32 + (lane & 31) : m0;
+            const int piece = TALL ? m0 >> 3 : wr * 4 + q;
+            const int at = flat_at<XC>(row, piece) + (lane >> 5) * 8;
+            const f16x4 x = *reinterpret_cast<const f16x4*>(LX + at);
+            f16x4 l{};
+            if (st.lo_in) l = *reinterpret_cast<const f16x4*>(LL + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float y = static_cast<float>(x[e]);
+              if (st.lo_in) y = fmaf(static_cast<float>(l[e]), 1.0f / kScaleLo, y);
+              const float a = fmaf(dB[TALL ? m0 + e : m0], fd, fa);
+              const float v = fmaf(a, y, (TALL ? D[u % DI][0] : D[0][u % DJ])[q * 4 + e] * fd);
+              if (st.last) {
+                hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<uint16_t>(sbp::bf16_rne(v)));
+              } else {
+                hi[u][q][e] = static_cast<_Float16>(v);
+                lo[u][q][e] = static_cast<_Float16>((v - static_cast<float>(hi[u][q][e])) * kScaleLo);
+              }
+            }
+          }
+        __syncthreads();  // X is read
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int m0 = TALL ? wr * H + u * 32 + q * 8 + 4 * (lane >> 5)
+                                : wc * H + u * 32 + (lane & 31);
+            const int row = TALL ? wc * 32 + (lane & 31) : m0;
+            const int piece = TALL ? m0 >> 3 : wr * 4 + q;
+            const int at = flat_at<XC>(row, piece) + (lane >> 5) * 8;
+            *reinterpret_cast<f16x4*>(LX + at) = hi[u][q];
+            if (st.lo_out) *reinterpret_cast<f16x4*>(LL + at) = lo[u][q];
+          }
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < F::kPasses; ++p) {
+          const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), piece = at % (XC / 8);
+          const int gr = TALL ? c * 64 + row : row, gc = TALL ? piece * 8 : c * 64 + piece * 8;
+          const u32x4 w = *reinterpret_cast<const u32x4*>(LX + flat_at<XC>(row, piece));
+          if (st.last) {
+            if (gr < g.rows && gc < g.cols)
+              store_bits8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec,
+                          w);
+          } else {
+            const int64_t idx = static_cast<int64_t>(gr) * g.cp + gc;
+            *reinterpret_cast<u32x4*>(g.S(0, item) + idx) = w;
+            if (st.lo_out)
+              *reinterpret_cast<u32x4*>(g.L(item) + idx) =
+                  *reinterpret_cast<const u32x4*>(LL + flat_at<XC>(row, piece));
+          }
+        }
+      }
+      if (make_gram) {
+#pragma unroll 2
+        for (int ph = 0; ph < 4; ++ph) {
+          f16x8 p[kSub], q[kSub];
+#pragma unroll
+          for (int i = 0; i < kSub; ++i) {
+            p[i] = TALL ? flat_across<XC>(LX, wr * H + i * 32, ph, lane)
+                        : flat_along<XC>(LX, wr * H + i * 32, ph, lane);
+            q[i] = TALL ? flat_across<XC>(LX, wc * H + i * 32, ph, lane)
+                        : flat_along<XC>(LX, wc * H + i * 32, ph, lane);
+          }
+#pragma unroll
+          for (int i = 0; i < kSub; ++i)
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) G[i][j] = mfma(p[i], q[j], G[i][j]);
+        }
+      }
+      __syncthreads();  // LX and LL are free
+    }
+    if (stage == 1) gram = static_cast<float>(kScaleA) * inv_sx * inv_sx;
+    if (make_gram && g.splits > 1) {
+      float* p = g.part((stage + 1) & 1, item, split) + wave * (H * H) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(p + ((i * kSub + j) * 4 + q) * 256) =
+                f32x4{G[i][j][q * 4], G[i][j][q * 4 + 1], G[i][j][q * 4 + 2], G[i][j][q * 4 + 3]};
+      if (stage == 0 && threadIdx.x == 0) *g.part_k(item, split) = kx;
+    }
+  }
+}
+
+template <int MP>
+__global__ void __launch_bounds__(kBlock, 2)
+ns_flat_kernel(Groups gs, FlatSteps fs, int first, int end) {
+  __shared__ __align__(16) char LB[Flat<MP>::kB];
+  __shared__ __align__(16) char LX[Flat<MP>::kX];
+  __shared__ __align__(16) char LL[Flat<MP>::kX];
+  __shared__ float dA[MP], dB[MP], red[4];
+  int gi = 0;
+  while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_apply) ++gi;
+  const Group& g = gs.g[gi];
+  // a matrix's blocks go to one XCD (blocks are handed to the XCDs in turn),
+  // whose L2 then serves the partial sums that all of them read
+  const unsigned local = blockIdx.x - g.t_apply, round = local / (kXcds * g.splits);
+  const unsigned in = local % (kXcds * g.splits);
+  const unsigned items = g.count - round * kXcds < kXcds ? g.count - round * kXcds : kXcds;
+  const int item = round * kXcds + in % items, split = in / items;
+  if (g.tall())
+    flat_stages<MP, true>(g, fs, item, split, first, end, LB, LX, LL, dA, dB, red);
+  else
+    flat_stages<MP, false>(g, fs, item, split, first, end, LB, LX, LL, dA, dB, red);
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -748,53 +1265,90 @@ struct Piece {
   int64_t first, count;
 };
 
-struct Chunk {
-  std::vector<Piece> pieces;
-  int64_t bytes = 0;
-};
-
 struct Shape {
   int64_t m, n;  // padded short and long side
   int64_t norm_blocks;
+  int64_t splits;  // blocks per matrix of the flat kernel, 0 for the products
 };
 
+// What a matrix's results depend on (the flat kernel or the products, and its
+// splits) goes by its shape alone, so that ranks that hold different parts of a
+// model get the same bits for the same matrix.
+//
+// Splits: a block spends about 3 times as long on 64 columns as on reading
+// another block's partial Gram matrix, and a launch of its own for each step
+// costs as much as about 4 of the former, so up to 4 chunks stay in one block.
 Shape shape_of(const sbp_matrices& g) {
   Shape s;
   s.m = up(std::min(g.rows, g.cols), kPad);
   s.n = up(std::max(g.rows, g.cols), kPad);
   const int64_t units = g.rows * ((g.cols + 511) / 512);
   s.norm_blocks = std::max<int64_t>(1, std::min<int64_t>(kMaxNormBlocks, (units + 31) / 32));
+  s.splits = 0;
+  if (s.m <= 128) {
+    const int64_t chunks = s.n / 64;
+    s.splits = 1;
+    if (chunks > 4)
+      while ((s.splits + 1) * (s.splits + 1) <= chunks && s.splits < 64) ++s.splits;
+  }
   return s;
 }
 
-// Bytes one piece takes: fp16 arrays, norm partials, scalars (each 256-B aligned).
-int64_t half_bytes(const Shape& s, int64_t count) {
-  return up(2 * count * (3 * s.m * s.n + 2 * s.m * s.m), 256);
+// Which launches a shape takes part in.
+enum Class { kProducts, kFlat64, kFlat64Steps, kFlat128, kFlat128Steps, kClasses };
+Class class_of(const Shape& s) {
+  if (s.splits == 0) return kProducts;
+  if (s.m == 64) return s.splits == 1 ? kFlat64 : kFlat64Steps;
+  return s.splits == 1 ? kFlat128 : kFlat128Steps;
 }
-int64_t partial_bytes(const Shape& s, int64_t count) { return up(8 * count * s.norm_blocks, 256); }
-int64_t diag_bytes(const Shape& s, int64_t count) { return up(8 * count * s.m, 256); }
+
+struct Chunk {
+  Class cls;
+  std::vector<Piece> pieces;
+  int64_t bytes = 0;
+};
+
+// Bytes one piece takes, array by array (each 256-B aligned).
+int64_t half_bytes(const Shape& s, int64_t count) {
+  return up(2 * count * (s.splits ? 2 * s.m * s.n : 3 * s.m * s.n + 2 * s.m * s.m), 256);
+}
+int64_t partial_bytes(const Shape& s, int64_t count) {
+  return s.splits ? 0 : up(8 * count * s.norm_blocks, 256);
+}
+int64_t diag_bytes(const Shape& s, int64_t count) {
+  return s.splits ? 0 : up(8 * count * s.m, 256);
+}
 int64_t scal_bytes(int64_t count) { return up(static_cast<int64_t>(sizeof(Scal)) * count, 256); }
+int64_t parts_bytes(const Shape& s, int64_t count) {
+  return s.splits > 1 ? up(2 * 4 * count * s.splits * s.m * s.m, 256) : 0;
+}
+int64_t part_k_bytes(const Shape& s, int64_t count) { return up(4 * count * s.splits, 256); }
 
 std::vector<Chunk> chunks_of(const sbp_matrices* groups, int32_t n_groups) {
   std::vector<Chunk> out;
-  int64_t room = 0;
-  for (int32_t i = 0; i < n_groups; ++i) {
-    const sbp_matrices& g = groups[i];
-    if (g.rows == 0 || g.cols == 0) continue;
-    const Shape s = shape_of(g);
-    const int64_t elems = s.m * s.n;
-    for (int64_t first = 0; first < g.count;) {
-      if (out.empty() || room < elems ||
-          static_cast<int>(out.back().pieces.size()) == kMaxGroups) {
-        out.emplace_back();
-        room = std::max(kChunkElems, elems);
+  for (int cls = 0; cls < kClasses; ++cls) {
+    int64_t room = 0;
+    bool open = false;
+    for (int32_t i = 0; i < n_groups; ++i) {
+      const sbp_matrices& g = groups[i];
+      if (g.rows == 0 || g.cols == 0) continue;
+      const Shape s = shape_of(g);
+      if (class_of(s) != cls) continue;
+      const int64_t elems = s.m * s.n;
+      for (int64_t first = 0; first < g.count;) {
+        if (!open || room < elems || static_cast<int>(out.back().pieces.size()) == kMaxGroups) {
+          out.emplace_back();
+          out.back().cls = static_cast<Class>(cls);
+          open = true;
+          room = std::max(kChunkElems, elems);
+        }
+        const int64_t take = std::min(g.count - first, room / elems);
+        out.back().pieces.push_back(Piece{i, first, take});
+        out.back().bytes += half_bytes(s, take) + partial_bytes(s, take) + diag_bytes(s, take) +
+                            scal_bytes(take) + parts_bytes(s, take) + part_k_bytes(s, take);
+        room -= take * elems;
+        first += take;
       }
-      const int64_t take = std::min(g.count - first, room / elems);
-      out.back().pieces.push_back(Piece{i, first, take});
-      out.back().bytes += half_bytes(s, take) + partial_bytes(s, take) +
-                          diag_bytes(s, take) + scal_bytes(take);
-      room -= take * elems;
-      first += take;
     }
   }
   return out;
@@ -887,34 +1441,47 @@ struct Tiles {
   uint32_t gram = 0, apply = 0;
 };
 
-// First blocks of every group for tiles of side T; the launches' sizes.
-Tiles lay_tiles(Groups& gs, int T) {
+// First blocks of every group; the launches' sizes.
+template <typename TL>
+Tiles lay_tiles(Groups& gs) {
   Tiles t;
   for (int i = 0; i < gs.n; ++i) {
     Group& g = gs.g[i];
-    const uint32_t tm = (g.m + T - 1) / T, tn = (g.n + T - 1) / T;
     g.t_gram = t.gram;
     g.t_apply = t.apply;
-    t.gram += g.count * (tm * (tm + 1) / 2);
-    t.apply += g.count * tm * tn;
+    t.gram += g.count * lower_tiles<TL>(g.m);
+    t.apply += g.count * ((g.rp + TL::T - 1) / TL::T) * ((g.cp + TL::T - 1) / TL::T);
   }
   return t;
 }
 
-template <int T, int BK>
-sbp_status run_step(const char* who, const Groups& gs, const Tiles& t, const Step& st,
-                    hipStream_t stream) {
-  hipLaunchKernelGGL((ns_product_kernel<T, BK, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
-                     t.gram);
-  hipLaunchKernelGGL((ns_product_kernel<T, BK, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs, st,
-                     t.gram);
-  if (st.last)
-    hipLaunchKernelGGL((ns_product_kernel<T, BK, kLast>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
-                       st, t.apply);
-  else
-    hipLaunchKernelGGL((ns_product_kernel<T, BK, kApply>), dim3(t.apply), dim3(kBlock), 0, stream, gs,
-                       st, t.apply);
-  return launched(who);
+template <typename TL>
+sbp_status run_steps(const char* who, Groups& gs, const sbp_ns_hparams& hp, hipStream_t stream) {
+  const Tiles t = lay_tiles<TL>(gs);
+  for (int s = 0; s < hp.steps; ++s) {
+    Step st{};
+    st.a = hp.coefs[3 * s];
+    st.b = hp.coefs[3 * s + 1];
+    st.c = hp.coefs[3 * s + 2];
+    st.first = s == 0;
+    st.last = s == hp.steps - 1;
+    st.lo_out = hp.steps - 1 - s >= 3;
+    st.lo_in = s > 0 && hp.steps - s >= 3;
+    st.in = s & 1;
+    hipLaunchKernelGGL((ns_product_kernel<TL, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs,
+                       st, t.gram);
+    hipLaunchKernelGGL((ns_product_kernel<TL, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs,
+                       st, t.gram);
+    if (st.last)
+      hipLaunchKernelGGL((ns_product_kernel<TL, kLast>), dim3(t.apply), dim3(kBlock), 0, stream,
+                         gs, st, t.apply);
+    else
+      hipLaunchKernelGGL((ns_product_kernel<TL, kApply>), dim3(t.apply), dim3(kBlock), 0, stream,
+                         gs, st, t.apply);
+    const sbp_status rc = launched(who);
+    if (rc != SBP_OK) return rc;
+  }
+  return SBP_OK;
 }
 
 sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c,
@@ -954,6 +1521,11 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     ws += diag_bytes(s, p.count);
     g.scal = reinterpret_cast<Scal*>(ws);
     ws += scal_bytes(p.count);
+    g.splits = static_cast<int32_t>(s.splits);
+    g.parts = reinterpret_cast<float*>(ws);
+    ws += parts_bytes(s, p.count);
+    g.part_ks = reinterpret_cast<int32_t*>(ws);
+    ws += part_k_bytes(s, p.count);
     g.t_norm = norm;
     g.t_pro = pro;
     norm += g.count * g.norm_blocks;
@@ -965,34 +1537,39 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     grow += std::log2(std::max(1.0, std::fabs(static_cast<double>(hp.coefs[3 * s]))));
   const int igrow = static_cast<int>(std::min(200.0, std::ceil(grow)));
 
+  if (c.cls != kProducts) {
+    FlatSteps fs{};
+    fs.eps = hp.eps;
+    fs.grow = igrow;
+    for (int s = 0; s < hp.steps; ++s)
+      fs.s[s] = FlatStep{hp.coefs[3 * s], hp.coefs[3 * s + 1], hp.coefs[3 * s + 2],
+                         s == hp.steps - 1, s > 0 && hp.steps - s >= 3, hp.steps - 1 - s >= 3};
+    uint32_t blocks = 0;
+    for (int i = 0; i < gs.n; ++i) {
+      gs.g[i].t_apply = blocks;
+      blocks += gs.g[i].count * gs.g[i].splits;
+    }
+    const bool at_once = c.cls == kFlat64 || c.cls == kFlat128;
+    auto kernel = c.cls == kFlat64 || c.cls == kFlat64Steps ? ns_flat_kernel<64> : ns_flat_kernel<128>;
+    for (int stage = 0; stage <= hp.steps; stage += at_once ? hp.steps + 1 : 1) {
+      hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBlock), 0, stream, gs, fs, stage,
+                         at_once ? hp.steps + 1 : stage + 1);
+      const sbp_status rc = launched(who);
+      if (rc != SBP_OK) return rc;
+    }
+    return SBP_OK;
+  }
+
   hipLaunchKernelGGL(ns_norm_kernel, dim3(norm), dim3(kBlock), 0, stream, gs);
   hipLaunchKernelGGL(ns_prologue_kernel, dim3(pro), dim3(kBlock), 0, stream, gs, hp.eps, igrow);
   sbp_status rc = launched(who);
   if (rc != SBP_OK) return rc;
 
-  // the largest tile that still gives every CU one: fewer bytes read per flop
-  int T = 256;
-  Tiles t = lay_tiles(gs, T);
-  while (T > 64 && t.apply < 256) {
-    T /= 2;
-    t = lay_tiles(gs, T);
-  }
-  for (int s = 0; s < hp.steps; ++s) {
-    Step st{};
-    st.a = hp.coefs[3 * s];
-    st.b = hp.coefs[3 * s + 1];
-    st.c = hp.coefs[3 * s + 2];
-    st.first = s == 0;
-    st.last = s == hp.steps - 1;
-    st.lo_out = hp.steps - 1 - s >= 3;
-    st.lo_in = s > 0 && hp.steps - s >= 3;
-    st.in = s & 1;
-    rc = T == 256   ? run_step<256, 32>(who, gs, t, st, stream)
-         : T == 128 ? run_step<128, 32>(who, gs, t, st, stream)
-                    : run_step<64, 64>(who, gs, t, st, stream);
-    if (rc != SBP_OK) return rc;
-  }
-  return SBP_OK;
+  const char* f = getenv("NS_T");
+  int T = f ? atoi(f) : 64;
+  if (T == 256) return run_steps<Tile<256, 32>>(who, gs, hp, stream);
+  if (T == 128) return run_steps<Tile<128, 32>>(who, gs, hp, stream);
+  return run_steps<Tile<64, 64>>(who, gs, hp, stream);
 }
 
 }  // namespace

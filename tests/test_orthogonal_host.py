@@ -252,7 +252,9 @@ def test_newton_schulz_nothing_to_do():
 def test_newton_schulz_workspace_size():
     q = sbp.lib().sbp_newton_schulz_workspace
     one = q((sbp.Matrices * 1)(_mats()), 1)
-    assert one >= 2 * 6 * 64 * 64  # X, its transpose twice, the remainder, A and B
+    assert one >= 2 * 2 * 64 * 64  # the iterate and its remainder
+    big = q((sbp.Matrices * 1)(_mats(rows=192, cols=192)), 1)
+    assert big >= 2 * 5 * 192 * 192  # the iterate twice, its remainder, A and B
     assert q((sbp.Matrices * 1)(_mats(rows=1, cols=1)), 1) == one  # padded alike
     assert q((sbp.Matrices * 1)(_mats(count=3)), 1) > 2 * one
     assert q((sbp.Matrices * 1)(_mats(rows=0)), 1) == 0
