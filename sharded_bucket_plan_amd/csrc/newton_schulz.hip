@@ -45,7 +45,6 @@
 // same from run to run.
 #include <hip/hip_runtime.h>
 #include <math.h>
-#include <stdlib.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -100,8 +99,10 @@ struct Group {
   int32_t in_vec, out_vec;  // 16-byte rows
   uint32_t t_norm, t_pro, t_gram, t_apply;  // first block of the group in each launch
   // short side of at most 128 only: blocks per matrix; their partial Gram
-  // matrices (twice, for steps in turn) and the powers of two of the first
+  // matrices (twice, for steps in turn) and the powers of two of the first;
+  // whether a kernel sums those, into the first of them, between the steps
   int32_t splits;
+  int32_t summed;
   float* parts;
   int32_t* part_ks;
 
@@ -119,8 +120,8 @@ struct Group {
   __device__ float* part(int which, int item, int split) const {
     return parts + ((static_cast<int64_t>(which) * count + item) * splits + split) * m * m;
   }
-  __device__ int32_t* part_k(int item, int split) const {
-    return part_ks + static_cast<int64_t>(item) * splits + split;
+  __device__ int32_t* part_k(int item, int split) const {  // [splits]: the sum's
+    return part_ks + static_cast<int64_t>(item) * (splits + 1) + split;
   }
   __device__ _Float16* A(int which, int item) const {
     return base + static_cast<int64_t>(3) * count * mn() +
@@ -264,10 +265,9 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
 
 // ---- the product ------------------------------------------------------------------
 
-// Tiles of the lower triangle of an m x m matrix.
-template <typename TL>
-__host__ __device__ __forceinline__ int lower_tiles(int m) {
-  const int side = (m + TL::T - 1) / TL::T;
+// Tiles of side T of the lower triangle of an m x m matrix.
+__host__ __device__ __forceinline__ int lower_tiles(int m, int T) {
+  const int side = (m + T - 1) / T;
   return side * (side + 1) / 2;
 }
 
@@ -570,10 +570,12 @@ __device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) 
   return half + (row & 31) * TL::T + turned;
 }
 
-template <typename TL, Mode M>
+// SUB: the blocks' tiles are the quarters of tiles of twice the side, from tile
+// `from` on.
+template <typename TL, Mode M, bool SUB>
 __global__ void __launch_bounds__(kBlock, TL::T == 256 ? 1 : 2)
-ns_product_kernel(Groups gs, Step st, unsigned total) {
-  constexpr int T = TL::T, BK = TL::BK;
+ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
+  constexpr int T = TL::T, BK = TL::BK, PT = SUB ? 2 * T : T;
   // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[TL::kBuf];
   __shared__ __align__(16) char buf1[TL::kBuf];
@@ -586,6 +588,8 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
   unsigned b = blockIdx.x;
   const unsigned per_xcd = total / kXcds;
   if (b < per_xcd * kXcds) b = (b % kXcds) * per_xcd + b / kXcds;
+  const unsigned quarter = b & 3;
+  if constexpr (SUB) b = from + b / 4;
   int gi = 0;
   while (gi + 1 < gs.n && b >= (kApplies ? gs.g[gi + 1].t_apply : gs.g[gi + 1].t_gram)) ++gi;
   const Group& g = gs.g[gi];
@@ -594,7 +598,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
   const int crows = kApplies ? g.rp : m, ccols = kApplies ? g.cp : m;  // of C
   int item, ti, tj;
   if constexpr (kApplies) {
-    const int tr = (crows + T - 1) / T, tc = (ccols + T - 1) / T;
+    const int tr = (crows + PT - 1) / PT, tc = (ccols + PT - 1) / PT;
     const int local = b - g.t_apply;
     item = local / (tr * tc);
     const int t = local % (tr * tc);
@@ -606,7 +610,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     ti = strip * kStrip + s % high;
     tj = s / high;
   } else {
-    const int per = lower_tiles<TL>(m);
+    const int per = lower_tiles(m, PT);
     const int local = b - g.t_gram;
     item = local / per;
     const int t = local % per;
@@ -615,7 +619,12 @@ ns_product_kernel(Groups gs, Step st, unsigned total) {
     while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
     tj = t - ti * (ti + 1) / 2;
   }
-  const int r0 = ti * T, c0 = tj * T;  // inside C: both tile counts are rounded up
+  if constexpr (SUB) {
+    ti = 2 * ti + (quarter >> 1);
+    tj = 2 * tj + (quarter & 1);
+    if (ti * T >= crows || tj * T >= ccols || (!kApplies && tj > ti)) return;
+  }
+  const int r0 = ti * T, c0 = tj * T;  // inside C
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = wave >> 1, wc = wave & 1;
 
@@ -862,27 +871,47 @@ struct Flat {
 template <int COLS>
 __device__ __forceinline__ int flat_at(int row, int piece) {
   constexpr int kMask = (COLS / 8 < 16 ? COLS / 8 : 16) - 1;
-  return row * (COLS * 2) + (piece ^ (row & kMask)) * 16;
+  return row * (COLS * 2) + ((piece * 16) ^ ((row & kMask) * 16));
 }
 
-// MFMA operand fragments of phase ph (16 k): 32 rows from `row`, k along them;
-// or 32 columns from `col`, k running over the rows.
+// A lane's part of an MFMA operand: 32 rows of a matrix of COLS columns, k along
+// them, or 32 columns, k running over the rows.
 template <int COLS>
-__device__ __forceinline__ f16x8 flat_along(const char* mat, int row, int ph, int lane) {
-  return *reinterpret_cast<const f16x8*>(mat +
-                                         flat_at<COLS>(row + (lane & 31), ph * 2 + (lane >> 5)));
-}
+struct Along {
+  const char* at;
+  int turn;
+  __device__ __forceinline__ Along(const char* mat, int row, int lane) {
+    at = mat + (row + (lane & 31)) * (COLS * 2);
+    turn = flat_at<COLS>(lane & 31, lane >> 5) - (lane & 31) * (COLS * 2);
+  }
+  // phase ph (16 k), 32 rows further on for each i
+  __device__ __forceinline__ f16x8 read(int ph, int i) const {
+    return *reinterpret_cast<const f16x8*>(at + ((ph * 32) ^ turn) + i * 32 * (COLS * 2));
+  }
+};
 template <int COLS>
-__device__ __forceinline__ f16x8 flat_across(const char* mat, int col, int ph, int lane) {
-  typedef __fp16 h4 __attribute__((__vector_size__(8)));
-  typedef __attribute__((address_space(3))) h4* lds_h4;
-  const int k = ph * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
-  const int piece = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-  const char* p = mat + (lane & 1) * 8;
-  const h4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + flat_at<COLS>(k, piece)));
-  const h4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + flat_at<COLS>(k + 4, piece)));
-  return __builtin_bit_cast(f16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
+struct Across {
+  const char* lo;
+  const char* hi;
+  int turn_lo, turn_hi;
+  __device__ __forceinline__ Across(const char* mat, int col, int lane) {
+    const int k = (lane >> 5) * 8 + ((lane >> 2) & 3);
+    const int piece = (col >> 3) + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+    lo = mat + (lane & 1) * 8 + k * (COLS * 2);
+    hi = lo + 4 * (COLS * 2);
+    turn_lo = flat_at<COLS>(k, piece) - k * (COLS * 2);
+    turn_hi = flat_at<COLS>(k + 4, piece) - (k + 4) * (COLS * 2);
+  }
+  // phase ph: 16 rows further on, whose rotation is the same; i: 32 columns
+  __device__ __forceinline__ f16x8 read(int ph, int i) const {
+    typedef __fp16 h4 __attribute__((__vector_size__(8)));
+    typedef __attribute__((address_space(3))) h4* lds_h4;
+    const int step = ph * 16 * (COLS * 2);
+    const h4 a = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(lo + (turn_lo ^ (i * 64)) + step));
+    const h4 b = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(hi + (turn_hi ^ (i * 64)) + step));
+    return __builtin_bit_cast(f16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
 
 __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -898,26 +927,245 @@ struct FlatSteps {
   int32_t grow;
 };
 
-// Stages first .. end-1: stage 0 is the input's Gram matrix, stage s step s.
-// TALL: X lies across (rows of 64 columns' groups hold MP elements).
-template <int MP, bool TALL>
-__device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs, int item,
-                                            int split, int first, int end, char* LB, char* LX,
-                                            char* LL, float* dA, float* dB, float* red) {
+// A Gram matrix of values times 2^-by, brought back (by <= 0; what lies 2^70
+// below counts for nothing).
+__device__ __forceinline__ float gram_scale(int by) { return ldexpf(1.0f, 2 * (by < -70 ? -70 : by)); }
+
+// What a stage does with a block's columns: the input's Gram matrix; a step from
+// the input or from the stored X, with X's remainder kept, without it, or to the
+// caller's matrix.
+enum Kind { kInputGram, kInput, kInputLast, kKept, kPlain, kStoredLast };
+
+struct Columns {
+  int lo, hi;     // chunks of 64
+  int k;          // the input times 2^k
+  float fa, fd;   // X' = fa X + fd * accumulators, with the diagonal's remainder * fd
+  bool keep;      // store the remainder
+};
+
+template <int MP>
+struct Buffers {
+  char *B, *X, *L;
+  float *dA, *dB, *red;
+};
+
+// TALL: X lies across, a row of the chunk holds MP elements.  G: the products
+// of this block's columns of the result (of the input * 2^kx).
+template <int MP, bool TALL, Kind K>
+__device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& lds, int item,
+                                             const Columns& cs, int wave, int lane,
+                                             f32x16 (&G)[MP / 64][MP / 64], int& kx) {
   using F = Flat<MP>;
   constexpr int kSub = F::kSub, H = MP / 2;
-  constexpr int XC = TALL ? MP : 64;  // elements of a row of LX and LL
+  constexpr int XC = TALL ? MP : 64;
+  constexpr bool kFromInput = K == kInputGram || K == kInput || K == kInputLast;
+  constexpr bool kStep = K != kInputGram, kLast = K == kInputLast || K == kStoredLast;
+  constexpr bool kLoIn = K == kKept, kLo = K == kKept || K == kInput;
+  const int wr = wave >> 1, wc = wave & 1;
+  const uint16_t* in = g.in + item * g.in_stride;
+  uint16_t* out = g.out + item * g.out_stride;
+  _Float16* S = g.S(0, item);
+  _Float16* L = g.L(item);
+  const int ld = g.cp;
+  // this thread's pieces of a chunk
+  auto row_of = [&](int p) { return (p * kBlock + wave * 64 + lane) / (XC / 8); };
+  const int piece = lane % (XC / 8);
+  u32x4 next[F::kPasses], next_lo[F::kPasses];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int p = 0; p < F::kPasses; ++p) {
+      const int gr = TALL ? c * 64 + row_of(p) : row_of(p), gc = TALL ? piece * 8 : c * 64 + piece * 8;
+      if constexpr (kFromInput) {
+        u32x4 v{0, 0, 0, 0};
+        if (gr < g.rows && gc < g.cols) v = load_row8(in + gr * g.in_ld + gc, g.cols - gc, g.in_vec);
+        next[p] = v;
+      } else {
+        const int64_t idx = static_cast<int64_t>(gr) * ld + gc;
+        next[p] = *reinterpret_cast<const u32x4*>(S + idx);
+        if constexpr (kLoIn) next_lo[p] = *reinterpret_cast<const u32x4*>(L + idx);
+      }
+    }
+  };
+  // where a lane's accumulators lie in X: 4 neighbours of a row for each u and q
+  const int x_row = TALL ? wc * 32 + (lane & 31) : wc * H + (lane & 31);
+  auto x_at = [&](int u, int q) {
+    return TALL ? flat_at<XC>(x_row, (wr * H + u * 32) / 8 + q) + (lane >> 5) * 8
+                : flat_at<XC>(x_row, wr * 4 + q) + (lane >> 5) * 8 + u * 32 * (XC * 2);
+  };
+  fetch(cs.lo);
+#pragma unroll 1
+  for (int c = cs.lo; c < cs.hi; ++c) {
+    if constexpr (K == kInputGram) {  // the chunk's largest magnitude sets its power of two
+      float big = 0.0f;
+      auto two = [&](uint32_t x) {
+        big = fmaxf(big, fmaxf(fabsf(sbp::bf16_lo(x)), fabsf(sbp::bf16_hi(x))));
+      };
+#pragma unroll
+      for (int p = 0; p < F::kPasses; ++p)
+        two(next[p].x), two(next[p].y), two(next[p].z), two(next[p].w);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+      if (lane == 0) lds.red[wave] = big;
+      lds_barrier();
+      big = fmaxf(fmaxf(lds.red[0], lds.red[1]), fmaxf(lds.red[2], lds.red[3]));
+      // 2^7 <= big * 2^k < 2^8; an infinity needs no room
+      const int k = big > 0.0f && big < __builtin_huge_valf() ? 7 - ilogbf(big) : 200;
+      if (k < kx) {
+        const float by = kx == 200 ? 1.0f : gram_scale(k - kx);
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) G[i][j] = G[i][j] * by;
+        kx = k;
+      }
+    }
+    const int k = K == kInputGram ? kx : cs.k;
+#pragma unroll
+    for (int p = 0; p < F::kPasses; ++p) {
+      const int at = flat_at<XC>(row_of(p), piece);
+      *reinterpret_cast<u32x4*>(lds.X + at) =
+          kFromInput ? __builtin_bit_cast(u32x4, half8(next[p], k)) : next[p];
+      if constexpr (kLoIn) *reinterpret_cast<u32x4*>(lds.L + at) = next_lo[p];
+    }
+    lds_barrier();
+    if (c + 1 < cs.hi) fetch(c + 1);
+    if constexpr (kStep) {
+      // D = 64 columns x MP (wide) or MP x 64 columns (tall): a lane's 4 rows of D
+      // are 4 neighbours of one row of X
+      constexpr int DI = TALL ? kSub : 1, DJ = TALL ? 1 : kSub;
+      f32x16 D[DI][DJ] = {};
+      const Along<MP> b(lds.B, (TALL ? wr : wc) * H, lane);
+      const Along<XC> xa(lds.X, wc * 32, lane);
+      const Across<XC> xt(lds.X, wr * 32, lane);
+#pragma unroll 4
+      for (int ph = 0; ph < MP / 16; ++ph) {
+        const f16x8 x = TALL ? xa.read(ph, 0) : xt.read(ph, 0);
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+          if constexpr (TALL) D[u][0] = mfma(b.read(ph, u), x, D[u][0]);
+          else D[0][u] = mfma(x, b.read(ph, u), D[0][u]);
+        }
+      }
+      f16x4 hi[kSub][4], rest[kSub][4];
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f16x4 x = *reinterpret_cast<const f16x4*>(lds.X + x_at(u, q));
+          f16x4 l{};
+          if constexpr (kLoIn) l = *reinterpret_cast<const f16x4*>(lds.L + x_at(u, q));
+          f32x4 d;
+          if constexpr (TALL)
+            d = *reinterpret_cast<const f32x4*>(lds.dB + wr * H + u * 32 + q * 8 + 4 * (lane >> 5));
+          else
+            d = f32x4{} + lds.dB[wc * H + u * 32 + (lane & 31)];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y = static_cast<float>(x[e]);
+            if constexpr (kLoIn) y = fmaf(static_cast<float>(l[e]), 1.0f / kScaleLo, y);
+            const float acc = TALL ? D[u % DI][0][q * 4 + e] : D[0][u % DJ][q * 4 + e];
+            const float v = fmaf(fmaf(d[e], cs.fd, cs.fa), y, acc * cs.fd);
+            if constexpr (kLast) {
+              hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<uint16_t>(sbp::bf16_rne(v)));
+            } else {
+              hi[u][q][e] = static_cast<_Float16>(v);
+              if constexpr (kLo)
+                rest[u][q][e] =
+                    static_cast<_Float16>((v - static_cast<float>(hi[u][q][e])) * kScaleLo);
+            }
+          }
+        }
+      lds_barrier();  // X is read
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          *reinterpret_cast<f16x4*>(lds.X + x_at(u, q)) = hi[u][q];
+          if constexpr (kLo) *reinterpret_cast<f16x4*>(lds.L + x_at(u, q)) = rest[u][q];
+        }
+      lds_barrier();
+#pragma unroll
+      for (int p = 0; p < F::kPasses; ++p) {
+        const int gr = TALL ? c * 64 + row_of(p) : row_of(p);
+        const int gc = TALL ? piece * 8 : c * 64 + piece * 8;
+        const int at = flat_at<XC>(row_of(p), piece);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(lds.X + at);
+        if constexpr (kLast) {
+          if (gr < g.rows && gc < g.cols)
+            store_bits8(out + gr * g.out_ld + gc, g.cols - gc, g.out_vec, w);
+        } else {
+          const int64_t idx = static_cast<int64_t>(gr) * ld + gc;
+          *reinterpret_cast<u32x4*>(S + idx) = w;
+          if (kLo && cs.keep)
+            *reinterpret_cast<u32x4*>(L + idx) = *reinterpret_cast<const u32x4*>(lds.L + at);
+        }
+      }
+    }
+    if constexpr (!kLast) {
+      const Along<XC> pa(lds.X, wr * H, lane), qa(lds.X, wc * H, lane);
+      const Across<XC> pt(lds.X, wr * H, lane), qt(lds.X, wc * H, lane);
+#pragma unroll
+      for (int ph = 0; ph < 4; ++ph) {
+        f16x8 p[kSub], q[kSub];
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) {
+          p[i] = TALL ? pt.read(ph, i) : pa.read(ph, i);
+          q[i] = TALL ? qt.read(ph, i) : qa.read(ph, i);
+        }
+#pragma unroll
+        for (int i = 0; i < kSub; ++i)
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) G[i][j] = mfma(p[i], q[j], G[i][j]);
+      }
+    }
+    lds_barrier();  // X and L are free
+  }
+}
+
+__device__ __forceinline__ int least(const int32_t* k, int count) {
+  int r = k[0];
+  for (int i = 1; i < count; ++i) r = k[i] < r ? k[i] : r;
+  return r;
+}
+
+// Sums a matrix's partial Gram matrices into the first: 1024 elements a block.
+__global__ void __launch_bounds__(kBlock) ns_flat_sum_kernel(Groups gs, int which, int scaled) {
+  int gi = 0;
+  while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_gram) ++gi;
+  const Group& g = gs.g[gi];
+  const int per = g.m * g.m / 1024;
+  const int local = blockIdx.x - g.t_gram, item = local / per;
+  const int64_t at = static_cast<int64_t>(local % per) * 1024 + threadIdx.x * 4;
+  const int32_t* pk = g.part_k(item, 0);
+  const int kx = scaled ? least(pk, g.splits) : 0;
+  f32x4 sum{};
+#pragma unroll 8
+  for (int s = 0; s < g.splits; ++s) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(g.part(which, item, s) + at);
+    const float by = scaled ? gram_scale(kx - pk[s]) : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(v[e], by, sum[e]);
+  }
+  *reinterpret_cast<f32x4*>(g.part(which, item, 0) + at) = sum;
+  if (local % per == 0 && threadIdx.x == 0) *g.part_k(item, g.splits) = kx;
+}
+
+// Stages first .. end-1: stage 0 is the input's Gram matrix, stage s step s.
+template <int MP, bool TALL>
+__device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs, int item,
+                                            int split, int first, int end,
+                                            const Buffers<MP>& lds) {
+  constexpr int kSub = MP / 64, H = MP / 2;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int lane = threadIdx.x & 63;
   const int wr = wave >> 1, wc = wave & 1;
   const int chunks = g.n / 64;
-  // this block's 64-column chunks
-  const int c_lo = static_cast<int>(static_cast<int64_t>(chunks) * split / g.splits);
-  const int c_hi = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / g.splits);
+  Columns cs{};
+  cs.lo = static_cast<int>(static_cast<int64_t>(chunks) * split / g.splits);
+  cs.hi = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / g.splits);
   f32x16 G[kSub][kSub];
-  int kx = 0;          // stage 0: G is of the input * 2^kx
+  int kx = 0;
   float inv_sx = 0.0f, gram = 0.0f, apply_first = 0.0f;
-  int k_in = 0;
   if (first > 1) {
     const Scal sc = g.scal[item];
     inv_sx = sc.inv_sx;
@@ -925,26 +1173,24 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
   }
 #pragma unroll 1
   for (int stage = first; stage < end; ++stage) {
-    FlatStep st{};
     // offsets are worked out again each stage: kept, they would not fit the registers
     asm volatile("" : "+v"(lane));
     if (stage > 0) {
-      st = fs.s[stage - 1];
+      const FlatStep st = fs.s[stage - 1];
       // -- the Gram matrix of the stage before
       if (g.splits > 1) {
-        const float* part = g.part(stage & 1, item, 0);
-        const int32_t* pk = g.part_k(item, 0);
-        kx = INT32_MAX;
-        if (stage == 1)
-          for (int s = 0; s < g.splits; ++s) kx = pk[s] < kx ? pk[s] : kx;
+        const float* part = g.part(stage & 1, item, 0) + wave * (H * H) + lane * 4;
+        const int parts = g.summed ? 1 : g.splits;
+        const int32_t* pk = g.part_k(item, g.summed ? g.splits : 0);
+        kx = stage == 1 ? least(pk, parts) : 0;
 #pragma unroll
         for (int i = 0; i < kSub; ++i)
 #pragma unroll
           for (int j = 0; j < kSub; ++j) G[i][j] = f32x16{};
-#pragma unroll 1
-        for (int s = 0; s < g.splits; ++s) {
-          const float by = stage == 1 ? ldexpf(1.0f, 2 * (kx - pk[s] < -70 ? -70 : kx - pk[s])) : 1.0f;
-          const float* p = part + static_cast<int64_t>(s) * (MP * MP) + wave * (H * H) + lane * 4;
+#pragma unroll 2
+        for (int s = 0; s < parts; ++s) {
+          const float by = stage == 1 ? gram_scale(kx - pk[s]) : 1.0f;
+          const float* p = part + static_cast<int64_t>(s) * (MP * MP);
 #pragma unroll
           for (int i = 0; i < kSub; ++i)
 #pragma unroll
@@ -964,18 +1210,19 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
           for (int i = 0; i < kSub; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) == (lane & 31)) tr = tr + G[i][i][e];
+              tr = tr + (8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) == (lane & 31) ? G[i][i][e] : 0.0f);
         }
         const double norm = sqrt(block_sum_all(tr)) * ldexp(1.0, -kx);
         const Norm nm = norm_of(norm, fs.eps, fs.grow);
-        k_in = nm.k;
+        cs.k = nm.k;
         inv_sx = static_cast<float>(1.0 / nm.sx);
         apply_first = static_cast<float>(nm.rho * nm.sx);
         gram = static_cast<float>(kScaleA * ldexp(1.0, -2 * kx) / (nm.floor_norm * nm.floor_norm));
         if (split == 0 && threadIdx.x == 0)
           g.scal[item] = Scal{0.0f, static_cast<float>(kScaleA / (nm.sx * nm.sx)), 0.0f, inv_sx};
       }
-      // -- A in LDS (symmetric: a lane's 4 rows of a column go into the column's row)
+      // -- A, then B, into LDS (symmetric: a lane's 4 rows of a column go into the
+      // column's row), their diagonals' remainders next to them
       auto put = [&](const f32x16 (&v)[kSub][kSub], float* d) {
 #pragma unroll
         for (int i = 0; i < kSub; ++i)
@@ -985,15 +1232,17 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
             float rest = 0.0f;  // of this lane's diagonal element, if it has one
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int row = wr * H + i * 32 + q * 8 + 4 * (lane >> 5);
               f16x4 h;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 h[e] = static_cast<_Float16>(v[i][j][q * 4 + e]);
                 if (i == j)
-                  rest = row + e == col ? v[i][j][q * 4 + e] - static_cast<float>(h[e]) : rest;
+                  rest = q * 8 + 4 * (lane >> 5) + e == (lane & 31)
+                             ? v[i][j][q * 4 + e] - static_cast<float>(h[e])
+                             : rest;
               }
-              *reinterpret_cast<f16x4*>(LB + flat_at<MP>(col, row >> 3) + (lane >> 5) * 8) = h;
+              *reinterpret_cast<f16x4*>(lds.B + flat_at<MP>(col, (wr * H + i * 32) / 8 + q) +
+                                        (lane >> 5) * 8) = h;
             }
             if (i == j && wr == wc && ((lane >> 2) & 1) == lane >> 5) d[col] = rest;
           }
@@ -1002,220 +1251,79 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
       for (int i = 0; i < kSub; ++i)
 #pragma unroll
         for (int j = 0; j < kSub; ++j) G[i][j] = G[i][j] * gram;
-      put(G, dA);
-      __syncthreads();
+      put(G, lds.dA);
+      lds_barrier();
       f32x16 sq[kSub][kSub] = {};
+      {
+        const Along<MP> pa(lds.B, wr * H, lane), qa(lds.B, wc * H, lane);
 #pragma unroll 2
-      for (int ph = 0; ph < MP / 16; ++ph) {
-        f16x8 p[kSub], q[kSub];
+        for (int ph = 0; ph < MP / 16; ++ph) {
+          f16x8 p[kSub], q[kSub];
 #pragma unroll
-        for (int i = 0; i < kSub; ++i) {
-          p[i] = flat_along<MP>(LB, wr * H + i * 32, ph, lane);
-          q[i] = flat_along<MP>(LB, wc * H + i * 32, ph, lane);
+          for (int i = 0; i < kSub; ++i) {
+            p[i] = pa.read(ph, i);
+            q[i] = qa.read(ph, i);
+          }
+#pragma unroll
+          for (int i = 0; i < kSub; ++i)
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) sq[i][j] = mfma(p[i], q[j], sq[i][j]);
         }
-#pragma unroll
-        for (int i = 0; i < kSub; ++i)
-#pragma unroll
-          for (int j = 0; j < kSub; ++j) sq[i][j] = mfma(p[i], q[j], sq[i][j]);
       }
       const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
 #pragma unroll
       for (int i = 0; i < kSub; ++i)
 #pragma unroll
         for (int j = 0; j < kSub; ++j) {
-          const int col = wc * H + j * 32 + (lane & 31);
-          const float dc = dA[col];
+          const float dc = lds.dA[wc * H + j * 32 + (lane & 31)];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int row = wr * H + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-            // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
-            const float a = G[i][j][e], x = static_cast<float>(static_cast<_Float16>(a));
-            float s = fmaf(dA[row] + dc, x, sq[i][j][e]);
-            if (row == col) s = fmaf(dc, dc, s);
-            sq[i][j][e] = fmaf(fc, s, fb * a);
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 dr = *reinterpret_cast<const f32x4*>(lds.dA + wr * H + i * 32 + q * 8 +
+                                                             4 * (lane >> 5));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // (A + D)^2 = A^2 + D A + A D + D^2 for the diagonal remainder D
+              const float a = G[i][j][q * 4 + e], x = static_cast<float>(static_cast<_Float16>(a));
+              float s = fmaf(dr[e] + dc, x, sq[i][j][q * 4 + e]);
+              if (i == j)
+                s = wr == wc && q * 8 + 4 * (lane >> 5) + e == (lane & 31) ? fmaf(dc, dc, s) : s;
+              sq[i][j][q * 4 + e] = fmaf(fc, s, fb * a);
+            }
           }
         }
-      __syncthreads();  // A is read
-      put(sq, dB);
-      __syncthreads();
+      lds_barrier();  // A is read
+      put(sq, lds.dB);
+      lds_barrier();
     }
-    const bool make_gram = stage == 0 || !st.last;
 #pragma unroll
     for (int i = 0; i < kSub; ++i)
 #pragma unroll
       for (int j = 0; j < kSub; ++j) G[i][j] = f32x16{};
-    if (stage == 0) kx = 200;
-    const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_scale * inv_sx : 1.0f);
-    const float fd = fx * (1.0f / kScaleB), fa = fx * st.a;
 
     // -- this block's columns
-    u32x4 next[F::kPasses], next_lo[F::kPasses];
-    auto fetch_one = [&](int c, int p) {
-      const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), col = at % (XC / 8) * 8;
-      const int gr = TALL ? c * 64 + row : row, gc = TALL ? col : c * 64 + col;
-      if (stage > 1)
-        return *reinterpret_cast<const u32x4*>(g.S(0, item) + static_cast<int64_t>(gr) * g.cp + gc);
-      if (gr < g.rows && gc < g.cols)
-        return load_row8(g.in + item * g.in_stride + gr * g.in_ld + gc, g.cols - gc, g.in_vec);
-      return u32x4{0, 0, 0, 0};
-    };
-    auto fetch_lo = [&](int c, int p) {
-      const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), col = at % (XC / 8) * 8;
-      const int gr = TALL ? c * 64 + row : row, gc = TALL ? col : c * 64 + col;
-      if (!st.lo_in) return u32x4{0, 0, 0, 0};
-      return *reinterpret_cast<const u32x4*>(g.L(item) + static_cast<int64_t>(gr) * g.cp + gc);
-    };
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int p = 0; p < F::kPasses; ++p) {
-        const u32x4 v = fetch_one(c, p);
-        next[p] = v;
-      }
-#pragma unroll
-      for (int p = 0; p < F::kPasses; ++p) {
-        const u32x4 v = fetch_lo(c, p);
-        next_lo[p] = v;
-      }
-    };
-    if (c_lo < c_hi) fetch(c_lo);
-#pragma unroll 1
-    for (int c = c_lo; c < c_hi; ++c) {
-      asm volatile("" : "+v"(lane));
-      if (stage == 0) {  // the chunk's largest magnitude sets its power of two
-        float big = 0.0f;
-        auto two = [&](uint32_t x) {
-          big = fmaxf(big, fmaxf(fabsf(sbp::bf16_lo(x)), fabsf(sbp::bf16_hi(x))));
-        };
-#pragma unroll
-        for (int p = 0; p < F::kPasses; ++p)
-          two(next[p].x), two(next[p].y), two(next[p].z), two(next[p].w);
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
-        if (lane == 0) red[wave] = big;
-        __syncthreads();
-        big = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        // 2^7 <= big * 2^k < 2^8; an infinity needs no room
-        const int k = big > 0.0f && big < __builtin_huge_valf() ? 7 - ilogbf(big) : 200;
-        if (k < kx) {
-          const float by = kx == 200 ? 1.0f : ldexpf(1.0f, 2 * (k - kx < -70 ? -70 : k - kx));
-#pragma unroll
-          for (int i = 0; i < kSub; ++i)
-#pragma unroll
-            for (int j = 0; j < kSub; ++j) G[i][j] = G[i][j] * by;
-          kx = k;
-        }
-      }
-      const int k = stage == 0 ? kx : k_in;
-#pragma unroll
-      for (int p = 0; p < F::kPasses; ++p) {
-        const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), piece = at % (XC / 8);
-        const u32x4 w = stage <= 1 ? __builtin_bit_cast(u32x4, half8(next[p], k)) : next[p];
-        *reinterpret_cast<u32x4*>(LX + flat_at<XC>(row, piece)) = w;
-        if (st.lo_in) *reinterpret_cast<u32x4*>(LL + flat_at<XC>(row, piece)) = next_lo[p];
-      }
-      __syncthreads();
-      if (c + 1 < c_hi) fetch(c + 1);
-      if (stage > 0) {
-        // D = 64 columns x MP (wide) or MP x 64 columns (tall): a lane's 4 rows of D
-        // are 4 neighbours of one row of LX
-        constexpr int DI = TALL ? kSub : 1, DJ = TALL ? 1 : kSub;
-        f32x16 D[DI][DJ] = {};
-#pragma unroll 2
-        for (int ph = 0; ph < MP / 16; ++ph) {
-          f16x8 p[DI], q[DJ];
-#pragma unroll
-          for (int i = 0; i < DI; ++i)
-            p[i] = TALL ? flat_along<MP>(LB, wr * H + i * 32, ph, lane)
-                        : flat_across<XC>(LX, wr * 32, ph, lane);
-#pragma unroll
-          for (int j = 0; j < DJ; ++j)
-            q[j] = TALL ? flat_along<XC>(LX, wc * 32, ph, lane)
-                        : flat_along<MP>(LB, wc * H + j * 32, ph, lane);
-#pragma unroll
-          for (int i = 0; i < DI; ++i)
-#pragma unroll
-            for (int j = 0; j < DJ; ++j) D[i][j] = mfma(p[i], q[j], D[i][j]);
-        }
-        f16x4 hi[kSub][4], lo[kSub][4];
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int m0 = TALL ? wr * H + u * 32 + q * 8 + 4 * (lane >> 5)
-                                : wc * H + u * 32 + (lane & 31);
-            const int row = TALL ? wc * 32 + (lane & 31) : m0;
-            const int piece = TALL ? m0 >> 3 : wr * 4 + q;
-            const int at = flat_at<XC>(row, piece) + (lane >> 5) * 8;
-            const f16x4 x = *reinterpret_cast<const f16x4*>(LX + at);
-            f16x4 l{};
-            if (st.lo_in) l = *reinterpret_cast<const f16x4*>(LL + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float y = static_cast<float>(x[e]);
-              if (st.lo_in) y = fmaf(static_cast<float>(l[e]), 1.0f / kScaleLo, y);
-              const float a = fmaf(dB[TALL ? m0 + e : m0], fd, fa);
-              const float v = fmaf(a, y, (TALL ? D[u % DI][0] : D[0][u % DJ])[q * 4 + e] * fd);
-              if (st.last) {
-                hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<uint16_t>(sbp::bf16_rne(v)));
-              } else {
-                hi[u][q][e] = static_cast<_Float16>(v);
-                lo[u][q][e] = static_cast<_Float16>((v - static_cast<float>(hi[u][q][e])) * kScaleLo);
-              }
-            }
-          }
-        __syncthreads();  // X is read
-#pragma unroll
-        for (int u = 0; u < kSub; ++u)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int m0 = TALL ? wr * H + u * 32 + q * 8 + 4 * (lane >> 5)
-                                : wc * H + u * 32 + (lane & 31);
-            const int row = TALL ? wc * 32 + (lane & 31) : m0;
-            const int piece = TALL ? m0 >> 3 : wr * 4 + q;
-            const int at = flat_at<XC>(row, piece) + (lane >> 5) * 8;
-            *reinterpret_cast<f16x4*>(LX + at) = hi[u][q];
-            if (st.lo_out) *reinterpret_cast<f16x4*>(LL + at) = lo[u][q];
-          }
-        __syncthreads();
-#pragma unroll
-        for (int p = 0; p < F::kPasses; ++p) {
-          const int at = p * kBlock + wave * 64 + lane, row = at / (XC / 8), piece = at % (XC / 8);
-          const int gr = TALL ? c * 64 + row : row, gc = TALL ? piece * 8 : c * 64 + piece * 8;
-          const u32x4 w = *reinterpret_cast<const u32x4*>(LX + flat_at<XC>(row, piece));
-          if (st.last) {
-            if (gr < g.rows && gc < g.cols)
-              store_bits8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec,
-                          w);
-          } else {
-            const int64_t idx = static_cast<int64_t>(gr) * g.cp + gc;
-            *reinterpret_cast<u32x4*>(g.S(0, item) + idx) = w;
-            if (st.lo_out)
-              *reinterpret_cast<u32x4*>(g.L(item) + idx) =
-                  *reinterpret_cast<const u32x4*>(LL + flat_at<XC>(row, piece));
-          }
-        }
-      }
-      if (make_gram) {
-#pragma unroll 2
-        for (int ph = 0; ph < 4; ++ph) {
-          f16x8 p[kSub], q[kSub];
-#pragma unroll
-          for (int i = 0; i < kSub; ++i) {
-            p[i] = TALL ? flat_across<XC>(LX, wr * H + i * 32, ph, lane)
-                        : flat_along<XC>(LX, wr * H + i * 32, ph, lane);
-            q[i] = TALL ? flat_across<XC>(LX, wc * H + i * 32, ph, lane)
-                        : flat_along<XC>(LX, wc * H + i * 32, ph, lane);
-          }
-#pragma unroll
-          for (int i = 0; i < kSub; ++i)
-#pragma unroll
-            for (int j = 0; j < kSub; ++j) G[i][j] = mfma(p[i], q[j], G[i][j]);
-        }
-      }
-      __syncthreads();  // LX and LL are free
+    if (stage == 0) {
+      kx = 200;  // nothing yet
+      flat_columns<MP, TALL, kInputGram>(g, lds, item, cs, wave, lane, G, kx);
+    } else {
+      const FlatStep st = fs.s[stage - 1];
+      const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_scale * inv_sx : 1.0f);
+      cs.fd = fx * (1.0f / kScaleB);
+      cs.fa = fx * st.a;
+      cs.keep = st.lo_out;
+      if (stage == 1 && st.last)
+        flat_columns<MP, TALL, kInputLast>(g, lds, item, cs, wave, lane, G, kx);
+      else if (stage == 1)
+        flat_columns<MP, TALL, kInput>(g, lds, item, cs, wave, lane, G, kx);
+      else if (st.last)
+        flat_columns<MP, TALL, kStoredLast>(g, lds, item, cs, wave, lane, G, kx);
+      else if (st.lo_in)
+        flat_columns<MP, TALL, kKept>(g, lds, item, cs, wave, lane, G, kx);
+      else
+        flat_columns<MP, TALL, kPlain>(g, lds, item, cs, wave, lane, G, kx);
+      if (stage == 1) gram = static_cast<float>(kScaleA) * inv_sx * inv_sx;
+      if (st.last) return;
     }
-    if (stage == 1) gram = static_cast<float>(kScaleA) * inv_sx * inv_sx;
-    if (make_gram && g.splits > 1) {
+    if (g.splits > 1) {
       float* p = g.part((stage + 1) & 1, item, split) + wave * (H * H) + lane * 4;
 #pragma unroll
       for (int i = 0; i < kSub; ++i)
@@ -1227,6 +1335,7 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
                 f32x4{G[i][j][q * 4], G[i][j][q * 4 + 1], G[i][j][q * 4 + 2], G[i][j][q * 4 + 3]};
       if (stage == 0 && threadIdx.x == 0) *g.part_k(item, split) = kx;
     }
+    __syncthreads();  // a block that goes on by itself reads what it stored
   }
 }
 
@@ -1236,7 +1345,8 @@ ns_flat_kernel(Groups gs, FlatSteps fs, int first, int end) {
   __shared__ __align__(16) char LB[Flat<MP>::kB];
   __shared__ __align__(16) char LX[Flat<MP>::kX];
   __shared__ __align__(16) char LL[Flat<MP>::kX];
-  __shared__ float dA[MP], dB[MP], red[4];
+  __shared__ __align__(16) float dA[MP], dB[MP], red[4];
+  const Buffers<MP> lds{LB, LX, LL, dA, dB, red};
   int gi = 0;
   while (gi + 1 < gs.n && blockIdx.x >= gs.g[gi + 1].t_apply) ++gi;
   const Group& g = gs.g[gi];
@@ -1247,9 +1357,9 @@ ns_flat_kernel(Groups gs, FlatSteps fs, int first, int end) {
   const unsigned items = g.count - round * kXcds < kXcds ? g.count - round * kXcds : kXcds;
   const int item = round * kXcds + in % items, split = in / items;
   if (g.tall())
-    flat_stages<MP, true>(g, fs, item, split, first, end, LB, LX, LL, dA, dB, red);
+    flat_stages<MP, true>(g, fs, item, split, first, end, lds);
   else
-    flat_stages<MP, false>(g, fs, item, split, first, end, LB, LX, LL, dA, dB, red);
+    flat_stages<MP, false>(g, fs, item, split, first, end, lds);
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -1269,15 +1379,19 @@ struct Shape {
   int64_t m, n;  // padded short and long side
   int64_t norm_blocks;
   int64_t splits;  // blocks per matrix of the flat kernel, 0 for the products
+  bool summed;     // their partial sums added by a kernel of its own
 };
 
 // What a matrix's results depend on (the flat kernel or the products, and its
 // splits) goes by its shape alone, so that ranks that hold different parts of a
 // model get the same bits for the same matrix.
 //
-// Splits: a block spends about 3 times as long on 64 columns as on reading
-// another block's partial Gram matrix, and a launch of its own for each step
-// costs as much as about 4 of the former, so up to 4 chunks stay in one block.
+// Splits, measured: a block takes about 2.5 us for 64 columns, as long as for
+// reading another block's 128 x 128 partial Gram matrix (a quarter of it at 64 x
+// 64), and a launch of its own for each step costs about as much as 4 chunks,
+// so up to 4 chunks stay in one block; beyond, reading and working balance at the
+// square root.  Where 128-wide matrices have 32 chunks and more a kernel of their
+// own sums the partials (5 us), and blocks take 4 chunks.
 Shape shape_of(const sbp_matrices& g) {
   Shape s;
   s.m = up(std::min(g.rows, g.cols), kPad);
@@ -1285,21 +1399,26 @@ Shape shape_of(const sbp_matrices& g) {
   const int64_t units = g.rows * ((g.cols + 511) / 512);
   s.norm_blocks = std::max<int64_t>(1, std::min<int64_t>(kMaxNormBlocks, (units + 31) / 32));
   s.splits = 0;
+  s.summed = false;
   if (s.m <= 128) {
     const int64_t chunks = s.n / 64;
     s.splits = 1;
     if (chunks > 4)
       while ((s.splits + 1) * (s.splits + 1) <= chunks && s.splits < 64) ++s.splits;
+    s.summed = s.m == 128 && chunks >= 32;
+    if (s.summed) s.splits = std::min<int64_t>(64, chunks / 4);
   }
   return s;
 }
 
 // Which launches a shape takes part in.
-enum Class { kProducts, kFlat64, kFlat64Steps, kFlat128, kFlat128Steps, kClasses };
+enum Class {
+  kProducts, kFlat64, kFlat64Steps, kFlat128, kFlat128Steps, kFlat128Summed, kClasses
+};
 Class class_of(const Shape& s) {
   if (s.splits == 0) return kProducts;
   if (s.m == 64) return s.splits == 1 ? kFlat64 : kFlat64Steps;
-  return s.splits == 1 ? kFlat128 : kFlat128Steps;
+  return s.summed ? kFlat128Summed : s.splits == 1 ? kFlat128 : kFlat128Steps;
 }
 
 struct Chunk {
@@ -1322,7 +1441,7 @@ int64_t scal_bytes(int64_t count) { return up(static_cast<int64_t>(sizeof(Scal))
 int64_t parts_bytes(const Shape& s, int64_t count) {
   return s.splits > 1 ? up(2 * 4 * count * s.splits * s.m * s.m, 256) : 0;
 }
-int64_t part_k_bytes(const Shape& s, int64_t count) { return up(4 * count * s.splits, 256); }
+int64_t part_k_bytes(const Shape& s, int64_t count) { return up(4 * count * (s.splits + 1), 256); }
 
 std::vector<Chunk> chunks_of(const sbp_matrices* groups, int32_t n_groups) {
   std::vector<Chunk> out;
@@ -1437,27 +1556,74 @@ sbp_status launched(const char* who) {
   return SBP_OK;
 }
 
-struct Tiles {
-  uint32_t gram = 0, apply = 0;
+// How a product's tiles are launched: `tiles` of side T, then those of side 256
+// from `tiles` on as quarters.
+struct Launches {
+  int T;
+  uint32_t tiles, quarters;
 };
 
-// First blocks of every group; the launches' sizes.
-template <typename TL>
-Tiles lay_tiles(Groups& gs) {
-  Tiles t;
-  for (int i = 0; i < gs.n; ++i) {
-    Group& g = gs.g[i];
-    g.t_gram = t.gram;
-    g.t_apply = t.apply;
-    t.gram += g.count * lower_tiles<TL>(g.m);
-    t.apply += g.count * ((g.rp + TL::T - 1) / TL::T) * ((g.cp + TL::T - 1) / TL::T);
+// Measured, at k = 4096: a round of 256 tiles of side 256, one a CU, takes 111
+// us, one of 512 of side 128, two a CU, 94 us (a quarter of a round's flops in
+// 0.4 of its time, where there are no more).  So side 256 takes whole rounds, and
+// what is left over where that is more than half a round; less goes by quarters
+// (292 tiles: 212 us in two rounds, 160 so).  Under one round, side 128
+// where it gives most CUs a tile (504 tiles: 59 us against 67 of side 64 and
+// 65 of side 256), else side 64 (30 tiles of side 128: 13.1 us, 108 of side
+// 64: 8.2).
+Launches launches_of(uint32_t at256, uint32_t at128, uint32_t at64) {
+  const uint32_t left = at256 % 256;
+  if (at256 >= 256) {
+    if (left > 0 && left <= 128) return Launches{256, at256 - left, 4 * left};
+    return Launches{256, at256, 0};
   }
-  return t;
+  if (at128 >= 192) return Launches{128, at128, 0};
+  return Launches{64, at64, 0};
 }
 
-template <typename TL>
+uint32_t gram_tiles(const Group& g, int T) {
+  return static_cast<uint32_t>(g.count) * lower_tiles(g.m, T);
+}
+uint32_t apply_tiles(const Group& g, int T) {
+  return static_cast<uint32_t>(g.count) * ((g.rp + T - 1) / T) * ((g.cp + T - 1) / T);
+}
+
+// Launches of one kind of product for all groups, whose first tiles are set.
+template <uint32_t (*TILES)(const Group&, int)>
+Launches lay_out(Groups& gs, uint32_t Group::*first) {
+  uint32_t at[3] = {0, 0, 0};
+  constexpr int kSides[3] = {256, 128, 64};
+  for (int i = 0; i < gs.n; ++i)
+    for (int k = 0; k < 3; ++k) at[k] += TILES(gs.g[i], kSides[k]);
+  const Launches l = launches_of(at[0], at[1], at[2]);
+  uint32_t next = 0;
+  for (int i = 0; i < gs.n; ++i) {
+    gs.g[i].*first = next;
+    next += TILES(gs.g[i], l.T);
+  }
+  return l;
+}
+
+template <Mode M>
+void launch_product(const Launches& l, const Groups& gs, const Step& st, hipStream_t stream) {
+  const dim3 block(kBlock);
+  if (l.T == 256)
+    hipLaunchKernelGGL((ns_product_kernel<Tile<256, 32>, M, false>), dim3(l.tiles), block, 0,
+                       stream, gs, st, l.tiles, 0u);
+  else if (l.T == 128)
+    hipLaunchKernelGGL((ns_product_kernel<Tile<128, 32>, M, false>), dim3(l.tiles), block, 0,
+                       stream, gs, st, l.tiles, 0u);
+  else
+    hipLaunchKernelGGL((ns_product_kernel<Tile<64, 64>, M, false>), dim3(l.tiles), block, 0,
+                       stream, gs, st, l.tiles, 0u);
+  if (l.quarters > 0)
+    hipLaunchKernelGGL((ns_product_kernel<Tile<128, 32>, M, true>), dim3(l.quarters), block, 0,
+                       stream, gs, st, l.quarters, l.tiles);
+}
+
 sbp_status run_steps(const char* who, Groups& gs, const sbp_ns_hparams& hp, hipStream_t stream) {
-  const Tiles t = lay_tiles<TL>(gs);
+  const Launches gram = lay_out<gram_tiles>(gs, &Group::t_gram);
+  const Launches apply = lay_out<apply_tiles>(gs, &Group::t_apply);
   for (int s = 0; s < hp.steps; ++s) {
     Step st{};
     st.a = hp.coefs[3 * s];
@@ -1468,16 +1634,10 @@ sbp_status run_steps(const char* who, Groups& gs, const sbp_ns_hparams& hp, hipS
     st.lo_out = hp.steps - 1 - s >= 3;
     st.lo_in = s > 0 && hp.steps - s >= 3;
     st.in = s & 1;
-    hipLaunchKernelGGL((ns_product_kernel<TL, kGram>), dim3(t.gram), dim3(kBlock), 0, stream, gs,
-                       st, t.gram);
-    hipLaunchKernelGGL((ns_product_kernel<TL, kPoly>), dim3(t.gram), dim3(kBlock), 0, stream, gs,
-                       st, t.gram);
-    if (st.last)
-      hipLaunchKernelGGL((ns_product_kernel<TL, kLast>), dim3(t.apply), dim3(kBlock), 0, stream,
-                         gs, st, t.apply);
-    else
-      hipLaunchKernelGGL((ns_product_kernel<TL, kApply>), dim3(t.apply), dim3(kBlock), 0, stream,
-                         gs, st, t.apply);
+    launch_product<kGram>(gram, gs, st, stream);
+    launch_product<kPoly>(gram, gs, st, stream);
+    if (st.last) launch_product<kLast>(apply, gs, st, stream);
+    else launch_product<kApply>(apply, gs, st, stream);
     const sbp_status rc = launched(who);
     if (rc != SBP_OK) return rc;
   }
@@ -1522,6 +1682,7 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     g.scal = reinterpret_cast<Scal*>(ws);
     ws += scal_bytes(p.count);
     g.splits = static_cast<int32_t>(s.splits);
+    g.summed = s.summed;
     g.parts = reinterpret_cast<float*>(ws);
     ws += parts_bytes(s, p.count);
     g.part_ks = reinterpret_cast<int32_t*>(ws);
@@ -1544,16 +1705,22 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     for (int s = 0; s < hp.steps; ++s)
       fs.s[s] = FlatStep{hp.coefs[3 * s], hp.coefs[3 * s + 1], hp.coefs[3 * s + 2],
                          s == hp.steps - 1, s > 0 && hp.steps - s >= 3, hp.steps - 1 - s >= 3};
-    uint32_t blocks = 0;
+    uint32_t blocks = 0, sums = 0;
     for (int i = 0; i < gs.n; ++i) {
       gs.g[i].t_apply = blocks;
+      gs.g[i].t_gram = sums;
       blocks += gs.g[i].count * gs.g[i].splits;
+      sums += gs.g[i].count * (gs.g[i].m * gs.g[i].m / 1024);
     }
     const bool at_once = c.cls == kFlat64 || c.cls == kFlat128;
-    auto kernel = c.cls == kFlat64 || c.cls == kFlat64Steps ? ns_flat_kernel<64> : ns_flat_kernel<128>;
+    const bool wide = c.cls == kFlat128 || c.cls == kFlat128Steps || c.cls == kFlat128Summed;
+    auto kernel = wide ? ns_flat_kernel<128> : ns_flat_kernel<64>;
     for (int stage = 0; stage <= hp.steps; stage += at_once ? hp.steps + 1 : 1) {
       hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBlock), 0, stream, gs, fs, stage,
                          at_once ? hp.steps + 1 : stage + 1);
+      if (c.cls == kFlat128Summed && stage < hp.steps)
+        hipLaunchKernelGGL(ns_flat_sum_kernel, dim3(sums), dim3(kBlock), 0, stream, gs,
+                           (stage + 1) & 1, stage == 0 ? 1 : 0);
       const sbp_status rc = launched(who);
       if (rc != SBP_OK) return rc;
     }
@@ -1565,11 +1732,7 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
   sbp_status rc = launched(who);
   if (rc != SBP_OK) return rc;
 
-  const char* f = getenv("NS_T");
-  int T = f ? atoi(f) : 64;
-  if (T == 256) return run_steps<Tile<256, 32>>(who, gs, hp, stream);
-  if (T == 128) return run_steps<Tile<128, 32>>(who, gs, hp, stream);
-  return run_steps<Tile<64, 64>>(who, gs, hp, stream);
+  return run_steps(who, gs, hp, stream);
 }
 
 }  // namespace

@@ -161,7 +161,8 @@ def _check_ns(out, bits, steps=5, coefs=sbp.NS_COEFS, eps=1e-7, scale=1.0, what=
 
 
 SHAPES = [(1, 1), (1, 7), (5, 1), (2, 3), (16, 16), (63, 65), (64, 64), (65, 64), (64, 130),
-          (130, 64), (127, 300), (300, 128), (256, 1024), (1024, 256), (509, 1021), (777, 640)]
+          (130, 64), (127, 300), (300, 128), (256, 1024), (1024, 256), (509, 1021), (777, 640),
+          (40, 700), (700, 40), (120, 700), (700, 120), (100, 2500), (2500, 100)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -229,6 +230,30 @@ def test_newton_schulz_more_groups_than_one_launch_takes():
     outs = sbp.newton_schulz([_bf(b) for b in bits])
     for i, (o, b) in enumerate(zip(outs, bits)):
         _check_ns(o, b, what=f"group {i}")
+
+
+@pytest.mark.parametrize("shapes", [
+    [(30, 400, 500)], [(30, 500, 400)],  # tiles of side 128
+    [(48, 700, 900)], [(48, 900, 700)],  # whole rounds of side 256, the rest by quarters
+    [(20, 130, 1100), (36, 1000, 520), (3, 777, 2000)],  # both ways up, ragged
+])
+def test_newton_schulz_large_batches_equal_single_matrices(shapes):
+    """What a matrix comes out as does not depend on what else the call holds,
+    bit for bit, though larger calls take larger tiles; singles are held to the
+    64-bit iteration elsewhere."""
+    import torch
+    xs = [_bf(_u(s, 70 + i, "strong")) for i, s in enumerate(shapes)]
+    outs = sbp.newton_schulz(xs)
+    for x, o in zip(xs, outs):
+        for b in range(0, x.shape[0], 5):
+            alone, = sbp.newton_schulz([x[b]])
+            assert torch.equal(alone.view(torch.int16), o[b].view(torch.int16)), (x.shape, b)
+    _check_ns(outs[0][:1], _bits(xs[0][:1]), what=str(shapes))
+
+
+def _bits(t):
+    import torch
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
 
 
 def test_newton_schulz_many_small_matrices():
