@@ -860,6 +860,9 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
 //   LDS   B (A before it); 64 columns of X and their remainder
 // 16-byte pieces of LDS rows are rotated by row against bank conflicts.
 
+// Chunks of 64 columns that fit LDS together: such matrices never leave it.
+constexpr int kStay64 = 4, kStay128 = 3;
+
 template <int MP>
 struct Flat {
   static constexpr int kSub = MP / 64;          // 32 x 32 tiles per wave and side of MP
@@ -950,9 +953,10 @@ struct Buffers {
 };
 
 // TALL: X lies across, a row of the chunk holds MP elements.  G: the products
-// of this block's columns of the result (of the input * 2^kx).
-template <int MP, bool TALL, Kind K>
-__device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& lds, int item,
+// of this block's columns of the result (of the input * 2^kx).  STAYS: all of the
+// matrix's chunks have places of their own in LDS and stay there between stages.
+template <int MP, bool TALL, bool STAYS, Kind K>
+__device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& all, int item,
                                              const Columns& cs, int wave, int lane,
                                              f32x16 (&G)[MP / 64][MP / 64], int& kx) {
   using F = Flat<MP>;
@@ -961,6 +965,8 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
   constexpr bool kFromInput = K == kInputGram || K == kInput || K == kInputLast;
   constexpr bool kStep = K != kInputGram, kLast = K == kInputLast || K == kStoredLast;
   constexpr bool kLoIn = K == kKept, kLo = K == kKept || K == kInput;
+  constexpr bool kFetch = kFromInput || !STAYS;
+  Buffers<MP> lds = all;
   const int wr = wave >> 1, wc = wave & 1;
   const uint16_t* in = g.in + item * g.in_stride;
   uint16_t* out = g.out + item * g.out_stride;
@@ -992,9 +998,13 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
     return TALL ? flat_at<XC>(x_row, (wr * H + u * 32) / 8 + q) + (lane >> 5) * 8
                 : flat_at<XC>(x_row, wr * 4 + q) + (lane >> 5) * 8 + u * 32 * (XC * 2);
   };
-  fetch(cs.lo);
+  if constexpr (kFetch) fetch(cs.lo);
 #pragma unroll 1
   for (int c = cs.lo; c < cs.hi; ++c) {
+    if constexpr (STAYS) {
+      lds.X = all.X + c * F::kX;
+      lds.L = all.L + c * F::kX;
+    }
     if constexpr (K == kInputGram) {  // the chunk's largest magnitude sets its power of two
       float big = 0.0f;
       auto two = [&](uint32_t x) {
@@ -1019,16 +1029,18 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
         kx = k;
       }
     }
-    const int k = K == kInputGram ? kx : cs.k;
+    if constexpr (kFetch) {
+      const int k = K == kInputGram ? kx : cs.k;
 #pragma unroll
-    for (int p = 0; p < F::kPasses; ++p) {
-      const int at = flat_at<XC>(row_of(p), piece);
-      *reinterpret_cast<u32x4*>(lds.X + at) =
-          kFromInput ? __builtin_bit_cast(u32x4, half8(next[p], k)) : next[p];
-      if constexpr (kLoIn) *reinterpret_cast<u32x4*>(lds.L + at) = next_lo[p];
+      for (int p = 0; p < F::kPasses; ++p) {
+        const int at = flat_at<XC>(row_of(p), piece);
+        *reinterpret_cast<u32x4*>(lds.X + at) =
+            kFromInput ? __builtin_bit_cast(u32x4, half8(next[p], k)) : next[p];
+        if constexpr (kLoIn) *reinterpret_cast<u32x4*>(lds.L + at) = next_lo[p];
+      }
+      lds_barrier();
+      if (c + 1 < cs.hi) fetch(c + 1);
     }
-    lds_barrier();
-    if (c + 1 < cs.hi) fetch(c + 1);
     if constexpr (kStep) {
       // D = 64 columns x MP (wide) or MP x 64 columns (tall): a lane's 4 rows of D
       // are 4 neighbours of one row of X
@@ -1086,6 +1098,7 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
       lds_barrier();
 #pragma unroll
       for (int p = 0; p < F::kPasses; ++p) {
+        if constexpr (STAYS && !kLast) continue;
         const int gr = TALL ? c * 64 + row_of(p) : row_of(p);
         const int gc = TALL ? piece * 8 : c * 64 + piece * 8;
         const int at = flat_at<XC>(row_of(p), piece);
@@ -1118,7 +1131,7 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
           for (int j = 0; j < kSub; ++j) G[i][j] = mfma(p[i], q[j], G[i][j]);
       }
     }
-    lds_barrier();  // X and L are free
+    if constexpr (!STAYS) lds_barrier();  // X and L are free
   }
 }
 
@@ -1151,7 +1164,7 @@ __global__ void __launch_bounds__(kBlock) ns_flat_sum_kernel(Groups gs, int whic
 }
 
 // Stages first .. end-1: stage 0 is the input's Gram matrix, stage s step s.
-template <int MP, bool TALL>
+template <int MP, bool TALL, bool STAYS>
 __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs, int item,
                                             int split, int first, int end,
                                             const Buffers<MP>& lds) {
@@ -1303,7 +1316,7 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
     // -- this block's columns
     if (stage == 0) {
       kx = 200;  // nothing yet
-      flat_columns<MP, TALL, kInputGram>(g, lds, item, cs, wave, lane, G, kx);
+      flat_columns<MP, TALL, STAYS, kInputGram>(g, lds, item, cs, wave, lane, G, kx);
     } else {
       const FlatStep st = fs.s[stage - 1];
       const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_scale * inv_sx : 1.0f);
@@ -1311,15 +1324,15 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
       cs.fa = fx * st.a;
       cs.keep = st.lo_out;
       if (stage == 1 && st.last)
-        flat_columns<MP, TALL, kInputLast>(g, lds, item, cs, wave, lane, G, kx);
+        flat_columns<MP, TALL, STAYS, kInputLast>(g, lds, item, cs, wave, lane, G, kx);
       else if (stage == 1)
-        flat_columns<MP, TALL, kInput>(g, lds, item, cs, wave, lane, G, kx);
+        flat_columns<MP, TALL, STAYS, kInput>(g, lds, item, cs, wave, lane, G, kx);
       else if (st.last)
-        flat_columns<MP, TALL, kStoredLast>(g, lds, item, cs, wave, lane, G, kx);
+        flat_columns<MP, TALL, STAYS, kStoredLast>(g, lds, item, cs, wave, lane, G, kx);
       else if (st.lo_in)
-        flat_columns<MP, TALL, kKept>(g, lds, item, cs, wave, lane, G, kx);
+        flat_columns<MP, TALL, STAYS, kKept>(g, lds, item, cs, wave, lane, G, kx);
       else
-        flat_columns<MP, TALL, kPlain>(g, lds, item, cs, wave, lane, G, kx);
+        flat_columns<MP, TALL, STAYS, kPlain>(g, lds, item, cs, wave, lane, G, kx);
       if (stage == 1) gram = static_cast<float>(kScaleA) * inv_sx * inv_sx;
       if (st.last) return;
     }
@@ -1339,12 +1352,15 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
   }
 }
 
-template <int MP>
-__global__ void __launch_bounds__(kBlock, 2)
+// CHUNKS: places in LDS for the chunks of a matrix that one block handles alone;
+// 0: one place, the chunks come and go.
+template <int MP, int CHUNKS>
+__global__ void __launch_bounds__(kBlock, MP == 128 && CHUNKS > 0 ? 1 : 2)
 ns_flat_kernel(Groups gs, FlatSteps fs, int first, int end) {
+  constexpr int kPlaces = CHUNKS > 0 ? CHUNKS : 1;
   __shared__ __align__(16) char LB[Flat<MP>::kB];
-  __shared__ __align__(16) char LX[Flat<MP>::kX];
-  __shared__ __align__(16) char LL[Flat<MP>::kX];
+  __shared__ __align__(16) char LX[kPlaces * Flat<MP>::kX];
+  __shared__ __align__(16) char LL[kPlaces * Flat<MP>::kX];
   __shared__ __align__(16) float dA[MP], dB[MP], red[4];
   const Buffers<MP> lds{LB, LX, LL, dA, dB, red};
   int gi = 0;
@@ -1357,9 +1373,9 @@ ns_flat_kernel(Groups gs, FlatSteps fs, int first, int end) {
   const unsigned items = g.count - round * kXcds < kXcds ? g.count - round * kXcds : kXcds;
   const int item = round * kXcds + in % items, split = in / items;
   if (g.tall())
-    flat_stages<MP, true>(g, fs, item, split, first, end, lds);
+    flat_stages<MP, true, (CHUNKS > 0)>(g, fs, item, split, first, end, lds);
   else
-    flat_stages<MP, false>(g, fs, item, split, first, end, lds);
+    flat_stages<MP, false, (CHUNKS > 0)>(g, fs, item, split, first, end, lds);
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -1403,7 +1419,7 @@ Shape shape_of(const sbp_matrices& g) {
   if (s.m <= 128) {
     const int64_t chunks = s.n / 64;
     s.splits = 1;
-    if (chunks > 4)
+    if (chunks > (s.m == 64 ? kStay64 : kStay128))
       while ((s.splits + 1) * (s.splits + 1) <= chunks && s.splits < 64) ++s.splits;
     s.summed = s.m == 128 && chunks >= 32;
     if (s.summed) s.splits = std::min<int64_t>(64, chunks / 4);
@@ -1429,6 +1445,7 @@ struct Chunk {
 
 // Bytes one piece takes, array by array (each 256-B aligned).
 int64_t half_bytes(const Shape& s, int64_t count) {
+  if (s.splits == 1) return 0;  // all in LDS
   return up(2 * count * (s.splits ? 2 * s.m * s.n : 3 * s.m * s.n + 2 * s.m * s.m), 256);
 }
 int64_t partial_bytes(const Shape& s, int64_t count) {
@@ -1714,7 +1731,8 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     }
     const bool at_once = c.cls == kFlat64 || c.cls == kFlat128;
     const bool wide = c.cls == kFlat128 || c.cls == kFlat128Steps || c.cls == kFlat128Summed;
-    auto kernel = wide ? ns_flat_kernel<128> : ns_flat_kernel<64>;
+    auto kernel = at_once ? (wide ? ns_flat_kernel<128, kStay128> : ns_flat_kernel<64, kStay64>)
+                          : (wide ? ns_flat_kernel<128, 0> : ns_flat_kernel<64, 0>);
     for (int stage = 0; stage <= hp.steps; stage += at_once ? hp.steps + 1 : 1) {
       hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBlock), 0, stream, gs, fs, stage,
                          at_once ? hp.steps + 1 : stage + 1);
