@@ -271,7 +271,9 @@ __host__ __device__ __forceinline__ int lower_tiles(int m, int T) {
   return side * (side + 1) / 2;
 }
 
-enum Mode { kGram, kPoly, kApply, kLast };  // kLast: apply, to the caller's matrices
+// kApplyLo: apply where S's remainder is read or stored; kLast: to the caller's
+// matrices, after the steps that keep one.
+enum Mode { kGram, kPoly, kApplyLo, kApply, kLast };
 
 // One T x T tile of C = P Q' per block of 4 waves (2 x 2, each a quarter, in
 // 32 x 32 MFMA tiles).  Slices of BK k elements go straight from memory to one
@@ -551,11 +553,11 @@ __device__ __forceinline__ void store_bits8(uint16_t* p, int left, bool vec, u32
   }
 }
 __device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
-  u32x4 w;
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  bf16x8 b;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    w[q] = sbp::bf16_rne(v[2 * q]) | (sbp::bf16_rne(v[2 * q + 1]) << 16);
-  store_bits8(p, left, vec, w);
+  for (int q = 0; q < 8; ++q) b[q] = static_cast<__bf16>(v[q]);  // nearest, ties to even
+  store_bits8(p, left, vec, __builtin_bit_cast(u32x4, b));
 }
 
 // Where (row, col) of the epilogue's binary32 slab is kept: 32 rows in
@@ -582,7 +584,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
   __shared__ __align__(16) char buf2[TL::kBuf];
   __shared__ __align__(16) char buf3[TL::kBuf];
   char* const buf[TL::NB] = {buf0, buf1, buf2, buf3};
-  constexpr bool kApplies = M == kApply || M == kLast;
+  constexpr bool kApplies = M == kApplyLo || M == kApply || M == kLast;
 
   // neighbouring tiles to one XCD: its L2 then holds the rows they share
   unsigned b = blockIdx.x;
@@ -647,8 +649,8 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
   const int tile_bytes = have * ccols * 2;
   const int row_off = gc < ccols ? (prow * ccols + gc) * 2 : tile_bytes;
   const auto add = buffer(M == kPoly ? g.A(0, item) + tile_at : S + tile_at, tile_bytes);
-  const auto rem = buffer(g.L(item) + tile_at, kApplies && st.lo_in ? tile_bytes : 0);
-  const auto rem_out = buffer(g.L(item) + tile_at, M == kApply && st.lo_out ? tile_bytes : 0);
+  const auto rem = buffer(g.L(item) + tile_at, st.lo_in ? tile_bytes : 0);  // else zeros
+  const auto rem_out = buffer(g.L(item) + tile_at, st.lo_out ? tile_bytes : 0);
   const auto out = buffer((M == kGram   ? g.A(0, item)
                            : M == kPoly ? g.A(1, item)
                                         : g.S(st.in ^ 1, item)) + tile_at, tile_bytes);
@@ -668,7 +670,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
     }
   };
   auto ask_rem = [&](int sl, int p) {
-    if constexpr (kApplies)
+    if constexpr (M == kApplyLo)
       re[p] = load16<f16x8>(rem, row_off + (sl * kSlab + p * kRowsAtOnce) * ccols * 2);
   };
   // (the large tile has no registers left for it)
@@ -786,12 +788,13 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
         }
       } else {
         // the diagonal's remainder multiplies S's row (wide) or column (tall)
-        const float d = dr[p] * fd;
+        const float d = fmaf(dr[p], fd, fa);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           float x = static_cast<float>(ad[p][q]);
-          if (st.lo_in) x = fmaf(static_cast<float>(re[p][q]), 1.0f / kScaleLo, x);
-          v[q] = fmaf(dc[q] + d, x, v[q] * fd);
+          if constexpr (M == kApplyLo)
+            x = fmaf(static_cast<float>(re[p][q]), 1.0f / kScaleLo, x);
+          v[q] = fmaf(tall ? dc[q] : d, x, v[q] * fd);
         }
       }
       if (sl + 1 < T / kSlab) {
@@ -805,7 +808,7 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
         store16(out, h, row_off + off);
-        if (M == kApply && st.lo_out) {
+        if constexpr (M == kApplyLo) {
           f16x8 l;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -1078,7 +1081,7 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
             const float acc = TALL ? D[u % DI][0][q * 4 + e] : D[0][u % DJ][q * 4 + e];
             const float v = fmaf(fmaf(d[e], cs.fd, cs.fa), y, acc * cs.fd);
             if constexpr (kLast) {
-              hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<uint16_t>(sbp::bf16_rne(v)));
+              hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<__bf16>(v));
             } else {
               hi[u][q][e] = static_cast<_Float16>(v);
               if constexpr (kLo)
@@ -1413,7 +1416,7 @@ Shape shape_of(const sbp_matrices& g) {
   s.m = up(std::min(g.rows, g.cols), kPad);
   s.n = up(std::max(g.rows, g.cols), kPad);
   const int64_t units = g.rows * ((g.cols + 511) / 512);
-  s.norm_blocks = std::max<int64_t>(1, std::min<int64_t>(kMaxNormBlocks, (units + 31) / 32));
+  s.norm_blocks = std::max<int64_t>(1, std::min<int64_t>(kMaxNormBlocks, (units + 7) / 8));
   s.splits = 0;
   s.summed = false;
   if (s.m <= 128) {
@@ -1573,6 +1576,8 @@ sbp_status launched(const char* who) {
   return SBP_OK;
 }
 
+static_assert(sizeof(Groups) + sizeof(FlatSteps) + 8 <= 4096, "kernel arguments");
+
 // How a product's tiles are launched: `tiles` of side T, then those of side 256
 // from `tiles` on as quarters.
 struct Launches {
@@ -1654,6 +1659,7 @@ sbp_status run_steps(const char* who, Groups& gs, const sbp_ns_hparams& hp, hipS
     launch_product<kGram>(gram, gs, st, stream);
     launch_product<kPoly>(gram, gs, st, stream);
     if (st.last) launch_product<kLast>(apply, gs, st, stream);
+    else if (st.lo_in || st.lo_out) launch_product<kApplyLo>(apply, gs, st, stream);
     else launch_product<kApply>(apply, gs, st, stream);
     const sbp_status rc = launched(who);
     if (rc != SBP_OK) return rc;

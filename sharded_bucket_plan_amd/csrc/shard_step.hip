@@ -79,6 +79,13 @@
 #ifndef SBP_NORM_INFLIGHT_KB
 #define SBP_NORM_INFLIGHT_KB 112
 #endif
+// The momentum pass has one state array and no more arithmetic than a few
+// multiplications; with two blocks per CU at R = 8 it is ahead of one (one 8M..64M
+// shard +2..7%, 15.5M elements 72 -> 61 us; with an accumulator at 100M -1.5%),
+// and at fewer peers within 1%.
+#ifndef SBP_MOMENTUM_INFLIGHT_KB
+#define SBP_MOMENTUM_INFLIGHT_KB 80
+#endif
 #ifndef SBP_XCD_CHUNK
 #define SBP_XCD_CHUNK 64
 #endif
@@ -557,13 +564,15 @@ momentum_kernel(Peers P, const float* __restrict__ acc, float scale, float* __re
 // ---- update: th' = th*decay - lr*u, bf16 emit --------------------------------
 // Reads 6 and writes 6 bytes per element: bound by HBM.  The fused step's
 // split lane map (two runs of 4 elements per lane), so each 16-byte fp32
-// access of a wave covers one contiguous kilobyte.
+// access of a wave covers one contiguous kilobyte; the tile order is the plain
+// passes' 64 tiles per XCD (218M elements: 447 us against 465 at the fused
+// step's 32, 15.5M: 28 us at both).
 __global__ void __launch_bounds__(kBlock)
 update_kernel(const uint16_t* __restrict__ u, float* __restrict__ master,
               uint16_t* __restrict__ pout, int64_t n, float decay, float lr) {
   const int64_t full = (n >> 3) << 3;
   const int wv = threadIdx.x >> 6, ln = threadIdx.x & 63;
-  const int64_t tile0 = static_cast<int64_t>(my_tile<SBP_FUSED_XCD_CHUNK>()) * (kBlock * 8);
+  const int64_t tile0 = static_cast<int64_t>(my_tile()) * (kBlock * 8);
   const int64_t e[2] = {tile0 + wv * 512 + ln * 4, tile0 + wv * 512 + 256 + ln * 4};
   // a run of 4 lies wholly inside or outside [0, full): full is a multiple of 8
   const bool ok[2] = {e[0] < full, e[1] < full};
@@ -1169,8 +1178,8 @@ sbp_status sbp_momentum_shard(const void* const* peers, int32_t R, const float* 
   return dispatch_r(R, [&](auto rc) -> sbp_status {
     constexpr int RR = decltype(rc)::value;
     auto go = [&](auto kernel) {
-      return launch(who, kernel, n, lane_bytes, stream, P, acc, scale, m, uo, n, mu, omm,
-                    nesterov != 0);
+      return launch_capped(who, kernel, n, lane_bytes, SBP_MOMENTUM_INFLIGHT_KB, 1, stream, P, acc,
+                           scale, m, uo, n, mu, omm, nesterov != 0);
     };
     if constexpr (RR == 0) {
       return go(momentum_kernel<0, true>);

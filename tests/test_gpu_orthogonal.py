@@ -2,6 +2,8 @@
 momentum and update bit for bit, Newton-Schulz against the iteration in 64
 bits, and the three as one step."""
 
+import itertools
+
 import numpy as np
 import pytest
 
@@ -176,7 +178,8 @@ def test_newton_schulz_shapes(shape, kind):
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 16])
-@pytest.mark.parametrize("shape", [(70, 200), (200, 70)])
+@pytest.mark.parametrize("shape", [(30, 90), (500, 20), (70, 200), (200, 70), (90, 700),
+                                   (150, 200), (200, 150)])
 def test_newton_schulz_steps(steps, shape):
     bits = _u(shape, 32)
     out, = sbp.newton_schulz([_bf(bits)], steps=steps)
@@ -275,8 +278,9 @@ def test_newton_schulz_strided_rows_and_untouched_gaps():
     """Rows further apart than they are long, in and out; what lies between
     the output's rows, before and behind it stays as it was."""
     import torch
-    for pad, lead in ((0, 1), (3, 5), (8, 8), (77, 0)):
-        B, r, c = 2, 65, 130
+    sizes = ((65, 130), (130, 65), (140, 150), (300, 7))
+    for (pad, lead), (r, c) in itertools.product(((0, 1), (3, 5), (8, 8), (77, 0)), sizes):
+        B = 2
         bits = _u((B, r, c), 35)
         x = torch.zeros(B * (r + 1) * (c + pad) + lead + 9, dtype=torch.bfloat16, device=H.dev())
         shape, stride = (B, r, c), ((r + 1) * (c + pad), c + pad, 1)
@@ -289,22 +293,28 @@ def test_newton_schulz_strided_rows_and_untouched_gaps():
         got, = sbp.newton_schulz([view], out=[out])
         assert got.data_ptr() == out.data_ptr()
         torch.cuda.synchronize()
-        _check_ns(out, bits, what=f"pad {pad} lead {lead}")
-        assert bool((o[mask] == 7.0).all()), (pad, lead)
+        _check_ns(out, bits, what=f"pad {pad} lead {lead} {r}x{c}")
+        assert bool((o[mask] == 7.0).all()), (pad, lead, r, c)
+
+
+def _in_place_blocks(r, k):
+    import torch
+    bits = _u((r, 3 * k), 36)
+    w = _bf(bits).clone()
+    blocks = [w[:, k * i:k * (i + 1)] for i in range(3)]
+    sbp.newton_schulz(blocks, out=blocks)
+    torch.cuda.synchronize()
+    for i in range(3):
+        _check_ns(w[:, k * i:k * (i + 1)], np.ascontiguousarray(bits[:, k * i:k * (i + 1)]),
+                  what=f"block {i} of {r}x{k}")
 
 
 def test_newton_schulz_in_place_and_column_blocks():
     """In place, on three column blocks of one fused weight, and on heads that
     lie side by side in the rows."""
     import torch
-    bits = _u((48, 3 * 40), 36)
-    w = _bf(bits).clone()
-    blocks = [w[:, 40 * i:40 * (i + 1)] for i in range(3)]
-    sbp.newton_schulz(blocks, out=blocks)
-    torch.cuda.synchronize()
-    for i in range(3):
-        _check_ns(w[:, 40 * i:40 * (i + 1)], np.ascontiguousarray(bits[:, 40 * i:40 * (i + 1)]),
-                  what=f"block {i}")
+    for r, k in ((48, 40), (300, 140)):
+        _in_place_blocks(r, k)
     bits = _u((72, 4 * 16), 37)
     w = _bf(bits).clone()
     heads = w.view(72, 4, 16).permute(1, 0, 2)
@@ -327,16 +337,18 @@ def test_newton_schulz_broadcast_input():
 
 
 @pytest.mark.parametrize("size", [1e-37, 1e-20, 1e-3, 1e10, 1e36])
-def test_newton_schulz_any_size_of_norm(size):
+@pytest.mark.parametrize("shape", [(60, 100), (60, 700), (150, 140)])
+def test_newton_schulz_any_size_of_norm(size, shape):
     """The direction does not depend on U's size while the norm is above eps."""
-    bits = _u((60, 100), 39, size=size)
+    bits = _u(shape, 39, size=size)
     out, = sbp.newton_schulz([_bf(bits)], eps=1e-38)
     _check_ns(out, bits, eps=1e-38, what=f"size {size}")
 
 
 @pytest.mark.parametrize("size", [1e-30, 1e-14, 1e-9])
-def test_newton_schulz_norm_below_eps(size):
-    bits = _u((20, 30), 41, size=size)
+@pytest.mark.parametrize("shape", [(20, 30), (20, 400), (130, 140)])
+def test_newton_schulz_norm_below_eps(size, shape):
+    bits = _u(shape, 41, size=size / shape[1])
     out, = sbp.newton_schulz([_bf(bits)])
     U = OS.bf16_to_f32(bits).astype(np.float64)
     want = OS.newton_schulz(U, 5, sbp.NS_COEFS)
@@ -352,7 +364,7 @@ def test_newton_schulz_zero_nan_and_infinity():
     """Zeros give zeros; a NaN or an infinity fills its own matrix with NaN and
     leaves its neighbours' bits as they are without it."""
     import torch
-    for shape in ((40, 70), (70, 40), (1, 3)):
+    for shape in ((40, 70), (70, 40), (1, 3), (50, 600), (2200, 100), (140, 170), (170, 140)):
         bits = _u((5,) + shape, 42)
         bits[1] = 0
         clean, = sbp.newton_schulz([_bf(bits)])
@@ -378,18 +390,26 @@ def test_newton_schulz_empty():
 
 def test_newton_schulz_same_bits_every_time():
     import torch
-    x = _bf(_u((3, 200, 333), 44))
-    first, = sbp.newton_schulz([x])
-    for _ in range(3):
-        again, = sbp.newton_schulz([x])
-        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+    for shape in ((3, 200, 333), (3, 100, 2400), (3, 50, 90)):
+        x = _bf(_u(shape, 44))
+        first, = sbp.newton_schulz([x])
+        for _ in range(3):
+            again, = sbp.newton_schulz([x])
+            assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+def test_newton_schulz_one_input_twice():
+    import torch
+    x = _bf(_u((150, 160), 48))
+    a, b = sbp.newton_schulz([x, x])
+    assert a.data_ptr() != b.data_ptr() and torch.equal(a, b)
 
 
 def test_newton_schulz_dirty_workspace_and_streams():
     """A workspace full of NaN, and a call on a stream that is not the current
     one, with and without a workspace of its own."""
     import torch
-    bits = _u((2, 100, 150), 45)
+    bits = _u((2, 150, 250), 45)
     x = _bf(bits)
     want, = sbp.newton_schulz([x])
     ws = torch.full((sbp.newton_schulz_workspace([x]) // 2,), float("nan"), dtype=torch.float16,
@@ -409,7 +429,7 @@ def test_newton_schulz_captured_and_replayed():
     """Two graphs with a workspace each, replayed in turn with eager calls
     between; inputs change from replay to replay."""
     import torch
-    xs = [_bf(_u((2, 80, 120), 46)), _bf(_u((130, 64), 47))]
+    xs = [_bf(_u((2, 150, 250), 46)), _bf(_u((2300, 70), 47)), _bf(_u((3, 20, 30), 48))]
     outs = [torch.empty_like(x) for x in xs]
     ws = [torch.empty(sbp.newton_schulz_workspace([x]), dtype=torch.uint8, device=H.dev())
           for x in xs]
