@@ -276,16 +276,17 @@ __host__ __device__ __forceinline__ int lower_tiles(int m, int T) {
 enum Mode { kGram, kPoly, kApplyLo, kApply, kLast };
 
 // One T x T tile of C = P Q' per block of 4 waves (2 x 2, each a quarter, in
-// 32 x 32 MFMA tiles).  Slices of BK k elements go straight from memory to one
-// of four LDS buffers, three slices ahead of the one being multiplied.
+// 16 x 16 MFMA tiles, so that a slice of 32 k is one round of products).  Slices
+// of BK k elements go straight from memory to one of four LDS buffers, three
+// slices ahead of the one being multiplied.
 template <int T_, int BK_>
 struct Tile {
   static constexpr int T = T_, BK = BK_;
   static constexpr int NB = 4;
   static constexpr int kHalf = T * BK * 2;  // one operand's slice, bytes
   static constexpr int kBuf = 2 * kHalf;    // P, then Q
-  static constexpr int kSub = T / 64;       // 32 x 32 tiles per wave and side
-  static constexpr int kPhases = BK / 16;
+  static constexpr int kSub = T / 32;       // 16 x 16 tiles per wave and side
+  static constexpr int kPhases = BK / 32;
   static constexpr int kLoads = kHalf / 4096;  // per operand, slice and lane
   static_assert(32 * T * 4 <= kBuf, "half the epilogue's slab fits one buffer");
 };
@@ -306,32 +307,21 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t to, V v, int off)
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, off, 0, 0);
 }
 
-// This wave's share of one operand's slice, `bytes` from `from`.
-template <int LOADS>
-__device__ __forceinline__ void stage(char* buf, const char* from, int bytes, int wave, int voff,
-                                      int round_bytes) {
-  const __amdgpu_buffer_rsrc_t rows = buffer(from, bytes);
-#pragma unroll
-  for (int r = 0; r < LOADS; ++r)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rows, (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16,
-        voff + r * round_bytes, 0, 0, 0);
-}
-
 // One operand of a tile.  Along: the matrix's rows r0 .. are the operand's
 // rows, and a slice is BK consecutive elements of each; LDS keeps a row's
 // 16-byte pieces rotated by row.  Across: the matrix's columns r0 .. are the
 // operand's rows, and a slice is BK rows of T elements; LDS keeps a row's
-// 64-byte pieces rotated by row, and the reads transpose.  Both rotations come
+// 32-byte pieces rotated by row, and the reads transpose.  Both rotations come
 // from the lanes' global addresses and spread the reads over the banks.
 // Rows past the matrix read as zero or as a neighbour: they only reach
 // results that are not stored.
 template <int T, int BK, bool ACROSS>
 struct Operand {
-  static constexpr int kSub = T / 64, kPhases = BK / 16;
+  static constexpr int kSub = T / 32, kPhases = BK / 32;
   const char* from;  // next slice to load
   int64_t step;
-  int bytes, voff, round_bytes;
+  int bytes, round_bytes;
+  int voff[2];                       // of even and odd rounds
   int at;                            // LDS offset of this lane's first fragment
   int off[ACROSS ? kSub : kPhases];  // further offset by sub-tile or phase
 
@@ -342,14 +332,17 @@ struct Operand {
       from = reinterpret_cast<const char*>(mat + r0);
       step = static_cast<int64_t>(BK) * ld * 2;
       bytes = (BK * ld - r0) * 2;
-      const int row = wave * (64 / kLanes) + lane / kLanes;
-      const int piece = lane % kLanes;
-      voff = row * ld * 2 + ((((piece >> 2) ^ turn(row)) << 2) | (piece & 3)) * 16;
-      round_bytes = 4 * (64 / kLanes) * ld * 2;
-      const int k = (lane >> 5) * 8 + ((lane >> 2) & 3);  // of this lane's address
-      at = k * (T * 2) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+      constexpr int kRows = 64 / kLanes;  // per wave and round
 #pragma unroll
-      for (int i = 0; i < kSub; ++i) off[i] = ((wrow / 32 + i) ^ turn(k)) * 64;
+      for (int r = 0; r < 2; ++r) {
+        const int row = (r * 4 + wave) * kRows + lane / kLanes;
+        voff[r] = row * ld * 2 + (((lane % kLanes) * 16) ^ (turn(row) * 32)) - r * 4 * kRows * ld * 2;
+      }
+      round_bytes = 4 * (64 / kLanes) * ld * 2;
+      const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);  // of this lane's address
+      at = k * (T * 2) + (lane & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) off[i] = ((wrow / 16 + i) ^ turn(k)) * 32;
     } else {
       constexpr int kLanes = BK / 8;
       from = reinterpret_cast<const char*>(mat + static_cast<int64_t>(r0) * ld);
@@ -357,34 +350,47 @@ struct Operand {
       const int have = rows - r0 < T ? rows - r0 : T;
       bytes = have * ld * 2;
       const int row = wave * (64 / kLanes) + lane / kLanes;
-      voff = row * ld * 2 + ((lane % kLanes) ^ turn(row)) * 16;
+      voff[0] = voff[1] = row * ld * 2 + ((lane % kLanes) ^ turn(row)) * 16;
       round_bytes = 4 * (64 / kLanes) * ld * 2;
-      at = (wrow + (lane & 31)) * (BK * 2);
+      at = (wrow + (lane & 15)) * (BK * 2);
 #pragma unroll
-      for (int p = 0; p < kPhases; ++p) off[p] = ((p * 2 + (lane >> 5)) ^ turn(lane)) * 16;
+      for (int p = 0; p < kPhases; ++p) off[p] = ((p * 4 + (lane >> 4)) ^ turn(lane & 15)) * 16;
     }
   }
-  // The rotation of a row; rows that differ by 32 (along) or 4 (across) agree.
+  // The rotation of a row.  Along, rows that differ by 16 agree; across, those
+  // that differ by 4 (of a group of 8) and by 16.
   static __device__ __forceinline__ int turn(int row) {
-    if constexpr (ACROSS) return T >= 128 ? row & 3 : (row >> 1) & 1;
-    else return BK == 32 ? (row >> 2) & 3 : row & 7;
+    if constexpr (ACROSS)
+      return T >= 128 ? (row & 3) | ((row >> 3) & 1) << 2 : ((row >> 1) & 1) | ((row >> 3) & 1) << 1;
+    else
+      return BK == 32 ? ((row >> 1) ^ (row >> 2)) & 2 | ((row >> 3) ^ (row >> 1)) & 1 : row & 7;
+  }
+  __device__ __forceinline__ void load_round(char* buf, int wave, int r) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        buffer(from, bytes),
+        (__attribute__((address_space(3))) void*)(buf + (r * 4 + wave) * 1024), 16,
+        voff[r & 1] + r * round_bytes, 0, 0, 0);
   }
   // Along, the last rows' slices end before `bytes` does by what is consumed.
-  __device__ __forceinline__ void load(char* buf, int wave) {
-    stage<T * BK * 2 / 4096>(buf, from, bytes, wave, voff, round_bytes);
+  __device__ __forceinline__ void advance() {
     from += step;
     if constexpr (!ACROSS) bytes -= BK * 2;
+  }
+  __device__ __forceinline__ void load(char* buf, int wave) {
+#pragma unroll
+    for (int r = 0; r < T * BK * 2 / 4096; ++r) load_round(buf, wave, r);
+    advance();
   }
   __device__ __forceinline__ f16x8 read(const char* buf, int phase, int i) const {
     if constexpr (ACROSS) {
       typedef __fp16 h4 __attribute__((__vector_size__(8)));
       typedef __attribute__((address_space(3))) h4* lds_h4;
-      const char* p = buf + at + off[i] + phase * 16 * (T * 2);
+      const char* p = buf + at + off[i] + phase * 32 * (T * 2);
       const h4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)p);
       const h4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_h4)(p + 4 * (T * 2)));
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *reinterpret_cast<const f16x8*>(buf + at + off[phase] + i * 32 * (BK * 2));
+      return *reinterpret_cast<const f16x8*>(buf + at + off[phase] + i * 16 * (BK * 2));
     }
   }
 };
@@ -395,7 +401,7 @@ struct Frags {
 };
 
 template <typename TL>
-using Acc = f32x16[TL::kSub][TL::kSub];
+using Acc = f32x4[TL::kSub][TL::kSub];
 
 template <typename TL>
 __device__ __forceinline__ void multiply(const Frags<TL>& f, Acc<TL>& acc) {
@@ -403,7 +409,32 @@ __device__ __forceinline__ void multiply(const Frags<TL>& f, Acc<TL>& acc) {
   for (int i = 0; i < TL::kSub; ++i)
 #pragma unroll
     for (int j = 0; j < TL::kSub; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+}
+
+// The same for one accumulator, in its registers: at the large tile all 256 are
+// taken, and the compiler, free to give a product another place than its
+// summand, moved them about between the products (13% of apply).  It does not
+// see these as matrix instructions, so what it would see to is done by hand:
+// the operands have been waited for, an accumulator is used again 64 products
+// later, and settle() stands between the products and what else writes or reads
+// the accumulators.
+template <bool FIRST>
+__device__ __forceinline__ void multiply_in_place(f32x4& c, f16x8 p, f16x8 q) {
+  if constexpr (FIRST)
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=a"(c) : "v"(p), "v"(q));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
+}
+template <typename TL>
+__device__ __forceinline__ void settle(Acc<TL>& acc) {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < TL::kSub; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::kSub; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Order of a phase's instructions: MFMAs, LDS reads and loads to LDS in turn,
@@ -411,12 +442,18 @@ __device__ __forceinline__ void multiply(const Frags<TL>& f, Acc<TL>& acc) {
 template <typename TL, int READS, int LOADS>
 __device__ __forceinline__ void interleave() {
   constexpr int mfmas = TL::kSub * TL::kSub;
-  constexpr int r1 = (READS + mfmas - 1) / mfmas, l1 = (LOADS + mfmas - 1) / mfmas;
 #pragma unroll
   for (int i = 0; i < mfmas; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i * r1 < READS) __builtin_amdgcn_sched_group_barrier(0x100, r1, 0);
-    if (i * l1 < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, l1, 0);
+    constexpr int kOver = mfmas > 8 ? mfmas * 3 / 4 : mfmas;
+    const int a = i < kOver ? i : kOver, z = i + 1 < kOver ? i + 1 : kOver;
+    const int r = z * READS / kOver - a * READS / kOver, l = z * LOADS / kOver - a * LOADS / kOver;
+    if (r == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (r == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (r == 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+    if (r == 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+    if (l == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    if (l == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
 }
@@ -428,6 +465,13 @@ __device__ __forceinline__ void slice_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | 0x70);
   asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// This wave's LDS reads are done.
+__device__ __forceinline__ void lds_wait() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -443,7 +487,7 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
                                         Operand<TL::T, TL::BK, PX>& P,
                                         Operand<TL::T, TL::BK, QX>& Q, int slices, int wave,
                                         Acc<TL>& acc, F&& early) {
-  constexpr int NB = TL::NB, N = TL::kPhases, L = TL::kLoads;
+  constexpr int T = TL::T, NB = TL::NB, N = TL::kPhases, L = TL::kLoads;
   constexpr int kReads = TL::kSub * ((PX ? 2 : 1) + (QX ? 2 : 1));
   Frags<TL> f[2];
   auto load = [&](char* to) {
@@ -456,34 +500,63 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
 #pragma unroll
     for (int j = 0; j < TL::kSub; ++j) to.q[j] = Q.read(from + TL::kHalf, phase, j);
   };
-  // One slice: it is in `cur`, its first fragments in f[0].  The barrier sits
+  // One slice: it is in buf[i], its first fragments in f[..].  The barrier sits
   // before the last multiply, so that each multiply hides the next one's reads.
-  // LOAD: the slice NB - 1 further on is loaded into `to`; LEFT: loads that may
-  // still be under way when the next slice has to be there (-1: no next one).
-  auto slice = [&](const char* cur, const char* nxt, char* to, auto load_c, auto left_c) {
+  // LOAD: the slice NB - 1 further on is loaded; LEFT: loads that may still be
+  // under way when the next slice has to be there (-1: no next one).
+  auto slice = [&](int i, auto load_c, auto left_c, auto first_c) {
+    constexpr bool kFirst = decltype(first_c)::value;
     constexpr bool kLoad = decltype(load_c)::value;
     constexpr int kLeft = decltype(left_c)::value;
+    const int first = N == 1 ? i & 1 : 0;
+    char* const to = buf[(i + NB - 1) % NB];
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (T == 256) {
+      if constexpr (kLeft >= 0) slice_barrier<kLeft>();
+      else lds_wait();
+      constexpr int kSub = TL::kSub;
+#pragma unroll
+      for (int t = 0; t < kSub * kSub; ++t) {
+        multiply_in_place<kFirst>(acc[t / kSub][t % kSub], f[first].p[t / kSub], f[first].q[t % kSub]);
+        if (kLeft >= 0 && t % 3 == 0 && t / 3 < 2 * kSub) {
+          const int c = t / 3;
+          if (c < kSub) f[first ^ 1].p[c] = P.read(buf[(i + 1) % NB], 0, c);
+          else f[first ^ 1].q[c - kSub] = Q.read(buf[(i + 1) % NB] + TL::kHalf, 0, c - kSub);
+        }
+        if (kLoad && t % 6 == 2 && t / 6 < 2 * L) {
+          const int r = t / 6;
+          if (r < L) P.load_round(to, wave, r);
+          else Q.load_round(to + TL::kHalf, wave, r - L);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (kLoad) {
+        P.advance();
+        Q.advance();
+      }
+      return;
+    }
 #pragma unroll
     for (int ph = 0; ph < N - 1; ++ph) {
       if (kLoad && ph == 0) P.load(to, wave);
-      read(cur, ph + 1, f[(ph + 1) & 1]);
+      read(buf[i], ph + 1, f[(ph + 1) & 1]);
       multiply<TL>(f[ph & 1], acc);
       if (kLoad && ph == 0) interleave<TL, kReads, TL::kLoads>();
       else interleave<TL, kReads, 0>();
     }
     if constexpr (kLeft >= 0) {
       slice_barrier<kLeft>();
+      if constexpr (kLoad && N == 1) P.load(to, wave);
       if constexpr (kLoad) Q.load(to + TL::kHalf, wave);
-      read(nxt, 0, f[0]);
+      read(buf[(i + 1) % NB], 0, f[N == 1 ? first ^ 1 : 0]);
     }
-    multiply<TL>(f[1], acc);
-    interleave<TL, kLeft >= 0 ? kReads : 0, kLoad ? TL::kLoads : 0>();
+    multiply<TL>(f[N == 1 ? first : 1], acc);
+    interleave<TL, kLeft >= 0 ? kReads : 0, kLoad ? (N == 1 ? 2 : 1) * TL::kLoads : 0>();
   };
   constexpr std::true_type kYes{};
   constexpr std::false_type kNo{};
-  // two slices under way, and the first half of a third
-  constexpr std::integral_constant<int, 3 * L> kSteady{};
+  // one slice under way, and the first half of another
+  constexpr std::integral_constant<int, (N == 1 ? 2 : 3) * L> kSteady{};
   constexpr std::integral_constant<int, 2 * L + EARLY> kOne{};
   constexpr std::integral_constant<int, EARLY> kNone{};
   constexpr std::integral_constant<int, 0> kDrain{};
@@ -495,22 +568,23 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
   // whose own waits in the loop would else provide for the other way in).
   constexpr bool kEven = TL::BK == 32;  // both padded sides are multiples of 64
   const int rest = static_cast<unsigned>(slices) % NB;
-  if (slices < NB) {
+  if (!kEven && slices < NB) {
 #pragma unroll
     for (int r = kEven ? 2 : 1; r < NB; ++r) {  // r slices
       if (slices != r) continue;
 #pragma unroll
       for (int i = NB - r; i < NB; ++i) load(buf[i]);
       slice_barrier<0>();
-      read(buf[NB - r], 0, f[0]);
+      read(buf[NB - r], 0, f[N == 1 ? r & 1 : 0]);
 #pragma unroll
-      for (int i = NB - r; i < NB - 1; ++i) slice(buf[i], buf[i + 1], nullptr, kNo, kDrain);
+      for (int i = NB - r; i < NB - 1; ++i) slice(i, kNo, kDrain, kNo);
     }
     early();
   } else {
     if (rest == 0) {
 #pragma unroll
       for (int i = 0; i < NB - 1; ++i) load(buf[i]);
+      if constexpr (T == 256) settle<TL>(acc);
       slice_barrier<4 * L>();
       read(buf[0], 0, f[0]);
     } else {
@@ -520,24 +594,26 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
 #pragma unroll
         for (int i = 0; i < NB - 1; ++i) load(buf[(NB - r + i) % NB]);
         slice_barrier<4 * L>();
-        read(buf[NB - r], 0, f[0]);
+        read(buf[NB - r], 0, f[N == 1 ? r & 1 : 0]);
 #pragma unroll
-        for (int i = NB - r; i < NB; ++i)
-          slice(buf[i], buf[(i + 1) % NB], buf[(i + NB - 1) % NB], kYes, kSteady);
+        for (int i = NB - r; i < NB; ++i) {
+          if (i == NB - r) slice(i, kYes, kSteady, kYes);
+          else slice(i, kYes, kSteady, kNo);
+        }
       }
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     }
     for (int s = slices / NB; s > 1; --s) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
-        slice(buf[i], buf[(i + 1) % NB], buf[(i + NB - 1) % NB], kYes, kSteady);
+      for (int i = 0; i < NB; ++i) slice(i, kYes, kSteady, kNo);
     }
-    slice(buf[0], buf[1], buf[NB - 1], kYes, kSteady);
+    slice(0, kYes, kSteady, kNo);
     early();
-    slice(buf[1], buf[2], nullptr, kNo, kOne);
-    slice(buf[2], buf[3], nullptr, kNo, kNone);
+    slice(1, kNo, kOne, kNo);
+    slice(2, kNo, kNone, kNo);
   }
-  slice(buf[3], nullptr, nullptr, kNo, kEnd);
+  slice(3, kNo, kEnd, kNo);
+  if constexpr (T == 256) settle<TL>(acc);
 }
 
 // Up to 8 consecutive bf16 values of a row of the caller's output.
@@ -568,7 +644,8 @@ __device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, cons
 template <typename TL>
 __device__ __forceinline__ float* slab_at(char* lo, char* hi, int row, int col) {
   float* half = reinterpret_cast<float*>(row & 32 ? hi : lo);
-  const int turned = col ^ (((row >> 3) & 7) << 3) ^ (((row >> 2) & 1) << 5);
+  const int turned =
+      col ^ (((row >> 3) & 1) << 4) ^ (((row >> 4) & 1) << 3) ^ ((((row >> 5) ^ (row >> 2)) & 1) << 5);
   return half + (row & 31) * TL::T + turned;
 }
 
@@ -748,14 +825,14 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
       if (part != sl) continue;
 #pragma unroll
       for (int i = 0; i < TL::kSub; ++i) {
-        const int rb = wr * TL::kSub + i;  // 32-row block of the tile
-        if (rb / (kSlab / 32) == part) {
+        const int rb = wr * TL::kSub + i;  // 16-row block of the tile
+        if (rb / (kSlab / 16) == part) {
 #pragma unroll
           for (int j = 0; j < TL::kSub; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int row = rb * 32 % kSlab + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-              const int col = wc * (T / 2) + j * 32 + (lane & 31);
+            for (int e = 0; e < 4; ++e) {
+              const int row = rb * 16 % kSlab + 4 * (lane >> 4) + e;
+              const int col = wc * (T / 2) + j * 16 + (lane & 15);
               *slab_at<TL>(buf0, buf1, row, col) = acc[i][j][e];
             }
         }
