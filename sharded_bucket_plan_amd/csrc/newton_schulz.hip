@@ -276,13 +276,18 @@ __host__ __device__ __forceinline__ int lower_tiles(int m, int T) {
 enum Mode { kGram, kPoly, kApplyLo, kApply, kLast };
 
 // One T x T tile of C = P Q' per block of 4 waves (2 x 2, each a quarter, in
-// 16 x 16 MFMA tiles, so that a slice of 32 k is one round of products).  Slices
-// of BK k elements go straight from memory to one of four LDS buffers, three
-// slices ahead of the one being multiplied.
-template <int T_, int BK_>
+// 16 x 16 MFMA tiles, so that 32 k are one round of products).  Slices of BK k
+// elements go straight from memory to one of NB LDS buffers, NB slices ahead.
+// Rows along k come by lines of 128 bytes, which 64 elements use whole; with 32
+// each line passes the CU's cache twice (tile 128, half a round of 256-tiles of
+// k = 4096: 106 us, with 64 80 us).  At the largest tile two slices of 64 are all
+// of LDS, and their loads come in bursts that are not hidden where k is long
+// (three of 14336 x 4096: gram 707 us, with four slices of 32 613; apply 1200
+// and 1225), so it takes 32.
+template <int T_>
 struct Tile {
-  static constexpr int T = T_, BK = BK_;
-  static constexpr int NB = 4;
+  static constexpr int T = T_, BK = T == 256 ? 32 : 64;
+  static constexpr int NB = T == 128 ? 2 : 4;  // slices in LDS
   static constexpr int kHalf = T * BK * 2;  // one operand's slice, bytes
   static constexpr int kBuf = 2 * kHalf;    // P, then Q
   static constexpr int kSub = T / 32;       // 16 x 16 tiles per wave and side
@@ -483,12 +488,14 @@ __device__ __forceinline__ void lds_barrier() {
 // acc = P Q' over `slices` slices.  early() issues EARLY loads of the
 // epilogue's, once all slices are loaded or under way.
 template <typename TL, int EARLY, bool PX, bool QX, typename F>
-__device__ __forceinline__ void product(char* const (&buf)[TL::NB],
+__device__ __forceinline__ void product(char* (&buf)[TL::NB],
                                         Operand<TL::T, TL::BK, PX>& P,
                                         Operand<TL::T, TL::BK, QX>& Q, int slices, int wave,
                                         Acc<TL>& acc, F&& early) {
-  constexpr int T = TL::T, NB = TL::NB, N = TL::kPhases, L = TL::kLoads;
-  constexpr int kReads = TL::kSub * ((PX ? 2 : 1) + (QX ? 2 : 1));
+  constexpr int T = TL::T, NB = TL::NB, N = TL::kPhases, L = TL::kLoads, kSub = TL::kSub;
+  constexpr int kReads = kSub * ((PX ? 2 : 1) + (QX ? 2 : 1));
+  constexpr std::true_type kYes{};
+  constexpr std::false_type kNo{};
   Frags<TL> f[2];
   auto load = [&](char* to) {
     P.load(to, wave);
@@ -496,32 +503,25 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
   };
   auto read = [&](const char* from, int phase, Frags<TL>& to) {
 #pragma unroll
-    for (int i = 0; i < TL::kSub; ++i) to.p[i] = P.read(from, phase, i);
+    for (int i = 0; i < kSub; ++i) to.p[i] = P.read(from, phase, i);
 #pragma unroll
-    for (int j = 0; j < TL::kSub; ++j) to.q[j] = Q.read(from + TL::kHalf, phase, j);
+    for (int j = 0; j < kSub; ++j) to.q[j] = Q.read(from + TL::kHalf, phase, j);
   };
-  // One slice: it is in buf[i], its first fragments in f[..].  The barrier sits
-  // before the last multiply, so that each multiply hides the next one's reads.
-  // LOAD: the slice NB - 1 further on is loaded; LEFT: loads that may still be
-  // under way when the next slice has to be there (-1: no next one).
-  auto slice = [&](int i, auto load_c, auto left_c, auto first_c) {
-    constexpr bool kFirst = decltype(first_c)::value;
-    constexpr bool kLoad = decltype(load_c)::value;
-    constexpr int kLeft = decltype(left_c)::value;
-    const int first = N == 1 ? i & 1 : 0;
-    char* const to = buf[(i + NB - 1) % NB];
-    __builtin_amdgcn_sched_barrier(0);
+  // Products of f[h], under which the other half's fragments are read (READ:
+  // phase `phase` of `from`) and a slice is loaded into `to` (LOAD).  The first
+  // ones (FIRST) start the sums.
+  auto multiplies = [&](int h, const char* from, int phase, char* to, auto read_c, auto load_c,
+                        auto first_c) {
+    constexpr bool kRead = decltype(read_c)::value, kLoad = decltype(load_c)::value;
     if constexpr (T == 256) {
-      if constexpr (kLeft >= 0) slice_barrier<kLeft>();
-      else lds_wait();
-      constexpr int kSub = TL::kSub;
 #pragma unroll
       for (int t = 0; t < kSub * kSub; ++t) {
-        multiply_in_place<kFirst>(acc[t / kSub][t % kSub], f[first].p[t / kSub], f[first].q[t % kSub]);
-        if (kLeft >= 0 && t % 3 == 0 && t / 3 < 2 * kSub) {
+        multiply_in_place<decltype(first_c)::value>(acc[t / kSub][t % kSub], f[h].p[t / kSub],
+                                                    f[h].q[t % kSub]);
+        if (kRead && t % 3 == 0 && t / 3 < 2 * kSub) {
           const int c = t / 3;
-          if (c < kSub) f[first ^ 1].p[c] = P.read(buf[(i + 1) % NB], 0, c);
-          else f[first ^ 1].q[c - kSub] = Q.read(buf[(i + 1) % NB] + TL::kHalf, 0, c - kSub);
+          if (c < kSub) f[h ^ 1].p[c] = P.read(from, phase, c);
+          else f[h ^ 1].q[c - kSub] = Q.read(from + TL::kHalf, phase, c - kSub);
         }
         if (kLoad && t % 6 == 2 && t / 6 < 2 * L) {
           const int r = t / 6;
@@ -534,66 +534,70 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
         P.advance();
         Q.advance();
       }
-      return;
+    } else {
+      if constexpr (kLoad) load(to);
+      if constexpr (kRead) read(from, phase, f[h ^ 1]);
+      multiply<TL>(f[h], acc);
+      interleave<TL, kRead ? kReads : 0, kLoad ? 2 * L : 0>();
     }
-#pragma unroll
-    for (int ph = 0; ph < N - 1; ++ph) {
-      if (kLoad && ph == 0) P.load(to, wave);
-      read(buf[i], ph + 1, f[(ph + 1) & 1]);
-      multiply<TL>(f[ph & 1], acc);
-      if (kLoad && ph == 0) interleave<TL, kReads, TL::kLoads>();
-      else interleave<TL, kReads, 0>();
-    }
+  };
+  // One slice, in buf[i], its first fragments in f[0] (of slices of one phase:
+  // of odd ones in f[1]).  Before its last phase all of it is in registers and
+  // the next slice has to be there (but for LEFT newer loads; -1: no next one),
+  // so its buffer is loaded anew (LOAD) with the slice NB further on.
+  auto slice = [&](int i, auto load_c, auto left_c, auto first_c) {
+    constexpr int kLeft = decltype(left_c)::value;
+    const int h = N == 1 ? i & 1 : 1;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (N == 2) multiplies(0, buf[i], 1, nullptr, kYes, kNo, first_c);
+    std::conditional_t<N == 1, decltype(first_c), std::false_type> starts;
     if constexpr (kLeft >= 0) {
       slice_barrier<kLeft>();
-      if constexpr (kLoad && N == 1) P.load(to, wave);
-      if constexpr (kLoad) Q.load(to + TL::kHalf, wave);
-      read(buf[(i + 1) % NB], 0, f[N == 1 ? first ^ 1 : 0]);
+      multiplies(h, buf[(i + 1) % NB], 0, buf[i], kYes, load_c, starts);
+    } else {
+      lds_wait();
+      multiplies(h, nullptr, 0, nullptr, kNo, kNo, starts);
     }
-    multiply<TL>(f[N == 1 ? first : 1], acc);
-    interleave<TL, kLeft >= 0 ? kReads : 0, kLoad ? (N == 1 ? 2 : 1) * TL::kLoads : 0>();
   };
-  constexpr std::true_type kYes{};
-  constexpr std::false_type kNo{};
-  // one slice under way, and the first half of another
-  constexpr std::integral_constant<int, (N == 1 ? 2 : 3) * L> kSteady{};
-  constexpr std::integral_constant<int, 2 * L + EARLY> kOne{};
-  constexpr std::integral_constant<int, EARLY> kNone{};
-  constexpr std::integral_constant<int, 0> kDrain{};
-  static_assert(4 * L < 64 && 2 * L + EARLY < 64, "what vmcnt can count");
-  constexpr std::integral_constant<int, -1> kEnd{};
-  // The last slice is in the last buffer, so that there is one way into the
-  // loop's rounds of NB slices and one way out; a number that is no multiple of
-  // NB starts further on, and drains its loads once (known to the compiler,
-  // whose own waits in the loop would else provide for the other way in).
-  constexpr bool kEven = TL::BK == 32;  // both padded sides are multiples of 64
-  const int rest = static_cast<unsigned>(slices) % NB;
-  if (!kEven && slices < NB) {
-#pragma unroll
-    for (int r = kEven ? 2 : 1; r < NB; ++r) {  // r slices
-      if (slices != r) continue;
-#pragma unroll
-      for (int i = NB - r; i < NB; ++i) load(buf[i]);
-      slice_barrier<0>();
-      read(buf[NB - r], 0, f[N == 1 ? r & 1 : 0]);
-#pragma unroll
-      for (int i = NB - r; i < NB - 1; ++i) slice(i, kNo, kDrain, kNo);
+  // the last slices, of which the last is in the last buffer
+  auto tail = [&](auto self, auto i_c) {
+    constexpr int i = decltype(i_c)::value;
+    if constexpr (i < NB) {
+      constexpr int kLeft = i == NB - 1 ? -1 : (NB - 2 - i) * 2 * L + EARLY;
+      slice(i, kNo, std::integral_constant<int, kLeft>{}, kNo);
+      self(self, std::integral_constant<int, i + 1>{});
     }
+  };
+  constexpr std::integral_constant<int, (NB - 2) * 2 * L> kSteady{};
+  constexpr std::integral_constant<int, (NB - 1) * 2 * L> kStart{};
+  static_assert(NB * 2 * L + EARLY < 64, "what vmcnt can count");
+  // There is one way into the loop's rounds of NB slices and one way out; a
+  // number that is no multiple of NB starts further on, and drains its loads
+  // once (known to the compiler, whose own waits in the loop would else provide
+  // for the other way in).  At least 3 slices: both padded sides are multiples
+  // of 64 and more than 128.
+  const int rest = static_cast<unsigned>(slices) % NB;
+  if (NB > 192 / TL::BK && slices < NB) {
+#pragma unroll
+    for (int i = NB - 3; i < NB; ++i) load(buf[i]);
+    slice_barrier<0>();
+    read(buf[NB - 3], 0, f[0]);
     early();
+    tail(tail, std::integral_constant<int, NB - 3>{});
   } else {
     if (rest == 0) {
 #pragma unroll
-      for (int i = 0; i < NB - 1; ++i) load(buf[i]);
+      for (int i = 0; i < NB; ++i) load(buf[i]);
       if constexpr (T == 256) settle<TL>(acc);
-      slice_barrier<4 * L>();
+      slice_barrier<kStart>();
       read(buf[0], 0, f[0]);
     } else {
 #pragma unroll
-      for (int r = kEven ? 2 : 1; r < NB; ++r) {  // r slices before the rounds
-        if (kEven ? r != 2 : rest != r) continue;
+      for (int r = 1; r < NB; ++r) {  // r slices before the rounds
+        if (rest != r) continue;
 #pragma unroll
-        for (int i = 0; i < NB - 1; ++i) load(buf[(NB - r + i) % NB]);
-        slice_barrier<4 * L>();
+        for (int i = 0; i < NB; ++i) load(buf[(NB - r + i) % NB]);
+        slice_barrier<kStart>();
         read(buf[NB - r], 0, f[N == 1 ? r & 1 : 0]);
 #pragma unroll
         for (int i = NB - r; i < NB; ++i) {
@@ -607,12 +611,9 @@ __device__ __forceinline__ void product(char* const (&buf)[TL::NB],
 #pragma unroll
       for (int i = 0; i < NB; ++i) slice(i, kYes, kSteady, kNo);
     }
-    slice(0, kYes, kSteady, kNo);
     early();
-    slice(1, kNo, kOne, kNo);
-    slice(2, kNo, kNone, kNo);
+    tail(tail, std::integral_constant<int, 0>{});
   }
-  slice(3, kNo, kEnd, kNo);
   if constexpr (T == 256) settle<TL>(acc);
 }
 
@@ -658,9 +659,15 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
   // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[TL::kBuf];
   __shared__ __align__(16) char buf1[TL::kBuf];
-  __shared__ __align__(16) char buf2[TL::kBuf];
-  __shared__ __align__(16) char buf3[TL::kBuf];
-  char* const buf[TL::NB] = {buf0, buf1, buf2, buf3};
+  char* buf[TL::NB];
+  buf[0] = buf0;
+  buf[1] = buf1;
+  if constexpr (TL::NB == 4) {
+    __shared__ __align__(16) char buf2[TL::kBuf];
+    __shared__ __align__(16) char buf3[TL::kBuf];
+    buf[2] = buf2;
+    buf[3] = buf3;
+  }
   constexpr bool kApplies = M == kApplyLo || M == kApply || M == kLast;
 
   // neighbouring tiles to one XCD: its L2 then holds the rows they share
@@ -1707,16 +1714,16 @@ template <Mode M>
 void launch_product(const Launches& l, const Groups& gs, const Step& st, hipStream_t stream) {
   const dim3 block(kBlock);
   if (l.T == 256)
-    hipLaunchKernelGGL((ns_product_kernel<Tile<256, 32>, M, false>), dim3(l.tiles), block, 0,
+    hipLaunchKernelGGL((ns_product_kernel<Tile<256>, M, false>), dim3(l.tiles), block, 0,
                        stream, gs, st, l.tiles, 0u);
   else if (l.T == 128)
-    hipLaunchKernelGGL((ns_product_kernel<Tile<128, 32>, M, false>), dim3(l.tiles), block, 0,
+    hipLaunchKernelGGL((ns_product_kernel<Tile<128>, M, false>), dim3(l.tiles), block, 0,
                        stream, gs, st, l.tiles, 0u);
   else
-    hipLaunchKernelGGL((ns_product_kernel<Tile<64, 64>, M, false>), dim3(l.tiles), block, 0,
+    hipLaunchKernelGGL((ns_product_kernel<Tile<64>, M, false>), dim3(l.tiles), block, 0,
                        stream, gs, st, l.tiles, 0u);
   if (l.quarters > 0)
-    hipLaunchKernelGGL((ns_product_kernel<Tile<128, 32>, M, true>), dim3(l.quarters), block, 0,
+    hipLaunchKernelGGL((ns_product_kernel<Tile<128>, M, true>), dim3(l.quarters), block, 0,
                        stream, gs, st, l.quarters, l.tiles);
 }
 
