@@ -14,9 +14,8 @@
 //   apply  S' = a S + B S  (wide)  or  a S + S B  (tall)
 // C = P Q' wants rows of P and Q with the contracted index along the row.  A,
 // B, wide gram and tall apply have that; wide apply's and tall gram's S runs
-// across, and is read from LDS with the transposing reads of gfx950.  (Keeping
-// X in both orientations instead, written twice by every apply, took 45% of
-// apply's time in its epilogue at 14336 x 4096.)
+// across, and is read from LDS with the transposing reads of gfx950, so that X
+// is kept, and written by apply, in one orientation only.
 //
 // Numbers.  The products run on fp16 MFMA with binary32 accumulation: fp16
 // keeps 11 significand bits where bf16 keeps 8, at the same rate, and every
@@ -135,8 +134,7 @@ struct Groups {
 };
 
 struct Step {
-  float a, b, c, eps;
-  int32_t grow;   // the iterates of a matrix grow by less than 2^grow in all
+  float a, b, c;
   int32_t first, last, lo_in, lo_out;
   int32_t in;     // which of the two copies of S this step reads
 };
@@ -284,6 +282,11 @@ enum Mode { kGram, kPoly, kApplyLo, kApply, kLast };
 // of LDS, and their loads come in bursts that are not hidden where k is long
 // (three of 14336 x 4096: gram 707 us, with four slices of 32 613; apply 1200
 // and 1225), so it takes 32.
+// What bounds it: at 256 the main loop keeps the matrix units 78 to 84% busy, at
+// the clock of 1.85 GHz that full load leaves; a tile's epilogue adds about 20 us
+// to the 90 of k = 4096, as all CUs reach it together and read and write their
+// tiles of S at once.  Three of 14336 x 4096: gram 1.25 PFLOP/s of what it
+// computes, apply 1.15; of 4096 x 14336: 1.13 and 1.25.
 template <int T_>
 struct Tile {
   static constexpr int T = T_, BK = T == 256 ? 32 : 64;
@@ -1492,7 +1495,7 @@ struct Shape {
 // Splits, measured: a block takes about 2.5 us for 64 columns, as long as for
 // reading another block's 128 x 128 partial Gram matrix (a quarter of it at 64 x
 // 64), and a launch of its own for each step costs about as much as 4 chunks,
-// so up to 4 chunks stay in one block; beyond, reading and working balance at the
+// so what fits one block's LDS (kStay64, kStay128) stays in it; beyond, reading and working balance at the
 // square root.  Where 128-wide matrices have 32 chunks and more a kernel of their
 // own sums the partials (5 us), and blocks take 4 chunks.
 Shape shape_of(const sbp_matrices& g) {
@@ -1669,14 +1672,13 @@ struct Launches {
   uint32_t tiles, quarters;
 };
 
-// Measured, at k = 4096: a round of 256 tiles of side 256, one a CU, takes 111
-// us, one of 512 of side 128, two a CU, 94 us (a quarter of a round's flops in
-// 0.4 of its time, where there are no more).  So side 256 takes whole rounds, and
+// Measured, at k = 4096: a round of 256 tiles of side 256, one a CU, takes 112
+// us, 1024 of side 128, two a CU, 125 us.  So side 256 takes whole rounds, and
 // what is left over where that is more than half a round; less goes by quarters
-// (292 tiles: 212 us in two rounds, 160 so).  Under one round, side 128
-// where it gives most CUs a tile (504 tiles: 59 us against 67 of side 64 and
-// 65 of side 256), else side 64 (30 tiles of side 128: 13.1 us, 108 of side
-// 64: 8.2).
+// of side 128 (half a round in 80 us).  Under one round, side 128 where it gives
+// most CUs a tile (252 and 432 tiles at k = 768: 17 and 18 us against 40 and 28
+// of side 256), else side 64 (216 tiles of side 128: 13.2 us, 864 of side 64
+// 14.7; 126: 14.3 against 9.6; 30: 15.1 against 7.4).
 Launches launches_of(uint32_t at256, uint32_t at128, uint32_t at64) {
   const uint32_t left = at256 % 256;
   if (at256 >= 256) {
