@@ -505,9 +505,10 @@ sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
  *   entries of X, A and b A + c A A must stay below 16, 16 and 64 (a and b, c
  *   of the size above do; larger ones give infinities, then NaN).  Relative
  *   error in the 2-norm against exact arithmetic, the output's rounding to
- *   bf16 included: about 2e-3.  Results are the same from run to run, and do
- *   not depend on the other matrices of the call or on the tile sizes beyond
- *   that error.  A matrix of zeros gives zeros; one with a NaN or an infinity
+ *   bf16 included: about 2e-3 with those 5 steps (1.7e-3 is the output's
+ *   rounding).  Results are the same bits from run to run, whatever else the
+ *   call holds and wherever the matrix lies.  A matrix of zeros gives zeros
+ *   (eps > 0; with eps = 0 NaN, from 0 / 0); one with a NaN or an infinity
  *   gives NaN throughout, and leaves the others alone.
  *
  *   groups      host array of n_groups groups of equal matrices:

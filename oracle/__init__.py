@@ -22,8 +22,10 @@ Modules:
   step   pack / unpack / chunk / gather, ascending-rank reduce, accumulate,
          normalise, AdamW, bf16 cast, the whole shard step composed from
          them, global gradient-norm clipping (squared norm, coefficient,
-         scale), and parameter groups (per-element groups of a shard, the
-         grouped step)
+         scale), parameter groups (per-element groups of a shard, the
+         grouped step), and the momentum-orthogonalising step (momentum and
+         update in binary32, the Newton-Schulz iteration in float64, and once
+         more with the device's storage formats, for tolerances)
 
 Every function is pinned by tests/test_oracle_*.py against closed forms,
 invariants, special cases, library routines or brute force; none is

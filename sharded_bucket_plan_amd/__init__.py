@@ -17,6 +17,9 @@ Functions (same names as the C calls without the "sbp_" prefix):
                argument: the library's static per-GPU scratch)
   groups       group_runs (+ group_table: the run table on a device),
                adamw_shard_grouped
+  orthogonal   momentum_shard, newton_schulz (+ newton_schulz_workspace,
+               NsHParams, Matrices), update_shard: the momentum-orthogonalising
+               step of weight matrices
   placement    Arena (sbp_arena_create / _info / _free): device arrays whose
                physical pages are spread over the whole device memory
 """

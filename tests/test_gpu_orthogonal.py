@@ -238,6 +238,7 @@ def test_newton_schulz_more_groups_than_one_launch_takes():
 @pytest.mark.parametrize("shapes", [
     [(30, 400, 500)], [(30, 500, 400)],  # tiles of side 128
     [(48, 700, 900)], [(48, 900, 700)],  # whole rounds of side 256, the rest by quarters
+    [(48, 760, 1000)], [(48, 1000, 760)],  # the same, padded sides that are multiples of 128
     [(20, 130, 1100), (36, 1000, 520), (3, 777, 2000)],  # both ways up, ragged
 ])
 def test_newton_schulz_large_batches_equal_single_matrices(shapes):
@@ -376,6 +377,39 @@ def test_newton_schulz_zero_nan_and_infinity():
         assert bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[3]).all())
         for i in (0, 4):
             assert torch.equal(out[i], clean[i])
+
+
+def test_newton_schulz_of_zeros_without_a_floor():
+    """0 / max(0, 0)."""
+    import torch
+    for shape in ((40, 70), (70, 40), (50, 600), (140, 170), (170, 140)):
+        bits = _u((2,) + shape, 43)
+        bits[1] = 0
+        out, = sbp.newton_schulz([_bf(bits)], eps=0.0)
+        torch.cuda.synchronize()
+        assert bool(torch.isnan(out[1]).all()), shape
+        _check_ns(out[:1], bits[:1], eps=0.0, what=str(shape))
+
+
+def test_newton_schulz_two_streams_at_once():
+    """Calls that overlap in time, each with a workspace of its own: the
+    results of calls made one by one."""
+    import torch
+    xs = [_bf(_u((24, 300, 500), 51)), _bf(_u((24, 500, 300), 52))]
+    want = [sbp.newton_schulz([x])[0] for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    ws = [torch.empty(sbp.newton_schulz_workspace([x]), dtype=torch.uint8, device=H.dev())
+          for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        for x, o, w, s in zip(xs, outs, ws, streams):
+            with torch.cuda.stream(s):
+                sbp.newton_schulz([x], out=[o], workspace=w)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o.view(torch.int16), w.view(torch.int16))
 
 
 def test_newton_schulz_empty():
