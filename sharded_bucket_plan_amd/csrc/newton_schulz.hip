@@ -1675,13 +1675,18 @@ struct Launches {
 // Measured, at k = 4096: a round of 256 tiles of side 256, one a CU, takes 112
 // us, 1024 of side 128, two a CU, 125 us.  So side 256 takes whole rounds, and
 // what is left over where that is more than half a round; less goes by quarters
-// of side 128 (half a round in 80 us).  Under one round, side 128 where it gives
+// of side 128 (half a round in 80 us).  Short sums leave more of a large tile's
+// time to its first loads and its epilogue, which side 128 hides behind a second
+// block: between one and a half and two rounds it is faster up to k = 1024 (432
+// tiles of side 256, k = 768: 62 to 71 us against 56 to 60; 432, k = 1024: 72 to
+// 83 and 69 to 78; 448, k = 2048: 120 to 129 and 126 to 136).  Under one round, side 128 where it gives
 // most CUs a tile (252 and 432 tiles at k = 768: 17 and 18 us against 40 and 28
 // of side 256), else side 64 (216 tiles of side 128: 13.2 us, 864 of side 64
 // 14.7; 126: 14.3 against 9.6; 30: 15.1 against 7.4).
-Launches launches_of(uint32_t at256, uint32_t at128, uint32_t at64) {
+Launches launches_of(uint32_t at256, uint32_t at128, uint32_t at64, int k) {
   const uint32_t left = at256 % 256;
-  if (at256 >= 256) {
+  const bool few_short = at256 < 512 && left > 128 && k <= 1024;
+  if (at256 >= 256 && !few_short) {
     if (left > 0 && left <= 128) return Launches{256, at256 - left, 4 * left};
     return Launches{256, at256, 0};
   }
@@ -1697,13 +1702,16 @@ uint32_t apply_tiles(const Group& g, int T) {
 }
 
 // Launches of one kind of product for all groups, whose first tiles are set.
-template <uint32_t (*TILES)(const Group&, int)>
+template <uint32_t (*TILES)(const Group&, int), int32_t Group::*K>
 Launches lay_out(Groups& gs, uint32_t Group::*first) {
   uint32_t at[3] = {0, 0, 0};
+  int k = 0;  // the longest sum
   constexpr int kSides[3] = {256, 128, 64};
-  for (int i = 0; i < gs.n; ++i)
-    for (int k = 0; k < 3; ++k) at[k] += TILES(gs.g[i], kSides[k]);
-  const Launches l = launches_of(at[0], at[1], at[2]);
+  for (int i = 0; i < gs.n; ++i) {
+    for (int t = 0; t < 3; ++t) at[t] += TILES(gs.g[i], kSides[t]);
+    k = std::max(k, gs.g[i].*K);
+  }
+  const Launches l = launches_of(at[0], at[1], at[2], k);
   uint32_t next = 0;
   for (int i = 0; i < gs.n; ++i) {
     gs.g[i].*first = next;
@@ -1730,8 +1738,8 @@ void launch_product(const Launches& l, const Groups& gs, const Step& st, hipStre
 }
 
 sbp_status run_steps(const char* who, Groups& gs, const sbp_ns_hparams& hp, hipStream_t stream) {
-  const Launches gram = lay_out<gram_tiles>(gs, &Group::t_gram);
-  const Launches apply = lay_out<apply_tiles>(gs, &Group::t_apply);
+  const Launches gram = lay_out<gram_tiles, &Group::n>(gs, &Group::t_gram);
+  const Launches apply = lay_out<apply_tiles, &Group::m>(gs, &Group::t_apply);
   for (int s = 0; s < hp.steps; ++s) {
     Step st{};
     st.a = hp.coefs[3 * s];
