@@ -177,6 +177,33 @@ def test_newton_schulz_shapes(shape, kind):
     _check_ns(out, bits, what=f"{shape} {kind}")
 
 
+@pytest.mark.parametrize("shape", [(1, 1048576), (1048576, 3), (100, 200000), (200000, 100),
+                                   (130, 100000), (100000, 130)])
+def test_newton_schulz_long(shape):
+    """Up to SBP_NS_MAX_DIM.  Sums of 2^17.6 products off by 2^-24 of them at
+    random are off by 2^-15, which the tolerance's factor of two covers."""
+    import torch
+    bits = _u(shape, 37)
+    out, = sbp.newton_schulz([_bf(bits)])
+    torch.cuda.synchronize()
+    _check_ns(out, bits, what=str(shape))
+
+
+@pytest.mark.parametrize("steps", [1, 2])
+@pytest.mark.parametrize("shape", [(40, 70), (40, 900), (900, 40), (100, 2500), (2500, 100),
+                                   (150, 200), (200, 150)])
+def test_newton_schulz_few_steps_in_place(steps, shape):
+    """Where the first step is also the last one or next to it, the input is
+    read close to the output's stores."""
+    import torch
+    x = _bf(_u((3,) + shape, 38))
+    want, = sbp.newton_schulz([x], steps=steps)
+    got, = sbp.newton_schulz([x], out=[x], steps=steps)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == x.data_ptr()
+    assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 16])
 @pytest.mark.parametrize("shape", [(30, 90), (500, 20), (70, 200), (200, 70), (90, 700),
                                    (150, 200), (200, 150)])
