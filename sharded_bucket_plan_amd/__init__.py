@@ -24,6 +24,7 @@ Functions (same names as the C calls without the "sbp_" prefix):
                physical pages are spread over the whole device memory
 """
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -685,9 +686,24 @@ def update_shard(u, master, param_out, lr, weight_decay=0.0, stream=None):
         _stream(stream, master)))
 
 
-def _matrix_groups(mats, outs, out_scales, what):
-    """sbp_matrices of a list of 2-D or 3-D bf16 device tensors."""
+def _matrix(x, dev, what):
+    """One entry of a list of matrices: 2-D or 3-D bf16 on `dev`, rows of
+    consecutive elements."""
     import torch
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{what}: matrices are 2-D, or 3-D for equal ones")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: expected a device tensor")
+    if x.device != dev:
+        raise ValueError(f"{what}: tensors on different devices")
+    if x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise ValueError(f"{what}: expected bf16 (or its 16-bit storage), got {x.dtype}")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+
+
+def _matrix_groups(mats, outs, out_scales, what):
+    """sbp_matrices of a list of checked inputs and their outputs."""
     if len(outs) != len(mats):
         raise ValueError(f"{what}: one output per input")
     scales = list(out_scales) if hasattr(out_scales, "__len__") else [out_scales] * len(mats)
@@ -695,17 +711,9 @@ def _matrix_groups(mats, outs, out_scales, what):
         raise ValueError(f"{what}: one out_scale, or one per input")
     arr = (Matrices * max(len(mats), 1))()
     for g, x, o, sc in zip(arr, mats, outs, scales):
-        if x.shape != o.shape or x.dim() not in (2, 3):
-            raise ValueError(f"{what}: matrices are 2-D, or 3-D for equal ones; outputs match")
-        if x.device != mats[0].device or o.device != mats[0].device:
-            raise ValueError(f"{what}: tensors on different devices")
-        for t in (x, o):
-            if not t.is_cuda:
-                raise ValueError(f"{what}: expected a device tensor")
-            if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
-                raise ValueError(f"{what}: expected bf16 (or its 16-bit storage), got {t.dtype}")
-            if t.shape[-1] > 1 and t.stride(-1) != 1:
-                raise ValueError(f"{what}: the elements of a row must be consecutive")
+        _matrix(o, mats[0].device, what)
+        if x.shape != o.shape:
+            raise ValueError(f"{what}: an output's shape is not its input's")
         rows, cols = x.shape[-2:]
         g.in_, g.out = x.data_ptr(), o.data_ptr()
         g.rows, g.cols, g.count = rows, cols, x.shape[0] if x.dim() == 3 else 1
@@ -745,36 +753,44 @@ def newton_schulz(mats, out=None, steps=5, coefs=NS_COEFS, eps=1e-7, out_scales=
     one per step.  workspace: a device tensor of at least
     newton_schulz_workspace(mats) bytes; allocated with torch when not given.
     Returns the outputs.
+
+    With `stream`, what the call allocates belongs to that stream.  The caller
+    orders it after whatever wrote the inputs, and later work of other streams
+    after it; the outputs may then be used and freed on the current stream too.
     """
     import torch
     what = "newton_schulz"
     mats = list(mats)
     h = NsHParams.of(steps, coefs, eps, what)
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in mats] \
-        if out is None else list(out)
-    arr = _matrix_groups(mats, outs, out_scales, what)
+    for x in mats:
+        _matrix(x, mats[0].device, what)
+    outs = None if out is None else list(out)
     if not mats:
-        return outs
-    need = _ns_workspace_bytes(arr, len(mats))
+        _matrix_groups(mats, outs or [], out_scales, what)
+        return outs or []
     s = _stream(stream, mats[0])
     dev = mats[0].device
-    if stream is not None:
-        # the caching allocator reuses memory in the order of the stream it was
-        # taken on: take the workspace on the call's, and tell it of the outputs
-        on = torch.cuda.ExternalStream(s.value, device=dev) if s.value else \
-            torch.cuda.default_stream(dev)
-        if out is None:
-            for o in outs:
-                o.record_stream(on)
-    if workspace is None:
-        if stream is None:
+    # The caching allocator hands out a block in the order of the stream that it
+    # belongs to: one of the current stream's may still be in use by work queued
+    # there, which the call's stream does not wait for.
+    if stream is None:
+        on = contextlib.nullcontext()
+    elif s.value:
+        on = torch.cuda.stream(torch.cuda.ExternalStream(s.value, device=dev))
+    else:
+        on = torch.cuda.stream(torch.cuda.default_stream(dev))
+    with on:
+        if outs is None:
+            outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in mats]
+        arr = _matrix_groups(mats, outs, out_scales, what)
+        need = _ns_workspace_bytes(arr, len(mats))
+        if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(on):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or not workspace.is_contiguous() or \
-            workspace.device != dev:
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError(f"{what}: workspace must be a contiguous tensor on the matrices' device")
+    if out is None and stream is not None:
+        for o in outs:
+            o.record_stream(torch.cuda.current_stream(dev))
     _check(lib().sbp_newton_schulz(arr, len(mats), ctypes.byref(h), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), s))
     return outs

@@ -619,3 +619,21 @@ def test_step_of_row_shards_equals_whole_matrices():
 
     for a, b in zip(run(plan), run(whole)):
         H.assert_bits_equal(a, b, "parameters")
+
+
+def test_newton_schulz_outputs_belong_to_the_calls_stream():
+    """The block of an output that the call makes lies in memory of the stream
+    that writes it, so the allocator can not hand out one that other work still
+    uses."""
+    import torch
+    bits = _u((150, 250), 49)
+    x = _bf(bits)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream, 0):
+        out, = sbp.newton_schulz([x], stream=stream)
+        torch.cuda.synchronize()
+        _check_ns(out, bits)
+        where = [s["stream"] for s in torch.cuda.memory_snapshot()
+                 if s["address"] <= out.data_ptr() < s["address"] + s["total_size"]]
+        assert where == [stream if isinstance(stream, int) else stream.cuda_stream]

@@ -282,3 +282,82 @@ def test_newton_schulz_python_arguments():
     with pytest.raises(ValueError):
         sbp.newton_schulz([x])  # not a device tensor
     assert sbp.newton_schulz([]) == []
+
+
+class _Fake:
+    """What newton_schulz reads of a device tensor, and the stream it was made on."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device, made_on, at):
+        self.shape, self.dtype, self.device = tuple(shape), dtype, device
+        self.made_on, self.at, self.used_on = made_on, at, []
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, d):
+        return int(np.prod(self.shape[d % len(self.shape) + 1:]))
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def record_stream(self, s):
+        self.used_on.append(s)
+
+
+@pytest.mark.parametrize("given", [None, 0, 77])
+def test_newton_schulz_allocates_on_the_calls_stream(monkeypatch, given):
+    """Outputs and workspace that the call makes belong to the stream that the
+    kernels run on: a block of another stream may still be in use there."""
+    import torch
+    current, device, made = ["current"], torch.device("cuda", 0), []
+
+    class On:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current.append(self.s)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    def empty(*shape, dtype, device):
+        shape = shape[0] if isinstance(shape[0], tuple) else shape
+        made.append(_Fake(shape, dtype, device, current[-1], 0x10000000 * (len(made) + 2)))
+        return made[-1]
+
+    launched = []
+
+    class Lib:
+        sbp_newton_schulz_workspace = staticmethod(sbp.lib().sbp_newton_schulz_workspace)
+
+        @staticmethod
+        def sbp_newton_schulz(arr, n, hp, ws, ws_bytes, stream):
+            launched.append(stream)
+            return sbp.SBP_OK
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[-1])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: "default")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: f"stream {s}")
+    monkeypatch.setattr(sbp, "_stream", lambda s, t: ctypes.c_void_p(s))
+    monkeypatch.setattr(sbp, "lib", lambda: Lib)
+    x = _Fake((64, 300), torch.bfloat16, device, "current", 0x1000000)
+    out, = sbp.newton_schulz([x], stream=given)
+    on = {None: "current", 0: "default", 77: "stream 77"}[given]
+    assert [m.made_on for m in made] == [on, on] and out is made[0]
+    assert len(launched) == 1 and launched[0].value == (given or None)
+    # the outputs may be used and freed on the caller's stream
+    assert given is None or out.used_on == ["current"]
+    assert current == ["current"]
