@@ -358,6 +358,21 @@ def _stream(stream, tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(tensor.device).cuda_stream)
 
 
+def _allocating_on(stream, s, dev):
+    """Context in which torch allocates on a call's stream (s: _stream's answer).
+
+    The caching allocator hands out a block in the order of the stream that it
+    belongs to: one of the current stream's may still be in use by work queued
+    there, and is handed out there again once freed; the call's stream waits for
+    neither."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if s.value:
+        return torch.cuda.stream(torch.cuda.ExternalStream(s.value, device=dev))
+    return torch.cuda.stream(torch.cuda.default_stream(dev))
+
+
 def _dev(t, itemsize, what):
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
@@ -598,7 +613,8 @@ def grad_sq_norm(peers, acc, scale, n, g_sum_out=None, workspace=None, sq_out=No
     """sbp_grad_sq_norm: this rank's squared norm of g = fl(G*scale) (float64).
 
     Returns the device tensor holding it (float64[1]); workspace and sq_out are
-    allocated with torch when not given.  With g_sum_out, G is written too.
+    allocated with torch when not given, on the call's stream.  With g_sum_out,
+    G is written too.
     """
     import torch
     ref = peers[0] if peers else acc
@@ -609,10 +625,17 @@ def grad_sq_norm(peers, acc, scale, n, g_sum_out=None, workspace=None, sq_out=No
         raise ValueError("grad_sq_norm: peers/acc differ in size")
     if g_sum_out is not None and g_sum_out.numel() != n:
         raise ValueError("grad_sq_norm: g_sum_out has the wrong size")
-    if workspace is None:
-        workspace = torch.empty(grad_sq_norm_workspace(n), dtype=torch.float64, device=dev)
-    if sq_out is None:
-        sq_out = torch.empty(1, dtype=torch.float64, device=dev)
+    if not ref.is_cuda:
+        raise ValueError("grad_sq_norm: expected a device tensor")
+    s = _stream(stream, ref)
+    own_out = sq_out is None
+    with _allocating_on(stream, s, dev):
+        if workspace is None:
+            workspace = torch.empty(grad_sq_norm_workspace(n), dtype=torch.float64, device=dev)
+        if own_out:
+            sq_out = torch.empty(1, dtype=torch.float64, device=dev)
+    if own_out and stream is not None:
+        sq_out.record_stream(torch.cuda.current_stream(dev))
     for t, what in ((workspace, "workspace"), (sq_out, "sq_out")):
         if t.dtype != torch.float64 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"grad_sq_norm: {what} must be a contiguous float64 device tensor")
@@ -620,7 +643,7 @@ def grad_sq_norm(peers, acc, scale, n, g_sum_out=None, workspace=None, sq_out=No
         _ptrs(peers, "grad_sq_norm peers"), len(peers),
         None if acc is None else _f32(acc, "grad_sq_norm acc"), float(scale), int(n),
         None if g_sum_out is None else _f32(g_sum_out, "grad_sq_norm g_sum_out"),
-        workspace.data_ptr(), workspace.numel(), sq_out.data_ptr(), _stream(stream, ref)))
+        workspace.data_ptr(), workspace.numel(), sq_out.data_ptr(), s))
     return sq_out
 
 
@@ -770,16 +793,7 @@ def newton_schulz(mats, out=None, steps=5, coefs=NS_COEFS, eps=1e-7, out_scales=
         return outs or []
     s = _stream(stream, mats[0])
     dev = mats[0].device
-    # The caching allocator hands out a block in the order of the stream that it
-    # belongs to: one of the current stream's may still be in use by work queued
-    # there, which the call's stream does not wait for.
-    if stream is None:
-        on = contextlib.nullcontext()
-    elif s.value:
-        on = torch.cuda.stream(torch.cuda.ExternalStream(s.value, device=dev))
-    else:
-        on = torch.cuda.stream(torch.cuda.default_stream(dev))
-    with on:
+    with _allocating_on(stream, s, dev):
         if outs is None:
             outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in mats]
         arr = _matrix_groups(mats, outs, out_scales, what)

@@ -314,12 +314,11 @@ class _Fake:
         self.used_on.append(s)
 
 
-@pytest.mark.parametrize("given", [None, 0, 77])
-def test_newton_schulz_allocates_on_the_calls_stream(monkeypatch, given):
-    """Outputs and workspace that the call makes belong to the stream that the
-    kernels run on: a block of another stream may still be in use there."""
+def _fake_streams(monkeypatch):
+    """torch.empty and torch's streams without a GPU; the list of what is
+    allocated, each with the stream that was current."""
     import torch
-    current, device, made = ["current"], torch.device("cuda", 0), []
+    current, made = ["current"], []
 
     class On:
         def __init__(self, s):
@@ -336,28 +335,54 @@ def test_newton_schulz_allocates_on_the_calls_stream(monkeypatch, given):
         made.append(_Fake(shape, dtype, device, current[-1], 0x10000000 * (len(made) + 2)))
         return made[-1]
 
-    launched = []
-
-    class Lib:
-        sbp_newton_schulz_workspace = staticmethod(sbp.lib().sbp_newton_schulz_workspace)
-
-        @staticmethod
-        def sbp_newton_schulz(arr, n, hp, ws, ws_bytes, stream):
-            launched.append(stream)
-            return sbp.SBP_OK
-
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", On)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[-1])
     monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: "default")
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: f"stream {s}")
-    monkeypatch.setattr(sbp, "_stream", lambda s, t: ctypes.c_void_p(s))
-    monkeypatch.setattr(sbp, "lib", lambda: Lib)
-    x = _Fake((64, 300), torch.bfloat16, device, "current", 0x1000000)
+    monkeypatch.setattr(sbp, "_stream", lambda s, t: V(s))
+    return made
+
+
+class _NoLaunch:
+    """The library, but for one call that is noted down in place of being made."""
+
+    def __init__(self, name):
+        self.library, self.name, self.streams = sbp.lib(), name, []
+
+    def __getattr__(self, name):
+        if name != self.name:
+            return getattr(self.library, name)
+        return lambda *a: self.streams.append(a[-1].value) or sbp.SBP_OK
+
+
+ON = {None: "current", 0: "default", 77: "stream 77"}
+
+
+@pytest.mark.parametrize("given", list(ON))
+def test_newton_schulz_allocates_on_the_calls_stream(monkeypatch, given):
+    """Outputs and workspace that the call makes belong to the stream that the
+    kernels run on: a block of another stream may still be in use there."""
+    import torch
+    made = _fake_streams(monkeypatch)
+    library = _NoLaunch("sbp_newton_schulz")
+    monkeypatch.setattr(sbp, "lib", lambda: library)
+    x = _Fake((64, 300), torch.bfloat16, torch.device("cuda", 0), "current", 0x1000000)
     out, = sbp.newton_schulz([x], stream=given)
-    on = {None: "current", 0: "default", 77: "stream 77"}[given]
-    assert [m.made_on for m in made] == [on, on] and out is made[0]
-    assert len(launched) == 1 and launched[0].value == (given or None)
+    assert [m.made_on for m in made] == [ON[given]] * 2 and out is made[0]
+    assert library.streams == [given or None]
     # the outputs may be used and freed on the caller's stream
     assert given is None or out.used_on == ["current"]
-    assert current == ["current"]
+
+
+@pytest.mark.parametrize("given", list(ON))
+def test_grad_sq_norm_allocates_on_the_calls_stream(monkeypatch, given):
+    import torch
+    made = _fake_streams(monkeypatch)
+    library = _NoLaunch("sbp_grad_sq_norm")
+    monkeypatch.setattr(sbp, "lib", lambda: library)
+    x = _Fake((300,), torch.bfloat16, torch.device("cuda", 0), "current", 0x1000000)
+    out = sbp.grad_sq_norm([x], None, 1.0, 300, stream=given)
+    assert [m.made_on for m in made] == [ON[given]] * 2 and out is made[1]
+    assert library.streams == [given or None]
+    assert given is None or out.used_on == ["current"]
