@@ -423,10 +423,18 @@ __device__ __forceinline__ void multiply(const Frags<TL>& f, Acc<TL>& acc) {
 // The same for one accumulator, in its registers: at the large tile all 256 are
 // taken, and the compiler, free to give a product another place than its
 // summand, moved them about between the products (13% of apply).  It does not
-// see these as matrix instructions, so what it would see to is done by hand:
-// the operands have been waited for, an accumulator is used again 64 products
-// later, and settle() stands between the products and what else writes or reads
-// the accumulators.
+// see these as matrix instructions, so the wait states that it would fill in are
+// kept by hand:
+// - an accumulator is read or written by anything else 19 or more wait states
+//   after its last product (18 is the longest any needs): settle() ends every
+//   run of products, before the first way out of it, since moves may stand
+//   wherever two ways meet;
+// - a fragment or accumulator is written by a vector instruction 5 or more before
+//   a product reads it (2 are needed): fragments come from LDS, whose reads the
+//   compiler waits for, and the accumulators' zeros are settled too;
+// - a product's own accumulator is used again 64 products later.
+// That a build keeps both distances, on every path, is what
+// tests/test_matrix_unit_hazards.py reads from its disassembly.
 template <bool FIRST>
 __device__ __forceinline__ void multiply_in_place(f32x4& c, f16x8 p, f16x8 q) {
   if constexpr (FIRST)
@@ -597,7 +605,8 @@ __device__ __forceinline__ void product(char* (&buf)[TL::NB],
     } else {
 #pragma unroll
       for (int r = 1; r < NB; ++r) {  // r slices before the rounds
-        if (rest != r) continue;
+        // slices of 32 come in pairs: both padded sides are multiples of 64
+        if (rest != r || (TL::BK == 32 && r % 2 == 1)) continue;
 #pragma unroll
         for (int i = 0; i < NB; ++i) load(buf[(NB - r + i) % NB]);
         slice_barrier<kStart>();
@@ -607,6 +616,8 @@ __device__ __forceinline__ void product(char* (&buf)[TL::NB],
           if (i == NB - r) slice(i, kYes, kSteady, kYes);
           else slice(i, kYes, kSteady, kNo);
         }
+        // the compiler places moves where the ways in join
+        if constexpr (T == 256) settle<TL>(acc);
       }
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     }
