@@ -529,9 +529,10 @@ sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
  *               read, so it needs no clearing; calls that may overlap in time
  *               need one each
  *   Large calls run in parts that use the workspace one after the other.
- *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE, SBP_EHIP.
+ *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE, SBP_ENOMEM, SBP_EHIP.
  * sbp_newton_schulz_workspace (host): bytes for these groups (their pointers
- *   and distances are not read), or -1 if their sizes are refused.
+ *   and distances are not read), or -1 if their sizes are refused or host
+ *   memory runs out.
  * ---------------------------------------------------------------------- */
 #define SBP_NS_MAX_STEPS 16
 #define SBP_NS_MAX_DIM 1048576        /* rows, cols, count                   */

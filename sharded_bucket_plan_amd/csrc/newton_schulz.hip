@@ -1864,22 +1864,9 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
   return run_steps(who, gs, hp, stream);
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t sbp_newton_schulz_workspace(const sbp_matrices* groups, int32_t n_groups) {
-  if (check_shapes("sbp_newton_schulz_workspace", groups, n_groups) != SBP_OK) return -1;
-  (void)sbp::ok();
-  int64_t most = 0;
-  for (const Chunk& c : chunks_of(groups, n_groups)) most = std::max(most, c.bytes);
-  return most;
-}
-
-sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
-                             const sbp_ns_hparams* hp, void* workspace, int64_t workspace_bytes,
-                             hipStream_t stream) {
-  const char* who = "sbp_newton_schulz";
+sbp_status newton_schulz(const char* who, const sbp_matrices* groups, int32_t n_groups,
+                         const sbp_ns_hparams* hp, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream) {
   const std::string w(who);
   sbp_status st = check_shapes(w, groups, n_groups);
   if (st != SBP_OK) return st;
@@ -1943,6 +1930,36 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
     if (st != SBP_OK) return st;
   }
   return sbp::ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t sbp_newton_schulz_workspace(const sbp_matrices* groups, int32_t n_groups) {
+  const char* who = "sbp_newton_schulz_workspace";
+  try {
+    if (check_shapes(who, groups, n_groups) != SBP_OK) return -1;
+    int64_t most = 0;
+    for (const Chunk& c : chunks_of(groups, n_groups)) most = std::max(most, c.bytes);
+    (void)sbp::ok();
+    return most;
+  } catch (...) {
+    (void)sbp::fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+    return -1;
+  }
+}
+
+// The lists are made before anything is launched.
+sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
+                             const sbp_ns_hparams* hp, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream) {
+  const char* who = "sbp_newton_schulz";
+  try {
+    return newton_schulz(who, groups, n_groups, hp, workspace, workspace_bytes, stream);
+  } catch (...) {
+    return sbp::fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+  }
 }
 
 }  // extern "C"

@@ -3,6 +3,9 @@ momentum, update and Newton-Schulz iteration against closed forms, and every
 refusal of the three calls (the fake addresses are never dereferenced)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -10,6 +13,7 @@ import pytest
 import sharded_bucket_plan_amd as sbp
 from oracle import step as OS
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 V = ctypes.c_void_p
 F32 = np.float32
 
@@ -268,6 +272,33 @@ def test_newton_schulz_workspace_size():
     # a long list runs in parts: the workspace stays bounded
     many = (sbp.Matrices * 40)(*[_mats(rows=4096, cols=14336)] * 40)
     assert q(many, 40) < 8 * q(many, 1)
+
+
+@pytest.mark.parametrize("call", ["sbp_newton_schulz_workspace", "sbp_newton_schulz"])
+def test_newton_schulz_out_of_host_memory(call):
+    """A list whose parts do not fit host memory is refused, in a process of
+    small means: no exception leaves a C call, and nothing is launched."""
+    code = f"""
+import ctypes, resource, sys
+sys.path.insert(0, {ROOT!r})
+import sharded_bucket_plan_amd as sbp
+L = sbp.lib()
+n, big = 1 << 20, 1 << 14  # a part each: 2^20 entries of a list
+g = (sbp.Matrices * 1)(sbp.Matrices(1 << 20, 1 << 62, big, big, n, big, big, big * big, big * big, 1.0))
+hp = sbp.NsHParams.of(5, sbp.NS_COEFS, 1e-7, "t")
+L.sbp_newton_schulz_workspace((sbp.Matrices * 1)(sbp.Matrices(None, None, 64, 64, 1)), 1)
+now = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (now + (16 << 20),) * 2)
+if {call!r} == "sbp_newton_schulz_workspace":
+    r = L.sbp_newton_schulz_workspace(g, 1)
+else:
+    r = L.sbp_newton_schulz(g, 1, ctypes.byref(hp), 1 << 50, 1 << 60, None)
+print(r, L.sbp_last_error().decode())
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    want = -1 if call.endswith("workspace") else sbp.SBP_ENOMEM
+    assert r.stdout.strip() == f"{want} {call}: out of host memory"
 
 
 def test_newton_schulz_python_arguments():
