@@ -709,12 +709,16 @@ def update_shard(u, master, param_out, lr, weight_decay=0.0, stream=None):
         _stream(stream, master)))
 
 
+def _shape(x, what):
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{what}: matrices are 2-D, or 3-D for equal ones")
+
+
 def _matrix(x, dev, what):
     """One entry of a list of matrices: 2-D or 3-D bf16 on `dev`, rows of
     consecutive elements."""
     import torch
-    if x.dim() not in (2, 3):
-        raise ValueError(f"{what}: matrices are 2-D, or 3-D for equal ones")
+    _shape(x, what)
     if not x.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
     if x.device != dev:
@@ -753,6 +757,7 @@ def newton_schulz_workspace(mats):
     """Bytes of workspace sbp_newton_schulz needs for these 2-D or 3-D tensors."""
     arr = (Matrices * max(len(mats), 1))()
     for g, x in zip(arr, mats):
+        _shape(x, "newton_schulz_workspace")
         g.rows, g.cols = x.shape[-2:]
         g.count = x.shape[0] if x.dim() == 3 else 1
     return _ns_workspace_bytes(arr, len(mats))

@@ -417,3 +417,11 @@ def test_grad_sq_norm_allocates_on_the_calls_stream(monkeypatch, given):
     assert [m.made_on for m in made] == [ON[given]] * 2 and out is made[1]
     assert library.streams == [given or None]
     assert given is None or out.used_on == ["current"]
+
+
+@pytest.mark.parametrize("shape", [(7,), (2, 3, 4, 5)])
+def test_newton_schulz_workspace_of_other_dimensions(shape):
+    """The sizes are asked for what the call takes, and for nothing else."""
+    import torch
+    with pytest.raises(ValueError, match="2-D, or 3-D"):
+        sbp.newton_schulz_workspace([torch.empty(shape, dtype=torch.bfloat16, device="meta")])
