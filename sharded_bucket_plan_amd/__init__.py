@@ -766,7 +766,10 @@ def newton_schulz_workspace(mats):
 def _ns_workspace_bytes(arr, n):
     need = lib().sbp_newton_schulz_workspace(arr, n)
     if need < 0:
-        raise SbpError(SBP_EINVAL, lib().sbp_last_error().decode())
+        why = lib().sbp_last_error().decode()
+        # the call looks at the sizes first, and has a status for them
+        raise SbpError(SBP_ENOMEM if "out of host memory" in why else
+                       lib().sbp_newton_schulz(arr, n, None, None, 0, None), why)
     return int(need)
 
 

@@ -425,3 +425,12 @@ def test_newton_schulz_workspace_of_other_dimensions(shape):
     import torch
     with pytest.raises(ValueError, match="2-D, or 3-D"):
         sbp.newton_schulz_workspace([torch.empty(shape, dtype=torch.bfloat16, device="meta")])
+
+
+def test_newton_schulz_workspace_of_refused_sizes():
+    """Refused with the status that the call itself gives."""
+    import torch
+    x = torch.empty((1 << 20) + 1, 4, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(sbp.SbpError, match="SBP_NS_MAX_DIM") as e:
+        sbp.newton_schulz_workspace([x])
+    assert e.value.status == sbp.SBP_ERANGE
