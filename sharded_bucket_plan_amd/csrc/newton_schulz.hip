@@ -70,14 +70,15 @@ constexpr int kXcds = 8;
 constexpr int kPad = 64;        // both padded sides are multiples of this
 constexpr int kMaxGroups = 16;  // groups of equal matrices per launch
 constexpr int kMaxNormBlocks = 256;
-constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 1024.0f, kScaleLo = 2048.0f;
+constexpr int kLogX = 12;       // X is stored times 2^12
+constexpr float kScaleA = 4096.0f, kScaleB = 1024.0f, kScaleLo = 2048.0f;
 
 // Per-matrix scalars, written by the prologue.
 // Stored X_0 = X_0 / rho, stored X_k = X_k * sx for k >= 1.
 struct Scal {
   float gram_first, gram;  // accumulator -> stored A: rho^2 * 2^12, 2^12 / sx^2
   float apply_first;       // step 1's accumulator -> stored X_1: rho * sx
-  float inv_sx;
+  int32_t log_sx;
 };
 
 // One group: `count` matrices of one shape, at equal distances.
@@ -94,7 +95,10 @@ struct Group {
   int32_t rp, cp;    // rows and cols padded
   int32_t m, n;      // the smaller and the larger of rp and cp
   int32_t norm_blocks;
-  float out_scale;
+  // out_scale = out_frac * 2^out_exp, the former in [1/2, 1) or 0: the power of
+  // two is applied last, with X's, so that no factor leaves binary32's range
+  float out_frac;
+  int32_t out_exp;
   int32_t in_vec, out_vec;  // 16-byte rows
   uint32_t t_norm, t_pro, t_gram, t_apply;  // first block of the group in each launch
   // short side of at most 128 only: blocks per matrix; their partial Gram
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kBlock) ns_norm_kernel(Groups gs) {
 // 2^14) (k = 0 for a zero, infinite or NaN norm), X_0 = stored * rho, later
 // X = stored / sx.
 struct Norm {
-  int k;
+  int k, log_sx;
   double floor_norm, rho, sx;
 };
 __device__ __forceinline__ Norm norm_of(double norm, float eps, int grow) {
@@ -229,9 +233,9 @@ __device__ __forceinline__ Norm norm_of(double norm, float eps, int grow) {
   r.floor_norm = norm < eps ? static_cast<double>(eps) : norm;  // NaN stays
   int below = plain && norm < eps ? ilogb(static_cast<double>(eps)) - ilogb(norm) : 0;
   below = below > grow + 2 ? below - grow - 2 : 0;
-  below = below < 100 ? below : 100;
   r.rho = 1.0 / (r.floor_norm * ldexp(1.0, r.k));
-  r.sx = ldexp(static_cast<double>(kScaleX), below);
+  r.log_sx = kLogX + below;  // below 300: from bf16's least to binary32's largest
+  r.sx = ldexp(1.0, r.log_sx);
   return r;
 }
 
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(kBlock) ns_prologue_kernel(Groups gs, float ep
   if (t == 0 && threadIdx.x == 0)
     g.scal[item] = Scal{static_cast<float>(nm.rho * nm.rho * kScaleA),
                         static_cast<float>(kScaleA / (nm.sx * nm.sx)),
-                        static_cast<float>(nm.rho * nm.sx), static_cast<float>(1.0 / nm.sx)};
+                        static_cast<float>(nm.rho * nm.sx), nm.log_sx};
   const f16x8 h = half8(w, nm.k);
   *reinterpret_cast<f16x8*>(g.S(0, item) + static_cast<int64_t>(row) * g.cp + col) = h;
 }
@@ -643,11 +647,13 @@ __device__ __forceinline__ void store_bits8(uint16_t* p, int left, bool vec, u32
     one(4, w.z), one(5, w.z >> 16), one(6, w.w), one(7, w.w >> 16);
   }
 }
-__device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ void store_out8(uint16_t* p, int left, bool vec, const float (&v)[8],
+                                           int exp) {
   typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
   bf16x8 b;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) b[q] = static_cast<__bf16>(v[q]);  // nearest, ties to even
+  for (int q = 0; q < 8; ++q)
+    b[q] = static_cast<__bf16>(ldexpf(v[q], exp));  // nearest, ties to even
   store_bits8(p, left, vec, __builtin_bit_cast(u32x4, b));
 }
 
@@ -829,7 +835,8 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
   const float alpha = st.first ? sc.gram_first : sc.gram;
   const float fb = st.b * (kScaleB / kScaleA), fc = st.c * (kScaleB / (kScaleA * kScaleA));
   // apply: a x + acc / 2^10, scaled; the factors carry the scale
-  const float fx = (st.first ? sc.apply_first : 1.0f) * (M == kLast ? g.out_scale * sc.inv_sx : 1.0f);
+  const float fx = (st.first ? sc.apply_first : 1.0f) * (M == kLast ? g.out_frac : 1.0f);
+  const int out_exp = g.out_exp - sc.log_sx;
   const float fd = fx * (1.0f / kScaleB), fa = fx * st.a;
   if constexpr (!kAhead) ask_first();
 #pragma unroll
@@ -901,7 +908,8 @@ ns_product_kernel(Groups gs, Step st, unsigned total, unsigned from) {
       }
       if constexpr (M == kLast) {
         if (gr < g.rows && gc < g.cols)
-          store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v);
+          store_out8(g.out + item * g.out_stride + gr * g.out_ld + gc, g.cols - gc, g.out_vec, v,
+                     out_exp);
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) h[q] = static_cast<_Float16>(v[q]);
@@ -1044,6 +1052,7 @@ struct Columns {
   int lo, hi;     // chunks of 64
   int k;          // the input times 2^k
   float fa, fd;   // X' = fa X + fd * accumulators, with the diagonal's remainder * fd
+  int out_exp;    // the caller's matrix: X' * 2^out_exp
   bool keep;      // store the remainder
 };
 
@@ -1179,7 +1188,7 @@ __device__ __forceinline__ void flat_columns(const Group& g, const Buffers<MP>& 
             const float acc = TALL ? D[u % DI][0][q * 4 + e] : D[0][u % DJ][q * 4 + e];
             const float v = fmaf(fmaf(d[e], cs.fd, cs.fa), y, acc * cs.fd);
             if constexpr (kLast) {
-              hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<__bf16>(v));
+              hi[u][q][e] = __builtin_bit_cast(_Float16, static_cast<__bf16>(ldexpf(v, cs.out_exp)));
             } else {
               hi[u][q][e] = static_cast<_Float16>(v);
               if constexpr (kLo)
@@ -1279,10 +1288,11 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
   cs.hi = static_cast<int>(static_cast<int64_t>(chunks) * (split + 1) / g.splits);
   f32x16 G[kSub][kSub];
   int kx = 0;
-  float inv_sx = 0.0f, gram = 0.0f, apply_first = 0.0f;
+  int log_sx = 0;
+  float gram = 0.0f, apply_first = 0.0f;
   if (first > 1) {
     const Scal sc = g.scal[item];
-    inv_sx = sc.inv_sx;
+    log_sx = sc.log_sx;
     gram = sc.gram;
   }
 #pragma unroll 1
@@ -1329,11 +1339,11 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
         const double norm = sqrt(block_sum_all(tr)) * ldexp(1.0, -kx);
         const Norm nm = norm_of(norm, fs.eps, fs.grow);
         cs.k = nm.k;
-        inv_sx = static_cast<float>(1.0 / nm.sx);
+        log_sx = nm.log_sx;
         apply_first = static_cast<float>(nm.rho * nm.sx);
         gram = static_cast<float>(kScaleA * ldexp(1.0, -2 * kx) / (nm.floor_norm * nm.floor_norm));
         if (split == 0 && threadIdx.x == 0)
-          g.scal[item] = Scal{0.0f, static_cast<float>(kScaleA / (nm.sx * nm.sx)), 0.0f, inv_sx};
+          g.scal[item] = Scal{0.0f, static_cast<float>(kScaleA / (nm.sx * nm.sx)), 0.0f, log_sx};
       }
       // -- A, then B, into LDS (symmetric: a lane's 4 rows of a column go into the
       // column's row), their diagonals' remainders next to them
@@ -1420,9 +1430,10 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
       flat_columns<MP, TALL, STAYS, kInputGram>(g, lds, item, cs, wave, lane, G, kx);
     } else {
       const FlatStep st = fs.s[stage - 1];
-      const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_scale * inv_sx : 1.0f);
+      const float fx = (stage == 1 ? apply_first : 1.0f) * (st.last ? g.out_frac : 1.0f);
       cs.fd = fx * (1.0f / kScaleB);
       cs.fa = fx * st.a;
+      cs.out_exp = g.out_exp - log_sx;
       cs.keep = st.lo_out;
       if (stage == 1 && st.last)
         flat_columns<MP, TALL, STAYS, kInputLast>(g, lds, item, cs, wave, lane, G, kx);
@@ -1434,7 +1445,7 @@ __device__ __forceinline__ void flat_stages(const Group& g, const FlatSteps& fs,
         flat_columns<MP, TALL, STAYS, kKept>(g, lds, item, cs, wave, lane, G, kx);
       else
         flat_columns<MP, TALL, STAYS, kPlain>(g, lds, item, cs, wave, lane, G, kx);
-      if (stage == 1) gram = static_cast<float>(kScaleA) * inv_sx * inv_sx;
+      if (stage == 1) gram = ldexpf(kScaleA, -2 * log_sx);
       if (st.last) return;
     }
     if (g.splits > 1) {
@@ -1796,7 +1807,9 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     g.m = static_cast<int32_t>(s.m);
     g.n = static_cast<int32_t>(s.n);
     g.norm_blocks = static_cast<int32_t>(s.norm_blocks);
-    g.out_scale = src.out_scale;
+    int out_exp;
+    g.out_frac = std::frexp(src.out_scale, &out_exp);
+    g.out_exp = out_exp;
     const bool many = p.count > 1;
     g.in_vec = sbp::aligned(g.in, 16) && src.in_ld % 8 == 0 && (!many || src.in_stride % 8 == 0);
     g.out_vec =

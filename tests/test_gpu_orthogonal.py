@@ -637,3 +637,53 @@ def test_newton_schulz_outputs_belong_to_the_calls_stream():
         where = [s["stream"] for s in torch.cuda.memory_snapshot()
                  if s["address"] <= out.data_ptr() < s["address"] + s["total_size"]]
         assert where == [stream if isinstance(stream, int) else stream.cuda_stream]
+
+
+SCALE_SHAPES = [(1, 1), (4, 4), (60, 250), (128, 192), (40, 700), (700, 120), (100, 2500),
+                (150, 200), (200, 150)]
+
+
+def _check_scaled(out, U, scale, eps=1e-7, steps=5):
+    """bf16's subnormals are 2^-133 apart: half of that more for each entry."""
+    want = OS.newton_schulz(U, steps, sbp.NS_COEFS, eps)
+    tol = _tolerance(U, want, steps, sbp.NS_COEFS, eps) * abs(scale) + \
+        2.0 ** -134 * np.sqrt(want.size)
+    off = np.linalg.norm(_f64(out) - float(np.float32(scale)) * want)
+    assert off <= tol, f"{U.shape} times {scale}: off by {off:.3e}, tolerance {tol:.3e}"
+
+
+@pytest.mark.parametrize("shape", SCALE_SHAPES)
+@pytest.mark.parametrize("steps", [1, 5])
+def test_newton_schulz_any_out_scale(shape, steps):
+    """From binary32's subnormals to its largest."""
+    bits = _u(shape, 73)
+    U = OS.bf16_to_f32(bits).astype(np.float64)
+    for scale in (1e-30, -1e-36, 2.0 ** -126, 2.0 ** -130, 0.0, 1e30, 1.5e38):
+        out, = sbp.newton_schulz([_bf(bits)], steps=steps, out_scales=scale)
+        _check_scaled(out, U, scale, steps=steps)
+
+
+def test_newton_schulz_any_out_scale_large_tiles():
+    """The same on tiles of side 256 and quarters: the bits of single matrices."""
+    import torch
+    x = _bf(_u((48, 500, 1000), 74))
+    for scale in (1e-36, 2.0 ** -130):
+        out, = sbp.newton_schulz([x], out_scales=scale)
+        for i in (0, 30, 47):
+            alone, = sbp.newton_schulz([x[i]], out_scales=scale)
+            assert torch.equal(alone.view(torch.int16), out[i].view(torch.int16))
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (20, 30), (20, 400), (100, 2500), (130, 140), (140, 130)])
+def test_newton_schulz_norm_far_below_eps(shape):
+    """The result is next to nothing and out_scale brings it back.  Far below 1
+    the polynomial is its linear term: five roundings of X to binary16 (half a
+    step, 2^-11 of it) and the result's."""
+    for eps, size, scale in ((1e38, 1e-34, 1e38), (3e38, 1e-37, 3e38), (1.0, 1e-37, 1e30),
+                             (1e-7, 1e-30, 1e-4)):
+        bits = _u(shape, 75, size=size)
+        out, = sbp.newton_schulz([_bf(bits)], eps=eps, out_scales=scale)
+        U = OS.bf16_to_f32(bits).astype(np.float64)
+        want = OS.newton_schulz(U, 5, sbp.NS_COEFS, eps, scale)
+        tol = (2.0 ** -8 + 5 * 2.0 ** -11) * np.linalg.norm(want) + 2.0 ** -134 * np.sqrt(want.size)
+        assert np.linalg.norm(_f64(out) - want) <= tol, (eps, size, scale)
