@@ -363,32 +363,38 @@ def newton_schulz(U, steps, coefs, eps=1e-7, out_scale=1.0):
         return float(F32(out_scale)) * X
 
 
-def newton_schulz_rounded(U, steps, coefs, eps=1e-7):
+def newton_schulz_rounded(U, steps, coefs, eps=1e-7, diag_a=1.0, diag_b=1.0, rest_x=1.0,
+                          sums=np.float64):
     """The same with X, A and B = b A + c A A kept in binary16 as the device
     keeps them (scaled by 2^12, 2^12 and 2^10; the remainders of both diagonals
     kept, and X's next to it while three steps remain), all other arithmetic in
-    float64: how far those roundings by themselves move the result."""
+    float64: how far those roundings by themselves move the result.
+
+    diag_a, diag_b, rest_x: what the kept remainders count; 1 as the device
+    keeps them, others to see what it is that a result misses.  sums: the type
+    of all other arithmetic.
+    """
     X = np.asarray(U, np.float64)
     if X.shape[0] > X.shape[1]:
-        return newton_schulz_rounded(X.T, steps, coefs, eps).T
+        return newton_schulz_rounded(X.T, steps, coefs, eps, diag_a, diag_b, rest_x, sums).T
     coefs = [coefs] * steps if np.ndim(coefs[0]) == 0 else coefs
 
     def kept(x, scale):
-        return (x * scale).astype(np.float16).astype(np.float64) / scale
+        return (x * sums(scale)).astype(np.float16).astype(sums) / sums(scale)
 
     norm = max(np.sqrt(np.sum(X * X)), float(F32(eps)))
-    X = X / norm
+    X = (X / norm).astype(sums)
     whole = X  # the first step's X is exact: bf16 values times a power of two
-    for s, (a, b, c) in enumerate([[float(F32(x)) for x in t] for t in coefs]):
+    for s, (a, b, c) in enumerate([[sums(F32(x)) for x in t] for t in coefs]):
         exact = X @ X.T
         A = kept(exact, 4096.0)
-        d = np.diag(exact) - np.diag(A)
+        d = sums(diag_a) * (np.diag(exact) - np.diag(A))
         exact = b * (A + np.diag(d)) + c * (A @ A + (d[:, None] + d) * A + np.diag(d * d))
         B = kept(exact, 1024.0)
-        new = (a + np.diag(exact) - np.diag(B))[:, None] * whole + B @ X
+        new = (a + sums(diag_b) * (np.diag(exact) - np.diag(B)))[:, None] * whole + B @ X
         if s == steps - 1:
-            return new
+            return new.astype(np.float64)
         X = kept(new, 4096.0)
-        rest = kept(new - X, 4096.0 * 2048.0) if steps - 1 - s >= 3 else 0.0
+        rest = sums(rest_x) * kept(new - X, 4096.0 * 2048.0) if steps - 1 - s >= 3 else sums(0)
         whole = X + rest
     return X

@@ -11,6 +11,7 @@ import sharded_bucket_plan_amd as sbp
 import synth
 from oracle import step as OS
 from tests import helpers as H
+from tests import ns_models as NS
 
 pytestmark = pytest.mark.gpu
 
@@ -637,6 +638,28 @@ def test_newton_schulz_outputs_belong_to_the_calls_stream():
         where = [s["stream"] for s in torch.cuda.memory_snapshot()
                  if s["address"] <= out.data_ptr() < s["address"] + s["total_size"]]
         assert where == [stream if isinstance(stream, int) else stream.cuda_stream]
+
+
+@pytest.mark.parametrize("shape", NS.SHAPES)
+@pytest.mark.parametrize("steps", [3, 5])
+def test_newton_schulz_keeps_its_remainders(shape, steps):
+    """The result is nearer to the model of the device's formats than to one
+    that loses a remainder or counts it with the wrong sign."""
+    bits = NS.update(shape, 71, "flat")
+    out, = sbp.newton_schulz([_bf(bits)], steps=steps)
+    U = OS.bf16_to_f32(bits).astype(np.float64)
+    assert NS.nearest(_f64(out), U, steps, sbp.NS_COEFS) is None
+
+
+@pytest.mark.parametrize("shape", NS.SHAPES)
+@pytest.mark.parametrize("kind", ["flat", "strong", "steep", "sixteen"])
+def test_newton_schulz_is_as_far_off_as_its_formats(shape, kind):
+    bits = NS.update(shape, 72, kind)
+    U = OS.bf16_to_f32(bits).astype(np.float64)
+    for steps in (3, 5):
+        out, = sbp.newton_schulz([_bf(bits)], steps=steps)
+        off = NS.off(_f64(out), U, steps, sbp.NS_COEFS)
+        assert off < NS.ALLOWED, (steps, off)
 
 
 SCALE_SHAPES = [(1, 1), (4, 4), (60, 250), (128, 192), (40, 700), (700, 120), (100, 2500),

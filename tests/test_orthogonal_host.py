@@ -12,6 +12,7 @@ import pytest
 
 import sharded_bucket_plan_amd as sbp
 from oracle import step as OS
+from tests import ns_models as NS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 V = ctypes.c_void_p
@@ -434,3 +435,58 @@ def test_newton_schulz_workspace_of_refused_sizes():
     with pytest.raises(sbp.SbpError, match="SBP_NS_MAX_DIM") as e:
         sbp.newton_schulz_workspace([x])
     assert e.value.status == sbp.SBP_ERANGE
+
+
+# ---- the models that the device's results are told from ----------------------------
+
+def _values(shape, kind):
+    return OS.bf16_to_f32(NS.update(shape, 61, kind)).astype(np.float64)
+
+
+@pytest.mark.parametrize("shape", NS.SHAPES)
+@pytest.mark.parametrize("steps", [3, 5])
+def test_models_tell_a_mistake(shape, steps):
+    """Results of binary32 sums, rounded to bf16, with a mistake planted in the
+    oracle: each is told from the others, and none is seen where there is none."""
+    U = _values(shape, "flat")
+    result = lambda **kw: NS.rounded(OS.newton_schulz_rounded(  # noqa: E731
+        U, steps, COEFS, sums=np.float32, **kw))
+    assert NS.nearest(result(), U, steps, COEFS) is None
+    for what, kw in NS.MISTAKES.items():
+        if steps == 3 and "rest_x" in kw:
+            continue  # none is kept in the last three steps
+        found = NS.nearest(result(**kw), U, steps, COEFS)
+        assert found is not None, what
+        if 0.0 in kw.values():
+            assert found.split("'")[0].split()[0] == what.split("'")[0].split()[0], (what, found)
+
+
+@pytest.mark.parametrize("shape", NS.SHAPES)
+@pytest.mark.parametrize("kind", ["flat", "strong", "steep", "sixteen"])
+def test_models_size_of_the_error(shape, kind):
+    """Binary32 sums are as far off as said; without B's remainder (noise), or
+    without X's (steep spectra), further than is allowed."""
+    U = _values(shape, kind)
+    for steps in (3, 5):
+        y = NS.rounded(OS.newton_schulz_rounded(U, steps, COEFS, sums=np.float32))
+        assert NS.off(y, U, steps, COEFS) < NS.ALLOWED
+    worse = {"flat": dict(diag_a=0.0, diag_b=0.0), "steep": dict(rest_x=0.0),
+             "sixteen": dict(rest_x=0.0)}.get(kind)
+    if worse:
+        y = NS.rounded(OS.newton_schulz_rounded(U, 5, COEFS, sums=np.float32, **worse))
+        assert NS.off(y, U, 5, COEFS) > NS.ALLOWED
+
+
+def test_error_before_the_outputs_rounding():
+    """What the header says of the error: 5 steps, spectra from flat to few
+    directions over next to nothing."""
+    rng = np.random.default_rng(8)
+    for m, n in ((200, 300), (128, 512)):
+        g = rng.standard_normal((m, n))
+        for k in (1, 4, 16, 64):
+            low = rng.standard_normal((m, k)) @ rng.standard_normal((k, n))
+            for noise in (1.0, 0.1, 0.03, 0.01, 0.003, 0.0003):
+                U = NS.rounded(low + noise * g)
+                e = OS.newton_schulz(U, 5, COEFS)
+                r = OS.newton_schulz_rounded(U, 5, COEFS)
+                assert np.linalg.norm(r - e) < 2.6e-3 * np.linalg.norm(e), (m, k, noise)
