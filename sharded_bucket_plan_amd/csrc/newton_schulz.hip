@@ -1699,15 +1699,29 @@ struct Launches {
 // what is left over where that is more than half a round; less goes by quarters
 // of side 128 (half a round in 80 us).  Short sums leave more of a large tile's
 // time to its first loads and its epilogue, which side 128 hides behind a second
-// block: between one and a half and two rounds it is faster up to k = 1024 (432
-// tiles of side 256, k = 768: 62 to 71 us against 56 to 60; 432, k = 1024: 72 to
-// 83 and 69 to 78; 448, k = 2048: 120 to 129 and 126 to 136).  Under one round, side 128 where it gives
-// most CUs a tile (252 and 432 tiles at k = 768: 17 and 18 us against 40 and 28
-// of side 256), else side 64 (216 tiles of side 128: 13.2 us, 864 of side 64
-// 14.7; 126: 14.3 against 9.6; 30: 15.1 against 7.4).
+// block: between one and a half and two rounds of side 256 it is faster while it
+// makes at most 3.5 rounds of its own 512.  The five steps' applies, side 256
+// against side 128:
+//   k      tiles 256  128     us
+//   1024         400  1600   414   376
+//   1024         448  1792   429   419
+//   1024         496  1984   453   468  (so these take side 256)
+//    960         400  1600   380   360
+//    960         496  1984   409   440
+//    768         387  1548   365   345
+//    768         432  1728   380   363
+//    768         504  2016   410   416
+//    640         504  1400   323   248  (a third of the large tiles hangs over)
+//    512         388  1552   312   260
+//    512         508  2032   364   357
+// At k = 2048 side 256 is ahead again (448 tiles: 120 to 129 us against 126 to
+// 136).  Under one round, side 128 where it gives most CUs a tile (252 and 432
+// tiles at k = 768: 17 and 18 us against 40 and 28 of side 256), else side 64
+// (216 tiles of side 128: 13.2 us, 864 of side 64 14.7; 126: 14.3 against 9.6;
+// 30: 15.1 against 7.4).
 Launches launches_of(uint32_t at256, uint32_t at128, uint32_t at64, int k) {
   const uint32_t left = at256 % 256;
-  const bool few_short = at256 < 512 && left > 128 && k <= 1024;
+  const bool few_short = at256 < 512 && left > 128 && at128 <= 1792 && k <= 1024;
   if (at256 >= 256 && !few_short) {
     if (left > 0 && left <= 128) return Launches{256, at256 - left, 4 * left};
     return Launches{256, at256, 0};
