@@ -1132,3 +1132,20 @@ def test_shard_step_object_matches_the_call():
         assert torch.equal(x, y), f"ShardStep on a side stream: {what} differs"
     with pytest.raises(ValueError, match="wrong size"):
         sbp.ShardStep(peers, None, a[0], a[1][:-1], a[2], a[3])
+
+
+def test_grad_sq_norm_on_another_stream():
+    """A call on a stream that is not the current one, with what it allocates."""
+    import torch
+    n = 5 * 2048 + 3
+    peers = H.dev_peers(31, 1, 0, 3, n, 1e-3)
+    want = sbp.grad_sq_norm(peers, None, 0.5, n).item()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream, 0):
+        sq = sbp.grad_sq_norm(peers, None, 0.5, n, stream=stream)
+        torch.cuda.synchronize()
+        assert sq.item() == want
+        where = [s["stream"] for s in torch.cuda.memory_snapshot()
+                 if s["address"] <= sq.data_ptr() < s["address"] + s["total_size"]]
+        assert where == [stream if isinstance(stream, int) else stream.cuda_stream]

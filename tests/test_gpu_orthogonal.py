@@ -710,3 +710,31 @@ def test_newton_schulz_norm_far_below_eps(shape):
         want = OS.newton_schulz(U, 5, sbp.NS_COEFS, eps, scale)
         tol = (2.0 ** -8 + 5 * 2.0 ** -11) * np.linalg.norm(want) + 2.0 ** -134 * np.sqrt(want.size)
         assert np.linalg.norm(_f64(out) - want) <= tol, (eps, size, scale)
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 100), (39, 777), (64, 64), (100, 2000), (2000, 100),
+                                   (100, 200000), (130, 300), (1000, 700), (2048, 2048)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 5, 8])
+def test_newton_schulz_of_equal_entries(shape, steps):
+    """All entries alike, up to their signs: every rounding is the same for all
+    of them, so nothing averages out, and the result is the polynomial of one
+    number.  With s that number's square and p = a + b s + c s^2, X' = p X: X's
+    relative error e passes on times |p + 2 (b s + 2 c s^2)| / |p|, A's rounding
+    u = 2^-11 comes in times |b s + 2 c s^2| / |p|, B's times |b s + c s^2| /
+    |p|, X's own once, and the output's 2^-8 at the end."""
+    bits = OS.f32_to_bf16(np.full(shape, 1.0078125e-3, np.float32))
+    bits[::3] ^= 0x8000
+    bits[:, ::2] ^= 0x8000
+    out, = sbp.newton_schulz([_bf(bits)], steps=steps)
+    U = OS.bf16_to_f32(bits).astype(np.float64)
+    a, b, c = sbp.NS_COEFS
+    x, off = 1.0, 0.0
+    for _ in range(steps):
+        s, u = x * x, 2.0 ** -11
+        low, slope = b * s + c * s * s, b * s + 2 * c * s * s
+        p = a + low
+        off = (abs(p + 2 * slope) * off + (abs(slope) + abs(low)) * u) / abs(p) + u
+        x *= p
+    # in exact arithmetic: U over its norm, times x
+    want = x * np.sign(U) / np.sqrt(U.size)
+    assert np.max(np.abs(_f64(out) / want - 1)) <= off + 2.0 ** -8
