@@ -697,7 +697,8 @@ def test_newton_schulz_any_out_scale_large_tiles():
             assert torch.equal(alone.view(torch.int16), out[i].view(torch.int16))
 
 
-@pytest.mark.parametrize("shape", [(1, 1), (20, 30), (20, 400), (100, 2500), (130, 140), (140, 130)])
+@pytest.mark.parametrize("shape", [(1, 1), (20, 30), (20, 400), (100, 2500), (130, 140),
+                                   (140, 130)])
 def test_newton_schulz_norm_far_below_eps(shape):
     """The result is next to nothing and out_scale brings it back.  Far below 1
     the polynomial is its linear term: five roundings of X to binary16 (half a

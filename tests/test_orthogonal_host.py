@@ -285,7 +285,8 @@ sys.path.insert(0, {ROOT!r})
 import sharded_bucket_plan_amd as sbp
 L = sbp.lib()
 n, big = 1 << 20, 1 << 14  # a part each: 2^20 entries of a list
-g = (sbp.Matrices * 1)(sbp.Matrices(1 << 20, 1 << 62, big, big, n, big, big, big * big, big * big, 1.0))
+g = (sbp.Matrices * 1)(sbp.Matrices(1 << 20, 1 << 62, big, big, n, big, big, big * big,
+                                    big * big, 1.0))
 hp = sbp.NsHParams.of(5, sbp.NS_COEFS, 1e-7, "t")
 L.sbp_newton_schulz_workspace((sbp.Matrices * 1)(sbp.Matrices(None, None, 64, 64, 1)), 1)
 now = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
