@@ -504,9 +504,11 @@ sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
  *   Products run on fp16 matrix instructions with binary32 accumulation; the
  *   entries of X, A and b A + c A A must stay below 16, 16 and 64 (a and b, c
  *   of the size above do; larger ones give infinities, then NaN).  Relative
- *   error in the 2-norm against exact arithmetic, the output's rounding to
- *   bf16 included: about 2e-3 with those 5 steps (1.7e-3 is the output's
- *   rounding).  Results are the same bits from run to run, whatever else the
+ *   error in the 2-norm against exact arithmetic with those 5 steps, the
+ *   output's rounding to bf16 (1.7e-3) included: 1.7e-3 to 2e-3 for noise and
+ *   for strong directions over it, up to 3e-3 where all but a few directions
+ *   are next to nothing; up to 1e-2 where all entries are alike, and so are
+ *   their roundings.  Results are the same bits from run to run, whatever else the
  *   call holds and wherever the matrix lies.  A matrix of zeros gives zeros
  *   (eps > 0; with eps = 0 NaN, from 0 / 0); one with a NaN or an infinity
  *   gives NaN throughout, and leaves the others alone.

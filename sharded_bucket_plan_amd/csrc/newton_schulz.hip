@@ -36,12 +36,18 @@
 //     those directions; so while at least three steps remain, X's remainder
 //     is kept (fp16, * 2^11) and a X is formed from both parts.
 // Relative error against the iteration in 64 bits, 5 steps, before the
-// output's rounding (1.7e-3 by itself), on spectra from flat to rank 16 plus
-// 0.03 of noise: 4e-4 .. 1.0e-3 (rank 16 plus 0.003: 2.3e-3); without the
-// diagonals' remainders up to 2.2e-3, without either up to 2.6e-2, with bf16
-// products 7e-3 .. 2e-1.
-// The squared norm is summed in float64 in a fixed order, so results are the
-// same from run to run.
+// output's rounding (1.7e-3 by itself): 4e-4 .. 1.0e-3 for noise, and for strong
+// directions over noise of their size; up to 2.5e-3 where the noise is weaker
+// and its directions come up from next to nothing within the steps (rank 16
+// plus 0.03: 1.7e-3, plus 0.003: 2.4e-3).  Without the diagonals' remainders up
+// to 2.2e-3 for noise, without either up to 2.6e-2, with bf16 products 7e-3 ..
+// 2e-1.
+// Where all entries are alike their roundings are too, and do not average out:
+// up to 1e-2.
+// The squared norm: above a short side of 128 in float64; up to it the trace of
+// the first Gram matrix, whose sums are binary32 (at the longest sides 1024 in a
+// row a block, then 64 blocks': within 7e-5).  Both in a fixed order, so results
+// are the same from run to run.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -1847,7 +1853,9 @@ sbp_status run_chunk(const char* who, const sbp_matrices* groups, const Chunk& c
     norm += g.count * g.norm_blocks;
     pro += g.count * (g.rp / 32) * (g.cp / 64);
   }
-  // |x| grows by at most a factor sum |coefficients| per step while small
+  // While X is far below 1 a step multiplies it by a: b and c come in with its
+  // square.  What they add on the last steps before X gets near 1 has a factor
+  // 64 of room, between 2^10, where this bound puts X, and fp16's end.
   double grow = 0.0;
   for (int s = 0; s < hp.steps; ++s)
     grow += std::log2(std::max(1.0, std::fabs(static_cast<double>(hp.coefs[3 * s]))));

@@ -80,9 +80,12 @@
 #define SBP_NORM_INFLIGHT_KB 112
 #endif
 // The momentum pass has one state array and no more arithmetic than a few
-// multiplications; with two blocks per CU at R = 8 it is ahead of one (one 8M..64M
-// shard +2..7%, 15.5M elements 72 -> 61 us; with an accumulator at 100M -1.5%),
-// and at fewer peers within 1%.
+// multiplications.  This makes two blocks per CU at R = 8, three at R = 4, one at
+// R = 16.  On buffers that no cache still holds (3 GB of them in turn), against
+// one block: R = 8, 8M elements 43.4 and 46.0 us, 15.6M 74.5 and 77.5, 64M 318
+// and 322, 104M 486 and 495; with an accumulator 15.6M 86.4 and 87.3, but 64M 373
+// and 365, 104M 575 and 557; R = 2 and 4 within 1%.  112 and 160 KB are within 1%
+// of this at R = 8, and 2% behind at R = 2 and 4.
 #ifndef SBP_MOMENTUM_INFLIGHT_KB
 #define SBP_MOMENTUM_INFLIGHT_KB 80
 #endif
