@@ -508,9 +508,9 @@ sbp_status sbp_update_shard(const void* u, float* master, void* param_out,
  *   output's rounding to bf16 (1.7e-3) included: 1.7e-3 to 2e-3 for noise and
  *   for strong directions over it, up to 3e-3 where all but a few directions
  *   are next to nothing; up to 1e-2 where all entries are alike, and so are
- *   their roundings.  Results are the same bits from run to run, whatever else the
- *   call holds and wherever the matrix lies.  A matrix of zeros gives zeros
- *   (eps > 0; with eps = 0 NaN, from 0 / 0); one with a NaN or an infinity
+ *   their roundings.  Results are the same bits from run to run, whatever
+ *   else the call holds and wherever the matrix lies.  A matrix of zeros gives
+ *   zeros (eps > 0; with eps = 0 NaN, from 0 / 0); one with a NaN or an infinity
  *   gives NaN throughout, and leaves the others alone.
  *
  *   groups      host array of n_groups groups of equal matrices:
