@@ -281,28 +281,28 @@ def _own(s):
     case = s["case"]
     op = case["op"]
     if op == "quantize":
-        q = sbp.mx4_quantize(s["x"], along=case["along"],
+        q = sbp.mx_quantize(s["x"], along=case["along"],
                              seed=s["seed"] if case["random"] else None, offset=s["offset"])
-        return [sbp.mx4_dequantize(x) for x in (q if case["along"] == "both" else [q])]
+        return [sbp.mx_dequantize(x) for x in (q if case["along"] == "both" else [q])]
     if op == "reduce":
         peers = [sbp.Mx4(c, f, (1, case["n"])) for c, f in s["peers"]]
-        sbp.mx4_reduce_shard(peers, s["acc"], s["scale"], s["out"])
+        sbp.mx_reduce_shard(peers, s["acc"], s["scale"], s["out"])
         return s["out"]
     if op == "exchange":
-        peers = [sbp.mx4_quantize(c, seed=s["seed"], offset=s["offset"] + r)
+        peers = [sbp.mx_quantize(c, seed=s["seed"], offset=s["offset"] + r)
                  for r, c in enumerate(s["chunks"])]
-        sbp.mx4_reduce_shard(peers, None, s["scale"], s["out"])
+        sbp.mx_reduce_shard(peers, None, s["scale"], s["out"])
         return s["out"]
     if op == "product":
         a = sbp.Mx4(*s["a"], (case["m"], case["k"]))
         b = sbp.Mx4(*s["b"], (case["n"], case["k"]))
-        return sbp.mx4_matmul(a, b, out=s["c"], accumulate=case["accumulate"])
-    x, xt = sbp.mx4_quantize(s["x"], along="both")
-    w, wt = sbp.mx4_quantize(s["w"], along="both")
-    y = sbp.mx4_matmul(x, w)
-    dy, dyt = sbp.mx4_quantize(s["dy"], along="both", seed=s["seed"], offset=s["offset"])
-    dx = sbp.mx4_matmul(dy, wt)
-    sbp.mx4_matmul(dyt, xt, out=s["dw"], accumulate=True)
+        return sbp.mx_matmul(a, b, out=s["c"], accumulate=case["accumulate"])
+    x, xt = sbp.mx_quantize(s["x"], along="both")
+    w, wt = sbp.mx_quantize(s["w"], along="both")
+    y = sbp.mx_matmul(x, w)
+    dy, dyt = sbp.mx_quantize(s["dy"], along="both", seed=s["seed"], offset=s["offset"])
+    dx = sbp.mx_matmul(dy, wt)
+    sbp.mx_matmul(dyt, xt, out=s["dw"], accumulate=True)
     return {"y": y, "dx": dx, "dw": s["dw"]}
 
 
