@@ -562,6 +562,117 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
                              int64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit floats: the low-bit exchange, and products of what it
+ * carries.  ("Parallelisms", ZeRO-1 and ZeRO-3: gradient chunks go to the rank
+ * that owns them, updated shards come back; "ZeRO removes the copies without
+ * adding bandwidth".)  Both ways take 17 bits in place of 64 for four values:
+ *   gradients   sbp_mx_quantize (random rounding) of each peer's chunk ->
+ *               all-to-all of codes and scales -> sbp_mx_reduce_shard ->
+ *               sbp_adamw_shard(R = 0, acc)
+ *   parameters  sbp_mx_quantize of the fp32 master shard -> all-gather ->
+ *               sbp_mx_dequantize, or straight into sbp_mx_matmul: a tensor
+ *               of whole rows per rank (sbp_bucket_plan_per_tensor) with a
+ *               multiple of 32 columns is, after the all-gather, the operand
+ *   a layer     y = x W' of quantized x and W; its gradients dy W and dy' x are
+ *               the same call on the operands quantized along their columns,
+ *               the latter added to the fp32 accumulator of the gradients
+ *
+ * The format (OCP Microscaling MXFP4): each row of a rows x cols matrix is cut
+ * into blocks of 32 values, the last one filled up with zeros; kb =
+ * ceil(cols / 32) of them.
+ *   codes   uint8[rows][kb * 16], two codes a byte, the first in its low half;
+ *           16-byte aligned.  A code: a sign (8) over 0, 1/2, 1, 3/2, 2, 3, 4, 6
+ *   scales  uint8[rows][kb], any alignment: s stands for 2^(s - 127), 255 for a
+ *           block of NaN
+ * A flat buffer is a matrix of one row.
+ *
+ * sbp_mx_quantize: x (rows x cols, device SBP_BF16 or SBP_F32, aligned to its
+ *   type, rows ld elements apart; 16-byte rows take the vector path) into
+ *   codes and scales, and / or x' (cols x rows: blocks down x's columns) into
+ *   codes_t and scales_t; either pair may be null.  With a the largest
+ *   magnitude of a block and E its biased exponent:
+ *     random null    nearest: s = max(E - 2, 0); |x| * 2^(127 - s) to the nearest
+ *                    code, ties to the even one, above 6 to 6
+ *     random given   s is one more where a > 6 * 2^(s - 127); a magnitude between
+ *                    two codes goes up with the probability of its distance from
+ *                    the lower one, cut to 16 bits: unbiased within 2^-16 of a
+ *                    step.  Its 16 random bits come from Philox4x32-10 with key
+ *                    `seed` and counter (4 * block + octet, `offset`), blocks
+ *                    counted through the matrix (for x' with the first counter's
+ *                    bit 63 set); half word j of the four words, low halves
+ *                    first, is value j's of the octet.  Calls that should be
+ *                    independent take different seeds or offsets.
+ *   The sign is kept, of zeros too.  A block with a NaN or an infinity gets scale
+ *   255 and codes 0.  Values beyond the last column are zeros, with code 0.
+ *   Results depend on the values, the seed and the offset alone.
+ *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE (more than SBP_MAX_SHARD_NUMEL
+ *   values, counted in whole blocks of rows and of columns; ld above 2^40),
+ *   SBP_ENOMEM, SBP_EHIP.
+ *
+ * sbp_mx_dequantize: out (rows x cols, SBP_BF16 or SBP_F32, rows ld elements
+ *   apart) = the values; exact in both types (in SBP_BF16 and SBP_F32 alike,
+ *   scales above 252 may overflow to infinity).  Errors as above.
+ *
+ * sbp_mx_reduce_shard: out[i] = fl( (acc[i] + S[i]) * scale ), without acc
+ *   fl( S[i] * scale ): S[i] the R peers' values summed in ascending peer order,
+ *   one rounding per addition.  The peers are flat buffers of n values.
+ *   codes, scales  host arrays of R (1..SBP_MAX_PEERS) device pointers
+ *   acc            device fp32[n] or null; may be out itself (scale = 1 then
+ *                  accumulates microbatches in place)
+ *   out            device fp32[n]; 16-byte aligned, as acc
+ *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE (n > SBP_MAX_SHARD_NUMEL),
+ *   SBP_ENOMEM, SBP_EHIP.
+ * ---------------------------------------------------------------------- */
+#define SBP_BF16 0
+#define SBP_F32 1
+typedef struct {
+  uint64_t seed, offset;
+} sbp_mx_random;
+
+sbp_status sbp_mx_quantize(const void* x, int32_t type, int64_t rows,
+                            int64_t cols, int64_t ld, void* codes,
+                            void* scales, void* codes_t, void* scales_t,
+                            const sbp_mx_random* random, hipStream_t stream);
+sbp_status sbp_mx_dequantize(const void* codes, const void* scales,
+                              int64_t rows, int64_t cols, void* out,
+                              int32_t type, int64_t ld, hipStream_t stream);
+sbp_status sbp_mx_reduce_shard(const void* const* codes,
+                                const void* const* scales, int32_t R,
+                                int64_t n, const float* acc, float scale,
+                                float* out, hipStream_t stream);
+
+/*
+ * sbp_mx_matmul: out = A B' (m x n) of A (m x k) and B (n x k) in the format
+ *   above, on the scaled matrix instructions: products are exact, sums are
+ *   binary32, in an order that depends on m, n and k alone; the result is
+ *   rounded once to SBP_BF16, or kept as SBP_F32.
+ *   accumulate != 0 (SBP_F32 only): out = fl(out + A B').
+ *   out         device, aligned to its type, rows ld >= n elements apart; must
+ *               not overlap an operand
+ *   m, n, k     0 .. SBP_MX_MAX_DIM, k to SBP_MX_MAX_K; m or n == 0 does
+ *               nothing; k == 0 writes zeros (leaves out as it is where it
+ *               accumulates)
+ *   workspace   device memory, 256-byte aligned, workspace_bytes >=
+ *               sbp_mx_matmul_workspace(m, n, k) (null where that is 0);
+ *               written before read, so it needs no clearing; calls that may
+ *               overlap in time need one each; must not overlap another buffer
+ *   A block of NaN gives NaN in its row or column; the other rows and columns
+ *   are as without it.
+ *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE, SBP_ENOMEM, SBP_EHIP.
+ * sbp_mx_matmul_workspace (host): bytes, or -1 if a size is refused.
+ * ---------------------------------------------------------------------- */
+#define SBP_MX_MAX_DIM 134217728 /* m, n                                  */
+#define SBP_MX_MAX_K 8388608     /* k                                     */
+
+int64_t sbp_mx_matmul_workspace(int64_t m, int64_t n, int64_t k);
+sbp_status sbp_mx_matmul(const void* codes_a, const void* scales_a,
+                          const void* codes_b, const void* scales_b,
+                          int64_t m, int64_t n, int64_t k, void* out,
+                          int32_t type, int64_t ld, int32_t accumulate,
+                          void* workspace, int64_t workspace_bytes,
+                          hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Spread arena: device memory for a rank's shard state and receive buffers
  * ("Parallelisms", ZeRO-1 and ZeRO-3: each rank keeps its shard's fp32
  * master copy, first and second moments and parameter shard, and receives

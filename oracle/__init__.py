@@ -26,10 +26,12 @@ Modules:
          grouped step), and the momentum-orthogonalising step (momentum and
          update in binary32, the Newton-Schulz iteration in float64, and once
          more with the device's storage formats, for tolerances)
+  mx4    microscaled 4-bit floats: quantization (nearest, and at random from a
+         counter-based generator), values, the ascending-rank reduce of them
 
-Every function is pinned by tests/test_oracle_*.py against closed forms,
+Every function is pinned by tests/test_oracle_*.py and tests/test_mx4_host.py against closed forms,
 invariants, special cases, library routines or brute force; none is
 "parity unpinned".
 """
 
-from . import plan, step  # noqa: F401
+from . import mx4, plan, step  # noqa: F401

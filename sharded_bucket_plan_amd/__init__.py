@@ -20,6 +20,10 @@ Functions (same names as the C calls without the "sbp_" prefix):
   orthogonal   momentum_shard, newton_schulz (+ newton_schulz_workspace,
                NsHParams, Matrices), update_shard: the momentum-orthogonalising
                step of weight matrices
+  4 bits       Mx4 (a matrix in microscaled 4-bit floats), mx_quantize,
+               mx_dequantize, mx_reduce_shard, mx_matmul
+               (+ mx_matmul_workspace): the low-bit exchange, and products of
+               what it carries
   placement    Arena (sbp_arena_create / _info / _free): device arrays whose
                physical pages are spread over the whole device memory
 """
@@ -49,7 +53,8 @@ EXPORTS = (
     "sbp_group_runs", "sbp_adamw_shard_grouped", "sbp_unpack_shards",
     "sbp_grad_sq_norm_noalloc", "sbp_arena_create", "sbp_arena_info", "sbp_arena_free",
     "sbp_momentum_shard", "sbp_update_shard", "sbp_newton_schulz_workspace",
-    "sbp_newton_schulz",
+    "sbp_newton_schulz", "sbp_mx_quantize", "sbp_mx_dequantize", "sbp_mx_reduce_shard",
+    "sbp_mx_matmul_workspace", "sbp_mx_matmul",
 )
 
 MAX_GROUPS = 8
@@ -57,6 +62,9 @@ NOALLOC_SCRATCH_DOUBLES = 1 << 20  # SBP_NOALLOC_SCRATCH_DOUBLES
 NOALLOC_MAX_NUMEL = 2146435079  # SBP_NOALLOC_MAX_NUMEL
 ARENA_MAX_ARRAYS = 64  # SBP_ARENA_MAX_ARRAYS
 NS_MAX_STEPS = 16  # SBP_NS_MAX_STEPS
+MX_BLOCK = 32  # values that share a scale
+MX_MAX_DIM, MX_MAX_K = 1 << 27, 1 << 23  # SBP_MX_MAX_DIM, SBP_MX_MAX_K
+SBP_BF16, SBP_F32 = 0, 1
 NS_COEFS = (3.4445, -4.7750, 2.0315)  # the usual quintic's a, b, c
 
 
@@ -112,6 +120,10 @@ class NsHParams(ctypes.Structure):
         for i, r in enumerate(rows):
             h.coefs[3 * i:3 * i + 3] = [float(x) for x in r]
         return h
+
+
+class MxRandom(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 _lib = None
@@ -174,6 +186,18 @@ def lib():
         "sbp_newton_schulz": ([ctypes.POINTER(Matrices), ctypes.c_int32,
                                ctypes.POINTER(NsHParams), ctypes.c_void_p, ctypes.c_int64,
                                ctypes.c_void_p], st),
+        "sbp_mx_quantize": ([ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                              ctypes.c_int64] + [ctypes.c_void_p] * 4
+                             + [ctypes.POINTER(MxRandom), ctypes.c_void_p], st),
+        "sbp_mx_dequantize": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                                ctypes.c_void_p], st),
+        "sbp_mx_reduce_shard": ([_vpp, _vpp, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                  ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], st),
+        "sbp_mx_matmul_workspace": ([ctypes.c_int64] * 3, ctypes.c_int64),
+        "sbp_mx_matmul": ([ctypes.c_void_p] * 4 + [ctypes.c_int64] * 3
+                           + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                              ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p], st),
         "sbp_arena_create": ([_i64p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                               ctypes.c_uint64, _vpp, ctypes.POINTER(ctypes.c_void_p)], st),
         "sbp_arena_info": ([ctypes.c_void_p, _i64p, _i64p, _i64p], st),
@@ -816,6 +840,236 @@ def newton_schulz(mats, out=None, steps=5, coefs=NS_COEFS, eps=1e-7, out_scales=
     _check(lib().sbp_newton_schulz(arr, len(mats), ctypes.byref(h), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), s))
     return outs
+
+
+# ---- microscaled 4-bit floats ----------------------------------------------------
+
+class Mx4:
+    """A rows x cols matrix in microscaled 4-bit floats (see include/sbp.h):
+    codes uint8 [rows, kb * 16] and scales uint8 [rows, kb], kb = ceil(cols / 32).
+
+    Both are contiguous; views of whole rows of a larger buffer are fine (codes
+    16-byte aligned).  A flat buffer of n values is the matrix (1, n)."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes, scales, shape):
+        import torch
+        rows, cols = int(shape[0]), int(shape[1])
+        kb = -(-cols // MX_BLOCK)
+        if rows < 0 or cols < 0:
+            raise ValueError("Mx4: a negative size")
+        for t, width, what in ((codes, 16 * kb, "codes"), (scales, kb, "scales")):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (rows, width):
+                raise ValueError(f"Mx4: {what} must be uint8 of shape {(rows, width)}, got "
+                                 f"{t.dtype} of {tuple(t.shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"Mx4: {what} must be contiguous")
+        if codes.device != scales.device:
+            raise ValueError("Mx4: codes and scales on different devices")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+
+    @classmethod
+    def empty(cls, rows, cols, device):
+        import torch
+        kb = -(-int(cols) // MX_BLOCK)
+        return cls(torch.empty((rows, kb * 16), dtype=torch.uint8, device=device),
+                   torch.empty((rows, kb), dtype=torch.uint8, device=device), (rows, cols))
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def numel(self):
+        return self.rows * self.cols
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def rows_of(self, start, stop):
+        """The matrix of rows start .. stop - 1, a view."""
+        if not 0 <= start <= stop <= self.rows:
+            raise ValueError(f"Mx4.rows_of: {start}..{stop} outside {self.rows} rows")
+        return Mx4(self.codes[start:stop], self.scales[start:stop], (stop - start, self.cols))
+
+
+def _mx4_type(t, what):
+    import torch
+    if t.dtype == torch.float32:
+        return SBP_F32
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return SBP_BF16
+    raise ValueError(f"{what}: expected float32 or bf16 (or its 16-bit storage), got {t.dtype}")
+
+
+def _mx4_rows(t, rows, cols, what):
+    """Row distance of a 1-D or 2-D device tensor that is rows x cols."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a device tensor")
+    if t.dim() not in (1, 2) or (1,) * (2 - t.dim()) + tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(t.shape)}")
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+    # torch leaves the distance of a dimension of one element open
+    return t.stride(0) if t.dim() == 2 and rows > 1 else max(cols, 1)
+
+
+def _same_device(dev, tensors, what):
+    if any(t is not None and t.device != dev for t in tensors):
+        raise ValueError(f"{what}: tensors on different devices")
+
+
+def mx_quantize(x, along="rows", out=None, seed=None, offset=0, stream=None):
+    """sbp_mx_quantize: x in microscaled 4-bit floats.
+
+    x: 1-D (one row) or 2-D device tensor, bf16 or float32; rows may be further
+    apart than they are long.  along: "rows" (blocks of 32 along x's rows),
+    "cols" (down its columns: the result is x' in the format) or "both", which
+    reads x once and returns the pair.  out: the Mx4 (or pair) to write; new
+    ones when not given.  seed: None rounds to nearest; an integer rounds at
+    random, from a counter-based generator keyed by it (and by offset).
+
+    With `stream`, what the call allocates belongs to that stream, as in
+    newton_schulz.
+    """
+    import torch
+    what = "mx_quantize"
+    if along not in ("rows", "cols", "both"):
+        raise ValueError(f"{what}: along must be 'rows', 'cols' or 'both'")
+    if x.dim() not in (1, 2):
+        raise ValueError(f"{what}: x must be 1-D or 2-D")
+    rows, cols = x.shape if x.dim() == 2 else (1, x.shape[0])
+    kind = _mx4_type(x, what)
+    ld = _mx4_rows(x, rows, cols, what)
+    shapes = {"rows": [(rows, cols)], "cols": [(cols, rows)],
+              "both": [(rows, cols), (cols, rows)]}[along]
+    rnd = None
+    if seed is not None:
+        if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+            raise ValueError(f"{what}: seed and offset must be in 0..2^64 - 1")
+        rnd = MxRandom(seed, offset)
+    s = _stream(stream, x)
+    if out is None:
+        with _allocating_on(stream, s, x.device):
+            outs = [Mx4.empty(*sh, x.device) for sh in shapes]
+        if stream is not None:
+            for o in outs:
+                o.codes.record_stream(torch.cuda.current_stream(x.device))
+                o.scales.record_stream(torch.cuda.current_stream(x.device))
+    else:
+        outs = list(out) if along == "both" else [out]
+        if [o.shape for o in outs] != shapes:
+            raise ValueError(f"{what}: out has the wrong shape")
+        _same_device(x.device, [o.codes for o in outs], what)
+    a = outs[0] if along != "cols" else None
+    t = outs[-1] if along != "rows" else None
+    _check(lib().sbp_mx_quantize(
+        x.data_ptr(), kind, rows, cols, ld,
+        a.codes.data_ptr() if a else None, a.scales.data_ptr() if a else None,
+        t.codes.data_ptr() if t else None, t.scales.data_ptr() if t else None,
+        ctypes.byref(rnd) if rnd else None, s))
+    return tuple(outs) if along == "both" else outs[0]
+
+
+def mx_dequantize(q, out=None, dtype=None, stream=None):
+    """sbp_mx_dequantize: an Mx4's values, bf16 unless `dtype` (or out) says
+    float32.  out: device tensor of q's shape, rows at any distance (1-D for one
+    row); a new one [rows, cols] when not given."""
+    import torch
+    what = "mx_dequantize"
+    s = _stream(stream, q.codes)
+    if out is None:
+        with _allocating_on(stream, s, q.device):
+            out = torch.empty(q.shape, dtype=dtype or torch.bfloat16, device=q.device)
+        if stream is not None:
+            out.record_stream(torch.cuda.current_stream(q.device))
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"{what}: out is {out.dtype}, not {dtype}")
+    kind = _mx4_type(out, what)
+    ld = _mx4_rows(out, q.rows, q.cols, what)
+    _same_device(q.device, [out], what)
+    _check(lib().sbp_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+                                    out.data_ptr(), kind, ld, s))
+    return out
+
+
+def mx_reduce_shard(peers, acc, scale, out, stream=None):
+    """sbp_mx_reduce_shard: out = (acc + ascending fp32 sum of the peers) * scale.
+
+    peers: Mx4 of out.numel() values each, as flat buffers: one row, or rows of a
+    multiple of 32 values.  acc: float32 or None; may be out itself."""
+    what = "mx_reduce_shard"
+    n = out.numel()
+    if acc is not None and acc.numel() != n:
+        raise ValueError(f"{what}: acc and out differ in size")
+    for p in peers:
+        if p.numel != n:
+            raise ValueError(f"{what}: a peer has {p.numel} values, out {n}")
+        if p.rows > 1 and p.cols % MX_BLOCK:
+            raise ValueError(f"{what}: a peer of several rows needs a multiple of {MX_BLOCK} "
+                             "columns")
+    _same_device(out.device, [acc] + [p.codes for p in peers], what)
+    R = len(peers)
+    codes = (ctypes.c_void_p * max(R, 1))(*[_dev(p.codes, 1, what) for p in peers])
+    scales = (ctypes.c_void_p * max(R, 1))(*[p.scales.data_ptr() for p in peers])
+    _check(lib().sbp_mx_reduce_shard(
+        codes, scales, R, n, None if acc is None else _f32(acc, f"{what} acc"), float(scale),
+        _f32(out, f"{what} out"), _stream(stream, out)))
+
+
+def mx_matmul_workspace(m, n, k):
+    """Bytes of workspace sbp_mx_matmul needs for m x k times (n x k)'."""
+    need = lib().sbp_mx_matmul_workspace(int(m), int(n), int(k))
+    if need < 0:
+        raise SbpError(SBP_EINVAL if min(m, n, k) < 0 else SBP_ERANGE,
+                       lib().sbp_last_error().decode())
+    return int(need)
+
+
+def mx_matmul(a, b, out=None, dtype=None, accumulate=False, workspace=None, stream=None):
+    """sbp_mx_matmul: a b' of two Mx4 with the same number of columns.
+
+    out: device tensor [a.rows, b.rows], bf16 or float32, rows at any distance;
+    a new one (bf16 unless `dtype` says float32) when not given.  accumulate:
+    add to out (float32).  workspace: a device tensor of at least
+    mx_matmul_workspace(a.rows, b.rows, a.cols) bytes; allocated with torch when
+    not given.  Returns out.
+
+    With `stream`, what the call allocates belongs to that stream, as in
+    newton_schulz.
+    """
+    import torch
+    what = "mx_matmul"
+    if a.cols != b.cols:
+        raise ValueError(f"{what}: operands of {a.cols} and {b.cols} columns")
+    m, n, k = a.rows, b.rows, a.cols
+    if accumulate and out is None:
+        raise ValueError(f"{what}: nothing to accumulate into")
+    s = _stream(stream, a.codes)
+    need = mx_matmul_workspace(m, n, k)
+    with _allocating_on(stream, s, a.device):
+        own_out = out is None
+        if own_out:
+            out = torch.empty((m, n), dtype=dtype or torch.bfloat16, device=a.device)
+        elif dtype is not None and out.dtype != dtype:
+            raise ValueError(f"{what}: out is {out.dtype}, not {dtype}")
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+    if own_out and stream is not None:
+        out.record_stream(torch.cuda.current_stream(a.device))
+    kind = _mx4_type(out, what)
+    ld = _mx4_rows(out, m, n, what)
+    _same_device(a.device, [b.codes, out, workspace], what)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be contiguous")
+    _check(lib().sbp_mx_matmul(
+        a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), m, n, k,
+        out.data_ptr(), kind, ld, 1 if accumulate else 0,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+    return out
 
 
 def unpack_params(plan, flat, params, bucket=-1, stream=None):
