@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "bf16.h"
 #include "internal.h"
@@ -125,6 +126,301 @@ __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
   }
 }
 
+// ---- tiles --------------------------------------------------------------------------
+// One T x T tile of C per block of 4 waves (2 x 2, each a quarter in 16 x 16 MFMA
+// tiles).  Slices of 128 contracted values (64 bytes of codes a row) go straight
+// from memory to one of four LDS buffers, four slices ahead; the scales, packed
+// beforehand as the instruction takes them, a chunk of four slices at a time.
+template <int T_>
+struct Tile {
+  static constexpr int T = T_, NB = 4;
+  static constexpr int kHalf = T * 64;       // one operand's slice, bytes
+  static constexpr int kBuf = 2 * kHalf;     // A, then B
+  static constexpr int kSub = T / 32;        // 16 x 16 tiles per wave and side
+  static constexpr int kLoads = T * 64 / 4096;  // per operand, slice and lane
+  static constexpr int kScales = T * 16;     // one operand's scales of a chunk, bytes
+  // bytes a lane loads of the two operands' scales at once, and how often
+  static constexpr int kScaleBytes = T >= 128 ? 16 : 4;
+  static constexpr int kScaleLoads = 2 * kScales / (256 * kScaleBytes);
+};
+
+// Row of B (inside a wave's columns) that row i of MFMA tile j holds.  With bf16
+// results a lane's values of two tiles are 8 neighbours, 16 bytes; with fp32 the
+// 4 of one tile are.
+template <bool PAIRS>
+__host__ __device__ __forceinline__ int row_of(int j, int i) {
+  return PAIRS ? (j >> 1) * 32 + (i >> 2) * 8 + (j & 1) * 4 + (i & 3) : j * 16 + i;
+}
+
+// Scales of 16 rows and a chunk of 16 blocks as a wave takes them: lane (r, g)'s
+// word holds those of row r, blocks 4s + g of its slices s = 0 .. 3.  Zeros past
+// the matrix.  packed: [chunk][tile of 16 rows][lane].
+struct Pack {
+  const uint8_t* scales;
+  uint32_t* packed;
+  int64_t rows;
+  int32_t tiles, pairs, sub;  // 16-row tiles, padded; B's order for bf16; tiles per wave
+};
+__global__ void __launch_bounds__(256)
+mx4_pack_kernel(Pack a, Pack b, int64_t kb, unsigned blocks_a) {
+  const bool second = blockIdx.x >= blocks_a;
+  const Pack p = second ? b : a;
+  const int64_t w = static_cast<int64_t>(second ? blockIdx.x - blocks_a : blockIdx.x) * 4 +
+                    (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t chunks = (kb + 15) / 16;
+  if (w >= chunks * p.tiles) return;
+  const int64_t c = w / p.tiles;
+  const int t = static_cast<int>(w - c * p.tiles);
+  const int j = t % p.sub;
+  const int64_t row = static_cast<int64_t>(t - j) * 16 + (p.pairs ? row_of<true>(j, r) : j * 16 + r);
+  uint32_t word = 0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t block = c * 16 + s * 4 + g;
+    if (row < p.rows && block < kb) word |= static_cast<uint32_t>(p.scales[row * kb + block]) << (8 * s);
+  }
+  p.packed[w * 64 + lane] = word;
+}
+
+// `bytes` from p on as a buffer; loads from beyond them give zeros.  Whole offsets
+// go into the vector one: a scalar offset past the end would lift the bound.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// One operand of a tile.  LDS keeps a row's four 16-byte pieces (the blocks of a
+// slice) rotated by row, which spreads the reads over the banks; the rotation
+// comes from the lanes' global addresses.
+template <typename TL, bool PAIRS>
+struct Operand {
+  static constexpr int kSub = TL::kSub;
+  static constexpr int kOut = 0x7FFFFFF0;  // an offset beyond every buffer
+  const char* from;                        // next slice to load
+  int bytes, round_bytes, voff, piece;
+  int at[PAIRS ? 2 : 1];                   // LDS offsets of this lane's first fragments
+  // of the packed scales
+  const char* scales;
+  int scale_voff;
+  int64_t scale_step;
+
+  static __device__ __forceinline__ int turn(int i) {  // of row i of an MFMA tile
+    return (((i >> 1) ^ (i >> 2)) & 2) | (((i >> 3) ^ (i >> 1)) & 1);
+  }
+  static __device__ __forceinline__ int index(int row) {  // its row in its MFMA tile
+    return PAIRS ? ((row >> 3) & 3) * 4 + (row & 3) : row & 15;
+  }
+  // wrow: the wave's first row in the tile
+  __device__ __forceinline__ void init(const char* codes, int64_t rows, int64_t kb, int64_t r0,
+                                       int wave, int lane, int wrow) {
+    from = codes + r0 * kb * 16;
+    const int64_t have = rows - r0 < TL::T ? rows - r0 : TL::T;
+    bytes = static_cast<int>(have * kb * 16);
+    const int row = wave * 16 + lane / 4;
+    piece = (lane & 3) ^ turn(index(row));
+    voff = row * static_cast<int>(kb) * 16 + piece * 16;
+    round_bytes = 64 * static_cast<int>(kb) * 16;
+    const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < (PAIRS ? 2 : 1); ++h)
+      at[h] = (wrow + row_of<PAIRS>(h, i)) * 64 + (g ^ turn(i)) * 16;
+  }
+  __device__ __forceinline__ void load(char* buf, int wave) {
+#pragma unroll
+    for (int r = 0; r < TL::kLoads; ++r)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(from, bytes),
+                                               (lds_ptr)(buf + (r * 4 + wave) * 1024), 16,
+                                               voff + r * round_bytes, 0, 0, 0);
+  }
+  // To the next slice.  A length below 0 would count as a huge one.
+  __device__ __forceinline__ void advance() {
+    from += 64;
+    bytes = bytes > 64 ? bytes - 64 : 0;
+  }
+  // `left` blocks of the rows remain for the next slice: the rest reads as zeros.
+  __device__ __forceinline__ void cut(int64_t left) {
+    if (left < 4) voff = piece < left ? voff : kOut;
+  }
+  __device__ __forceinline__ u32x4 read(const char* buf, int i) const {
+    const int off = PAIRS ? at[i & 1] + (i >> 1) * 32 * 64 : at[0] + i * 16 * 64;
+    return *reinterpret_cast<const u32x4*>(buf + off);
+  }
+};
+
+template <typename TL>
+struct Frags {
+  u32x4 a[TL::kSub], b[TL::kSub];
+};
+template <typename TL>
+struct Scales {
+  uint32_t a[TL::kSub], b[TL::kSub];
+};
+template <typename TL>
+using Acc = f32x4[TL::kSub][TL::kSub];
+
+template <int S>
+__device__ __forceinline__ f32x4 product_of(u32x4 b, uint32_t sb, u32x4 a, uint32_t sa, f32x4 c) {
+  const i32x8 x{static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z),
+                static_cast<int>(b.w), 0, 0, 0, 0};
+  const i32x8 y{static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z),
+                static_cast<int>(a.w), 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, S,
+                                                          static_cast<int>(sb), S,
+                                                          static_cast<int>(sa));
+}
+
+// This wave's loads but the newest LEFT and its LDS reads are done; then everyone's.
+template <int LEFT>
+__device__ __forceinline__ void slice_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | 0x70);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+struct Packed {
+  const char* a;
+  const char* b;
+  int64_t step_a, step_b;  // bytes from chunk to chunk
+};
+
+// kSplit: fp32 partial sums of a part of the contracted axis, to the workspace.
+enum Out { kBf16, kF32, kSplit };
+
+template <typename TL, Out O>
+__global__ void __launch_bounds__(256, TL::T == 256 ? 1 : 2)
+mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
+  constexpr int T = TL::T, kSub = TL::kSub;
+  constexpr bool kPairs = O == kBf16;
+  // separate arrays: reads of one do not wait for loads into another
+  __shared__ __align__(16) char buf0[TL::kBuf];
+  __shared__ __align__(16) char buf1[TL::kBuf];
+  __shared__ __align__(16) char buf2[TL::kBuf];
+  __shared__ __align__(16) char buf3[TL::kBuf];
+  __shared__ __align__(16) char scl0[2 * TL::kScales];
+  __shared__ __align__(16) char scl1[2 * TL::kScales];
+  char* buf[4] = {buf0, buf1, buf2, buf3};
+  char* scl[2] = {scl0, scl1};
+  const unsigned tr = static_cast<unsigned>((p.m + T - 1) / T);
+  const unsigned tc = static_cast<unsigned>((p.n + T - 1) / T);
+  // neighbouring tiles to one XCD, in strips of 8 tile rows, column by column
+  unsigned t = blockIdx.x;
+  const unsigned per = total / 8;
+  if (t < per * 8) t = (t % 8) * per + t / 8;
+  constexpr unsigned kStrip = 8;
+  const unsigned strip = t / (kStrip * tc), left = tr - strip * kStrip;
+  const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
+  const unsigned ti = strip * kStrip + s % high, tj = s / high;
+  const int64_t r0 = static_cast<int64_t>(ti) * T, c0 = static_cast<int64_t>(tj) * T;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wr = (wave >> 1) * (T / 2), wc = (wave & 1) * (T / 2);
+
+  Operand<TL, false> A;
+  Operand<TL, kPairs> B;
+  A.init(p.a, p.m, p.kb, r0, wave, lane, wr);
+  B.init(p.b, p.n, p.kb, c0, wave, lane, wc);
+  const char* pa = packed.a + static_cast<int64_t>(ti) * TL::kScales;
+  const char* pb = packed.b + static_cast<int64_t>(tj) * TL::kScales;
+  int64_t ahead = p.kb;  // blocks from the next slice to load on
+  auto load = [&](char* to) {
+    A.cut(ahead);
+    B.cut(ahead);
+    A.load(to, wave);
+    B.load(to + TL::kHalf, wave);
+    ahead -= 4;
+    A.advance();
+    B.advance();
+  };
+  int scales_left = static_cast<int>((p.kb + 15) / 16);  // the last chunk's are loaded twice
+  auto load_scales = [&](char* to) {
+    constexpr int kWave = 64 * TL::kScaleBytes;
+#pragma unroll
+    for (int r = 0; r < TL::kScaleLoads; ++r) {
+      const int off = (r * 4 + wave) * kWave;  // in A's scales, then B's
+      const char* src = off < TL::kScales ? pa + off : pb + (off - TL::kScales);
+      if constexpr (TL::kScaleBytes == 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(to + off), 16,
+                                                 lane * 16, 0, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(to + off), 4,
+                                                 lane * 4, 0, 0, 0);
+    }
+    if (--scales_left > 0) {
+      pa += packed.step_a;
+      pb += packed.step_b;
+    }
+  };
+  Frags<TL> f[2];
+  Scales<TL> sc[2];
+  auto read = [&](const char* from, Frags<TL>& to) {
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) to.a[i] = A.read(from, i);
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) to.b[j] = B.read(from + TL::kHalf, j);
+  };
+  auto read_scales = [&](const char* from, Scales<TL>& to) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(from) + lane;
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) to.a[i] = w[(wr / 16 + i) * 64];
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) to.b[j] = w[TL::kScales / 4 + (wc / 16 + j) * 64];
+  };
+  Acc<TL> acc;
+#pragma unroll
+  for (int i = 0; i < kSub; ++i)
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  const int chunks = static_cast<int>((p.kb + 15) / 16);
+  constexpr int L = 2 * TL::kLoads, K = TL::kScaleLoads;
+  load_scales(scl[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load(buf[i]);
+  slice_barrier<3 * L>();
+  read_scales(scl[0], sc[0]);
+  read(buf[0], f[0]);
+  // Slice I of chunk c, its fragments in f[I & 1]: once all waves have read it and
+  // the next one is there, its buffer is loaded anew.
+  auto slice = [&](auto i_c, auto chunk_c) {
+    constexpr int I = decltype(i_c)::value, C = decltype(chunk_c)::value;
+    // newer than the next slice: two slices, and scales asked for in their time
+    slice_barrier<2 * L + (I == 1 || I == 2 ? K : 0)>();
+    if constexpr (I == 0) load_scales(scl[C ^ 1]);
+    load(buf[I]);
+    if constexpr (I == 3) read_scales(scl[C ^ 1], sc[C ^ 1]);
+    read(buf[(I + 1) & 3], f[(I + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < kSub; ++i)
+#pragma unroll
+      for (int j = 0; j < kSub; ++j)
+        acc[i][j] = product_of<I>(f[I & 1].b[j], sc[C].b[j], f[I & 1].a[i], sc[C].a[i], acc[i][j]);
+  };
+  auto round = [&](auto chunk_c) {
+    slice(std::integral_constant<int, 0>{}, chunk_c);
+    slice(std::integral_constant<int, 1>{}, chunk_c);
+    slice(std::integral_constant<int, 2>{}, chunk_c);
+    slice(std::integral_constant<int, 3>{}, chunk_c);
+  };
+  for (int c = 0; c < chunks; c += 2) {
+    round(std::integral_constant<int, 0>{});
+    if (c + 1 < chunks) round(std::integral_constant<int, 1>{});
+  }
+  // nothing is left under way into LDS when the block ends
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+
+  const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < kSub; ++i) {
+    const int64_t row = r0 + wr + i * 16 + r;
+    if (row < p.m) {
+#pragma unroll
+      for (int j = 0; j < kSub; ++j)
+        store4(p, row, c0 + wc + row_of<kPairs>(j, g * 4), acc[i][j]);
+    }
+  }
+}
+
 // k == 0
 __global__ void __launch_bounds__(256) mx4_zero_kernel(Problem p) {
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
@@ -143,13 +439,62 @@ sbp_status check_sizes(const Text& w, int64_t m, int64_t n, int64_t k) {
   return SBP_OK;
 }
 
-int64_t workspace_of(int64_t, int64_t, int64_t) { return 0; }
+constexpr int64_t kFewRows = 64;
+
+// Side of the tiles.
+int tile_of(int64_t m, int64_t n) {
+  auto tiles = [&](int64_t T) { return ((m + T - 1) / T) * ((n + T - 1) / T); };
+  if (tiles(256) >= 128) return 256;
+  return tiles(128) >= 192 ? 128 : 64;
+}
+
+struct Layout {
+  int64_t step_a, step_b, bytes;  // of a chunk's packed scales
+};
+Layout layout_of(int64_t m, int64_t n, int64_t kb, int T) {
+  const int64_t a = (m + T - 1) / T * T * 16, b = (n + T - 1) / T * T * 16;
+  return {a, b, (kb + 15) / 16 * (a + b)};
+}
+
+int64_t workspace_of(int64_t m, int64_t n, int64_t k) {
+  if (m <= kFewRows || n == 0 || k == 0) return 0;
+  return layout_of(m, n, sbp::mx4_blocks(k), tile_of(m, n)).bytes;
+}
+
+template <int T>
+sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t stream);
 
 sbp_status launched(const char* who) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess)
     return sbp::fail(SBP_EHIP, Text(who) + ": launch failed: " + hipGetErrorString(e));
   return sbp::ok();
+}
+
+template <int T>
+sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t stream) {
+  using TL = Tile<T>;
+  const Layout l = layout_of(p.m, p.n, p.kb, T);
+  const int64_t chunks = (p.kb + 15) / 16, words_a = l.step_a / 256 * chunks,
+                words_b = l.step_b / 256 * chunks;
+  const Pack a{p.sa, reinterpret_cast<uint32_t*>(ws), p.m, static_cast<int32_t>(l.step_a / 256), 0,
+               TL::kSub};
+  const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * l.step_a), p.n,
+               static_cast<int32_t>(l.step_b / 256), p.f32 ? 0 : 1, TL::kSub};
+  const unsigned blocks_a = static_cast<unsigned>((words_a + 3) / 4);
+  const unsigned blocks_b = static_cast<unsigned>((words_b + 3) / 4);
+  hipLaunchKernelGGL(mx4_pack_kernel, dim3(blocks_a + blocks_b), dim3(256), 0, stream, a, b, p.kb,
+                     blocks_a);
+  sbp_status st = launched(who);
+  if (st != SBP_OK) return st;
+  const unsigned total =
+      static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T));
+  const Packed packed{ws, ws + chunks * l.step_a, l.step_a, l.step_b};
+  if (p.f32)
+    hipLaunchKernelGGL((mx4_tile_kernel<TL, kF32>), dim3(total), dim3(256), 0, stream, p, packed, total);
+  else
+    hipLaunchKernelGGL((mx4_tile_kernel<TL, kBf16>), dim3(total), dim3(256), 0, stream, p, packed, total);
+  return launched(who);
 }
 
 sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_a,
@@ -204,6 +549,13 @@ sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_
                     static_cast<unsigned>(std::min<int64_t>(m, 1024)));
     hipLaunchKernelGGL(mx4_zero_kernel, grid, dim3(256), 0, stream, p);
     return launched(who);
+  }
+  if (m > kFewRows) {
+    char* ws = static_cast<char*>(workspace);
+    const int T = tile_of(m, n);
+    return T == 256   ? run_tiles<256>(who, p, ws, stream)
+           : T == 128 ? run_tiles<128>(who, p, ws, stream)
+                      : run_tiles<64>(who, p, ws, stream);
   }
   const int64_t tiles = ((n + 15) / 16) * ((m + 15) / 16);
   if (tiles >= int64_t{1} << 24) return sbp::fail(SBP_ERANGE, w + ": too many results");

@@ -273,6 +273,24 @@ def test_matmul(m, n, k, form):
     assert bool((rest == 9.0).all())
 
 
+@pytest.mark.parametrize("m,n", [(1700, 1750), (2900, 2950), (2817, 2817)])
+@pytest.mark.parametrize("k", [1, 33, 97, 128, 129, 500, 512, 520, 1100])
+@pytest.mark.parametrize("form", ["bf16", "accumulate"])
+def test_matmul_large(m, n, k, form):
+    """Larger tiles, at contracted lengths that end anywhere in a slice and in a
+    chunk of four."""
+    import torch
+    a, av = _operand(m, k, 15)
+    b, bv = _operand(n, k, 25)
+    if form == "bf16":
+        out, before = sbp.mx_matmul(a, b), None
+    else:
+        out = torch.randn(m, n, device=H.dev())
+        before = out.cpu().numpy()
+        sbp.mx_matmul(a, b, out, accumulate=True)
+    _check_product(out.float().cpu().numpy(), av, bv, form == "bf16", before, f"{m}x{n}x{k}")
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 512, 1024), (50, 70, 300), (300, 512, 512), (513, 300, 640)])
 @pytest.mark.parametrize("ld,shift", [(0, 0), (1, 0), (8, 1), (3, 5)])
 def test_matmul_output_strides(m, n, k, ld, shift):
@@ -289,7 +307,8 @@ def test_matmul_output_strides(m, n, k, ld, shift):
         assert bool((rest == 9.0).all())
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 40, 200), (70, 90, 1000), (300, 280, 700), (520, 530, 300)])
+@pytest.mark.parametrize("m,n,k", [(3, 40, 200), (70, 90, 1000), (300, 280, 700), (520, 530, 300),
+                                   (1700, 1730, 300), (2900, 2950, 300)])
 def test_matmul_nan_stays_in_its_row(m, n, k):
     """A NaN block of A takes its row of C, one of B its column; the rest has the
     same bits as without them."""
