@@ -215,8 +215,10 @@ struct Operand {
   __device__ __forceinline__ void init(const char* codes, int64_t rows, int64_t kb, int64_t r0,
                                        int wave, int lane, int wrow) {
     from = codes + r0 * kb * 16;
-    const int64_t have = rows - r0 < TL::T ? rows - r0 : TL::T;
-    bytes = static_cast<int>(have * kb * 16);
+    // a 64-bit comparison is a vector instruction: the descriptor has to be scalar
+    const int have = __builtin_amdgcn_readfirstlane(
+        rows - r0 < TL::T ? static_cast<int>(rows - r0) : TL::T);
+    bytes = have * static_cast<int>(kb) * 16;
     const int row = wave * 16 + lane / 4;
     piece = (lane & 3) ^ turn(index(row));
     voff = row * static_cast<int>(kb) * 16 + piece * 16;
@@ -226,20 +228,19 @@ struct Operand {
     for (int h = 0; h < (PAIRS ? 2 : 1); ++h)
       at[h] = (wrow + row_of<PAIRS>(h, i)) * 64 + (g ^ turn(i)) * 16;
   }
-  __device__ __forceinline__ void load(char* buf, int wave) {
-#pragma unroll
-    for (int r = 0; r < TL::kLoads; ++r)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(from, bytes),
-                                               (lds_ptr)(buf + (r * 4 + wave) * 1024), 16,
-                                               voff + r * round_bytes, 0, 0, 0);
+  __device__ __forceinline__ void load_round(char* buf, int wave, int r) const {
+    // a length below 0 would count as a huge one
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(from, bytes > 0 ? bytes : 0),
+                                             (lds_ptr)(buf + (r * 4 + wave) * 1024), 16,
+                                             voff + r * round_bytes, 0, 0, 0);
   }
-  // To the next slice.  A length below 0 would count as a huge one.
+  // To the next slice; `bytes` may go below 0.
   __device__ __forceinline__ void advance() {
     from += 64;
-    bytes = bytes > 64 ? bytes - 64 : 0;
+    bytes -= 64;
   }
   // `left` blocks of the rows remain for the next slice: the rest reads as zeros.
-  __device__ __forceinline__ void cut(int64_t left) {
+  __device__ __forceinline__ void cut(int left) {
     if (left < 4) voff = piece < left ? voff : kOut;
   }
   __device__ __forceinline__ u32x4 read(const char* buf, int i) const {
@@ -268,6 +269,44 @@ __device__ __forceinline__ f32x4 product_of(u32x4 b, uint32_t sb, u32x4 a, uint3
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, S,
                                                           static_cast<int>(sb), S,
                                                           static_cast<int>(sa));
+}
+
+// The same for one accumulator, in its registers: at the large tile all 256 are
+// taken, and the compiler, free to give a product another place than its summand,
+// moves them about between the products.  It does not see these as matrix
+// instructions, so the wait states that it would fill in are kept by hand:
+// - an accumulator is read or written by anything else 19 or more wait states
+//   after its last product (18 is the longest any needs): settle() ends every run
+//   of products, before any two ways through the code join;
+// - a fragment, scale or accumulator is written by a vector instruction 5 or more
+//   before a product reads it (2 are needed): fragments and scales come from LDS,
+//   whose reads the compiler waits for, and the accumulators' zeros are settled;
+// - a product's own accumulator is used again 64 products later.
+// tests/test_matrix_unit_distances.py reads from a build's disassembly that both
+// distances hold on every path.
+template <int S>
+__device__ __forceinline__ void multiply_in_place(f32x4& c, u32x4 b, uint32_t sb, u32x4 a,
+                                                  uint32_t sa) {
+#define SBP_MX_PRODUCT(LO, HI)                                                       \
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO \
+               "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:4 blgp:4"                 \
+               : "+a"(c)                                                              \
+               : "v"(b), "v"(a), "v"(sb), "v"(sa))
+  if constexpr (S == 0) SBP_MX_PRODUCT("0", "0");
+  if constexpr (S == 1) SBP_MX_PRODUCT("1", "0");
+  if constexpr (S == 2) SBP_MX_PRODUCT("0", "1");
+  if constexpr (S == 3) SBP_MX_PRODUCT("1", "1");
+#undef SBP_MX_PRODUCT
+}
+template <typename TL>
+__device__ __forceinline__ void settle(Acc<TL>& acc) {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < TL::kSub; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::kSub; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // This wave's loads but the newest LEFT and its LDS reads are done; then everyone's.
@@ -311,7 +350,9 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   constexpr unsigned kStrip = 8;
   const unsigned strip = t / (kStrip * tc), left = tr - strip * kStrip;
   const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
-  const unsigned ti = strip * kStrip + s % high, tj = s / high;
+  // the divisions go by vector instructions: back to scalars
+  const unsigned ti = __builtin_amdgcn_readfirstlane(strip * kStrip + s % high);
+  const unsigned tj = __builtin_amdgcn_readfirstlane(s / high);
   const int64_t r0 = static_cast<int64_t>(ti) * T, c0 = static_cast<int64_t>(tj) * T;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = (wave >> 1) * (T / 2), wc = (wave & 1) * (T / 2);
@@ -322,15 +363,23 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   B.init(p.b, p.n, p.kb, c0, wave, lane, wc);
   const char* pa = packed.a + static_cast<int64_t>(ti) * TL::kScales;
   const char* pb = packed.b + static_cast<int64_t>(tj) * TL::kScales;
-  int64_t ahead = p.kb;  // blocks from the next slice to load on
-  auto load = [&](char* to) {
+  int ahead = static_cast<int>(p.kb);  // blocks from the next slice to load on
+  auto begin_load = [&]() {
     A.cut(ahead);
     B.cut(ahead);
-    A.load(to, wave);
-    B.load(to + TL::kHalf, wave);
+  };
+  auto end_load = [&]() {
     ahead -= 4;
     A.advance();
     B.advance();
+  };
+  auto load = [&](char* to) {
+    begin_load();
+#pragma unroll
+    for (int r = 0; r < TL::kLoads; ++r) A.load_round(to, wave, r);
+#pragma unroll
+    for (int r = 0; r < TL::kLoads; ++r) B.load_round(to + TL::kHalf, wave, r);
+    end_load();
   };
   int scales_left = static_cast<int>((p.kb + 15) / 16);  // the last chunk's are loaded twice
   auto load_scales = [&](char* to) {
@@ -372,29 +421,51 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
 #pragma unroll
     for (int j = 0; j < kSub; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  const int chunks = static_cast<int>((p.kb + 15) / 16);
   constexpr int L = 2 * TL::kLoads, K = TL::kScaleLoads;
-  load_scales(scl[0]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load(buf[i]);
-  slice_barrier<3 * L>();
-  read_scales(scl[0], sc[0]);
-  read(buf[0], f[0]);
-  // Slice I of chunk c, its fragments in f[I & 1]: once all waves have read it and
-  // the next one is there, its buffer is loaded anew.
+  // Slice I of a chunk of scales in sc[C], its fragments in f[I & 1]: once all waves
+  // have read it and the next one is there, its buffer is loaded anew.
   auto slice = [&](auto i_c, auto chunk_c) {
     constexpr int I = decltype(i_c)::value, C = decltype(chunk_c)::value;
+    constexpr int now = I & 1, next = now ^ 1;
     // newer than the next slice: two slices, and scales asked for in their time
     slice_barrier<2 * L + (I == 1 || I == 2 ? K : 0)>();
     if constexpr (I == 0) load_scales(scl[C ^ 1]);
-    load(buf[I]);
-    if constexpr (I == 3) read_scales(scl[C ^ 1], sc[C ^ 1]);
-    read(buf[(I + 1) & 3], f[(I + 1) & 1]);
+    const char* from = buf[(I + 1) & 3];
+    if constexpr (T == 256) {
+      begin_load();
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(scl[C ^ 1]) + lane;
 #pragma unroll
-    for (int i = 0; i < kSub; ++i)
+      for (int t = 0; t < kSub * kSub; ++t) {
+        const int i = t / kSub, j = t % kSub;
+        multiply_in_place<I>(acc[i][j], f[now].b[j], sc[C].b[j], f[now].a[i], sc[C].a[i]);
+        if (t % 3 == 0 && t / 3 < 2 * kSub) {
+          const int c = t / 3;
+          if (c < kSub) f[next].a[c] = A.read(from, c);
+          else f[next].b[c - kSub] = B.read(from + TL::kHalf, c - kSub);
+        }
+        if (t % 6 == 2 && t / 6 < L) {
+          const int r = t / 6;
+          if (r < TL::kLoads) A.load_round(buf[I], wave, r);
+          else B.load_round(buf[I] + TL::kHalf, wave, r - TL::kLoads);
+        }
+        if (I == 3 && t % 3 == 1 && t / 3 < 2 * kSub) {
+          const int c = t / 3;
+          if (c < kSub) sc[C ^ 1].a[c] = words[(wr / 16 + c) * 64];
+          else sc[C ^ 1].b[c - kSub] = words[TL::kScales / 4 + (wc / 16 + c - kSub) * 64];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      end_load();
+    } else {
+      load(buf[I]);
+      if constexpr (I == 3) read_scales(scl[C ^ 1], sc[C ^ 1]);
+      read(from, f[next]);
 #pragma unroll
-      for (int j = 0; j < kSub; ++j)
-        acc[i][j] = product_of<I>(f[I & 1].b[j], sc[C].b[j], f[I & 1].a[i], sc[C].a[i], acc[i][j]);
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j)
+          acc[i][j] = product_of<I>(f[now].b[j], sc[C].b[j], f[now].a[i], sc[C].a[i], acc[i][j]);
+    }
   };
   auto round = [&](auto chunk_c) {
     slice(std::integral_constant<int, 0>{}, chunk_c);
@@ -402,10 +473,31 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     slice(std::integral_constant<int, 2>{}, chunk_c);
     slice(std::integral_constant<int, 3>{}, chunk_c);
   };
-  for (int c = 0; c < chunks; c += 2) {
-    round(std::integral_constant<int, 0>{});
-    if (c + 1 < chunks) round(std::integral_constant<int, 1>{});
+  const int chunks = static_cast<int>((p.kb + 15) / 16);
+  auto start = [&](auto chunk_c) {  // with its scales in place C
+    constexpr int C = decltype(chunk_c)::value;
+    load_scales(scl[C]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(buf[i]);
+    if constexpr (T == 256) settle<TL>(acc);
+    slice_barrier<3 * L>();
+    read_scales(scl[C], sc[C]);
+    read(buf[0], f[0]);
+  };
+  // pairs of chunks; an odd one goes before them
+  if (chunks & 1) {
+    start(std::integral_constant<int, 1>{});
+    round(std::integral_constant<int, 1>{});
+    // the compiler places moves where the ways in join
+    if constexpr (T == 256) settle<TL>(acc);
+  } else {
+    start(std::integral_constant<int, 0>{});
   }
+  for (int c = chunks / 2; c > 0; --c) {
+    round(std::integral_constant<int, 0>{});
+    round(std::integral_constant<int, 1>{});
+  }
+  if constexpr (T == 256) settle<TL>(acc);
   // nothing is left under way into LDS when the block ends
   __builtin_amdgcn_s_waitcnt(0x0F70);
 
