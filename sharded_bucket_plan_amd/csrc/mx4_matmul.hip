@@ -23,6 +23,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kFp4 = 4;  // the instruction's operand format
@@ -127,60 +128,61 @@ __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
 }
 
 // ---- tiles --------------------------------------------------------------------------
-// One T x T tile of C per block of 4 waves (2 x 2, each a quarter in 16 x 16 MFMA
-// tiles).  Slices of 128 contracted values (64 bytes of codes a row) go straight
-// from memory to one of four LDS buffers, four slices ahead; the scales, packed
-// beforehand as the instruction takes them, a chunk of four slices at a time.
+// One T x T tile of C per block of 4 waves (2 x 2, each a quarter in 32 x 32 MFMA
+// tiles, 64 contracted values at a time: lane l holds row l % 32's block l / 32).
+// Slices of 128 contracted values (64 bytes of codes a row) go straight from memory
+// to one of four LDS buffers, four slices ahead; the scales, packed beforehand as
+// the instruction takes them, a chunk of four slices at a time.
 template <int T_>
 struct Tile {
-  static constexpr int T = T_, NB = 4;
-  static constexpr int kHalf = T * 64;       // one operand's slice, bytes
-  static constexpr int kBuf = 2 * kHalf;     // A, then B
-  static constexpr int kSub = T / 32;        // 16 x 16 tiles per wave and side
+  static constexpr int T = T_;
+  static constexpr int kHalf = T * 64;          // one operand's slice, bytes
+  static constexpr int kBuf = 2 * kHalf;        // A, then B
+  static constexpr int kSub = T / 64;           // 32 x 32 tiles per wave and side
   static constexpr int kLoads = T * 64 / 4096;  // per operand, slice and lane
-  static constexpr int kScales = T * 16;     // one operand's scales of a chunk, bytes
+  static constexpr int kScales = T * 16;        // one operand's scales of a chunk, bytes
   // bytes a lane loads of the two operands' scales at once, and how often
   static constexpr int kScaleBytes = T >= 128 ? 16 : 4;
   static constexpr int kScaleLoads = 2 * kScales / (256 * kScaleBytes);
 };
 
-// Row of B (inside a wave's columns) that row i of MFMA tile j holds.  With bf16
-// results a lane's values of two tiles are 8 neighbours, 16 bytes; with fp32 the
-// 4 of one tile are.
+// Row of B that row i of an MFMA tile holds.  A lane's results are rows 8q + 4h + t
+// of B for its half h: with fp32 results four neighbours are 16 bytes; with bf16
+// bits 2 and 3 change places, which makes 8 neighbours of two of the fours.
 template <bool PAIRS>
-__host__ __device__ __forceinline__ int row_of(int j, int i) {
-  return PAIRS ? (j >> 1) * 32 + (i >> 2) * 8 + (j & 1) * 4 + (i & 3) : j * 16 + i;
+__host__ __device__ __forceinline__ int row_of(int i) {
+  return PAIRS ? (i & ~12) | ((i >> 1) & 4) | ((i << 1) & 8) : i;
 }
 
-// Scales of 16 rows and a chunk of 16 blocks as a wave takes them: lane (r, g)'s
-// word holds those of row r, blocks 4s + g of its slices s = 0 .. 3.  Zeros past
-// the matrix.  packed: [chunk][tile of 16 rows][lane].
+// Scales of 32 rows and a chunk of 16 blocks as a wave takes them: lane (r, h) has
+// two words, byte s % 4 of word s / 4 the scale of row r, block 2s + h, for its
+// steps s = 0 .. 7 of 64 values.  Zeros past the matrix.
+// packed: [chunk][tile of 32 rows][lane][word].
 struct Pack {
   const uint8_t* scales;
   uint32_t* packed;
   int64_t rows;
-  int32_t tiles, pairs, sub;  // 16-row tiles, padded; B's order for bf16; tiles per wave
+  int32_t tiles, pairs;  // 32-row tiles, padded; B's order for bf16
 };
 __global__ void __launch_bounds__(256)
 mx4_pack_kernel(Pack a, Pack b, int64_t kb, unsigned blocks_a) {
   const bool second = blockIdx.x >= blocks_a;
   const Pack p = second ? b : a;
-  const int64_t w = static_cast<int64_t>(second ? blockIdx.x - blocks_a : blockIdx.x) * 4 +
-                    (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t w = static_cast<int64_t>(second ? blockIdx.x - blocks_a : blockIdx.x) * 2 +
+                    (threadIdx.x >> 7);
+  const int lane = (threadIdx.x >> 1) & 63, word = threadIdx.x & 1, h = lane >> 5;
   const int64_t chunks = (kb + 15) / 16;
   if (w >= chunks * p.tiles) return;
-  const int64_t c = w / p.tiles;
-  const int t = static_cast<int>(w - c * p.tiles);
-  const int j = t % p.sub;
-  const int64_t row = static_cast<int64_t>(t - j) * 16 + (p.pairs ? row_of<true>(j, r) : j * 16 + r);
-  uint32_t word = 0;
+  const int64_t c = w / p.tiles, t = w - c * p.tiles;
+  const int64_t row = t * 32 + (p.pairs ? row_of<true>(lane & 31) : lane & 31);
+  uint32_t out = 0;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int64_t block = c * 16 + s * 4 + g;
-    if (row < p.rows && block < kb) word |= static_cast<uint32_t>(p.scales[row * kb + block]) << (8 * s);
+    const int64_t block = c * 16 + (word * 4 + s) * 2 + h;
+    if (row < p.rows && block < kb)
+      out |= static_cast<uint32_t>(p.scales[row * kb + block]) << (8 * s);
   }
-  p.packed[w * 64 + lane] = word;
+  p.packed[w * 128 + (threadIdx.x & 127)] = out;
 }
 
 // `bytes` from p on as a buffer; loads from beyond them give zeros.  Whole offsets
@@ -195,21 +197,13 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // comes from the lanes' global addresses.
 template <typename TL, bool PAIRS>
 struct Operand {
-  static constexpr int kSub = TL::kSub;
   static constexpr int kOut = 0x7FFFFFF0;  // an offset beyond every buffer
   const char* from;                        // next slice to load
   int bytes, round_bytes, voff, piece;
-  int at[PAIRS ? 2 : 1];                   // LDS offsets of this lane's first fragments
-  // of the packed scales
-  const char* scales;
-  int scale_voff;
-  int64_t scale_step;
+  int at[2];                               // LDS offsets of this lane's first fragments
 
   static __device__ __forceinline__ int turn(int i) {  // of row i of an MFMA tile
     return (((i >> 1) ^ (i >> 2)) & 2) | (((i >> 3) ^ (i >> 1)) & 1);
-  }
-  static __device__ __forceinline__ int index(int row) {  // its row in its MFMA tile
-    return PAIRS ? ((row >> 3) & 3) * 4 + (row & 3) : row & 15;
   }
   // wrow: the wave's first row in the tile
   __device__ __forceinline__ void init(const char* codes, int64_t rows, int64_t kb, int64_t r0,
@@ -220,13 +214,13 @@ struct Operand {
         rows - r0 < TL::T ? static_cast<int>(rows - r0) : TL::T);
     bytes = have * static_cast<int>(kb) * 16;
     const int row = wave * 16 + lane / 4;
-    piece = (lane & 3) ^ turn(index(row));
+    piece = (lane & 3) ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
     voff = row * static_cast<int>(kb) * 16 + piece * 16;
     round_bytes = 64 * static_cast<int>(kb) * 16;
-    const int i = lane & 15, g = lane >> 4;
+    const int i = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int h = 0; h < (PAIRS ? 2 : 1); ++h)
-      at[h] = (wrow + row_of<PAIRS>(h, i)) * 64 + (g ^ turn(i)) * 16;
+    for (int k = 0; k < 2; ++k)
+      at[k] = (wrow + row_of<PAIRS>(i)) * 64 + ((2 * k + h) ^ turn(i)) * 16;
   }
   __device__ __forceinline__ void load_round(char* buf, int wave, int r) const {
     // a length below 0 would count as a huge one
@@ -243,32 +237,33 @@ struct Operand {
   __device__ __forceinline__ void cut(int left) {
     if (left < 4) voff = piece < left ? voff : kOut;
   }
-  __device__ __forceinline__ u32x4 read(const char* buf, int i) const {
-    const int off = PAIRS ? at[i & 1] + (i >> 1) * 32 * 64 : at[0] + i * 16 * 64;
-    return *reinterpret_cast<const u32x4*>(buf + off);
+  // Step k of a slice, MFMA tile i.
+  __device__ __forceinline__ u32x4 read(const char* buf, int k, int i) const {
+    return *reinterpret_cast<const u32x4*>(buf + at[k] + i * 32 * 64);
   }
 };
 
 template <typename TL>
-struct Frags {
-  u32x4 a[TL::kSub], b[TL::kSub];
+struct Frags {  // of a slice's two steps
+  u32x4 a[2][TL::kSub], b[2][TL::kSub];
 };
 template <typename TL>
-struct Scales {
-  uint32_t a[TL::kSub], b[TL::kSub];
+struct Scales {  // of a chunk
+  u32x2 a[TL::kSub], b[TL::kSub];
 };
 template <typename TL>
-using Acc = f32x4[TL::kSub][TL::kSub];
+using Acc = f32x16[TL::kSub][TL::kSub];
 
+// Step S of a chunk.
 template <int S>
-__device__ __forceinline__ f32x4 product_of(u32x4 b, uint32_t sb, u32x4 a, uint32_t sa, f32x4 c) {
+__device__ __forceinline__ f32x16 product_of(u32x4 b, u32x2 sb, u32x4 a, u32x2 sa, f32x16 c) {
   const i32x8 x{static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z),
                 static_cast<int>(b.w), 0, 0, 0, 0};
   const i32x8 y{static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z),
                 static_cast<int>(a.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, S,
-                                                          static_cast<int>(sb), S,
-                                                          static_cast<int>(sa));
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kFp4, kFp4, S & 3,
+                                                         static_cast<int>(sb[S >> 2]), S & 3,
+                                                         static_cast<int>(sa[S >> 2]));
 }
 
 // The same for one accumulator, in its registers: at the large tile all 256 are
@@ -281,21 +276,22 @@ __device__ __forceinline__ f32x4 product_of(u32x4 b, uint32_t sb, u32x4 a, uint3
 // - a fragment, scale or accumulator is written by a vector instruction 5 or more
 //   before a product reads it (2 are needed): fragments and scales come from LDS,
 //   whose reads the compiler waits for, and the accumulators' zeros are settled;
-// - a product's own accumulator is used again 64 products later.
+// - a product's own accumulator is used again 16 products later.
 // tests/test_matrix_unit_distances.py reads from a build's disassembly that both
 // distances hold on every path.
 template <int S>
-__device__ __forceinline__ void multiply_in_place(f32x4& c, u32x4 b, uint32_t sb, u32x4 a,
-                                                  uint32_t sa) {
-#define SBP_MX_PRODUCT(LO, HI)                                                       \
-  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO \
+__device__ __forceinline__ void multiply_in_place(f32x16& c, u32x4 b, u32x2 sb, u32x4 a,
+                                                  u32x2 sa) {
+  const uint32_t wb = sb[S >> 2], wa = sa[S >> 2];
+#define SBP_MX_PRODUCT(LO, HI)                                                        \
+  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO  \
                "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:4 blgp:4"                 \
                : "+a"(c)                                                              \
-               : "v"(b), "v"(a), "v"(sb), "v"(sa))
-  if constexpr (S == 0) SBP_MX_PRODUCT("0", "0");
-  if constexpr (S == 1) SBP_MX_PRODUCT("1", "0");
-  if constexpr (S == 2) SBP_MX_PRODUCT("0", "1");
-  if constexpr (S == 3) SBP_MX_PRODUCT("1", "1");
+               : "v"(b), "v"(a), "v"(wb), "v"(wa))
+  if constexpr ((S & 3) == 0) SBP_MX_PRODUCT("0", "0");
+  if constexpr ((S & 3) == 1) SBP_MX_PRODUCT("1", "0");
+  if constexpr ((S & 3) == 2) SBP_MX_PRODUCT("0", "1");
+  if constexpr ((S & 3) == 3) SBP_MX_PRODUCT("1", "1");
 #undef SBP_MX_PRODUCT
 }
 template <typename TL>
@@ -324,8 +320,35 @@ struct Packed {
   int64_t step_a, step_b;  // bytes from chunk to chunk
 };
 
-// kSplit: fp32 partial sums of a part of the contracted axis, to the workspace.
-enum Out { kBf16, kF32, kSplit };
+enum Out { kBf16, kF32, kAdd };
+
+// The 16 bytes at `c` (a multiple of their number of values) of a row of C.
+template <Out O>
+__device__ __forceinline__ void store_piece(const Problem& p, int64_t row, int64_t c, u32x4 w) {
+  constexpr int kN = O == kBf16 ? 8 : 4;
+  const int64_t at = row * p.ld + c;
+  if constexpr (O == kBf16) {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+    if (p.vec && c + kN <= p.n) {
+      *reinterpret_cast<u32x4*>(o) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (c + i < p.n) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    float* o = static_cast<float*>(p.out) + at;
+    f32x4 v = __builtin_bit_cast(f32x4, w);
+    if (p.vec && c + kN <= p.n) {
+      if constexpr (O == kAdd) v = *reinterpret_cast<const f32x4*>(o) + v;
+      *reinterpret_cast<f32x4*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (c + i < p.n) o[i] = O == kAdd ? o[i] + v[i] : v[i];
+    }
+  }
+}
 
 template <typename TL, Out O>
 __global__ void __launch_bounds__(256, TL::T == 256 ? 1 : 2)
@@ -402,24 +425,32 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   };
   Frags<TL> f[2];
   Scales<TL> sc[2];
+  constexpr int kReads = 4 * kSub;
+  auto read_one = [&](const char* from, Frags<TL>& to, int c) {  // c: 0 .. kReads - 1
+    const int k = c / (2 * kSub), i = c % (2 * kSub);
+    if (i < kSub) to.a[k][i] = A.read(from, k, i);
+    else to.b[k][i - kSub] = B.read(from + TL::kHalf, k, i - kSub);
+  };
+  auto read_scale = [&](const char* from, Scales<TL>& to, int c) {  // c: 0 .. 2 * kSub - 1
+    const u32x2* w = reinterpret_cast<const u32x2*>(from) + lane;
+    if (c < kSub) to.a[c] = w[(wr / 32 + c) * 64];
+    else to.b[c - kSub] = w[TL::kScales / 8 + (wc / 32 + c - kSub) * 64];
+  };
   auto read = [&](const char* from, Frags<TL>& to) {
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) to.a[i] = A.read(from, i);
-#pragma unroll
-    for (int j = 0; j < kSub; ++j) to.b[j] = B.read(from + TL::kHalf, j);
+    for (int c = 0; c < kReads; ++c) read_one(from, to, c);
   };
   auto read_scales = [&](const char* from, Scales<TL>& to) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(from) + lane;
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) to.a[i] = w[(wr / 16 + i) * 64];
-#pragma unroll
-    for (int j = 0; j < kSub; ++j) to.b[j] = w[TL::kScales / 4 + (wc / 16 + j) * 64];
+    for (int c = 0; c < 2 * kSub; ++c) read_scale(from, to, c);
   };
   Acc<TL> acc;
 #pragma unroll
   for (int i = 0; i < kSub; ++i)
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < kSub; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   constexpr int L = 2 * TL::kLoads, K = TL::kScaleLoads;
   // Slice I of a chunk of scales in sc[C], its fragments in f[I & 1]: once all waves
@@ -433,25 +464,19 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     const char* from = buf[(I + 1) & 3];
     if constexpr (T == 256) {
       begin_load();
-      const uint32_t* words = reinterpret_cast<const uint32_t*>(scl[C ^ 1]) + lane;
+      constexpr int kAll = kSub * kSub;
 #pragma unroll
-      for (int t = 0; t < kSub * kSub; ++t) {
-        const int i = t / kSub, j = t % kSub;
-        multiply_in_place<I>(acc[i][j], f[now].b[j], sc[C].b[j], f[now].a[i], sc[C].a[i]);
-        if (t % 3 == 0 && t / 3 < 2 * kSub) {
-          const int c = t / 3;
-          if (c < kSub) f[next].a[c] = A.read(from, c);
-          else f[next].b[c - kSub] = B.read(from + TL::kHalf, c - kSub);
-        }
-        if (t % 6 == 2 && t / 6 < L) {
-          const int r = t / 6;
+      for (int t = 0; t < 2 * kAll; ++t) {
+        const int i = t % kAll / kSub, j = t % kSub;
+        if (t < kAll) multiply_in_place<2 * I>(acc[i][j], f[now].b[0][j], sc[C].b[j], f[now].a[0][i], sc[C].a[i]);
+        else multiply_in_place<2 * I + 1>(acc[i][j], f[now].b[1][j], sc[C].b[j], f[now].a[1][i], sc[C].a[i]);
+        // two reads, then a load, under each three products
+        if (t % 3 < 2 && t / 3 * 2 + t % 3 < kReads) read_one(from, f[next], t / 3 * 2 + t % 3);
+        if (t % 3 == 2 && t / 3 < L) {
+          const int r = t / 3;
           if (r < TL::kLoads) A.load_round(buf[I], wave, r);
           else B.load_round(buf[I] + TL::kHalf, wave, r - TL::kLoads);
-        }
-        if (I == 3 && t % 3 == 1 && t / 3 < 2 * kSub) {
-          const int c = t / 3;
-          if (c < kSub) sc[C ^ 1].a[c] = words[(wr / 16 + c) * 64];
-          else sc[C ^ 1].b[c - kSub] = words[TL::kScales / 4 + (wc / 16 + c - kSub) * 64];
+          if (I == 3) read_scale(scl[C ^ 1], sc[C ^ 1], r);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -464,7 +489,12 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
       for (int i = 0; i < kSub; ++i)
 #pragma unroll
         for (int j = 0; j < kSub; ++j)
-          acc[i][j] = product_of<I>(f[now].b[j], sc[C].b[j], f[now].a[i], sc[C].a[i], acc[i][j]);
+          acc[i][j] = product_of<2 * I>(f[now].b[0][j], sc[C].b[j], f[now].a[0][i], sc[C].a[i], acc[i][j]);
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j)
+          acc[i][j] = product_of<2 * I + 1>(f[now].b[1][j], sc[C].b[j], f[now].a[1][i], sc[C].a[i], acc[i][j]);
     }
   };
   auto round = [&](auto chunk_c) {
@@ -498,17 +528,51 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     round(std::integral_constant<int, 1>{});
   }
   if constexpr (T == 256) settle<TL>(acc);
-  // nothing is left under way into LDS when the block ends
-  __builtin_amdgcn_s_waitcnt(0x0F70);
-
-  const int r = lane & 15, g = lane >> 4;
+  // All loads into LDS have ended and all waves have read theirs: its buffers are
+  // free.  Results pass through it, 32 rows of the wave's at a time, for stores of
+  // whole rows; 16-byte pieces are rotated by row against bank conflicts.
+  slice_barrier<0>();
+  constexpr int kPiece = O == kBf16 ? 8 : 4;              // values
+  constexpr int kPieces = (T / 2) / kPiece;               // of a row
+  constexpr int kTurn = kPieces < 16 ? kPieces : 16;
+  constexpr int kRows = 64 / kPieces;                     // a store covers
+  static_assert(32 * kPieces * 16 <= TL::kBuf, "a wave's rows fit one buffer");
+  char* slab = buf[0];
+  if (wave == 1) slab = buf[1];
+  if (wave == 2) slab = buf[2];
+  if (wave == 3) slab = buf[3];
+  auto place = [&](int row, int piece) {
+    return reinterpret_cast<u32x4*>(slab + row * (kPieces * 16) +
+                                    (piece ^ (row / (16 / kTurn) % kTurn)) * 16);
+  };
+  const int r = lane & 31, h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < kSub; ++i) {
-    const int64_t row = r0 + wr + i * 16 + r;
-    if (row < p.m) {
 #pragma unroll
-      for (int j = 0; j < kSub; ++j)
-        store4(p, row, c0 + wc + row_of<kPairs>(j, g * 4), acc[i][j]);
+    for (int j = 0; j < kSub; ++j) {
+      const f32x16 v = acc[i][j];
+      if constexpr (O == kBf16) {
+        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          bf16x8 w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = static_cast<__bf16>(v[q * 8 + e]);
+          *place(r, j * 4 + q * 2 + h) = __builtin_bit_cast(u32x4, w);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *place(r, j * 8 + q * 2 + h) = __builtin_bit_cast(
+              u32x4, f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]});
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 32 / kRows; ++q) {
+      const int row = q * kRows + lane / kPieces, piece = lane % kPieces;
+      const u32x4 w = *place(row, piece);
+      const int64_t at = r0 + wr + i * 32 + row, c = c0 + wc + piece * kPiece;
+      if (at < p.m && c < p.n) store_piece<O>(p, at, c, w);
     }
   }
 }
@@ -567,26 +631,25 @@ template <int T>
 sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t stream) {
   using TL = Tile<T>;
   const Layout l = layout_of(p.m, p.n, p.kb, T);
-  const int64_t chunks = (p.kb + 15) / 16, words_a = l.step_a / 256 * chunks,
-                words_b = l.step_b / 256 * chunks;
-  const Pack a{p.sa, reinterpret_cast<uint32_t*>(ws), p.m, static_cast<int32_t>(l.step_a / 256), 0,
-               TL::kSub};
-  const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * l.step_a), p.n,
-               static_cast<int32_t>(l.step_b / 256), p.f32 ? 0 : 1, TL::kSub};
-  const unsigned blocks_a = static_cast<unsigned>((words_a + 3) / 4);
-  const unsigned blocks_b = static_cast<unsigned>((words_b + 3) / 4);
+  const int64_t chunks = (p.kb + 15) / 16;
+  const int32_t tiles_a = static_cast<int32_t>(l.step_a / 512);
+  const int32_t tiles_b = static_cast<int32_t>(l.step_b / 512);
+  const Pack a{p.sa, reinterpret_cast<uint32_t*>(ws), p.m, tiles_a, 0};
+  const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * l.step_a), p.n, tiles_b, !p.f32};
+  const unsigned blocks_a = static_cast<unsigned>((chunks * tiles_a + 1) / 2);
+  const unsigned blocks_b = static_cast<unsigned>((chunks * tiles_b + 1) / 2);
   hipLaunchKernelGGL(mx4_pack_kernel, dim3(blocks_a + blocks_b), dim3(256), 0, stream, a, b, p.kb,
                      blocks_a);
   sbp_status st = launched(who);
   if (st != SBP_OK) return st;
-  const unsigned total =
-      static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T));
+  const unsigned total = static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T));
   const Packed packed{ws, ws + chunks * l.step_a, l.step_a, l.step_b};
-  if (p.f32)
-    hipLaunchKernelGGL((mx4_tile_kernel<TL, kF32>), dim3(total), dim3(256), 0, stream, p, packed, total);
-  else
-    hipLaunchKernelGGL((mx4_tile_kernel<TL, kBf16>), dim3(total), dim3(256), 0, stream, p, packed, total);
-  return launched(who);
+  auto go = [&](auto kernel) -> sbp_status {
+    hipLaunchKernelGGL(kernel, dim3(total), dim3(256), 0, stream, p, packed, total);
+    return launched(who);
+  };
+  if (!p.f32) return go(mx4_tile_kernel<TL, kBf16>);
+  return p.accumulate ? go(mx4_tile_kernel<TL, kAdd>) : go(mx4_tile_kernel<TL, kF32>);
 }
 
 sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_a,

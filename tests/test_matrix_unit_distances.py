@@ -15,7 +15,7 @@ from tests import test_matrix_unit_hazards as HZ
 
 def test_hazards_of_scaled_products_are_found():
     """The scales are operands too: one that a vector instruction just wrote."""
-    mfma = ("v_mfma_scale_f32_16x16x128_f8f6f4 a[0:3], v[0:3], v[4:7], a[0:3], v8, v9 "
+    mfma = ("v_mfma_scale_f32_32x32x64_f8f6f4 a[0:15], v[0:3], v[4:7], a[0:15], v8, v9 "
             "op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4", "")
     end = ("s_endpgm", "")
     assert HZ.hazards(HZ._body([mfma, end])) == []
@@ -54,5 +54,5 @@ def test_large_tile_keeps_its_distances(tmp_path):
             last = max(k for k, i in enumerate(body) if i.mfma)
             moves = [i.text for i in body[first:last] if "accvgpr" in i.op]
             assert all(re.fullmatch(r"v_accvgpr_write_b32 a\d+, 0", m) for m in moves), name
-    # both kinds of results; 64 products a slice, three rounds of four slices
-    assert len(checked) >= 2 and all(n == 64 * 12 for n in checked.values()), checked
+    # the three kinds of results; 32 products a slice, three rounds of four slices
+    assert len(checked) == 3 and all(n == 32 * 12 for n in checked.values()), checked
