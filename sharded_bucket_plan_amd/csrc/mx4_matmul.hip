@@ -157,7 +157,7 @@ __host__ __device__ __forceinline__ int row_of(int i) {
 // Scales of 32 rows and a chunk of 16 blocks as a wave takes them: lane (r, h) has
 // two words, byte s % 4 of word s / 4 the scale of row r, block 2s + h, for its
 // steps s = 0 .. 7 of 64 values.  Zeros past the matrix.
-// packed: [chunk][tile of 32 rows][lane][word].
+// packed: [chunk][tile of 32 rows][word][lane].
 struct Pack {
   const uint8_t* scales;
   uint32_t* packed;
@@ -170,7 +170,7 @@ mx4_pack_kernel(Pack a, Pack b, int64_t kb, unsigned blocks_a) {
   const Pack p = second ? b : a;
   const int64_t w = static_cast<int64_t>(second ? blockIdx.x - blocks_a : blockIdx.x) * 2 +
                     (threadIdx.x >> 7);
-  const int lane = (threadIdx.x >> 1) & 63, word = threadIdx.x & 1, h = lane >> 5;
+  const int lane = threadIdx.x & 63, word = (threadIdx.x >> 6) & 1, h = lane >> 5;
   const int64_t chunks = (kb + 15) / 16;
   if (w >= chunks * p.tiles) return;
   const int64_t c = w / p.tiles, t = w - c * p.tiles;
@@ -199,28 +199,31 @@ template <typename TL, bool PAIRS>
 struct Operand {
   static constexpr int kOut = 0x7FFFFFF0;  // an offset beyond every buffer
   const char* from;                        // next slice to load
-  int bytes, round_bytes, voff, piece;
+  int bytes, round_bytes, all, voff, piece;  // voff: `all`, or kOut past the rows' end
   int at[2];                               // LDS offsets of this lane's first fragments
 
   static __device__ __forceinline__ int turn(int i) {  // of row i of an MFMA tile
     return (((i >> 1) ^ (i >> 2)) & 2) | (((i >> 3) ^ (i >> 1)) & 1);
   }
   // wrow: the wave's first row in the tile
-  __device__ __forceinline__ void init(const char* codes, int64_t rows, int64_t kb, int64_t r0,
-                                       int wave, int lane, int wrow) {
+  __device__ __forceinline__ void init(int kb, int wave, int lane, int wrow) {
+    const int row = wave * 16 + lane / 4;
+    piece = (lane & 3) ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
+    all = row * kb * 16 + piece * 16;
+    round_bytes = 64 * kb * 16;
+    const int i = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      at[k] = (wrow + row_of<PAIRS>(i)) * 64 + ((2 * k + h) ^ turn(i)) * 16;
+  }
+  // At the first slice of the tile of rows r0 ..
+  __device__ __forceinline__ void aim(const char* codes, int64_t rows, int64_t kb, int64_t r0) {
     from = codes + r0 * kb * 16;
     // a 64-bit comparison is a vector instruction: the descriptor has to be scalar
     const int have = __builtin_amdgcn_readfirstlane(
         rows - r0 < TL::T ? static_cast<int>(rows - r0) : TL::T);
     bytes = have * static_cast<int>(kb) * 16;
-    const int row = wave * 16 + lane / 4;
-    piece = (lane & 3) ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
-    voff = row * static_cast<int>(kb) * 16 + piece * 16;
-    round_bytes = 64 * static_cast<int>(kb) * 16;
-    const int i = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      at[k] = (wrow + row_of<PAIRS>(i)) * 64 + ((2 * k + h) ^ turn(i)) * 16;
+    voff = all;
   }
   __device__ __forceinline__ void load_round(char* buf, int wave, int r) const {
     // a length below 0 would count as a huge one
@@ -275,24 +278,29 @@ __device__ __forceinline__ f32x16 product_of(u32x4 b, u32x2 sb, u32x4 a, u32x2 s
 //   of products, before any two ways through the code join;
 // - a fragment, scale or accumulator is written by a vector instruction 5 or more
 //   before a product reads it (2 are needed): fragments and scales come from LDS,
-//   whose reads the compiler waits for, and the accumulators' zeros are settled;
+//   whose reads the compiler waits for;
 // - a product's own accumulator is used again 16 products later.
 // tests/test_matrix_unit_distances.py reads from a build's disassembly that both
 // distances hold on every path.
-template <int S>
+// FIRST: in place of a sum with what was there.
+template <int S, bool FIRST>
 __device__ __forceinline__ void multiply_in_place(f32x16& c, u32x4 b, u32x2 sb, u32x4 a,
                                                   u32x2 sa) {
   const uint32_t wb = sb[S >> 2], wa = sa[S >> 2];
-#define SBP_MX_PRODUCT(LO, HI)                                                        \
-  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO  \
-               "," LO ",0] op_sel_hi:[" HI "," HI ",0] cbsz:4 blgp:4"                 \
-               : "+a"(c)                                                              \
-               : "v"(b), "v"(a), "v"(wb), "v"(wa))
-  if constexpr ((S & 3) == 0) SBP_MX_PRODUCT("0", "0");
-  if constexpr ((S & 3) == 1) SBP_MX_PRODUCT("1", "0");
-  if constexpr ((S & 3) == 2) SBP_MX_PRODUCT("0", "1");
-  if constexpr ((S & 3) == 3) SBP_MX_PRODUCT("1", "1");
+#define SBP_MX_FORM(SUM, LO, HI)                                                           \
+  "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, " SUM ", %3, %4 op_sel:[" LO "," LO        \
+  ",0] op_sel_hi:[" HI "," HI ",0] cbsz:4 blgp:4"
+#define SBP_MX_PRODUCT(LO, HI)                                                             \
+  if constexpr (FIRST)                                                                     \
+    asm volatile(SBP_MX_FORM("0", LO, HI) : "=a"(c) : "v"(b), "v"(a), "v"(wb), "v"(wa));   \
+  else                                                                                     \
+    asm volatile(SBP_MX_FORM("%0", LO, HI) : "+a"(c) : "v"(b), "v"(a), "v"(wb), "v"(wa))
+  if constexpr ((S & 3) == 0) { SBP_MX_PRODUCT("0", "0"); }
+  if constexpr ((S & 3) == 1) { SBP_MX_PRODUCT("1", "0"); }
+  if constexpr ((S & 3) == 2) { SBP_MX_PRODUCT("0", "1"); }
+  if constexpr ((S & 3) == 3) { SBP_MX_PRODUCT("1", "1"); }
 #undef SBP_MX_PRODUCT
+#undef SBP_MX_FORM
 }
 template <typename TL>
 __device__ __forceinline__ void settle(Acc<TL>& acc) {
@@ -322,71 +330,80 @@ struct Packed {
 
 enum Out { kBf16, kF32, kAdd };
 
-// The 16 bytes at `c` (a multiple of their number of values) of a row of C.
+// The 16 bytes of a row of C from column c on, those of them that there are.
 template <Out O>
 __device__ __forceinline__ void store_piece(const Problem& p, int64_t row, int64_t c, u32x4 w) {
   constexpr int kN = O == kBf16 ? 8 : 4;
   const int64_t at = row * p.ld + c;
   if constexpr (O == kBf16) {
     uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-    if (p.vec && c + kN <= p.n) {
-      *reinterpret_cast<u32x4*>(o) = w;
-    } else {
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (c + i < p.n) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
+    for (int i = 0; i < kN; ++i)
+      if (c + i < p.n) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
   } else {
     float* o = static_cast<float*>(p.out) + at;
-    f32x4 v = __builtin_bit_cast(f32x4, w);
-    if (p.vec && c + kN <= p.n) {
-      if constexpr (O == kAdd) v = *reinterpret_cast<const f32x4*>(o) + v;
-      *reinterpret_cast<f32x4*>(o) = v;
-    } else {
+    const f32x4 v = __builtin_bit_cast(f32x4, w);
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (c + i < p.n) o[i] = O == kAdd ? o[i] + v[i] : v[i];
-    }
+    for (int i = 0; i < kN; ++i)
+      if (c + i < p.n) o[i] = O == kAdd ? o[i] + v[i] : v[i];
   }
 }
 
-template <typename TL, Out O>
+// DIRECT: C's rows are made of whole 16-byte pieces on such addresses, a tile's within
+// 2^31 bytes.
+template <typename TL, Out O, bool DIRECT>
 __global__ void __launch_bounds__(256, TL::T == 256 ? 1 : 2)
 mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   constexpr int T = TL::T, kSub = TL::kSub;
-  constexpr bool kPairs = O == kBf16;
+  constexpr bool kPairs = O == kBf16, kLarge = T == 256;
   // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[TL::kBuf];
   __shared__ __align__(16) char buf1[TL::kBuf];
   __shared__ __align__(16) char buf2[TL::kBuf];
   __shared__ __align__(16) char buf3[TL::kBuf];
-  __shared__ __align__(16) char scl0[2 * TL::kScales];
-  __shared__ __align__(16) char scl1[2 * TL::kScales];
+  __shared__ __align__(16) char scl[2 * TL::kScales];
+  // for the results: the large tile's buffers hold the next tile meanwhile
+  constexpr int kSlab = T == 64 && O == kBf16 ? 2048 : 4096;  // a wave's
+  constexpr bool kOwnSlabs = kLarge || 4 * kSlab > TL::kBuf;
+  __shared__ __align__(16) char slabs[kOwnSlabs ? 4 * kSlab : 16];
   char* buf[4] = {buf0, buf1, buf2, buf3};
-  char* scl[2] = {scl0, scl1};
   const unsigned tr = static_cast<unsigned>((p.m + T - 1) / T);
   const unsigned tc = static_cast<unsigned>((p.n + T - 1) / T);
-  // neighbouring tiles to one XCD, in strips of 8 tile rows, column by column
-  unsigned t = blockIdx.x;
-  const unsigned per = total / 8;
-  if (t < per * 8) t = (t % 8) * per + t / 8;
-  constexpr unsigned kStrip = 8;
-  const unsigned strip = t / (kStrip * tc), left = tr - strip * kStrip;
-  const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
-  // the divisions go by vector instructions: back to scalars
-  const unsigned ti = __builtin_amdgcn_readfirstlane(strip * kStrip + s % high);
-  const unsigned tj = __builtin_amdgcn_readfirstlane(s / high);
-  const int64_t r0 = static_cast<int64_t>(ti) * T, c0 = static_cast<int64_t>(tj) * T;
+  // Neighbouring tiles to one XCD: an eighth of them to each.  Of the large ones a
+  // block takes every (blocks / 8)-th of its XCD's.
+  const unsigned per = (total + 7) / 8, step = gridDim.x / 8;
+  unsigned index = blockIdx.x / 8;  // in the XCD's eighth
+  const unsigned base = blockIdx.x % 8 * per;
+  auto exists = [&](unsigned i) { return i < per && base + i < total; };
+  if (!exists(index)) return;
+  struct Place {
+    unsigned ti, tj;
+  };
+  auto place_of = [&](unsigned i) {  // strips of 8 tile rows, column by column
+    constexpr unsigned kStrip = 8;
+    const unsigned t = base + i, strip = t / (kStrip * tc), left = tr - strip * kStrip;
+    const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
+    // the divisions go by vector instructions: back to scalars
+    return Place{static_cast<unsigned>(__builtin_amdgcn_readfirstlane(strip * kStrip + s % high)),
+                 static_cast<unsigned>(__builtin_amdgcn_readfirstlane(s / high))};
+  };
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wr = (wave >> 1) * (T / 2), wc = (wave & 1) * (T / 2);
 
+  // The loads run four slices ahead of the products, on into the next tile.
   Operand<TL, false> A;
   Operand<TL, kPairs> B;
-  A.init(p.a, p.m, p.kb, r0, wave, lane, wr);
-  B.init(p.b, p.n, p.kb, c0, wave, lane, wc);
-  const char* pa = packed.a + static_cast<int64_t>(ti) * TL::kScales;
-  const char* pb = packed.b + static_cast<int64_t>(tj) * TL::kScales;
-  int ahead = static_cast<int>(p.kb);  // blocks from the next slice to load on
+  A.init(static_cast<int>(p.kb), wave, lane, wr);
+  B.init(static_cast<int>(p.kb), wave, lane, wc);
+  const char *pa, *pb;
+  int ahead;  // blocks from the next slice to load on
+  auto aim = [&](Place t) {
+    A.aim(p.a, p.m, p.kb, static_cast<int64_t>(t.ti) * T);
+    B.aim(p.b, p.n, p.kb, static_cast<int64_t>(t.tj) * T);
+    pa = packed.a + static_cast<int64_t>(t.ti) * TL::kScales;
+    pb = packed.b + static_cast<int64_t>(t.tj) * TL::kScales;
+    ahead = static_cast<int>(p.kb);
+  };
   auto begin_load = [&]() {
     A.cut(ahead);
     B.cut(ahead);
@@ -404,177 +421,251 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     for (int r = 0; r < TL::kLoads; ++r) B.load_round(to + TL::kHalf, wave, r);
     end_load();
   };
-  int scales_left = static_cast<int>((p.kb + 15) / 16);  // the last chunk's are loaded twice
-  auto load_scales = [&](char* to) {
+  auto load_scales = [&]() {
     constexpr int kWave = 64 * TL::kScaleBytes;
 #pragma unroll
     for (int r = 0; r < TL::kScaleLoads; ++r) {
       const int off = (r * 4 + wave) * kWave;  // in A's scales, then B's
       const char* src = off < TL::kScales ? pa + off : pb + (off - TL::kScales);
       if constexpr (TL::kScaleBytes == 16)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(to + off), 16,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(scl + off), 16,
                                                  lane * 16, 0, 0, 0);
       else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(to + off), 4,
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(scl + off), 4,
                                                  lane * 4, 0, 0, 0);
     }
-    if (--scales_left > 0) {
-      pa += packed.step_a;
-      pb += packed.step_b;
-    }
+    pa += packed.step_a;
+    pb += packed.step_b;
   };
   Frags<TL> f[2];
-  Scales<TL> sc[2];
+  Scales<TL> sc;
   constexpr int kReads = 4 * kSub;
   auto read_one = [&](const char* from, Frags<TL>& to, int c) {  // c: 0 .. kReads - 1
     const int k = c / (2 * kSub), i = c % (2 * kSub);
     if (i < kSub) to.a[k][i] = A.read(from, k, i);
     else to.b[k][i - kSub] = B.read(from + TL::kHalf, k, i - kSub);
   };
-  auto read_scale = [&](const char* from, Scales<TL>& to, int c) {  // c: 0 .. 2 * kSub - 1
-    const u32x2* w = reinterpret_cast<const u32x2*>(from) + lane;
-    if (c < kSub) to.a[c] = w[(wr / 32 + c) * 64];
-    else to.b[c - kSub] = w[TL::kScales / 8 + (wc / 32 + c - kSub) * 64];
-  };
-  auto read = [&](const char* from, Frags<TL>& to) {
-#pragma unroll
-    for (int c = 0; c < kReads; ++c) read_one(from, to, c);
-  };
-  auto read_scales = [&](const char* from, Scales<TL>& to) {
-#pragma unroll
-    for (int c = 0; c < 2 * kSub; ++c) read_scale(from, to, c);
+  auto read_scale = [&](int word, int c) {  // c: 0 .. 2 * kSub - 1
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(scl) + word * 64 + lane;
+    if (c < kSub) sc.a[c][word] = w[(wr / 32 + c) * 128];
+    else sc.b[c - kSub][word] = w[TL::kScales / 4 + (wc / 32 + c - kSub) * 128];
   };
   Acc<TL> acc;
-#pragma unroll
-  for (int i = 0; i < kSub; ++i)
-#pragma unroll
-    for (int j = 0; j < kSub; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   constexpr int L = 2 * TL::kLoads, K = TL::kScaleLoads;
-  // Slice I of a chunk of scales in sc[C], its fragments in f[I & 1]: once all waves
-  // have read it and the next one is there, its buffer is loaded anew.
-  auto slice = [&](auto i_c, auto chunk_c) {
-    constexpr int I = decltype(i_c)::value, C = decltype(chunk_c)::value;
+  // Stores of a whole tile's results, a wave; 63 is what vmcnt can count.
+  constexpr int kStores = kLarge && DIRECT ? (T / 2) * (T / 2) * (O == kBf16 ? 2 : 4) / 1024 : 0;
+  // Slice I of a chunk, its fragments in f[I & 1]: once all waves have read it and
+  // the next one is there, its buffer is loaded anew.  Slices 0 and 1 use the first
+  // word of a chunk's scales, 2 and 3 the second: that one is read in slice 0, the
+  // next chunk's first in slice 3, and the next chunk's are asked for in slice 1, when
+  // all waves have read this one's.  FIRST: of a tile.
+  auto slice = [&](auto i_c, auto first_c) {
+    constexpr int I = decltype(i_c)::value;
+    constexpr bool kFirst = decltype(first_c)::value;
     constexpr int now = I & 1, next = now ^ 1;
-    // newer than the next slice: two slices, and scales asked for in their time
-    slice_barrier<2 * L + (I == 1 || I == 2 ? K : 0)>();
-    if constexpr (I == 0) load_scales(scl[C ^ 1]);
+    // newer than the next slice: two slices, scales asked for in their time, and the
+    // last tile's stores where the next slice was asked for before them
+    constexpr int kNewer = 2 * L + (I == 2 ? K : 0) + (kFirst && I < 3 ? kStores : 0);
+    slice_barrier<(kNewer < 63 ? kNewer : 63)>();
+    if constexpr (I == 1) load_scales();
     const char* from = buf[(I + 1) & 3];
-    if constexpr (T == 256) {
+    if constexpr (kLarge) {
       begin_load();
       constexpr int kAll = kSub * kSub;
 #pragma unroll
       for (int t = 0; t < 2 * kAll; ++t) {
         const int i = t % kAll / kSub, j = t % kSub;
-        if (t < kAll) multiply_in_place<2 * I>(acc[i][j], f[now].b[0][j], sc[C].b[j], f[now].a[0][i], sc[C].a[i]);
-        else multiply_in_place<2 * I + 1>(acc[i][j], f[now].b[1][j], sc[C].b[j], f[now].a[1][i], sc[C].a[i]);
+        if (t < kAll)
+          multiply_in_place<2 * I, kFirst && I == 0>(acc[i][j], f[now].b[0][j], sc.b[j],
+                                                     f[now].a[0][i], sc.a[i]);
+        else
+          multiply_in_place<2 * I + 1, false>(acc[i][j], f[now].b[1][j], sc.b[j], f[now].a[1][i],
+                                              sc.a[i]);
         // two reads, then a load, under each three products
         if (t % 3 < 2 && t / 3 * 2 + t % 3 < kReads) read_one(from, f[next], t / 3 * 2 + t % 3);
         if (t % 3 == 2 && t / 3 < L) {
           const int r = t / 3;
           if (r < TL::kLoads) A.load_round(buf[I], wave, r);
           else B.load_round(buf[I] + TL::kHalf, wave, r - TL::kLoads);
-          if (I == 3) read_scale(scl[C ^ 1], sc[C ^ 1], r);
+          if (I == 3) read_scale(0, r);
+          if (I == 0) read_scale(1, r);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       end_load();
     } else {
       load(buf[I]);
-      if constexpr (I == 3) read_scales(scl[C ^ 1], sc[C ^ 1]);
-      read(from, f[next]);
+      if constexpr (I == 0 || I == 3) {
+#pragma unroll
+        for (int c = 0; c < 2 * kSub; ++c) read_scale(I == 0 ? 1 : 0, c);
+      }
+#pragma unroll
+      for (int c = 0; c < kReads; ++c) read_one(from, f[next], c);
 #pragma unroll
       for (int i = 0; i < kSub; ++i)
 #pragma unroll
         for (int j = 0; j < kSub; ++j)
-          acc[i][j] = product_of<2 * I>(f[now].b[0][j], sc[C].b[j], f[now].a[0][i], sc[C].a[i], acc[i][j]);
+          acc[i][j] = product_of<2 * I>(f[now].b[0][j], sc.b[j], f[now].a[0][i], sc.a[i],
+                                        acc[i][j]);
 #pragma unroll
       for (int i = 0; i < kSub; ++i)
 #pragma unroll
         for (int j = 0; j < kSub; ++j)
-          acc[i][j] = product_of<2 * I + 1>(f[now].b[1][j], sc[C].b[j], f[now].a[1][i], sc[C].a[i], acc[i][j]);
+          acc[i][j] = product_of<2 * I + 1>(f[now].b[1][j], sc.b[j], f[now].a[1][i], sc.a[i],
+                                            acc[i][j]);
     }
   };
-  auto round = [&](auto chunk_c) {
-    slice(std::integral_constant<int, 0>{}, chunk_c);
-    slice(std::integral_constant<int, 1>{}, chunk_c);
-    slice(std::integral_constant<int, 2>{}, chunk_c);
-    slice(std::integral_constant<int, 3>{}, chunk_c);
+  auto round = [&](auto first_c) {
+    slice(std::integral_constant<int, 0>{}, first_c);
+    slice(std::integral_constant<int, 1>{}, first_c);
+    slice(std::integral_constant<int, 2>{}, first_c);
+    slice(std::integral_constant<int, 3>{}, first_c);
   };
-  const int chunks = static_cast<int>((p.kb + 15) / 16);
-  auto start = [&](auto chunk_c) {  // with its scales in place C
-    constexpr int C = decltype(chunk_c)::value;
-    load_scales(scl[C]);
+
+  constexpr int kPiece = O == kBf16 ? 8 : 4;                   // values
+  constexpr int kSpan = T == 64 ? 32 : 16 * kPiece / 2;        // columns at a time
+  constexpr int kPieces = kSpan / kPiece;                      // of a row: 8 or 4
+  constexpr int kAtOnce = kSpan / 32;                          // MFMA tiles
+  constexpr int kRows = 64 / kPieces;                          // a store covers
+  static_assert(32 * kPieces * 16 == kSlab, "a wave's slab");
+  // Results pass through LDS, 32 rows of 128 bytes at a time, for stores of whole
+  // lines; 16-byte pieces are rotated by row against bank conflicts.  DIRECT: the rows
+  // of C are a buffer, and what lies past C's end is dropped by its bound: always the
+  // same number of stores.
+  auto results = [&](Place t) {
+    // addresses are worked out here, not kept in registers through the products
+    unsigned lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const unsigned r = lane & 31, h = lane >> 5;
+    char* slab = (kOwnSlabs ? slabs : buf0) + wave * kSlab;
+    char* to = slab + r * (kPieces * 16);
+    const unsigned key = (r / (16 / kPieces) % kPieces) ^ h;
+    const unsigned row0 = lane / kPieces, piece = lane % kPieces;
+    const unsigned turned = row0 * (kPieces * 16) + (piece ^ (row0 / (16 / kPieces))) * 16;
+    constexpr int kSize = O == kBf16 ? 2 : 4;
+    const int64_t r0 = static_cast<int64_t>(t.ti) * T + wr;
+    const int64_t c0 = static_cast<int64_t>(t.tj) * T + wc;
+    // as scalars: 64-bit comparisons are vector instructions
+    const int have = __builtin_amdgcn_readfirstlane(
+        static_cast<int>(p.m - r0 < T / 2 ? (p.m > r0 ? p.m - r0 : 0) : T / 2));
+    const int wide = __builtin_amdgcn_readfirstlane(
+        static_cast<int>(p.n - c0 < T / 2 ? (p.n > c0 ? p.n - c0 : 0) : T / 2));
+    char* corner = static_cast<char*>(p.out) + (r0 * p.ld + c0) * kSize;
+    const int line = static_cast<int>(p.ld) * kSize;  // DIRECT: below 2^23
+    // the last row ends with its last column
+    const auto rows = buffer(corner, have > 0 && wide > 0 ? (have - 1) * line + wide * kSize : 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load(buf[i]);
-    if constexpr (T == 256) settle<TL>(acc);
-    slice_barrier<3 * L>();
-    read_scales(scl[C], sc[C]);
-    read(buf[0], f[0]);
-  };
-  // pairs of chunks; an odd one goes before them
-  if (chunks & 1) {
-    start(std::integral_constant<int, 1>{});
-    round(std::integral_constant<int, 1>{});
-    // the compiler places moves where the ways in join
-    if constexpr (T == 256) settle<TL>(acc);
-  } else {
-    start(std::integral_constant<int, 0>{});
-  }
-  for (int c = chunks / 2; c > 0; --c) {
-    round(std::integral_constant<int, 0>{});
-    round(std::integral_constant<int, 1>{});
-  }
-  if constexpr (T == 256) settle<TL>(acc);
-  // All loads into LDS have ended and all waves have read theirs: its buffers are
-  // free.  Results pass through it, 32 rows of the wave's at a time, for stores of
-  // whole rows; 16-byte pieces are rotated by row against bank conflicts.
-  slice_barrier<0>();
-  constexpr int kPiece = O == kBf16 ? 8 : 4;              // values
-  constexpr int kPieces = (T / 2) / kPiece;               // of a row
-  constexpr int kTurn = kPieces < 16 ? kPieces : 16;
-  constexpr int kRows = 64 / kPieces;                     // a store covers
-  static_assert(32 * kPieces * 16 <= TL::kBuf, "a wave's rows fit one buffer");
-  char* slab = buf[0];
-  if (wave == 1) slab = buf[1];
-  if (wave == 2) slab = buf[2];
-  if (wave == 3) slab = buf[3];
-  auto place = [&](int row, int piece) {
-    return reinterpret_cast<u32x4*>(slab + row * (kPieces * 16) +
-                                    (piece ^ (row / (16 / kTurn) % kTurn)) * 16);
-  };
-  const int r = lane & 31, h = lane >> 5;
+    for (int i = 0; i < kSub; ++i) {
 #pragma unroll
-  for (int i = 0; i < kSub; ++i) {
+      for (int j0 = 0; j0 < kSub; j0 += kAtOnce) {
 #pragma unroll
-    for (int j = 0; j < kSub; ++j) {
-      const f32x16 v = acc[i][j];
-      if constexpr (O == kBf16) {
-        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+        for (int j = 0; j < kAtOnce; ++j) {
+          // one after the other: registers are short
+          __builtin_amdgcn_sched_barrier(0);
+          // and not read before their turn
+          if constexpr (kLarge) asm volatile("" : "+a"(acc[i][j0 + j]));
+          const f32x16 v = acc[i][j0 + j];
+          if constexpr (O == kBf16) {
+            typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          bf16x8 w;
+            for (int q = 0; q < 2; ++q) {
+              bf16x8 w;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = static_cast<__bf16>(v[q * 8 + e]);
-          *place(r, j * 4 + q * 2 + h) = __builtin_bit_cast(u32x4, w);
+              for (int e = 0; e < 8; ++e) w[e] = static_cast<__bf16>(v[q * 8 + e]);
+              *reinterpret_cast<u32x4*>(to + ((j * 4 + q * 2) ^ key) * 16) =
+                  __builtin_bit_cast(u32x4, w);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<f32x4*>(to + ((j * 8 + q * 2) ^ key) * 16) =
+                  f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+          }
         }
-      } else {
+        constexpr int kTimes = 32 / kRows;
+        auto from = [&](int q) {  // rows q * kRows ..
+          return reinterpret_cast<const u32x4*>(
+              slab + (q * 1024 + (kPieces == 8 ? turned ^ ((q & 1) * 64u) : turned)));
+        };
+        const int c = j0 * 32 + piece * kPiece;
+        if constexpr (DIRECT) {
+          const unsigned off =
+              c < wide ? (i * 32 + row0) * line + c * kSize : 0x7FFFFFF0u;
+          u32x4 w[kTimes];
+          if constexpr (O == kAdd) {
+            f32x4 old[kTimes];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *place(r, j * 8 + q * 2 + h) = __builtin_bit_cast(
-              u32x4, f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]});
+            for (int q = 0; q < kTimes; ++q)
+              old[q] = __builtin_bit_cast(
+                  f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, off + q * kRows * line, 0, 0));
+#pragma unroll
+            for (int q = 0; q < kTimes; ++q)
+              w[q] = __builtin_bit_cast(u32x4, old[q] + *reinterpret_cast<const f32x4*>(from(q)));
+          } else {
+#pragma unroll
+            for (int q = 0; q < kTimes; ++q) w[q] = *from(q);
+          }
+#pragma unroll
+          for (int q = 0; q < kTimes; ++q)
+            __builtin_amdgcn_raw_buffer_store_b128(w[q], rows, off + q * kRows * line, 0, 0);
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < kTimes; ++q) {
+            const int row = i * 32 + q * kRows + row0;
+            if (row < have && c < wide) store_piece<O>(p, r0 + row, c0 + c, *from(q));
+          }
+        }
       }
     }
+  };
+
+  Place now = place_of(index);
+  aim(now);
+  load_scales();
 #pragma unroll
-    for (int q = 0; q < 32 / kRows; ++q) {
-      const int row = q * kRows + lane / kPieces, piece = lane % kPieces;
-      const u32x4 w = *place(row, piece);
-      const int64_t at = r0 + wr + i * 32 + row, c = c0 + wc + piece * kPiece;
-      if (at < p.m && c < p.n) store_piece<O>(p, at, c, w);
+  for (int i = 0; i < 4; ++i) load(buf[i]);
+  slice_barrier<0>();
+#pragma unroll
+  for (int c = 0; c < 2 * kSub; ++c) read_scale(0, c);
+#pragma unroll
+  for (int c = 0; c < kReads; ++c) read_one(buf[0], f[0], c);
+  const int chunks = static_cast<int>((p.kb + 15) / 16);
+  for (;;) {
+    const bool more = kLarge && exists(index + step);
+    const Place then = more ? place_of(index + step) : now;
+    // from the last chunk on the loads are the next tile's, or none (a length of 0,
+    // and scales that are not used)
+    auto turn_to_next = [&]() {
+      aim(then);
+      if (!more) A.bytes = B.bytes = 0;
+    };
+    if constexpr (!kLarge) {
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+#pragma unroll
+        for (int j = 0; j < kSub; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     }
+    if (chunks == 1) turn_to_next();
+    round(std::true_type{});
+    // the compiler places moves where the ways join
+    if constexpr (kLarge) settle<TL>(acc);
+    for (int c = 1; c < chunks; ++c) {
+      if (c + 1 == chunks) turn_to_next();
+      round(std::false_type{});
+    }
+    if constexpr (kLarge) settle<TL>(acc);
+    else slice_barrier<0>();  // the buffers are free
+    results(now);
+    if constexpr (!DIRECT) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): any number of them
+    if (!more) break;
+    index += step;
+    now = then;
   }
+  // nothing is left under way into LDS when the block ends
+  __builtin_amdgcn_s_waitcnt(0x0F70);
 }
 
 // k == 0
@@ -645,11 +736,21 @@ sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t st
   const unsigned total = static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T));
   const Packed packed{ws, ws + chunks * l.step_a, l.step_a, l.step_b};
   auto go = [&](auto kernel) -> sbp_status {
-    hipLaunchKernelGGL(kernel, dim3(total), dim3(256), 0, stream, p, packed, total);
+    const unsigned per = (total + 7) / 8;  // large tiles: one block a CU, 32 an XCD
+    const unsigned blocks = 8 * (T == 256 && per > 32 ? 32 : per);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, p, packed, total);
     return launched(who);
   };
-  if (!p.f32) return go(mx4_tile_kernel<TL, kBf16>);
-  return p.accumulate ? go(mx4_tile_kernel<TL, kAdd>) : go(mx4_tile_kernel<TL, kF32>);
+  const int64_t size = p.f32 ? 4 : 2;
+  auto of = [&](auto direct_c) -> sbp_status {
+    constexpr bool kDirect = decltype(direct_c)::value;
+    if (!p.f32) return go(mx4_tile_kernel<TL, kBf16, kDirect>);
+    if (p.accumulate) return go(mx4_tile_kernel<TL, kAdd, kDirect>);
+    return go(mx4_tile_kernel<TL, kF32, kDirect>);
+  };
+  // m > 1 here: the row distance counts
+  if (p.vec && p.n * size % 16 == 0 && p.ld * size < int64_t{1} << 23) return of(std::true_type{});
+  return of(std::false_type{});
 }
 
 sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_a,

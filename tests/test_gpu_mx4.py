@@ -273,8 +273,11 @@ def test_matmul(m, n, k, form):
     assert bool((rest == 9.0).all())
 
 
-@pytest.mark.parametrize("m,n", [(1700, 1750), (2900, 2950), (2817, 2817)])
-@pytest.mark.parametrize("k", [1, 33, 97, 128, 129, 500, 512, 520, 1100])
+@pytest.mark.parametrize("m,n,k", [(m, n, k) for m, n in ((1700, 1750), (2900, 2952), (2817, 2817))
+                                   for k in (1, 33, 97, 128, 129, 500, 512, 520, 1100)]
+                         # more tiles than compute units: several to a block
+                         + [(4400, 4304, k) for k in (100, 512, 1600)]
+                         + [(4353, 4351, 700), (1100, 20008, 200), (20001, 1000, 40)])
 @pytest.mark.parametrize("form", ["bf16", "accumulate"])
 def test_matmul_large(m, n, k, form):
     """Larger tiles, at contracted lengths that end anywhere in a slice and in a

@@ -3,7 +3,6 @@ inline assembly (CPU only, on the disassembly of the built library): the same tw
 as newton_schulz.hip's, on every path, by the same reading of the code."""
 
 import os
-import re
 import shutil
 import subprocess
 
@@ -49,10 +48,9 @@ def test_large_tile_keeps_its_distances(tmp_path):
             checked[name] = len([i for i in body if i.mfma])
             found = HZ.hazards(body)
             assert not found, f"{name}: {len(found)}, of them {found[:5]}"
-            # accumulators are not moved about between the products, only zeroed
+            # accumulators are not moved about between the products
             first = min(k for k, i in enumerate(body) if i.mfma)
             last = max(k for k, i in enumerate(body) if i.mfma)
-            moves = [i.text for i in body[first:last] if "accvgpr" in i.op]
-            assert all(re.fullmatch(r"v_accvgpr_write_b32 a\d+, 0", m) for m in moves), name
-    # the three kinds of results; 32 products a slice, three rounds of four slices
-    assert len(checked) == 3 and all(n == 32 * 12 for n in checked.values()), checked
+            assert not [i.text for i in body[first:last] if "accvgpr" in i.op], name
+    # the three kinds of results, stored two ways; 32 products a slice, two rounds of four slices
+    assert len(checked) == 6 and all(n == 32 * 8 for n in checked.values()), checked
