@@ -649,8 +649,9 @@ sbp_status sbp_mx_reduce_shard(const void* const* codes,
  *   accumulate != 0 (SBP_F32 only): out = fl(out + A B').
  *   out         device, aligned to its type, rows ld >= n elements apart; must
  *               not overlap an operand
- *   m, n, k     0 .. SBP_MX_MAX_DIM, k to SBP_MX_MAX_K; m or n == 0 does
- *               nothing; k == 0 writes zeros (leaves out as it is where it
+ *   m, n, k     0 .. SBP_MX_MAX_DIM, k to SBP_MX_MAX_K; an operand has at most
+ *               2^32 blocks (64 GiB of codes), out 2^36 values; m or n == 0
+ *               does nothing; k == 0 writes zeros (leaves out as it is where it
  *               accumulates)
  *   workspace   device memory, 256-byte aligned, workspace_bytes >=
  *               sbp_mx_matmul_workspace(m, n, k) (null where that is 0);

@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <string>
 #include <type_traits>
 
@@ -38,6 +39,11 @@ struct Problem {
   int64_t ld;
   int32_t f32, accumulate;
   int32_t vec;  // out's rows are 16-byte aligned
+  // small tiles: parts of the contracted axis, each of so many chunks of 512 values
+  // and with sums of its own, this many elements further on
+  int32_t parts, part_chunks;
+  int64_t part_step;
+  int64_t cols;  // of a row of out that may be written: n, padded for parts' sums
 };
 
 __device__ __forceinline__ f32x4 product(u32x4 b, uint32_t sb, u32x4 a, uint32_t sa, f32x4 c) {
@@ -77,74 +83,113 @@ __device__ __forceinline__ void store4(const Problem& p, int64_t row, int64_t c,
   }
 }
 
-// ---- few rows: 16 columns and 16 * MT rows of C a block ---------------------------
-// Its W waves share the contracted axis in runs of steps (128 values), each with
-// operands straight from memory; their sums meet in LDS, in the waves' order.
-template <int MT, int W>
+// ---- few rows: 16 columns and 16 * MT rows of C a block ------------------------------
+// Its W waves share the contracted axis: a wave takes every W-th chunk of 512 values
+// (16 blocks, four products), with operands straight from memory, 4 KB of B's codes
+// under way a wave.  The waves' sums meet in LDS, in the waves' order.
+// WIDE: rows of whole chunks, scales on 16-byte addresses, so that a lane takes its
+// row's 16 scales at once; else block by block.
+struct FewOperand {
+  const char* codes;  // of this lane's row and its first block
+  const uint8_t* scales;
+};
+template <bool WIDE>
+struct Chunk {
+  u32x4 codes[4];
+  uint32_t scale[4];
+  __device__ __forceinline__ void load(const FewOperand& o, int64_t c, int g, int64_t kb) {
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        codes[s] = *reinterpret_cast<const u32x4*>(o.codes + c * 256 + s * 64);
+      const u32x4 w = *reinterpret_cast<const u32x4*>(o.scales + c * 16);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) scale[s] = w[s];
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int64_t block = c * 16 + s * 4;
+        const bool in = block + g < kb;
+        codes[s] = u32x4{0, 0, 0, 0};
+        scale[s] = 0;
+        if (in) {
+          codes[s] = *reinterpret_cast<const u32x4*>(o.codes + block * 16);
+          scale[s] = o.scales[block + g];
+        }
+      }
+    }
+  }
+  // The lane's scale in the lowest byte.
+  __device__ __forceinline__ uint32_t of(int s, int g) const {
+    return WIDE ? scale[s] >> (8 * g) : scale[s];
+  }
+};
+
+template <int MT, int W, bool WIDE>
 __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
   __shared__ f32x4 sums[W][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const unsigned across = static_cast<unsigned>((p.n + 15) / 16);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x % across) * 16;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / across) * (16 * MT);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
   // rows past the matrix read the last one; their results are not stored
-  auto row = [](int64_t x, int64_t rows) { return x < rows ? x : rows - 1; };
-  const int64_t br = row(n0 + r, p.n) * p.kb;
-  int64_t ar[MT];
+  auto operand = [&](const char* codes, const uint8_t* scales, int64_t row, int64_t rows) {
+    const int64_t at = (row < rows ? row : rows - 1) * p.kb;
+    return FewOperand{codes + (at + g) * 16, scales + at};
+  };
+  const FewOperand B = operand(p.b, p.sb, n0 + r, p.n);
+  FewOperand A[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) ar[i] = row(m0 + i * 16 + r, p.m) * p.kb;
-  const int64_t steps = (p.kb + 3) / 4, per = (steps + W - 1) / W;
-  const int64_t last = (wave + 1) * per < steps ? (wave + 1) * per : steps;
+  for (int i = 0; i < MT; ++i) A[i] = operand(p.a, p.sa, i * 16 + r, p.m);
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-  for (int64_t s = wave * per; s < last; ++s) {
-    const int64_t block = s * 4 + g;
-    const bool in = block < p.kb;
-    const int64_t at = in ? block : p.kb - 1;
-    auto codes = [&](const char* base, int64_t row_at) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(base + (row_at + at) * 16);
-      return in ? w : u32x4{0, 0, 0, 0};
-    };
-    auto scale = [&](const uint8_t* base, int64_t row_at) -> uint32_t {
-      return in ? base[row_at + at] : 0u;
-    };
-    const u32x4 b = codes(p.b, br);
-    const uint32_t sb = scale(p.sb, br);
+  const int64_t chunks = (p.kb + 15) / 16;
+  for (int64_t c = wave; c < chunks; c += W) {
+    Chunk<WIDE> a[MT], b;
+    b.load(B, c, g, p.kb);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      acc[i] = product(b, sb, codes(p.a, ar[i]), scale(p.sa, ar[i]), acc[i]);
+    for (int i = 0; i < MT; ++i) a[i].load(A[i], c, g, p.kb);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = product(b.codes[s], b.of(s, g), a[i].codes[s], a[i].of(s, g), acc[i]);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) sums[wave][i][lane] = acc[i];
   __syncthreads();
-  for (int i = wave; i < MT; i += W) {
-    f32x4 v = sums[0][i][lane];
-    for (int w = 1; w < W; ++w) v = v + sums[w][i][lane];
-    const int64_t at = m0 + i * 16 + r;
-    if (at < p.m) store4(p, at, n0 + g * 4, v);
+  if (wave < MT) {
+    f32x4 v = sums[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = v + sums[w][wave][lane];
+    if (wave * 16 + r < p.m) store4(p, wave * 16 + r, n0 + g * 4, v);
   }
 }
 
 // ---- tiles --------------------------------------------------------------------------
 // One T x T tile of C per block of 4 waves (2 x 2, each a quarter in 32 x 32 MFMA
 // tiles, 64 contracted values at a time: lane l holds row l % 32's block l / 32).
-// Slices of 128 contracted values (64 bytes of codes a row) go straight from memory
-// to one of four LDS buffers, four slices ahead; the scales, packed beforehand as
-// the instruction takes them, a chunk of four slices at a time.
-template <int T_>
+// Slices of 128 contracted values (64 bytes of codes a row; 256 at the small tile) go
+// straight from memory to one of four LDS buffers, four slices ahead.  The scales go
+// by chunks of 512 values: at the large tile packed beforehand as the instruction
+// takes them, and through LDS; else each lane takes its rows' from memory.
+template <int T_, int BYTES>
 struct Tile {
-  static constexpr int T = T_;
-  static constexpr int kHalf = T * 64;          // one operand's slice, bytes
-  static constexpr int kBuf = 2 * kHalf;        // A, then B
-  static constexpr int kSub = T / 64;           // 32 x 32 tiles per wave and side
-  static constexpr int kLoads = T * 64 / 4096;  // per operand, slice and lane
-  static constexpr int kScales = T * 16;        // one operand's scales of a chunk, bytes
-  // bytes a lane loads of the two operands' scales at once, and how often
-  static constexpr int kScaleBytes = T >= 128 ? 16 : 4;
-  static constexpr int kScaleLoads = 2 * kScales / (256 * kScaleBytes);
+  static constexpr int T = T_, NB = 4;
+  static constexpr bool kLarge = T == 256;
+  static constexpr int kRow = BYTES;               // a row's part of a slice
+  static constexpr int kSteps = kRow / 32;         // of 64 values
+  static constexpr int kChunk = 256 / kRow;        // slices
+  static constexpr int kHalf = T * kRow;           // one operand's slice, bytes
+  static constexpr int kBuf = 2 * kHalf;           // A, then B
+  static constexpr int kSub = T / 64;              // 32 x 32 tiles per wave and side
+  static constexpr int kLoads = kHalf / 4096;      // per operand, slice and lane
+  static constexpr int kScales = T * 16;           // one operand's scales of a chunk, bytes
+  static constexpr int kScaleLoads = kLarge ? 2 * kScales / 4096 : 0;  // a lane's
 };
+using Large = Tile<256, 64>;
+using Middle = Tile<128, 64>;
+using Small = Tile<64, 128>;
 
 // Row of B that row i of an MFMA tile holds.  A lane's results are rows 8q + 4h + t
 // of B for its half h: with fp32 results four neighbours are 16 bytes; with bf16
@@ -192,37 +237,41 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int byte
 }
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// One operand of a tile.  LDS keeps a row's four 16-byte pieces (the blocks of a
-// slice) rotated by row, which spreads the reads over the banks; the rotation
+// One operand of a tile.  LDS keeps a row's 16-byte pieces (the blocks of a slice)
+// rotated by row, which spreads the reads over the banks; the rotation
 // comes from the lanes' global addresses.
 template <typename TL, bool PAIRS>
 struct Operand {
   static constexpr int kOut = 0x7FFFFFF0;  // an offset beyond every buffer
   const char* from;                        // next slice to load
   int bytes, round_bytes, all, voff, piece;  // voff: `all`, or kOut past the rows' end
-  int at[2];                               // LDS offsets of this lane's first fragments
+  int at[TL::kSteps];                      // LDS offsets of this lane's first fragments
+  static constexpr int kLanes = TL::kRow / 16;  // that load a row
 
   static __device__ __forceinline__ int turn(int i) {  // of row i of an MFMA tile
-    return (((i >> 1) ^ (i >> 2)) & 2) | (((i >> 3) ^ (i >> 1)) & 1);
+    if constexpr (kLanes == 8) return (i >> 1) & 7;
+    else return (((i >> 1) ^ (i >> 2)) & 2) | (((i >> 3) ^ (i >> 1)) & 1);
   }
   // wrow: the wave's first row in the tile
   __device__ __forceinline__ void init(int kb, int wave, int lane, int wrow) {
-    const int row = wave * 16 + lane / 4;
-    piece = (lane & 3) ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
+    const int row = wave * (64 / kLanes) + lane / kLanes;
+    piece = lane % kLanes ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
     all = row * kb * 16 + piece * 16;
-    round_bytes = 64 * kb * 16;
+    round_bytes = (256 / kLanes) * kb * 16;
     const int i = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      at[k] = (wrow + row_of<PAIRS>(i)) * 64 + ((2 * k + h) ^ turn(i)) * 16;
+    for (int k = 0; k < TL::kSteps; ++k)
+      at[k] = (wrow + row_of<PAIRS>(i)) * TL::kRow + ((2 * k + h) ^ turn(i)) * 16;
   }
   // At the first slice of the tile of rows r0 ..
-  __device__ __forceinline__ void aim(const char* codes, int64_t rows, int64_t kb, int64_t r0) {
-    from = codes + r0 * kb * 16;
+  // and the chunk c0.
+  __device__ __forceinline__ void aim(const char* codes, int64_t rows, int64_t kb, int64_t r0,
+                                      int c0) {
+    from = codes + r0 * kb * 16 + c0 * 256;
     // a 64-bit comparison is a vector instruction: the descriptor has to be scalar
     const int have = __builtin_amdgcn_readfirstlane(
         rows - r0 < TL::T ? static_cast<int>(rows - r0) : TL::T);
-    bytes = have * static_cast<int>(kb) * 16;
+    bytes = have * static_cast<int>(kb) * 16 - c0 * 256;
     voff = all;
   }
   __device__ __forceinline__ void load_round(char* buf, int wave, int r) const {
@@ -233,27 +282,45 @@ struct Operand {
   }
   // To the next slice; `bytes` may go below 0.
   __device__ __forceinline__ void advance() {
-    from += 64;
-    bytes -= 64;
+    from += TL::kRow;
+    bytes -= TL::kRow;
   }
   // `left` blocks of the rows remain for the next slice: the rest reads as zeros.
   __device__ __forceinline__ void cut(int left) {
-    if (left < 4) voff = piece < left ? voff : kOut;
+    if (left < kLanes) voff = piece < left ? voff : kOut;
   }
   // Step k of a slice, MFMA tile i.
   __device__ __forceinline__ u32x4 read(const char* buf, int k, int i) const {
-    return *reinterpret_cast<const u32x4*>(buf + at[k] + i * 32 * 64);
+    return *reinterpret_cast<const u32x4*>(buf + at[k] + i * 32 * TL::kRow);
   }
 };
 
 template <typename TL>
-struct Frags {  // of a slice's two steps
-  u32x4 a[2][TL::kSub], b[2][TL::kSub];
+struct Frags {  // of a slice
+  u32x4 a[TL::kSteps][TL::kSub], b[TL::kSteps][TL::kSub];
 };
 template <typename TL>
-struct Scales {  // of a chunk
+struct Scales {  // of a chunk: byte s % 4 of word s / 4 for its steps s of 64 values
   u32x2 a[TL::kSub], b[TL::kSub];
 };
+// The same from memory: of a row's 16 scales the even or (h) odd ones.  WIDE: they
+// all exist, on a 16-byte address.
+template <bool WIDE>
+__device__ __forceinline__ u32x2 row_scales(const uint8_t* row, int64_t block, int64_t kb, int h) {
+  if constexpr (WIDE) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(row + block);
+    const uint32_t pick = h ? 0x07050301u : 0x06040200u;
+    return u32x2{__builtin_amdgcn_perm(w.y, w.x, pick), __builtin_amdgcn_perm(w.w, w.z, pick)};
+  } else {
+    u32x2 out{0, 0};
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int64_t b = block + 2 * s + h;
+      if (b < kb) out[s >> 2] |= static_cast<uint32_t>(row[b]) << (8 * (s & 3));
+    }
+    return out;
+  }
+}
 template <typename TL>
 using Acc = f32x16[TL::kSub][TL::kSub];
 
@@ -330,43 +397,26 @@ struct Packed {
 
 enum Out { kBf16, kF32, kAdd };
 
-// The 16 bytes of a row of C from column c on, those of them that there are.
-template <Out O>
-__device__ __forceinline__ void store_piece(const Problem& p, int64_t row, int64_t c, u32x4 w) {
-  constexpr int kN = O == kBf16 ? 8 : 4;
-  const int64_t at = row * p.ld + c;
-  if constexpr (O == kBf16) {
-    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (c + i < p.n) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-  } else {
-    float* o = static_cast<float*>(p.out) + at;
-    const f32x4 v = __builtin_bit_cast(f32x4, w);
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (c + i < p.n) o[i] = O == kAdd ? o[i] + v[i] : v[i];
-  }
-}
-
 // DIRECT: C's rows are made of whole 16-byte pieces on such addresses, a tile's within
 // 2^31 bytes.
-template <typename TL, Out O, bool DIRECT>
-__global__ void __launch_bounds__(256, TL::T == 256 ? 1 : 2)
+// WIDE: rows of whole chunks, scales on 16-byte addresses (small tiles).
+template <typename TL, Out O, bool DIRECT, bool WIDE>
+__global__ void __launch_bounds__(256, TL::kLarge ? 1 : 2)
 mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   constexpr int T = TL::T, kSub = TL::kSub;
-  constexpr bool kPairs = O == kBf16, kLarge = T == 256;
+  constexpr bool kPairs = O == kBf16, kLarge = TL::kLarge;
   // separate arrays: reads of one do not wait for loads into another
   __shared__ __align__(16) char buf0[TL::kBuf];
   __shared__ __align__(16) char buf1[TL::kBuf];
   __shared__ __align__(16) char buf2[TL::kBuf];
   __shared__ __align__(16) char buf3[TL::kBuf];
-  __shared__ __align__(16) char scl[2 * TL::kScales];
+  __shared__ __align__(16) char scl[kLarge ? 2 * TL::kScales : 16];
   // for the results: the large tile's buffers hold the next tile meanwhile
   constexpr int kSlab = T == 64 && O == kBf16 ? 2048 : 4096;  // a wave's
   constexpr bool kOwnSlabs = kLarge || 4 * kSlab > TL::kBuf;
   __shared__ __align__(16) char slabs[kOwnSlabs ? 4 * kSlab : 16];
-  char* buf[4] = {buf0, buf1, buf2, buf3};
+  constexpr int NB = TL::NB, kChunk = TL::kChunk, kSteps = TL::kSteps;
+  char* buf[NB] = {buf0, buf1, buf2, buf3};
   const unsigned tr = static_cast<unsigned>((p.m + T - 1) / T);
   const unsigned tc = static_cast<unsigned>((p.n + T - 1) / T);
   // Neighbouring tiles to one XCD: an eighth of them to each.  Of the large ones a
@@ -381,7 +431,8 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   };
   auto place_of = [&](unsigned i) {  // strips of 8 tile rows, column by column
     constexpr unsigned kStrip = 8;
-    const unsigned t = base + i, strip = t / (kStrip * tc), left = tr - strip * kStrip;
+    const unsigned t = (base + i) % (tr * tc);
+    const unsigned strip = t / (kStrip * tc), left = tr - strip * kStrip;
     const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
     // the divisions go by vector instructions: back to scalars
     return Place{static_cast<unsigned>(__builtin_amdgcn_readfirstlane(strip * kStrip + s % high)),
@@ -397,19 +448,26 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   B.init(static_cast<int>(p.kb), wave, lane, wc);
   const char *pa, *pb;
   int ahead;  // blocks from the next slice to load on
+  const int part = kLarge ? 0 : __builtin_amdgcn_readfirstlane((base + index) / (tr * tc));
+  const int first_chunk = part * p.part_chunks;
   auto aim = [&](Place t) {
-    A.aim(p.a, p.m, p.kb, static_cast<int64_t>(t.ti) * T);
-    B.aim(p.b, p.n, p.kb, static_cast<int64_t>(t.tj) * T);
-    pa = packed.a + static_cast<int64_t>(t.ti) * TL::kScales;
-    pb = packed.b + static_cast<int64_t>(t.tj) * TL::kScales;
-    ahead = static_cast<int>(p.kb);
+    A.aim(p.a, p.m, p.kb, static_cast<int64_t>(t.ti) * T, first_chunk);
+    B.aim(p.b, p.n, p.kb, static_cast<int64_t>(t.tj) * T, first_chunk);
+    if constexpr (kLarge) {
+      pa = packed.a + static_cast<int64_t>(t.ti) * TL::kScales;
+      pb = packed.b + static_cast<int64_t>(t.tj) * TL::kScales;
+    }
+    // up to a part's end: the rest reads as zeros
+    const int64_t end = kLarge ? p.kb : static_cast<int64_t>(first_chunk + p.part_chunks) * 16;
+    ahead = __builtin_amdgcn_readfirstlane(static_cast<int>(end < p.kb ? end : p.kb)) -
+            first_chunk * 16;
   };
   auto begin_load = [&]() {
     A.cut(ahead);
     B.cut(ahead);
   };
   auto end_load = [&]() {
-    ahead -= 4;
+    ahead -= TL::kRow / 16;
     A.advance();
     B.advance();
   };
@@ -422,24 +480,33 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     end_load();
   };
   auto load_scales = [&]() {
-    constexpr int kWave = 64 * TL::kScaleBytes;
 #pragma unroll
     for (int r = 0; r < TL::kScaleLoads; ++r) {
-      const int off = (r * 4 + wave) * kWave;  // in A's scales, then B's
+      const int off = (r * 4 + wave) * 1024;  // in A's scales, then B's
       const char* src = off < TL::kScales ? pa + off : pb + (off - TL::kScales);
-      if constexpr (TL::kScaleBytes == 16)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(scl + off), 16,
-                                                 lane * 16, 0, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, kWave), (lds_ptr)(scl + off), 4,
-                                                 lane * 4, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(src, 1024), (lds_ptr)(scl + off), 16,
+                                               lane * 16, 0, 0, 0);
     }
     pa += packed.step_a;
     pb += packed.step_b;
   };
+  // small tiles: the lane's rows' scales; past the matrix the last row's
+  const uint8_t *row_a[kSub], *row_b[kSub];
+  int64_t scale_block = static_cast<int64_t>(first_chunk) * 16;
   Frags<TL> f[2];
-  Scales<TL> sc;
-  constexpr int kReads = 4 * kSub;
+  Scales<TL> sc, next_sc;
+  auto take_scales = [&](Scales<TL>& to) {
+    // a chunk past the end repeats the last one's blocks; it is not used
+    const int64_t last = (p.kb - 1) / 16 * 16;
+    const int64_t at = scale_block < last ? scale_block : last;
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      to.a[i] = row_scales<WIDE>(row_a[i], at, p.kb, lane >> 5);
+      to.b[i] = row_scales<WIDE>(row_b[i], at, p.kb, lane >> 5);
+    }
+    scale_block += 16;
+  };
+  constexpr int kReads = 2 * kSteps * kSub;
   auto read_one = [&](const char* from, Frags<TL>& to, int c) {  // c: 0 .. kReads - 1
     const int k = c / (2 * kSub), i = c % (2 * kSub);
     if (i < kSub) to.a[k][i] = A.read(from, k, i);
@@ -464,12 +531,13 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     constexpr int I = decltype(i_c)::value;
     constexpr bool kFirst = decltype(first_c)::value;
     constexpr int now = I & 1, next = now ^ 1;
-    // newer than the next slice: two slices, scales asked for in their time, and the
-    // last tile's stores where the next slice was asked for before them
-    constexpr int kNewer = 2 * L + (I == 2 ? K : 0) + (kFirst && I < 3 ? kStores : 0);
+    // newer than the next slice: all other slices, scales asked for in their time, and
+    // the last tile's stores where the next slice was asked for before them
+    constexpr int kNewer = (NB - 2) * L + (I == 2 ? K : 0) + (kFirst && I < 3 ? kStores : 0);
     slice_barrier<(kNewer < 63 ? kNewer : 63)>();
-    if constexpr (I == 1) load_scales();
-    const char* from = buf[(I + 1) & 3];
+    if constexpr (I == 1 && kLarge) load_scales();
+    if constexpr (I % kChunk == 0 && !kLarge) take_scales(next_sc);
+    const char* from = buf[(I + 1) % NB];
     if constexpr (kLarge) {
       begin_load();
       constexpr int kAll = kSub * kSub;
@@ -496,24 +564,24 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
       end_load();
     } else {
       load(buf[I]);
-      if constexpr (I == 0 || I == 3) {
-#pragma unroll
-        for (int c = 0; c < 2 * kSub; ++c) read_scale(I == 0 ? 1 : 0, c);
-      }
 #pragma unroll
       for (int c = 0; c < kReads; ++c) read_one(from, f[next], c);
+      auto step = [&](auto k_c) {
+        constexpr int k = decltype(k_c)::value;
 #pragma unroll
-      for (int i = 0; i < kSub; ++i)
+        for (int i = 0; i < kSub; ++i)
 #pragma unroll
-        for (int j = 0; j < kSub; ++j)
-          acc[i][j] = product_of<2 * I>(f[now].b[0][j], sc.b[j], f[now].a[0][i], sc.a[i],
-                                        acc[i][j]);
-#pragma unroll
-      for (int i = 0; i < kSub; ++i)
-#pragma unroll
-        for (int j = 0; j < kSub; ++j)
-          acc[i][j] = product_of<2 * I + 1>(f[now].b[1][j], sc.b[j], f[now].a[1][i], sc.a[i],
-                                            acc[i][j]);
+          for (int j = 0; j < kSub; ++j)
+            acc[i][j] = product_of<I % kChunk * kSteps + k>(f[now].b[k][j], sc.b[j],
+                                                            f[now].a[k][i], sc.a[i], acc[i][j]);
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      if constexpr (kSteps == 4) {
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
+      }
+      if constexpr (I % kChunk == kChunk - 1) sc = next_sc;
     }
   };
   auto round = [&](auto first_c) {
@@ -550,8 +618,8 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     const int have = __builtin_amdgcn_readfirstlane(
         static_cast<int>(p.m - r0 < T / 2 ? (p.m > r0 ? p.m - r0 : 0) : T / 2));
     const int wide = __builtin_amdgcn_readfirstlane(
-        static_cast<int>(p.n - c0 < T / 2 ? (p.n > c0 ? p.n - c0 : 0) : T / 2));
-    char* corner = static_cast<char*>(p.out) + (r0 * p.ld + c0) * kSize;
+        static_cast<int>(p.cols - c0 < T / 2 ? (p.cols > c0 ? p.cols - c0 : 0) : T / 2));
+    char* corner = static_cast<char*>(p.out) + (r0 * p.ld + c0 + part * p.part_step) * kSize;
     const int line = static_cast<int>(p.ld) * kSize;  // DIRECT: below 2^23
     // the last row ends with its last column
     const auto rows = buffer(corner, have > 0 && wide > 0 ? (have - 1) * line + wide * kSize : 0);
@@ -610,10 +678,19 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
           for (int q = 0; q < kTimes; ++q)
             __builtin_amdgcn_raw_buffer_store_b128(w[q], rows, off + q * kRows * line, 0, 0);
         } else {
-#pragma unroll 1
-          for (int q = 0; q < kTimes; ++q) {
-            const int row = i * 32 + q * kRows + row0;
-            if (row < have && c < wide) store_piece<O>(p, r0 + row, c0 + c, *from(q));
+          // value by value, neighbouring lanes neighbouring columns
+          using V = std::conditional_t<O == kBf16, uint16_t, float>;
+#pragma unroll 4
+          for (int q = 0; q < kSpan / 2; ++q) {
+            const int row = (q * 64 + lane) / kSpan, col = lane % kSpan;
+            const int turn = row / (16 / kPieces) % kPieces;
+            const V v = *reinterpret_cast<const V*>(
+                slab + row * (kPieces * 16) + ((col / kPiece) ^ turn) * 16 + col % kPiece * kSize);
+            if (i * 32 + row < have && j0 * 32 + col < wide) {
+              V* o = reinterpret_cast<V*>(corner) + (i * 32 + row) * p.ld + j0 * 32 + col;
+              if constexpr (O == kAdd) *o = *o + v;
+              else *o = v;
+            }
           }
         }
       }
@@ -622,15 +699,31 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
 
   Place now = place_of(index);
   aim(now);
-  load_scales();
+  if constexpr (kLarge) {
+    load_scales();
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load(buf[i]);
-  slice_barrier<0>();
+    for (int i = 0; i < kSub; ++i) {
+      const int64_t ra = static_cast<int64_t>(now.ti) * T + wr + i * 32 + (lane & 31);
+      const int64_t rb =
+          static_cast<int64_t>(now.tj) * T + wc + i * 32 + row_of<kPairs>(lane & 31);
+      row_a[i] = p.sa + (ra < p.m ? ra : p.m - 1) * p.kb;
+      row_b[i] = p.sb + (rb < p.n ? rb : p.n - 1) * p.kb;
+    }
+    take_scales(sc);
+  }
 #pragma unroll
-  for (int c = 0; c < 2 * kSub; ++c) read_scale(0, c);
+  for (int i = 0; i < NB; ++i) load(buf[i]);
+  slice_barrier<kLarge ? 0 : (NB - 1) * L>();
+  if constexpr (kLarge) {
+#pragma unroll
+    for (int c = 0; c < 2 * kSub; ++c) read_scale(0, c);
+  }
 #pragma unroll
   for (int c = 0; c < kReads; ++c) read_one(buf[0], f[0], c);
-  const int chunks = static_cast<int>((p.kb + 15) / 16);
+  const int all_chunks = static_cast<int>((p.kb + 15) / 16) - first_chunk;
+  const int own = kLarge || all_chunks < p.part_chunks ? all_chunks : p.part_chunks;
+  const int rounds = (own + NB / kChunk - 1) / (NB / kChunk);
   for (;;) {
     const bool more = kLarge && exists(index + step);
     const Place then = more ? place_of(index + step) : now;
@@ -648,12 +741,12 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     }
-    if (chunks == 1) turn_to_next();
+    if (rounds == 1) turn_to_next();
     round(std::true_type{});
     // the compiler places moves where the ways join
     if constexpr (kLarge) settle<TL>(acc);
-    for (int c = 1; c < chunks; ++c) {
-      if (c + 1 == chunks) turn_to_next();
+    for (int c = 1; c < rounds; ++c) {
+      if (c + 1 == rounds) turn_to_next();
       round(std::false_type{});
     }
     if constexpr (kLarge) settle<TL>(acc);
@@ -666,6 +759,18 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   }
   // nothing is left under way into LDS when the block ends
   __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+// The parts' sums, in their order.
+__global__ void __launch_bounds__(256)
+mx4_join_kernel(Problem p, const float* parts, int32_t count, int64_t quads, int64_t step) {
+  const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = q / quads;
+  if (row >= p.m) return;
+  const float* from = parts + q * 4;
+  f32x4 v = *reinterpret_cast<const f32x4*>(from);
+  for (int s = 1; s < count; ++s) v = v + *reinterpret_cast<const f32x4*>(from + s * step);
+  store4(p, row, (q - row * quads) * 4, v);
 }
 
 // k == 0
@@ -683,33 +788,71 @@ sbp_status check_sizes(const Text& w, int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n < 0 || k < 0) return sbp::fail(SBP_EINVAL, w + ": m, n or k < 0");
   if (m > SBP_MX_MAX_DIM || n > SBP_MX_MAX_DIM || k > SBP_MX_MAX_K)
     return sbp::fail(SBP_ERANGE, w + ": a size above SBP_MX_MAX_DIM or SBP_MX_MAX_K");
+  // 2^32 blocks of an operand are 64 GiB of codes; 2^36 results of 4 bytes 256 GiB
+  const int64_t kb = sbp::mx4_blocks(k);
+  if (m * kb > int64_t{1} << 32 || n * kb > int64_t{1} << 32 || m * n > int64_t{1} << 36)
+    return sbp::fail(SBP_ERANGE, w + ": an operand above 2^32 blocks or a result above 2^36 values");
   return SBP_OK;
 }
 
-constexpr int64_t kFewRows = 64;
-
-// Side of the tiles.
-int tile_of(int64_t m, int64_t n) {
-  auto tiles = [&](int64_t T) { return ((m + T - 1) / T) * ((n + T - 1) / T); };
-  if (tiles(256) >= 128) return 256;
-  return tiles(128) >= 192 ? 128 : 64;
-}
-
-struct Layout {
-  int64_t step_a, step_b, bytes;  // of a chunk's packed scales
+// How a product goes about it: the tiles' side, the parts of the contracted axis
+// (chunks of 512 values each), and what the workspace holds.
+struct Form {
+  int T;  // 0: few rows
+  int parts, part_chunks;
+  int64_t step_a, step_b;  // large tile: bytes of a chunk's packed scales
+  int64_t part_ld;         // parts: a row of their sums, elements
+  int64_t bytes;
 };
-Layout layout_of(int64_t m, int64_t n, int64_t kb, int T) {
-  const int64_t a = (m + T - 1) / T * T * 16, b = (n + T - 1) / T * T * 16;
-  return {a, b, (kb + 15) / 16 * (a + b)};
+Form form_of(int64_t m, int64_t n, int64_t kb) {
+  auto tiles = [&](int64_t T) { return ((m + T - 1) / T) * ((n + T - 1) / T); };
+  const int64_t chunks = (kb + 15) / 16;
+  Form f{};
+  f.part_chunks = static_cast<int>(chunks);
+  f.parts = 1;
+  // Few rows: 16 x 8192 x 4096 5.4 to 6.2 us, with small tiles 6.7; 32 x 4096 x 4096
+  // 5.3 and 7.0; but 32 x 8192 x 4096 8.6 and 7.0, 16 x 16384 x 4096 10.9 and 8.8, since
+  // each 16 columns read all of A.
+  if (m == 1 || (m <= 32 && n <= 4096) || (m <= 16 && n <= 8192)) return f;
+  // Microseconds as measured (bf16 results), by the chunks c and the tiles; 512 of the
+  // small and the middle ones run at once, 256 of the large.
+  //   small   64 tiles c = 8 6.7, 28 18.3; 256 tiles 7.9, 21.3; 512 c = 8 11.5; 1024 21.0;
+  //           8192 c = 1 54, c = 4 86
+  //   middle  128 tiles c = 8 13.8; 256 c = 4 9.0, 8 15.3, 16 27.4; 512 c = 8 28.4;
+  //           1088 66; 2048 c = 1 23 to 34, c = 4 54
+  //   large   64 tiles c = 8 25; 128 30; 256 42, c = 16 72; 272 c = 8 61; 512 c = 1 22,
+  //           c = 2 30, c = 4 46, c = 8 77; 1792 c = 8 230
+  const double c = static_cast<double>(chunks);
+  const double t64 = tiles(64) / 512.0, t128 = tiles(128) / 512.0, t256 = tiles(256) / 256.0;
+  const double rounds = std::floor(t256), rest = t256 - rounds;
+  const double cost64 = t64 < 1 ? 3 + c * std::max(0.6, 1.15 * t64) : t64 * (2.5 + 0.95 * c);
+  const double cost128 = t128 < 1 ? 3 + c * std::max(1.3, 3.1 * t128) : t128 * (5 + 3.1 * c);
+  const double cost256 =
+      12 + rounds * (3 + 3.4 * c) + (rest > 0 ? 3 + c * (2.1 + 1.3 * rest) : 0);
+  f.T = cost64 <= std::min(cost128, cost256) ? 64 : cost128 <= cost256 ? 128 : 256;
+  // Few tiles and long sums: parts of at least four chunks, up to a tile a compute
+  // unit.  16 tiles c = 28 16.1, in 7 parts 9.6; 64 tiles 20.2, in 4 parts 12.7; but
+  // c = 8 7.5, in 2 parts 8.3: the joining takes 3 to 4.
+  int64_t parts = 1;
+  if (f.T == 64 && chunks >= 12)
+    parts = std::max<int64_t>(1, std::min(256 / tiles(64), chunks / 4));
+  f.part_chunks = static_cast<int>((chunks + parts - 1) / parts);
+  f.parts = static_cast<int>((chunks + f.part_chunks - 1) / f.part_chunks);
+  if (f.T == 256) {
+    f.step_a = (m + 255) / 256 * 4096;
+    f.step_b = (n + 255) / 256 * 4096;
+    f.bytes = chunks * (f.step_a + f.step_b);
+  } else if (f.parts > 1) {
+    f.part_ld = (n + 3) / 4 * 4;
+    f.bytes = f.parts * m * f.part_ld * 4;
+  }
+  return f;
 }
 
 int64_t workspace_of(int64_t m, int64_t n, int64_t k) {
-  if (m <= kFewRows || n == 0 || k == 0) return 0;
-  return layout_of(m, n, sbp::mx4_blocks(k), tile_of(m, n)).bytes;
+  if (m == 0 || n == 0 || k == 0) return 0;
+  return form_of(m, n, sbp::mx4_blocks(k)).bytes;
 }
-
-template <int T>
-sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t stream);
 
 sbp_status launched(const char* who) {
   hipError_t e = hipGetLastError();
@@ -718,39 +861,93 @@ sbp_status launched(const char* who) {
   return sbp::ok();
 }
 
-template <int T>
-sbp_status run_tiles(const char* who, const Problem& p, char* ws, hipStream_t stream) {
-  using TL = Tile<T>;
-  const Layout l = layout_of(p.m, p.n, p.kb, T);
+template <typename K>
+sbp_status launch_tiles(const char* who, K kernel, const Problem& p, const Packed& packed, int T,
+                        hipStream_t stream) {
+  const unsigned total =
+      static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T) * p.parts);
+  const unsigned per = (total + 7) / 8;
+  const unsigned blocks = 8 * (T == 256 && per > 32 ? 32 : per);  // large: one a CU, 32 an XCD
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, p, packed, total);
+  return launched(who);
+}
+
+// C's rows as whole 16-byte pieces on such addresses, those of a tile within 2^31 bytes.
+bool direct_of(const Problem& p) {
+  const int64_t size = p.f32 ? 4 : 2;
+  return p.vec && p.m > 1 && p.cols * size % 16 == 0 && p.ld * size < int64_t{1} << 23;
+}
+
+sbp_status run_large(const char* who, const Problem& p, const Form& f, char* ws,
+                     hipStream_t stream) {
+  using TL = Large;
   const int64_t chunks = (p.kb + 15) / 16;
-  const int32_t tiles_a = static_cast<int32_t>(l.step_a / 512);
-  const int32_t tiles_b = static_cast<int32_t>(l.step_b / 512);
+  const int32_t tiles_a = static_cast<int32_t>(f.step_a / 512);
+  const int32_t tiles_b = static_cast<int32_t>(f.step_b / 512);
   const Pack a{p.sa, reinterpret_cast<uint32_t*>(ws), p.m, tiles_a, 0};
-  const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * l.step_a), p.n, tiles_b, !p.f32};
+  const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * f.step_a), p.n, tiles_b, !p.f32};
   const unsigned blocks_a = static_cast<unsigned>((chunks * tiles_a + 1) / 2);
   const unsigned blocks_b = static_cast<unsigned>((chunks * tiles_b + 1) / 2);
   hipLaunchKernelGGL(mx4_pack_kernel, dim3(blocks_a + blocks_b), dim3(256), 0, stream, a, b, p.kb,
                      blocks_a);
   sbp_status st = launched(who);
   if (st != SBP_OK) return st;
-  const unsigned total = static_cast<unsigned>(((p.m + T - 1) / T) * ((p.n + T - 1) / T));
-  const Packed packed{ws, ws + chunks * l.step_a, l.step_a, l.step_b};
-  auto go = [&](auto kernel) -> sbp_status {
-    const unsigned per = (total + 7) / 8;  // large tiles: one block a CU, 32 an XCD
-    const unsigned blocks = 8 * (T == 256 && per > 32 ? 32 : per);
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, stream, p, packed, total);
-    return launched(who);
-  };
-  const int64_t size = p.f32 ? 4 : 2;
+  const Packed packed{ws, ws + chunks * f.step_a, f.step_a, f.step_b};
   auto of = [&](auto direct_c) -> sbp_status {
     constexpr bool kDirect = decltype(direct_c)::value;
-    if (!p.f32) return go(mx4_tile_kernel<TL, kBf16, kDirect>);
-    if (p.accumulate) return go(mx4_tile_kernel<TL, kAdd, kDirect>);
-    return go(mx4_tile_kernel<TL, kF32, kDirect>);
+    auto go = [&](auto kernel) { return launch_tiles(who, kernel, p, packed, 256, stream); };
+    if (!p.f32) return go(mx4_tile_kernel<TL, kBf16, kDirect, true>);
+    if (p.accumulate) return go(mx4_tile_kernel<TL, kAdd, kDirect, true>);
+    return go(mx4_tile_kernel<TL, kF32, kDirect, true>);
   };
-  // m > 1 here: the row distance counts
-  if (p.vec && p.n * size % 16 == 0 && p.ld * size < int64_t{1} << 23) return of(std::true_type{});
-  return of(std::false_type{});
+  return direct_of(p) ? of(std::true_type{}) : of(std::false_type{});
+}
+
+template <typename TL>
+sbp_status run_small(const char* who, Problem p, const Form& f, char* ws, hipStream_t stream) {
+  const bool wide = p.kb % 16 == 0 && sbp::aligned(p.sa, 16) && sbp::aligned(p.sb, 16);
+  const Problem whole = p;
+  p.parts = f.parts;
+  p.part_chunks = f.part_chunks;
+  if (f.parts > 1) {
+    p.out = ws;
+    p.ld = f.part_ld;
+    p.f32 = 1;
+    p.accumulate = 0;
+    p.vec = 1;
+    p.part_step = p.m * f.part_ld;
+    p.cols = f.part_ld;
+  }
+  auto of = [&](auto direct_c, auto wide_c) -> sbp_status {
+    constexpr bool kDirect = decltype(direct_c)::value, kWide = decltype(wide_c)::value;
+    auto go = [&](auto kernel) { return launch_tiles(who, kernel, p, Packed{}, TL::T, stream); };
+    if (!p.f32) return go(mx4_tile_kernel<TL, kBf16, kDirect, kWide>);
+    if (p.accumulate) return go(mx4_tile_kernel<TL, kAdd, kDirect, kWide>);
+    return go(mx4_tile_kernel<TL, kF32, kDirect, kWide>);
+  };
+  constexpr std::true_type kYes{};
+  constexpr std::false_type kNo{};
+  sbp_status st = direct_of(p) ? (wide ? of(kYes, kYes) : of(kYes, kNo))
+                               : (wide ? of(kNo, kYes) : of(kNo, kNo));
+  if (st != SBP_OK || f.parts == 1) return st;
+  const int64_t quads = f.part_ld / 4;
+  const dim3 grid(static_cast<unsigned>((quads * p.m + 255) / 256));
+  hipLaunchKernelGGL(mx4_join_kernel, grid, dim3(256), 0, stream, whole,
+                     reinterpret_cast<const float*>(ws), f.parts, quads, p.part_step);
+  return launched(who);
+}
+
+sbp_status run_few(const char* who, const Problem& p, hipStream_t stream) {
+  const bool wide = p.kb % 16 == 0 && sbp::aligned(p.sa, 16) && sbp::aligned(p.sb, 16);
+  constexpr int kWaves = 4;
+  auto go = [&](auto kernel) -> sbp_status {
+    const unsigned blocks = static_cast<unsigned>((p.n + 15) / 16);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kWaves * 64), 0, stream, p);
+    return launched(who);
+  };
+  if (p.m <= 16)
+    return wide ? go(mx4_few_kernel<1, kWaves, true>) : go(mx4_few_kernel<1, kWaves, false>);
+  return wide ? go(mx4_few_kernel<2, kWaves, true>) : go(mx4_few_kernel<2, kWaves, false>);
 }
 
 sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_a,
@@ -798,7 +995,8 @@ sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_
   Problem p{static_cast<const char*>(codes_a), static_cast<const char*>(codes_b),
             static_cast<const uint8_t*>(scales_a), static_cast<const uint8_t*>(scales_b),
             m, n, kb, out, ld, type == SBP_F32, accumulate != 0,
-            sbp::aligned(out, 16) && (m == 1 || ld * size % 16 == 0)};
+            sbp::aligned(out, 16) && (m == 1 || ld * size % 16 == 0), 1,
+            static_cast<int32_t>((kb + 15) / 16), 0, n};
   (void)hipGetLastError();
   if (k == 0) {
     const dim3 grid(static_cast<unsigned>((n + 1023) / 1024),
@@ -806,18 +1004,12 @@ sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_
     hipLaunchKernelGGL(mx4_zero_kernel, grid, dim3(256), 0, stream, p);
     return launched(who);
   }
-  if (m > kFewRows) {
-    char* ws = static_cast<char*>(workspace);
-    const int T = tile_of(m, n);
-    return T == 256   ? run_tiles<256>(who, p, ws, stream)
-           : T == 128 ? run_tiles<128>(who, p, ws, stream)
-                      : run_tiles<64>(who, p, ws, stream);
-  }
-  const int64_t tiles = ((n + 15) / 16) * ((m + 15) / 16);
-  if (tiles >= int64_t{1} << 24) return sbp::fail(SBP_ERANGE, w + ": too many results");
-  const dim3 grid(static_cast<unsigned>(tiles));
-  hipLaunchKernelGGL((mx4_few_kernel<1, 4>), grid, dim3(256), 0, stream, p);
-  return launched(who);
+  const Form f = form_of(m, n, kb);
+  char* ws = static_cast<char*>(workspace);
+  return f.T == 0     ? run_few(who, p, stream)
+         : f.T == 256 ? run_large(who, p, f, ws, stream)
+         : f.T == 128 ? run_small<Middle>(who, p, f, ws, stream)
+                      : run_small<Small>(who, p, f, ws, stream);
 }
 
 }  // namespace

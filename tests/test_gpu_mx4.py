@@ -250,7 +250,11 @@ def _check_product(got, a, b, bf16, before=None, what=""):
 PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 3, 5), (1, 4096, 4096), (7, 100, 777), (16, 1000, 256),
             (17, 33, 129), (40, 2000, 600), (64, 64, 64), (65, 130, 1000), (128, 128, 128),
             (130, 260, 100), (200, 300, 2080), (256, 256, 512), (257, 255, 545), (509, 1021, 777),
-            (640, 768, 768), (31, 5, 20000), (300, 140, 33), (1030, 520, 96)]
+            (640, 768, 768), (31, 5, 20000), (300, 140, 33), (1030, 520, 96),
+            # on both sides of where the form changes: few rows, tiles, parts of the sum
+            (1, 9000, 100), (2, 9000, 544), (16, 8192, 64), (17, 8192, 64), (32, 4096, 100),
+            (33, 4096, 100), (100, 300, 8192), (70, 61, 6144), (70, 61, 6113), (64, 1024, 7200),
+            (5, 8200, 6200), (1300, 1100, 544), (1300, 1101, 1056)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)

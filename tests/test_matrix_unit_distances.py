@@ -27,7 +27,7 @@ def _of_large_tiles(lines):
     on = False
     for line in lines:
         if line.endswith(">:"):
-            on = "mx4_tile_kernel" in line and "TileILi256" in line
+            on = "mx4_tile_kernel" in line and "TileILi256ELi64" in line
         if on:
             yield line
 

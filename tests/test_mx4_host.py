@@ -198,12 +198,16 @@ def _matmul(**kw):
         a["out"], a["type"], a["ld"], a["accumulate"], a["workspace"], a["bytes"], None)
 
 
+BIG = dict(m=8192, n=8192, k=512, ld=8192, codes_b=V(0x2000000), scales_a=V(0x3000000),
+           scales_b=V(0x4000000), out=V(0x50000000))
 DIM, MAX_K = sbp.MX_MAX_DIM, sbp.MX_MAX_K
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-1), EINVAL),
     (dict(m=DIM + 1), ERANGE), (dict(n=DIM + 1), ERANGE), (dict(k=MAX_K + 1), ERANGE),
+    (dict(m=1 << 20, k=MAX_K), ERANGE), (dict(n=1 << 20, ld=1 << 20, k=MAX_K), ERANGE),
+    (dict(m=1 << 20, n=(1 << 16) + 1, ld=1 << 20), ERANGE),
     (dict(type=2), EINVAL), (dict(accumulate=1), EINVAL),
     (dict(ld=199), EINVAL), (dict(ld=(1 << 32) + 1), ERANGE),
     (dict(codes_a=None), EINVAL), (dict(scales_a=None), EINVAL),
@@ -212,6 +216,11 @@ DIM, MAX_K = sbp.MX_MAX_DIM, sbp.MX_MAX_K
     (dict(out=V(0x5000001)), EALIGN), (dict(out=V(0x5000002), type=sbp.SBP_F32), EALIGN),
     (dict(out=V(0x1000000)), EINVAL), (dict(out=V(0x2000000)), EINVAL),
     (dict(out=V(0x3000000)), EINVAL), (dict(out=V(0x4000000)), EINVAL),
+    # 8192 x 8192: large tiles, whose workspace holds the packed scales
+    (dict(BIG, workspace=None), EINVAL), (dict(BIG, workspace=V(0x100000080)), EALIGN),
+    (dict(BIG, bytes=sbp.mx_matmul_workspace(8192, 8192, 512) - 1), EINVAL),
+    (dict(BIG, workspace=V(0x1000000)), EINVAL), (dict(BIG, workspace=V(0x4000000)), EINVAL),
+    (dict(BIG, workspace=V(0x50000000)), EINVAL),
 ])
 def test_matmul_refusals(kw, status):
     assert _matmul(**kw) == status
@@ -221,6 +230,16 @@ def test_matmul_refusals(kw, status):
 def test_nothing_to_multiply():
     for kw in (dict(m=0), dict(n=0), dict(k=0, type=sbp.SBP_F32, accumulate=1)):
         assert _matmul(codes_a=None, out=None, **kw) == sbp.SBP_OK
+
+
+def test_workspace_of_each_form():
+    """None for few rows and for tiles that are many or short; packed scales for large
+    ones; parts' sums for few tiles with long sums."""
+    assert sbp.mx_matmul_workspace(1, 4096, 4096) == 0
+    assert sbp.mx_matmul_workspace(512, 512, 512) == 0
+    assert sbp.mx_matmul_workspace(8192, 8192, 512) == 2 * 8192 * 16
+    assert sbp.mx_matmul_workspace(100, 300, 8192) == 4 * 100 * 300 * 4
+    assert sbp.mx_matmul_workspace(0, 10, 10) == 0
 
 
 def test_workspace_refuses_bad_sizes():
