@@ -843,6 +843,19 @@ def newton_schulz(mats, out=None, steps=5, coefs=NS_COEFS, eps=1e-7, out_scales=
 
 
 # ---- microscaled 4-bit floats ----------------------------------------------------
+# A product of one token takes a few microseconds of the device; these calls keep the
+# host's share near that: the stream as a number, no object made that is not needed.
+
+_torch = None  # the module, once a call has needed it
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
 
 class Mx4:
     """A rows x cols matrix in microscaled 4-bit floats (see include/sbp.h):
@@ -854,27 +867,38 @@ class Mx4:
     __slots__ = ("codes", "scales", "rows", "cols")
 
     def __init__(self, codes, scales, shape):
-        import torch
-        rows, cols = int(shape[0]), int(shape[1])
-        kb = -(-cols // MX_BLOCK)
+        u8 = _t().uint8
+        rows, cols = shape
         if rows < 0 or cols < 0:
             raise ValueError("Mx4: a negative size")
-        for t, width, what in ((codes, 16 * kb, "codes"), (scales, kb, "scales")):
-            if t.dtype != torch.uint8 or tuple(t.shape) != (rows, width):
-                raise ValueError(f"Mx4: {what} must be uint8 of shape {(rows, width)}, got "
-                                 f"{t.dtype} of {tuple(t.shape)}")
-            if not t.is_contiguous():
-                raise ValueError(f"Mx4: {what} must be contiguous")
+        kb = -(-cols // MX_BLOCK)
+        if (codes.dtype is not u8 or scales.dtype is not u8 or codes.shape != (rows, 16 * kb)
+                or scales.shape != (rows, kb)):
+            raise ValueError(f"Mx4: codes and scales must be uint8 of shapes {(rows, 16 * kb)} "
+                             f"and {(rows, kb)}, got {codes.dtype} of {tuple(codes.shape)} and "
+                             f"{scales.dtype} of {tuple(scales.shape)}")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("Mx4: codes and scales must be contiguous")
         if codes.device != scales.device:
             raise ValueError("Mx4: codes and scales on different devices")
         self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
 
     @classmethod
+    def _of(cls, codes, scales, rows, cols):
+        """Of tensors that are known to fit."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.rows, q.cols = codes, scales, rows, cols
+        return q
+
+    @classmethod
     def empty(cls, rows, cols, device):
-        import torch
-        kb = -(-int(cols) // MX_BLOCK)
-        return cls(torch.empty((rows, kb * 16), dtype=torch.uint8, device=device),
-                   torch.empty((rows, kb), dtype=torch.uint8, device=device), (rows, cols))
+        torch = _t()
+        rows, cols = int(rows), int(cols)
+        if rows < 0 or cols < 0:
+            raise ValueError("Mx4: a negative size")
+        kb = -(-cols // MX_BLOCK)
+        return cls._of(torch.empty((rows, kb * 16), dtype=torch.uint8, device=device),
+                       torch.empty((rows, kb), dtype=torch.uint8, device=device), rows, cols)
 
     @property
     def shape(self):
@@ -892,33 +916,64 @@ class Mx4:
         """The matrix of rows start .. stop - 1, a view."""
         if not 0 <= start <= stop <= self.rows:
             raise ValueError(f"Mx4.rows_of: {start}..{stop} outside {self.rows} rows")
-        return Mx4(self.codes[start:stop], self.scales[start:stop], (stop - start, self.cols))
+        return Mx4._of(self.codes[start:stop], self.scales[start:stop], stop - start, self.cols)
 
 
-def _mx4_type(t, what):
-    import torch
-    if t.dtype == torch.float32:
-        return SBP_F32
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+def _mx_type(t, what):
+    torch = _t()
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return SBP_BF16
-    raise ValueError(f"{what}: expected float32 or bf16 (or its 16-bit storage), got {t.dtype}")
+    if dtype is torch.float32:
+        return SBP_F32
+    if dtype in (torch.int16, torch.uint16):
+        return SBP_BF16
+    raise ValueError(f"{what}: expected float32 or bf16 (or its 16-bit storage), got {dtype}")
 
 
-def _mx4_rows(t, rows, cols, what):
-    """Row distance of a 1-D or 2-D device tensor that is rows x cols."""
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a device tensor")
-    if t.dim() not in (1, 2) or (1,) * (2 - t.dim()) + tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(t.shape)}")
-    if cols > 1 and t.stride(-1) != 1:
+def _mx_rows(t, rows, cols, what):
+    """Row distance of a 1-D or 2-D tensor that is rows x cols."""
+    shape = t.shape
+    if shape != (rows, cols) and not (rows == 1 and shape == (cols,)):
+        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(shape)}")
+    stride = t.stride()
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{what}: the elements of a row must be consecutive")
     # torch leaves the distance of a dimension of one element open
-    return t.stride(0) if t.dim() == 2 and rows > 1 else max(cols, 1)
+    return stride[0] if rows > 1 else max(cols, 1)
 
 
-def _same_device(dev, tensors, what):
-    if any(t is not None and t.device != dev for t in tensors):
-        raise ValueError(f"{what}: tensors on different devices")
+def _mx_stream(stream, index, what):
+    """The call's stream as a number: the given one, else the current one.  index:
+    the device of its tensors, which has to be the current one."""
+    torch = _t()
+    if index < 0:
+        raise ValueError(f"{what}: expected a device tensor")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors are on cuda:{index}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}; select it with torch.cuda.device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _mx_new(stream, s, dev, make):
+    """make()'s tensors on a call's stream s, and free to be used and freed on the
+    current one too."""
+    if stream is None:
+        return make()
+    torch = _t()
+    with _allocating_on(stream, ctypes.c_void_p(s), dev):
+        made = make()
+    for t in made:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return made
+
+
+def _mx_same(index, tensors, what):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{what}: tensors on different devices")
 
 
 def mx_quantize(x, along="rows", out=None, seed=None, offset=0, stream=None):
@@ -934,42 +989,54 @@ def mx_quantize(x, along="rows", out=None, seed=None, offset=0, stream=None):
     With `stream`, what the call allocates belongs to that stream, as in
     newton_schulz.
     """
-    import torch
     what = "mx_quantize"
-    if along not in ("rows", "cols", "both"):
-        raise ValueError(f"{what}: along must be 'rows', 'cols' or 'both'")
-    if x.dim() not in (1, 2):
+    shape = x.shape
+    if len(shape) == 2:
+        rows, cols = shape
+    elif len(shape) == 1:
+        rows, cols = 1, shape[0]
+    else:
         raise ValueError(f"{what}: x must be 1-D or 2-D")
-    rows, cols = x.shape if x.dim() == 2 else (1, x.shape[0])
-    kind = _mx4_type(x, what)
-    ld = _mx4_rows(x, rows, cols, what)
-    shapes = {"rows": [(rows, cols)], "cols": [(cols, rows)],
-              "both": [(rows, cols), (cols, rows)]}[along]
+    if along == "rows":
+        shapes = [(rows, cols)]
+    elif along == "cols":
+        shapes = [(cols, rows)]
+    elif along == "both":
+        shapes = [(rows, cols), (cols, rows)]
+    else:
+        raise ValueError(f"{what}: along must be 'rows', 'cols' or 'both'")
+    kind = _mx_type(x, what)
+    ld = _mx_rows(x, rows, cols, what)
     rnd = None
     if seed is not None:
         if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
             raise ValueError(f"{what}: seed and offset must be in 0..2^64 - 1")
-        rnd = MxRandom(seed, offset)
-    s = _stream(stream, x)
+        rnd = ctypes.byref(MxRandom(seed, offset))
+    index = x.get_device()
+    s = _mx_stream(stream, index, what)
     if out is None:
-        with _allocating_on(stream, s, x.device):
-            outs = [Mx4.empty(*sh, x.device) for sh in shapes]
-        if stream is not None:
-            for o in outs:
-                o.codes.record_stream(torch.cuda.current_stream(x.device))
-                o.scales.record_stream(torch.cuda.current_stream(x.device))
+        dev = x.device
+        outs = []
+
+        def make():
+            outs.extend([Mx4.empty(r, c, dev) for r, c in shapes])
+            return [t for o in outs for t in (o.codes, o.scales)]
+
+        _mx_new(stream, s, dev, make)
     else:
         outs = list(out) if along == "both" else [out]
         if [o.shape for o in outs] != shapes:
             raise ValueError(f"{what}: out has the wrong shape")
-        _same_device(x.device, [o.codes for o in outs], what)
-    a = outs[0] if along != "cols" else None
-    t = outs[-1] if along != "rows" else None
-    _check(lib().sbp_mx_quantize(
-        x.data_ptr(), kind, rows, cols, ld,
-        a.codes.data_ptr() if a else None, a.scales.data_ptr() if a else None,
-        t.codes.data_ptr() if t else None, t.scales.data_ptr() if t else None,
-        ctypes.byref(rnd) if rnd else None, s))
+        _mx_same(index, [o.codes for o in outs], what)
+    codes = scales = codes_t = scales_t = None
+    if along != "cols":
+        codes, scales = outs[0].codes.data_ptr(), outs[0].scales.data_ptr()
+    if along != "rows":
+        codes_t, scales_t = outs[-1].codes.data_ptr(), outs[-1].scales.data_ptr()
+    st = lib().sbp_mx_quantize(x.data_ptr(), kind, rows, cols, ld, codes, scales, codes_t, scales_t,
+                               rnd, s)
+    if st:
+        _check(st)
     return tuple(outs) if along == "both" else outs[0]
 
 
@@ -977,21 +1044,23 @@ def mx_dequantize(q, out=None, dtype=None, stream=None):
     """sbp_mx_dequantize: an Mx4's values, bf16 unless `dtype` (or out) says
     float32.  out: device tensor of q's shape, rows at any distance (1-D for one
     row); a new one [rows, cols] when not given."""
-    import torch
     what = "mx_dequantize"
-    s = _stream(stream, q.codes)
+    torch = _t()
+    codes = q.codes
+    index = codes.get_device()
+    s = _mx_stream(stream, index, what)
     if out is None:
-        with _allocating_on(stream, s, q.device):
-            out = torch.empty(q.shape, dtype=dtype or torch.bfloat16, device=q.device)
-        if stream is not None:
-            out.record_stream(torch.cuda.current_stream(q.device))
+        out, = _mx_new(stream, s, codes.device, lambda: [torch.empty(
+            (q.rows, q.cols), dtype=dtype or torch.bfloat16, device=codes.device)])
     elif dtype is not None and out.dtype != dtype:
         raise ValueError(f"{what}: out is {out.dtype}, not {dtype}")
-    kind = _mx4_type(out, what)
-    ld = _mx4_rows(out, q.rows, q.cols, what)
-    _same_device(q.device, [out], what)
-    _check(lib().sbp_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
-                                    out.data_ptr(), kind, ld, s))
+    kind = _mx_type(out, what)
+    ld = _mx_rows(out, q.rows, q.cols, what)
+    _mx_same(index, (out,), what)
+    st = lib().sbp_mx_dequantize(codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+                                 out.data_ptr(), kind, ld, s)
+    if st:
+        _check(st)
     return out
 
 
@@ -1004,28 +1073,35 @@ def mx_reduce_shard(peers, acc, scale, out, stream=None):
     n = out.numel()
     if acc is not None and acc.numel() != n:
         raise ValueError(f"{what}: acc and out differ in size")
-    for p in peers:
-        if p.numel != n:
+    index = out.get_device()
+    s = _mx_stream(stream, index, what)
+    R = len(peers)
+    codes = (ctypes.c_void_p * max(R, 1))()
+    scales = (ctypes.c_void_p * max(R, 1))()
+    for r, p in enumerate(peers):
+        if p.rows * p.cols != n:
             raise ValueError(f"{what}: a peer has {p.numel} values, out {n}")
         if p.rows > 1 and p.cols % MX_BLOCK:
             raise ValueError(f"{what}: a peer of several rows needs a multiple of {MX_BLOCK} "
                              "columns")
-    _same_device(out.device, [acc] + [p.codes for p in peers], what)
-    R = len(peers)
-    codes = (ctypes.c_void_p * max(R, 1))(*[_dev(p.codes, 1, what) for p in peers])
-    scales = (ctypes.c_void_p * max(R, 1))(*[p.scales.data_ptr() for p in peers])
-    _check(lib().sbp_mx_reduce_shard(
-        codes, scales, R, n, None if acc is None else _f32(acc, f"{what} acc"), float(scale),
-        _f32(out, f"{what} out"), _stream(stream, out)))
+        if p.codes.get_device() != index:
+            raise ValueError(f"{what}: tensors on different devices")
+        codes[r], scales[r] = p.codes.data_ptr(), p.scales.data_ptr()
+    _mx_same(index, (acc,), what)
+    st = lib().sbp_mx_reduce_shard(codes, scales, R, n,
+                                   None if acc is None else _f32(acc, f"{what} acc"),
+                                   float(scale), _f32(out, f"{what} out"), s)
+    if st:
+        _check(st)
 
 
 def mx_matmul_workspace(m, n, k):
     """Bytes of workspace sbp_mx_matmul needs for m x k times (n x k)'."""
-    need = lib().sbp_mx_matmul_workspace(int(m), int(n), int(k))
+    need = lib().sbp_mx_matmul_workspace(m, n, k)
     if need < 0:
         raise SbpError(SBP_EINVAL if min(m, n, k) < 0 else SBP_ERANGE,
                        lib().sbp_last_error().decode())
-    return int(need)
+    return need
 
 
 def mx_matmul(a, b, out=None, dtype=None, accumulate=False, workspace=None, stream=None):
@@ -1040,35 +1116,40 @@ def mx_matmul(a, b, out=None, dtype=None, accumulate=False, workspace=None, stre
     With `stream`, what the call allocates belongs to that stream, as in
     newton_schulz.
     """
-    import torch
     what = "mx_matmul"
-    if a.cols != b.cols:
-        raise ValueError(f"{what}: operands of {a.cols} and {b.cols} columns")
+    torch = _t()
     m, n, k = a.rows, b.rows, a.cols
+    if k != b.cols:
+        raise ValueError(f"{what}: operands of {k} and {b.cols} columns")
     if accumulate and out is None:
         raise ValueError(f"{what}: nothing to accumulate into")
-    s = _stream(stream, a.codes)
-    need = mx_matmul_workspace(m, n, k)
-    with _allocating_on(stream, s, a.device):
-        own_out = out is None
-        if own_out:
-            out = torch.empty((m, n), dtype=dtype or torch.bfloat16, device=a.device)
-        elif dtype is not None and out.dtype != dtype:
-            raise ValueError(f"{what}: out is {out.dtype}, not {dtype}")
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-    if own_out and stream is not None:
-        out.record_stream(torch.cuda.current_stream(a.device))
-    kind = _mx4_type(out, what)
-    ld = _mx4_rows(out, m, n, what)
-    _same_device(a.device, [b.codes, out, workspace], what)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError(f"{what}: workspace must be contiguous")
-    _check(lib().sbp_mx_matmul(
-        a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), m, n, k,
-        out.data_ptr(), kind, ld, 1 if accumulate else 0,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+    codes = a.codes
+    index = codes.get_device()
+    s = _mx_stream(stream, index, what)
+    if out is None:
+        out, = _mx_new(stream, s, codes.device, lambda: [torch.empty(
+            (m, n), dtype=dtype or torch.bfloat16, device=codes.device)])
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"{what}: out is {out.dtype}, not {dtype}")
+    kind = _mx_type(out, what)
+    ld = _mx_rows(out, m, n, what)
+    ws, size = None, 0
+    if workspace is None:
+        size = mx_matmul_workspace(m, n, k)
+        if size:
+            with _allocating_on(stream, ctypes.c_void_p(s), codes.device):
+                workspace = torch.empty(size, dtype=torch.uint8, device=codes.device)
+            ws = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous():
+            raise ValueError(f"{what}: workspace must be contiguous")
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _mx_same(index, (b.codes, out, workspace), what)
+    st = lib().sbp_mx_matmul(codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+                             b.scales.data_ptr(), m, n, k, out.data_ptr(), kind, ld,
+                             1 if accumulate else 0, ws, size, s)
+    if st:
+        _check(st)
     return out
 
 
