@@ -8,7 +8,7 @@
 //   random    s is one more where a > 6 * 2^(s - 127), so that nothing
 //             saturates; with Y = floor(|x| * 2^(127 - s) * 2^17) a code's step
 //             is 2^(16 + h), h = 0, 1, 2 for Y below 2^18, 2^19 and above, and
-//             code = ((Y + r * 2^h) >> (16 + h)) + 2h
+//             code = (((Y >> h) + r) >> 16) + 2h
 //             for 16 random bits r: up with the probability of what is cut off
 //             (its 16 highest bits), so the mean is x but for less than 2^-16
 //             of a step
@@ -48,6 +48,10 @@ struct Random {
   uint32_t key0, key1, off0, off1;
 };
 
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 // Philox4x32-10 of the counter (index, its highest bit set where `upper`; offset).
 __device__ __forceinline__ u32x4 philox(uint64_t index, bool upper, const Random& rnd) {
   uint32_t c0 = static_cast<uint32_t>(index);
@@ -57,9 +61,9 @@ __device__ __forceinline__ u32x4 philox(uint64_t index, bool upper, const Random
   for (int i = 0; i < 10; ++i) {
     const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
     const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
-    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+    c0 = xor3(static_cast<uint32_t>(p1 >> 32), c1, k0);
     c1 = static_cast<uint32_t>(p1);
-    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+    c2 = xor3(static_cast<uint32_t>(p0 >> 32), c3, k1);
     c3 = static_cast<uint32_t>(p0);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -171,7 +175,7 @@ __device__ __forceinline__ uint32_t random8(const Octet<T>& x, uint32_t s, u32x4
     const uint32_t Y =
         static_cast<uint32_t>(__builtin_ldexpf(fabsf(v), 144 - static_cast<int>(s)));
     const uint32_t top = Y >> 18, h = top < 2 ? top : 2;
-    const uint32_t code = ((Y + (r << h)) >> (16 + h)) + 2 * h;
+    const uint32_t code = ((Y >> h) + r + (h << 17)) >> 16;
     out |= (code | ((__float_as_uint(v) >> 28) & 8u)) << (4 * j);
   }
   return out;
@@ -188,34 +192,24 @@ __device__ __forceinline__ uint32_t codes_of(const Octet<T>& x, uint32_t s, uint
 }
 
 // ---- quantize: consecutive values ------------------------------------------------
-// U octets a lane, 64 lanes apart; n values, zeros up to the last block's end.
-template <typename T, bool RANDOM, bool VEC, int U>
+// n values, zeros up to the last block's end.  An octet a lane: with four (64 lanes
+// apart) 103.9M values in fp32 at random take 93 us, with one 79; in bf16 to nearest
+// 47 and 45.
+template <typename T, bool RANDOM, bool VEC>
 __global__ void __launch_bounds__(kBlock)
 quantize_flat_kernel(const T* __restrict__ x, int64_t n, int64_t blocks,
                      uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, Random rnd) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (64 * U);
-  const int64_t octets = blocks * 4;
-  Octet<T> v[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t at = (first + u * 64 + lane) * 8;
-    if (VEC && at + 8 <= n) v[u].load(x + at);
-    else if (at < n) v[u].load_some(x + at, n - at);
-    else v[u].zero();
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x, at = o * 8;
+  Octet<T> v;
+  if (VEC && at + 8 <= n) v.load(x + at);
+  else if (at < n) v.load_some(x + at, n - at);
+  else v.zero();
+  const uint32_t s = scale_of<RANDOM>(quad_max(v.top()));
+  const uint32_t c = codes_of<RANDOM>(v, s, static_cast<uint64_t>(o), false, rnd);
+  if (o < blocks * 4) {
+    codes[o] = c;
+    if ((o & 3) == 0) scales[o >> 2] = static_cast<uint8_t>(s);
   }
-  uint32_t mine = 0;  // of the scales that this lane stores
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t o = first + u * 64 + lane;
-    const uint32_t s = scale_of<RANDOM>(quad_max(v[u].top()));
-    const uint32_t c = codes_of<RANDOM>(v[u], s, static_cast<uint64_t>(o), false, rnd);
-    if (o < octets) codes[o] = c;
-    if ((lane & 3) == u) mine = s;
-  }
-  // lane 4i + u stores the scale of block i of the wave's run u
-  const int64_t b = first / 4 + (lane & 3) * 16 + (lane >> 2);
-  if ((lane & 3) < U && b < blocks) scales[b] = static_cast<uint8_t>(mine);
 }
 
 // ---- quantize: a matrix's rows, columns, or both ------------------------------------
@@ -232,17 +226,18 @@ __global__ void __launch_bounds__(kBlock)
 quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, int vec,
                        MatrixOut along, MatrixOut across, Random rnd, unsigned total) {
   __shared__ __align__(16) T tile[COLS ? kTile * kTile : 1];
-  // neighbouring tiles to one XCD, 2 x 2 of them together: lines that two tiles
-  // write parts of meet in its L2
+  // neighbouring tiles to one XCD, down strips of four: lines that several tiles write
+  // parts of (a column's codes and scales, a row's codes) meet in its L2.  8192 x 4096 in
+  // bf16, columns alone: along strips of two rows 26.2 us, this way 23.9
   unsigned t = blockIdx.x;
   const unsigned per = total / kXcds;
   if (t < per * kXcds) t = (t % kXcds) * per + t / kXcds;
   const unsigned tr = static_cast<unsigned>((rows + kTile - 1) / kTile);
   const unsigned tc = static_cast<unsigned>((cols + kTile - 1) / kTile);
-  const unsigned strip = t / (2 * tc), left = t - strip * 2 * tc;
-  const unsigned high = tr - 2 * strip < 2 ? 1 : 2;
-  const int64_t r0 = static_cast<int64_t>(2 * strip + left % high) * kTile;
-  const int64_t c0 = static_cast<int64_t>(left / high) * kTile;
+  const unsigned strip = t / (4 * tr), left = t - strip * 4 * tr;
+  const unsigned wide = tc - 4 * strip < 4 ? tc - 4 * strip : 4;
+  const int64_t c0 = static_cast<int64_t>(4 * strip + left % wide) * kTile;
+  const int64_t r0 = static_cast<int64_t>(left / wide) * kTile;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int oct = threadIdx.x & 15, row = threadIdx.x >> 4;
@@ -279,31 +274,31 @@ quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
     __syncthreads();
     const int64_t rb = r0 / 32 + wave;
     if (rb >= across.blocks) return;
-    // one octet of rows at a time would need the block's maximum first: two
-    // columns of 32 rows stay in registers
-    float a[2][32];
+    // two neighbouring columns of 32 rows stay in registers, each as four octets
+    Octet<T> q[2][4];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 32; i += 2) {
       const T* p = tile + (wave * 32 + i) * kTile + lane * 2;
       if constexpr (std::is_same_v<T, float>) {
-        a[0][i] = p[0];
-        a[1][i] = p[1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          q[k][i / 8].v[i % 8] = p[k];
+          q[k][i / 8].v[i % 8 + 1] = p[kTile + k];
+        }
       } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-        a[0][i] = sbp::bf16_lo(w);
-        a[1][i] = sbp::bf16_hi(w);
+        const uint32_t lo = *reinterpret_cast<const uint32_t*>(p);
+        const uint32_t hi = *reinterpret_cast<const uint32_t*>(p + kTile);
+        q[0][i / 8].w[i % 8 / 2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        q[1][i / 8].w[i % 8 / 2] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
       }
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int64_t col = c0 + lane * 2 + k;
-      Octet<float> q[4];
       uint32_t top = 0;
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[o].v[j] = a[k][o * 8 + j];
-        const uint32_t m = q[o].top();
+        const uint32_t m = q[k][o].top();
         top = m > top ? m : top;
       }
       const uint32_t s = scale_of<RANDOM>(top);
@@ -311,7 +306,7 @@ quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
       u32x4 w;
 #pragma unroll
       for (int o = 0; o < 4; ++o)
-        w[o] = codes_of<RANDOM>(q[o], s, static_cast<uint64_t>(b * 4 + o), true, rnd);
+        w[o] = codes_of<RANDOM>(q[k][o], s, static_cast<uint64_t>(b * 4 + o), true, rnd);
       if (col < cols) {
         reinterpret_cast<u32x4*>(across.codes)[b] = w;
         across.scales[b] = static_cast<uint8_t>(s);
@@ -348,36 +343,26 @@ __device__ __forceinline__ void store_octet(float* p, uint32_t w, float scale, b
   }
 }
 
-// FLAT: the rows' blocks and values lie one after the other.
-template <typename T, bool FLAT, int U>
+// FLAT: the rows' blocks and values lie one after the other.  An octet a lane, as
+// above: 103.9M values to bf16 52 us, with four 56.
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kBlock)
 dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                   int64_t octets, int64_t row_octets, int64_t cols, int64_t ld, int vec,
                   T* __restrict__ out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (64 * U);
-  uint32_t w[U], s[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t o = first + u * 64 + lane;
-    w[u] = o < octets ? codes[o] : 0u;
-    s[u] = o < octets ? scales[o >> 2] : 0u;
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  if (o >= octets) return;
+  const uint32_t w = codes[o], s = scales[o >> 2];
+  int64_t at = o * 8, left = cols - at;
+  if constexpr (!FLAT) {
+    const int64_t row = octets <= UINT32_MAX
+                            ? static_cast<uint32_t>(o) / static_cast<uint32_t>(row_octets)
+                            : o / row_octets;
+    const int64_t c = (o - row * row_octets) * 8;
+    at = row * ld + c;
+    left = cols - c;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t o = first + u * 64 + lane;
-    if (o >= octets) continue;
-    int64_t at = o * 8, left = cols - at;
-    if constexpr (!FLAT) {
-      const int64_t row = octets <= UINT32_MAX
-                              ? static_cast<uint32_t>(o) / static_cast<uint32_t>(row_octets)
-                              : o / row_octets;
-      const int64_t c = (o - row * row_octets) * 8;
-      at = row * ld + c;
-      left = cols - c;
-    }
-    if (left > 0) store_octet(out + at, w[u], sbp::mx4_scale(s[u]), vec, left);
-  }
+  if (left > 0) store_octet(out + at, w, sbp::mx4_scale(s), vec, left);
 }
 
 // ---- reduce: out = fl((acc + S) * scale) ------------------------------------------------
@@ -386,51 +371,45 @@ struct Mx4Peers {
   const uint8_t* scales[SBP_MAX_PEERS];
 };
 
-template <int R, bool ACC, int U>
+// An octet a lane: more of them fall behind as the peers grow (R = 8 with an
+// accumulator, 103.9M values 237 us, with two 250; R = 2 without 116, with four 127).
+template <int R, bool ACC>
 __global__ void __launch_bounds__(kBlock)
 reduce_mx4_kernel(Mx4Peers P, const float* acc, float scale, float* out, int64_t n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * (64 * U);
-  uint32_t w[U][R], s[U][R];
-  Octet<float> a[U];
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x, left = n - o * 8;
+  if (left <= 0) return;
+  uint32_t w[R], s[R];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t o = first + u * 64 + lane, left = n - o * 8;
+  for (int r = 0; r < R; ++r) {
+    w[r] = P.codes[r][o];
+    s[r] = P.scales[r][o >> 2];
+  }
+  Octet<float> a;
+  if constexpr (ACC) {
+    if (left >= 8) a.load(acc + o * 8);
+    else a.load_some(acc + o * 8, left);
+  }
+  float S[8], v[8];
+  sbp::mx4_octet(w[0], sbp::mx4_scale(s[0]), S);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      w[u][r] = left > 0 ? P.codes[r][o] : 0u;
-      s[u][r] = left > 0 ? P.scales[r][o >> 2] : 0u;
-    }
-    if constexpr (ACC) {
-      if (left >= 8) a[u].load(acc + o * 8);
-      else a[u].load_some(acc + o * 8, left);
-    }
+  for (int r = 1; r < R; ++r) {
+    sbp::mx4_octet(w[r], sbp::mx4_scale(s[r]), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) S[j] = S[j] + v[j];
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t o = first + u * 64 + lane, left = n - o * 8;
-    float S[8], v[8];
-    sbp::mx4_octet(w[u][0], sbp::mx4_scale(s[u][0]), S);
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (ACC) S[j] = a.v[j] + S[j];
+    S[j] = S[j] * scale;
+  }
+  if (left >= 8) {
+    f32x4* p = reinterpret_cast<f32x4*>(out + o * 8);
+    p[0] = f32x4{S[0], S[1], S[2], S[3]};
+    p[1] = f32x4{S[4], S[5], S[6], S[7]};
+  } else {
 #pragma unroll
-    for (int r = 1; r < R; ++r) {
-      sbp::mx4_octet(w[u][r], sbp::mx4_scale(s[u][r]), v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) S[j] = S[j] + v[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (ACC) S[j] = a[u].v[j] + S[j];
-      S[j] = S[j] * scale;
-    }
-    if (left >= 8) {
-      f32x4* p = reinterpret_cast<f32x4*>(out + o * 8);
-      p[0] = f32x4{S[0], S[1], S[2], S[3]};
-      p[1] = f32x4{S[4], S[5], S[6], S[7]};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < left) out[o * 8 + j] = S[j];
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j < left) out[o * 8 + j] = S[j];
   }
 }
 
@@ -477,9 +456,8 @@ bool any_overlap(const Bytes* r, int n, int outs) {
   return false;
 }
 
-unsigned grid_of(int64_t octets, int per_lane) {
-  const int64_t per = static_cast<int64_t>(kBlock) * per_lane;
-  return static_cast<unsigned>((octets + per - 1) / per);
+unsigned grid_of(int64_t octets) {
+  return static_cast<unsigned>((octets + kBlock - 1) / kBlock);
 }
 
 // Calls f(std::integral_constant<int, R>) for R in 1..16.
@@ -499,17 +477,13 @@ sbp_status quantize(const char* who, const T* x, int64_t rows, int64_t cols, int
     const bool aligned = sbp::aligned(x, 16);
     if (across.codes == nullptr && (rows == 1 || (ld == cols && cols % 32 == 0))) {
       const int64_t n = rows * cols, blocks = sbp::mx4_blocks(n);
-      // four octets a lane once they fill the chip
-      const bool many = blocks * 4 >= 4 * 256 * kBlock;
-      auto flat = [&](auto kernel, int per_lane) -> sbp_status {
-        hipLaunchKernelGGL(kernel, dim3(grid_of(blocks * 4, per_lane)), dim3(kBlock), 0, stream, x,
-                           n, blocks, along.codes, along.scales, rnd);
+      auto flat = [&](auto kernel) -> sbp_status {
+        hipLaunchKernelGGL(kernel, dim3(grid_of(blocks * 4)), dim3(kBlock), 0, stream, x, n, blocks,
+                           along.codes, along.scales, rnd);
         return launched(who);
       };
-      if (many && aligned) return flat(quantize_flat_kernel<T, kRandom, true, 4>, 4);
-      if (many) return flat(quantize_flat_kernel<T, kRandom, false, 4>, 4);
-      if (aligned) return flat(quantize_flat_kernel<T, kRandom, true, 1>, 1);
-      return flat(quantize_flat_kernel<T, kRandom, false, 1>, 1);
+      if (aligned) return flat(quantize_flat_kernel<T, kRandom, true>);
+      return flat(quantize_flat_kernel<T, kRandom, false>);
     }
     const int64_t tiles = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
     const int vec = aligned && (rows == 1 || ld * sizeof(T) % 16 == 0);
@@ -570,15 +544,13 @@ sbp_status dequantize(const char* who, const void* codes, const void* scales, in
   const bool flat = rows == 1 || (ld == cols && cols % 32 == 0);
   const int vec = sbp::aligned(out, 16) && (flat || ld * sizeof(T) % 16 == 0);
   const int64_t width = flat ? rows * cols : cols;
-  auto go = [&](auto kernel, int per_lane) -> sbp_status {
-    hipLaunchKernelGGL(kernel, dim3(grid_of(octets, per_lane)), dim3(kBlock), 0, stream,
+  auto go = [&](auto kernel) -> sbp_status {
+    hipLaunchKernelGGL(kernel, dim3(grid_of(octets)), dim3(kBlock), 0, stream,
                        static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales),
                        octets, row_octets, width, ld, vec, out);
     return launched(who);
   };
-  const bool many = octets >= 4 * 256 * kBlock;
-  if (flat) return many ? go(dequantize_kernel<T, true, 4>, 4) : go(dequantize_kernel<T, true, 1>, 1);
-  return many ? go(dequantize_kernel<T, false, 4>, 4) : go(dequantize_kernel<T, false, 1>, 1);
+  return flat ? go(dequantize_kernel<T, true>) : go(dequantize_kernel<T, false>);
 }
 
 sbp_status dequantize_call(const char* who, const void* codes, const void* scales, int64_t rows,
@@ -633,13 +605,12 @@ sbp_status reduce_call(const char* who, const void* const* codes, const void* co
   (void)hipGetLastError();
   return with_peers(R, [&](auto rc) -> sbp_status {
     constexpr int RR = decltype(rc)::value;
-    constexpr int U = RR <= 2 ? 4 : RR <= 4 ? 2 : 1;
     auto go = [&](auto kernel) -> sbp_status {
-      hipLaunchKernelGGL(kernel, dim3(grid_of(blocks * 4, U)), dim3(kBlock), 0, stream, P, acc,
+      hipLaunchKernelGGL(kernel, dim3(grid_of(blocks * 4)), dim3(kBlock), 0, stream, P, acc,
                          scale, out, n);
       return launched(who);
     };
-    return acc ? go(reduce_mx4_kernel<RR, true, U>) : go(reduce_mx4_kernel<RR, false, U>);
+    return acc ? go(reduce_mx4_kernel<RR, true>) : go(reduce_mx4_kernel<RR, false>);
   }, std::make_integer_sequence<int, SBP_MAX_PEERS>{});
 }
 
