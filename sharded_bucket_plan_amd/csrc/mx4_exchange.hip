@@ -19,7 +19,9 @@
 //
 // Every kernel is one pass over memory.  A lane works on octets of 8 values,
 // four neighbouring lanes on a block, so that loads and stores of a wave are
-// contiguous and the block's maximum takes two lane exchanges.
+// contiguous and the block's maximum takes two lane exchanges.  Whole octets are 16
+// bytes of bf16 (32 of fp32) at any address that fits their type: the hardware's
+// vector loads and stores take those.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -80,7 +82,7 @@ template <>
 struct Octet<uint16_t> {  // bf16 bits, two a word
   u32x4 w;
   __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
-  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void load(const uint16_t* p) { __builtin_memcpy(&w, p, 16); }
   __device__ __forceinline__ void load_some(const uint16_t* p, int64_t left) {
     auto one = [&](int j) -> uint32_t { return j < left ? p[j] : 0u; };
     w = u32x4{one(0) | one(1) << 16, one(2) | one(3) << 16, one(4) | one(5) << 16,
@@ -118,7 +120,9 @@ struct Octet<float> {
     for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   }
   __device__ __forceinline__ void load(const float* p) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+    f32x4 a, b;
+    __builtin_memcpy(&a, p, 16);
+    __builtin_memcpy(&b, p + 4, 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[j] = a[j];
@@ -195,13 +199,13 @@ __device__ __forceinline__ uint32_t codes_of(const Octet<T>& x, uint32_t s, uint
 // n values, zeros up to the last block's end.  An octet a lane: with four (64 lanes
 // apart) 103.9M values in fp32 at random take 93 us, with one 79; in bf16 to nearest
 // 47 and 45.
-template <typename T, bool RANDOM, bool VEC>
+template <typename T, bool RANDOM>
 __global__ void __launch_bounds__(kBlock)
 quantize_flat_kernel(const T* __restrict__ x, int64_t n, int64_t blocks,
                      uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, Random rnd) {
   const int64_t o = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x, at = o * 8;
   Octet<T> v;
-  if (VEC && at + 8 <= n) v.load(x + at);
+  if (at + 8 <= n) v.load(x + at);
   else if (at < n) v.load_some(x + at, n - at);
   else v.zero();
   const uint32_t s = scale_of<RANDOM>(quad_max(v.top()));
@@ -223,7 +227,7 @@ struct MatrixOut {
 
 template <typename T, bool RANDOM, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kBlock)
-quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, int vec,
+quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
                        MatrixOut along, MatrixOut across, Random rnd, unsigned total) {
   __shared__ __align__(16) T tile[COLS ? kTile * kTile : 1];
   // neighbouring tiles to one XCD, down strips of four: lines that several tiles write
@@ -248,7 +252,7 @@ quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
   for (int p = 0; p < kPasses; ++p) {
     const int64_t r = r0 + p * 16 + row;
     const T* from = x + r * ld + c;
-    if (r < rows && c + 8 <= cols && vec) v[p].load(from);
+    if (r < rows && c + 8 <= cols) v[p].load(from);
     else if (r < rows && c < cols) v[p].load_some(from, cols - c);
     else v[p].zero();
   }
@@ -317,25 +321,26 @@ quantize_matrix_kernel(const T* __restrict__ x, int64_t rows, int64_t cols, int6
 
 // ---- dequantize ---------------------------------------------------------------------
 
-__device__ __forceinline__ void store_octet(uint16_t* p, uint32_t w, float scale, bool vec,
+__device__ __forceinline__ void store_octet(uint16_t* p, uint32_t w, float scale,
                                             int64_t left) {
   const u32x4 v{sbp::mx4_pair_bf16<0>(w, scale), sbp::mx4_pair_bf16<1>(w, scale),
                 sbp::mx4_pair_bf16<2>(w, scale), sbp::mx4_pair_bf16<3>(w, scale)};
-  if (vec && left >= 8) {
-    *reinterpret_cast<u32x4*>(p) = v;
+  if (left >= 8) {
+    __builtin_memcpy(p, &v, 16);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < left) p[j] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
   }
 }
-__device__ __forceinline__ void store_octet(float* p, uint32_t w, float scale, bool vec,
+__device__ __forceinline__ void store_octet(float* p, uint32_t w, float scale,
                                             int64_t left) {
   float v[8];
   sbp::mx4_octet(w, scale, v);
-  if (vec && left >= 8) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  if (left >= 8) {
+    const f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+    __builtin_memcpy(p, &a, 16);
+    __builtin_memcpy(p + 4, &b, 16);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -348,7 +353,7 @@ __device__ __forceinline__ void store_octet(float* p, uint32_t w, float scale, b
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kBlock)
 dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                  int64_t octets, int64_t row_octets, int64_t cols, int64_t ld, int vec,
+                  int64_t octets, int64_t row_octets, int64_t cols, int64_t ld,
                   T* __restrict__ out) {
   const int64_t o = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
   if (o >= octets) return;
@@ -362,7 +367,7 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
     at = row * ld + c;
     left = cols - c;
   }
-  if (left > 0) store_octet(out + at, w, sbp::mx4_scale(s), vec, left);
+  if (left > 0) store_octet(out + at, w, sbp::mx4_scale(s), left);
 }
 
 // ---- reduce: out = fl((acc + S) * scale) ------------------------------------------------
@@ -474,7 +479,6 @@ sbp_status quantize(const char* who, const T* x, int64_t rows, int64_t cols, int
                     hipStream_t stream) {
   auto go = [&](auto random_c) -> sbp_status {
     constexpr bool kRandom = decltype(random_c)::value;
-    const bool aligned = sbp::aligned(x, 16);
     if (across.codes == nullptr && (rows == 1 || (ld == cols && cols % 32 == 0))) {
       const int64_t n = rows * cols, blocks = sbp::mx4_blocks(n);
       auto flat = [&](auto kernel) -> sbp_status {
@@ -482,14 +486,12 @@ sbp_status quantize(const char* who, const T* x, int64_t rows, int64_t cols, int
                            along.codes, along.scales, rnd);
         return launched(who);
       };
-      if (aligned) return flat(quantize_flat_kernel<T, kRandom, true>);
-      return flat(quantize_flat_kernel<T, kRandom, false>);
+      return flat(quantize_flat_kernel<T, kRandom>);
     }
     const int64_t tiles = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
-    const int vec = aligned && (rows == 1 || ld * sizeof(T) % 16 == 0);
     auto matrix = [&](auto kernel) -> sbp_status {
       hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles)), dim3(kBlock), 0, stream, x,
-                         rows, cols, ld, vec, along, across, rnd, static_cast<unsigned>(tiles));
+                         rows, cols, ld, along, across, rnd, static_cast<unsigned>(tiles));
       return launched(who);
     };
     if (across.codes == nullptr) return matrix(quantize_matrix_kernel<T, kRandom, true, false>);
@@ -542,12 +544,11 @@ sbp_status dequantize(const char* who, const void* codes, const void* scales, in
                       int64_t cols, T* out, int64_t ld, hipStream_t stream) {
   const int64_t row_octets = sbp::mx4_blocks(cols) * 4, octets = rows * row_octets;
   const bool flat = rows == 1 || (ld == cols && cols % 32 == 0);
-  const int vec = sbp::aligned(out, 16) && (flat || ld * sizeof(T) % 16 == 0);
   const int64_t width = flat ? rows * cols : cols;
   auto go = [&](auto kernel) -> sbp_status {
     hipLaunchKernelGGL(kernel, dim3(grid_of(octets)), dim3(kBlock), 0, stream,
                        static_cast<const uint32_t*>(codes), static_cast<const uint8_t*>(scales),
-                       octets, row_octets, width, ld, vec, out);
+                       octets, row_octets, width, ld, out);
     return launched(who);
   };
   return flat ? go(dequantize_kernel<T, true>) : go(dequantize_kernel<T, false>);

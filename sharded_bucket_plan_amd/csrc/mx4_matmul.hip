@@ -38,7 +38,6 @@ struct Problem {
   void* out;
   int64_t ld;
   int32_t f32, accumulate;
-  int32_t vec;  // out's rows are 16-byte aligned
   // small tiles: parts of the contracted axis, each of so many chunks of 512 values
   // and with sums of its own, this many elements further on
   int32_t parts, part_chunks;
@@ -56,14 +55,62 @@ __device__ __forceinline__ f32x4 product(u32x4 b, uint32_t sb, u32x4 a, uint32_t
                                                           static_cast<int>(sa));
 }
 
+// An operand's scales as a lane takes them: 4 * W of a row at a time, `skip` blocks on.
+// load() asks for them, at any address, and only fix() waits for them.  Past a row's end
+// there are zeros; its last ones may end the array (of at least 4 * W), where the bytes
+// before that are read.  No branch around the load, behind which the compiler would
+// wait for all loads on the way.  WIDE: rows of whole chunks.
+template <bool WIDE, int W>
+struct RowScales {
+  using Words = uint32_t __attribute__((ext_vector_type(W)));
+  const uint8_t* row;
+  const uint8_t* end;  // of all rows'
+  int skip;
+  __device__ __forceinline__ RowScales(const uint8_t* scales, int64_t r, int64_t rows, int64_t kb,
+                                       int skip_)
+      : row(scales + r * kb + skip_), end(scales + rows * kb), skip(skip_) {}
+  RowScales() = default;
+  __device__ __forceinline__ Words load(int64_t block) const {
+    Words w;
+    const uint8_t* from = row + block;
+    if constexpr (!WIDE) from = from + 4 * W > end ? end - 4 * W : from;
+    __builtin_memcpy(&w, from, 4 * W);
+    return w;
+  }
+  __device__ __forceinline__ Words fix(Words w, int64_t block, int64_t kb) const {
+    if (WIDE || block + 16 <= kb) return w;
+    const int64_t over = row + block + 4 * W - end;
+    const int shift = over > 0 ? static_cast<int>(over) : 0;  // bytes
+    const int have = static_cast<int>(kb - block) - skip;
+    Words out;
+#pragma unroll
+    for (int d = 0; d < W; ++d) {
+      uint32_t lo = 0, hi = 0;  // words d + shift / 4 and the next
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        lo = e == d + (shift >> 2) ? w[e] : lo;
+        hi = e == d + (shift >> 2) + 1 ? w[e] : hi;
+      }
+      const uint32_t x = __builtin_amdgcn_alignbyte(hi, lo, shift & 3);
+      const int n = have - 4 * d;
+      out[d] = n >= 4 ? x : n > 0 ? x & ((1u << (8 * n)) - 1) : 0u;
+    }
+    return out;
+  }
+};
+
 // Four neighbours of a row of C, from column c on.
 __device__ __forceinline__ void store4(const Problem& p, int64_t row, int64_t c, f32x4 v) {
   const int64_t at = row * p.ld + c;
   if (p.f32) {
     float* o = static_cast<float*>(p.out) + at;
-    if (p.vec && c + 4 <= p.n) {
-      if (p.accumulate) v = *reinterpret_cast<const f32x4*>(o) + v;
-      *reinterpret_cast<f32x4*>(o) = v;
+    if (c + 4 <= p.n) {
+      if (p.accumulate) {
+        f32x4 old;
+        __builtin_memcpy(&old, o, 16);
+        v = old + v;
+      }
+      __builtin_memcpy(o, &v, 16);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -73,8 +120,9 @@ __device__ __forceinline__ void store4(const Problem& p, int64_t row, int64_t c,
     uint16_t* o = static_cast<uint16_t*>(p.out) + at;
     const uint32_t w[4] = {sbp::bf16_rne(v.x), sbp::bf16_rne(v.y), sbp::bf16_rne(v.z),
                            sbp::bf16_rne(v.w)};
-    if (p.vec && c + 4 <= p.n) {
-      *reinterpret_cast<u32x2*>(o) = u32x2{w[0] | w[1] << 16, w[2] | w[3] << 16};
+    if (c + 4 <= p.n) {
+      const u32x2 x{w[0] | w[1] << 16, w[2] | w[3] << 16};
+      __builtin_memcpy(o, &x, 8);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -86,43 +134,39 @@ __device__ __forceinline__ void store4(const Problem& p, int64_t row, int64_t c,
 // ---- few rows: 16 columns and 16 * MT rows of C a block ------------------------------
 // Its W waves share the contracted axis: a wave takes every W-th chunk of 512 values
 // (16 blocks, four products), with operands straight from memory, 4 KB of B's codes
-// under way a wave.  The waves' sums meet in LDS, in the waves' order.
-// WIDE: rows of whole chunks, scales on 16-byte addresses, so that a lane takes its
-// row's 16 scales at once; else block by block.
+// under way a wave.  The waves' sums meet in LDS, in the waves' order.  Also for an
+// operand of fewer than 16 blocks in all, of any rows of A.
+template <bool WIDE>
 struct FewOperand {
   const char* codes;  // of this lane's row and its first block
-  const uint8_t* scales;
+  RowScales<WIDE, 4> scales;
+  bool tiny;  // fewer than 16 blocks in all
 };
 template <bool WIDE>
 struct Chunk {
   u32x4 codes[4];
-  uint32_t scale[4];
-  __device__ __forceinline__ void load(const FewOperand& o, int64_t c, int g, int64_t kb) {
-    if constexpr (WIDE) {
+  u32x4 scales;
+  __device__ __forceinline__ void load(const FewOperand<WIDE>& o, int64_t c, int g, int64_t kb) {
+    const bool whole = WIDE || c * 16 + 16 <= kb;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; ++s) {
+      codes[s] = u32x4{0, 0, 0, 0};
+      if (whole || c * 16 + s * 4 + g < kb)
         codes[s] = *reinterpret_cast<const u32x4*>(o.codes + c * 256 + s * 64);
-      const u32x4 w = *reinterpret_cast<const u32x4*>(o.scales + c * 16);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) scale[s] = w[s];
+    }
+    if (!WIDE && o.tiny) {  // then there is one chunk
+      scales = u32x4{0, 0, 0, 0};
+      for (int i = 0; i < kb; ++i)
+        scales[i >> 2] |= static_cast<uint32_t>(o.scales.row[i]) << (8 * (i & 3));
     } else {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int64_t block = c * 16 + s * 4;
-        const bool in = block + g < kb;
-        codes[s] = u32x4{0, 0, 0, 0};
-        scale[s] = 0;
-        if (in) {
-          codes[s] = *reinterpret_cast<const u32x4*>(o.codes + block * 16);
-          scale[s] = o.scales[block + g];
-        }
-      }
+      scales = o.scales.load(c * 16);
     }
   }
-  // The lane's scale in the lowest byte.
-  __device__ __forceinline__ uint32_t of(int s, int g) const {
-    return WIDE ? scale[s] >> (8 * g) : scale[s];
+  __device__ __forceinline__ void fix(const FewOperand<WIDE>& o, int64_t c, int64_t kb) {
+    if (WIDE || !o.tiny) scales = o.scales.fix(scales, c * 16, kb);
   }
+  // The lane's scale in the lowest byte.
+  __device__ __forceinline__ uint32_t of(int s, int g) const { return scales[s] >> (8 * g); }
 };
 
 template <int MT, int W, bool WIDE>
@@ -130,16 +174,19 @@ __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
   __shared__ f32x4 sums[W][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const unsigned across = static_cast<unsigned>((p.n + 15) / 16);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / across) * (16 * MT);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x % across) * 16;
   // rows past the matrix read the last one; their results are not stored
   auto operand = [&](const char* codes, const uint8_t* scales, int64_t row, int64_t rows) {
-    const int64_t at = (row < rows ? row : rows - 1) * p.kb;
-    return FewOperand{codes + (at + g) * 16, scales + at};
+    const int64_t at = row < rows ? row : rows - 1;
+    return FewOperand<WIDE>{codes + (at * p.kb + g) * 16,
+                            RowScales<WIDE, 4>(scales, at, rows, p.kb, 0), rows * p.kb < 16};
   };
-  const FewOperand B = operand(p.b, p.sb, n0 + r, p.n);
-  FewOperand A[MT];
+  const FewOperand<WIDE> B = operand(p.b, p.sb, n0 + r, p.n);
+  FewOperand<WIDE> A[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) A[i] = operand(p.a, p.sa, i * 16 + r, p.m);
+  for (int i = 0; i < MT; ++i) A[i] = operand(p.a, p.sa, m0 + i * 16 + r, p.m);
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
@@ -149,6 +196,9 @@ __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
     b.load(B, c, g, p.kb);
 #pragma unroll
     for (int i = 0; i < MT; ++i) a[i].load(A[i], c, g, p.kb);
+    b.fix(B, c, p.kb);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) a[i].fix(A[i], c, p.kb);
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -162,7 +212,8 @@ __global__ void __launch_bounds__(W * 64) mx4_few_kernel(Problem p) {
     f32x4 v = sums[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) v = v + sums[w][wave][lane];
-    if (wave * 16 + r < p.m) store4(p, wave * 16 + r, n0 + g * 4, v);
+    const int64_t row = m0 + wave * 16 + r;
+    if (row < p.m) store4(p, row, n0 + g * 4, v);
   }
 }
 
@@ -303,23 +354,13 @@ template <typename TL>
 struct Scales {  // of a chunk: byte s % 4 of word s / 4 for its steps s of 64 values
   u32x2 a[TL::kSub], b[TL::kSub];
 };
-// The same from memory: of a row's 16 scales the even or (h) odd ones.  WIDE: they
-// all exist, on a 16-byte address.
-template <bool WIDE>
-__device__ __forceinline__ u32x2 row_scales(const uint8_t* row, int64_t block, int64_t kb, int h) {
-  if constexpr (WIDE) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(row + block);
-    const uint32_t pick = h ? 0x07050301u : 0x06040200u;
-    return u32x2{__builtin_amdgcn_perm(w.y, w.x, pick), __builtin_amdgcn_perm(w.w, w.z, pick)};
-  } else {
-    u32x2 out{0, 0};
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const int64_t b = block + 2 * s + h;
-      if (b < kb) out[s >> 2] |= static_cast<uint32_t>(row[b]) << (8 * (s & 3));
-    }
-    return out;
-  }
+// The same of the 8 scales that a lane has of a row's 16, the lower half of the lanes the
+// first and the upper half the others: each half takes its own, even or odd, of both.
+__device__ __forceinline__ u32x2 every_other(u32x2 w) {
+  const uint32_t even = __builtin_amdgcn_perm(w.y, w.x, 0x06040200u);
+  const uint32_t odd = __builtin_amdgcn_perm(w.y, w.x, 0x07050301u);
+  const auto r = __builtin_amdgcn_permlane32_swap(even, odd, false, false);
+  return u32x2{r[0], r[1]};
 }
 template <typename TL>
 using Acc = f32x16[TL::kSub][TL::kSub];
@@ -397,9 +438,39 @@ struct Packed {
 
 enum Out { kBf16, kF32, kAdd };
 
+// The first `left` values of 16 bytes of results.
+template <Out O>
+__device__ __forceinline__ void store_piece(char* to, int left, u32x4 w) {
+  if constexpr (O == kBf16) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(to);
+    if (left >= 8) {
+      __builtin_memcpy(o, &w, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    float* o = reinterpret_cast<float*>(to);
+    f32x4 v = __builtin_bit_cast(f32x4, w);
+    if (left >= 4) {
+      if constexpr (O == kAdd) {
+        f32x4 old;
+        __builtin_memcpy(&old, o, 16);
+        v = old + v;
+      }
+      __builtin_memcpy(o, &v, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = O == kAdd ? o[i] + v[i] : v[i];
+    }
+  }
+}
+
 // DIRECT: C's rows are made of whole 16-byte pieces on such addresses, a tile's within
 // 2^31 bytes.
-// WIDE: rows of whole chunks, scales on 16-byte addresses (small tiles).
+// WIDE: rows of whole chunks (small and middle tiles).
 template <typename TL, Out O, bool DIRECT, bool WIDE>
 __global__ void __launch_bounds__(256, TL::kLarge ? 1 : 2)
 mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
@@ -429,8 +500,10 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   struct Place {
     unsigned ti, tj;
   };
-  auto place_of = [&](unsigned i) {  // strips of 8 tile rows, column by column
-    constexpr unsigned kStrip = 8;
+  // Strips of 4 tile rows, column by column (4096 x 4096 x 4096 40.2 us, of 8 41.1; at
+  // larger sizes within 0.5%, of 16 up to 2% behind).
+  auto place_of = [&](unsigned i) {
+    constexpr unsigned kStrip = 4;
     const unsigned t = (base + i) % (tr * tc);
     const unsigned strip = t / (kStrip * tc), left = tr - strip * kStrip;
     const unsigned high = left < kStrip ? left : kStrip, s = t - strip * kStrip * tc;
@@ -491,18 +564,26 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     pb += packed.step_b;
   };
   // small tiles: the lane's rows' scales; past the matrix the last row's
-  const uint8_t *row_a[kSub], *row_b[kSub];
+  RowScales<WIDE, 2> row_a[kSub], row_b[kSub];
   int64_t scale_block = static_cast<int64_t>(first_chunk) * 16;
   Frags<TL> f[2];
-  Scales<TL> sc, next_sc;
-  auto take_scales = [&](Scales<TL>& to) {
+  Scales<TL> sc;
+  u32x2 raw_a[kLarge ? 1 : kSub], raw_b[kLarge ? 1 : kSub];  // the next chunk's
+  auto ask_scales = [&]() {
     // a chunk past the end repeats the last one's blocks; it is not used
     const int64_t last = (p.kb - 1) / 16 * 16;
-    const int64_t at = scale_block < last ? scale_block : last;
+    if (scale_block > last) scale_block = last;
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
-      to.a[i] = row_scales<WIDE>(row_a[i], at, p.kb, lane >> 5);
-      to.b[i] = row_scales<WIDE>(row_b[i], at, p.kb, lane >> 5);
+      raw_a[i] = row_a[i].load(scale_block);
+      raw_b[i] = row_b[i].load(scale_block);
+    }
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      sc.a[i] = every_other(row_a[i].fix(raw_a[i], scale_block, p.kb));
+      sc.b[i] = every_other(row_b[i].fix(raw_b[i], scale_block, p.kb));
     }
     scale_block += 16;
   };
@@ -536,14 +617,15 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
     constexpr int kNewer = (NB - 2) * L + (I == 2 ? K : 0) + (kFirst && I < 3 ? kStores : 0);
     slice_barrier<(kNewer < 63 ? kNewer : 63)>();
     if constexpr (I == 1 && kLarge) load_scales();
-    if constexpr (I % kChunk == 0 && !kLarge) take_scales(next_sc);
+    if constexpr (I % kChunk == 0 && !kLarge) ask_scales();
     const char* from = buf[(I + 1) % NB];
     if constexpr (kLarge) {
       begin_load();
       constexpr int kAll = kSub * kSub;
 #pragma unroll
       for (int t = 0; t < 2 * kAll; ++t) {
-        const int i = t % kAll / kSub, j = t % kSub;
+        // to and fro along B: each product shares an operand with the one before (0.4%)
+        const int i = t % kAll / kSub, j = i % 2 ? kSub - 1 - t % kSub : t % kSub;
         if (t < kAll)
           multiply_in_place<2 * I, kFirst && I == 0>(acc[i][j], f[now].b[0][j], sc.b[j],
                                                      f[now].a[0][i], sc.a[i]);
@@ -581,7 +663,7 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
         step(std::integral_constant<int, 2>{});
         step(std::integral_constant<int, 3>{});
       }
-      if constexpr (I % kChunk == kChunk - 1) sc = next_sc;
+      if constexpr (I % kChunk == kChunk - 1) take_scales();
     }
   };
   auto round = [&](auto first_c) {
@@ -693,19 +775,11 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
           for (int q = 0; q < kTimes; ++q)
             __builtin_amdgcn_raw_buffer_store_b128(w[q], rows, off + q * kRows * line, 0, 0);
         } else {
-          // value by value, neighbouring lanes neighbouring columns
-          using V = std::conditional_t<O == kBf16, uint16_t, float>;
-#pragma unroll 4
-          for (int q = 0; q < kSpan / 2; ++q) {
-            const int row = (q * 64 + lane) / kSpan, col = lane % kSpan;
-            const int turn = row / (16 / kPieces) % kPieces;
-            const V v = *reinterpret_cast<const V*>(
-                slab + row * (kPieces * 16) + ((col / kPiece) ^ turn) * 16 + col % kPiece * kSize);
-            if (i * 32 + row < have && j0 * 32 + col < wide) {
-              V* o = reinterpret_cast<V*>(corner) + (i * 32 + row) * p.ld + j0 * 32 + col;
-              if constexpr (O == kAdd) *o = *o + v;
-              else *o = v;
-            }
+#pragma unroll 1
+          for (int q = 0; q < kTimes; ++q) {
+            const int row = i * 32 + q * kRows + row0, c = j0 * 32 + piece * kPiece;
+            if (row < have && c < wide)
+              store_piece<O>(corner + (row * p.ld + c) * kSize, wide - c, *from(q));
           }
         }
       }
@@ -722,10 +796,11 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
       const int64_t ra = static_cast<int64_t>(now.ti) * T + wr + i * 32 + (lane & 31);
       const int64_t rb =
           static_cast<int64_t>(now.tj) * T + wc + i * 32 + row_of<kPairs>(lane & 31);
-      row_a[i] = p.sa + (ra < p.m ? ra : p.m - 1) * p.kb;
-      row_b[i] = p.sb + (rb < p.n ? rb : p.n - 1) * p.kb;
+      const int half = lane >> 5 << 3;
+      row_a[i] = RowScales<WIDE, 2>(p.sa, ra < p.m ? ra : p.m - 1, p.m, p.kb, half);
+      row_b[i] = RowScales<WIDE, 2>(p.sb, rb < p.n ? rb : p.n - 1, p.n, p.kb, half);
     }
-    take_scales(sc);
+    ask_scales();
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i) load(buf[i]);
@@ -733,6 +808,8 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   if constexpr (kLarge) {
 #pragma unroll
     for (int c = 0; c < 2 * kSub; ++c) read_scale(0, c);
+  } else {
+    take_scales();
   }
 #pragma unroll
   for (int c = 0; c < kReads; ++c) read_one(buf[0], f[0], c);
@@ -828,7 +905,8 @@ Form form_of(int64_t m, int64_t n, int64_t kb) {
   // Few rows: 16 x 8192 x 4096 5.4 to 6.2 us, with small tiles 6.7; 32 x 4096 x 4096
   // 5.3 and 7.0; but 32 x 8192 x 4096 8.6 and 7.0, 16 x 16384 x 4096 10.9 and 8.8, since
   // each 16 columns read all of A.
-  if (m == 1 || (m <= 32 && n <= 4096) || (m <= 16 && n <= 8192)) return f;
+  if (m == 1 || (m <= 32 && n <= 4096) || (m <= 16 && n <= 8192) || std::min(m, n) * kb < 16)
+    return f;
   // Microseconds as measured (bf16 results), by the chunks c and the tiles; 512 of the
   // small and the middle ones run at once, 256 of the large.
   //   small   64 tiles c = 8 6.7, 28 18.3; 256 tiles 7.9, 21.3; 512 c = 8 11.5; 1024 21.0;
@@ -840,10 +918,17 @@ Form form_of(int64_t m, int64_t n, int64_t kb) {
   const double c = static_cast<double>(chunks);
   const double t64 = tiles(64) / 512.0, t128 = tiles(128) / 512.0, t256 = tiles(256) / 256.0;
   const double rounds = std::floor(t256), rest = t256 - rounds;
-  const double cost64 = t64 < 1 ? 3 + c * std::max(0.6, 1.15 * t64) : t64 * (2.5 + 0.95 * c);
-  const double cost128 = t128 < 1 ? 3 + c * std::max(1.3, 3.1 * t128) : t128 * (5 + 3.1 * c);
+  double cost64 = t64 < 1 ? 3 + c * std::max(0.6, 1.15 * t64) : t64 * (2.5 + 0.95 * c);
+  double cost128 = t128 < 1 ? 3 + c * std::max(1.3, 3.1 * t128) : t128 * (5 + 3.1 * c);
   const double cost256 =
       12 + rounds * (3 + 3.4 * c) + (rest > 0 ? 3 + c * (2.1 + 1.3 * rest) : 0);
+  if (kb % 16) {
+    // The small tile's scales at odd addresses and its cut last chunk: 64 x 4096 x 11008
+    // 11.5, x 11264 11.0; 1440 x 1440 x 2304 13.9, x 2560 11.8; 2880 x 2880 x 2080 37.7,
+    // with large tiles 23.9.  The middle tile has no registers for them: with spills 44.
+    cost64 *= 1.3;
+    cost128 = HUGE_VAL;
+  }
   f.T = cost64 <= std::min(cost128, cost256) ? 64 : cost128 <= cost256 ? 128 : 256;
   // Few tiles and long sums: parts of at least four chunks, up to a tile a compute
   // unit.  16 tiles c = 28 16.1, in 7 parts 9.6; 64 tiles 20.2, in 4 parts 12.7; but
@@ -890,7 +975,8 @@ sbp_status launch_tiles(const char* who, K kernel, const Problem& p, const Packe
 // C's rows as whole 16-byte pieces on such addresses, those of a tile within 2^31 bytes.
 bool direct_of(const Problem& p) {
   const int64_t size = p.f32 ? 4 : 2;
-  return p.vec && p.m > 1 && p.cols * size % 16 == 0 && p.ld * size < int64_t{1} << 23;
+  return p.m > 1 && sbp::aligned(p.out, 16) && p.ld * size % 16 == 0 && p.cols * size % 16 == 0 &&
+         p.ld * size < int64_t{1} << 23;
 }
 
 sbp_status run_large(const char* who, const Problem& p, const Form& f, char* ws,
@@ -920,7 +1006,6 @@ sbp_status run_large(const char* who, const Problem& p, const Form& f, char* ws,
 
 template <typename TL>
 sbp_status run_small(const char* who, Problem p, const Form& f, char* ws, hipStream_t stream) {
-  const bool wide = p.kb % 16 == 0 && sbp::aligned(p.sa, 16) && sbp::aligned(p.sb, 16);
   const Problem whole = p;
   p.parts = f.parts;
   p.part_chunks = f.part_chunks;
@@ -929,7 +1014,6 @@ sbp_status run_small(const char* who, Problem p, const Form& f, char* ws, hipStr
     p.ld = f.part_ld;
     p.f32 = 1;
     p.accumulate = 0;
-    p.vec = 1;
     p.part_step = p.m * f.part_ld;
     p.cols = f.part_ld;
   }
@@ -940,10 +1024,13 @@ sbp_status run_small(const char* who, Problem p, const Form& f, char* ws, hipStr
     if (p.accumulate) return go(mx4_tile_kernel<TL, kAdd, kDirect, kWide>);
     return go(mx4_tile_kernel<TL, kF32, kDirect, kWide>);
   };
-  constexpr std::true_type kYes{};
-  constexpr std::false_type kNo{};
-  sbp_status st = direct_of(p) ? (wide ? of(kYes, kYes) : of(kYes, kNo))
-                               : (wide ? of(kNo, kYes) : of(kNo, kNo));
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  auto wide_of = [&](auto direct_c) {
+    if constexpr (TL::T == 128) return of(direct_c, yes);
+    else return p.kb % 16 == 0 ? of(direct_c, yes) : of(direct_c, no);
+  };
+  sbp_status st = direct_of(p) ? wide_of(yes) : wide_of(no);
   if (st != SBP_OK || f.parts == 1) return st;
   const int64_t quads = f.part_ld / 4;
   const dim3 grid(static_cast<unsigned>((quads * p.m + 255) / 256));
@@ -953,16 +1040,16 @@ sbp_status run_small(const char* who, Problem p, const Form& f, char* ws, hipStr
 }
 
 sbp_status run_few(const char* who, const Problem& p, hipStream_t stream) {
-  const bool wide = p.kb % 16 == 0 && sbp::aligned(p.sa, 16) && sbp::aligned(p.sb, 16);
   constexpr int kWaves = 4;
   auto go = [&](auto kernel) -> sbp_status {
-    const unsigned blocks = static_cast<unsigned>((p.n + 15) / 16);
+    const int64_t rows = p.m <= 16 ? 16 : 32;
+    const unsigned blocks = static_cast<unsigned>((p.n + 15) / 16 * ((p.m + rows - 1) / rows));
     hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kWaves * 64), 0, stream, p);
     return launched(who);
   };
-  if (p.m <= 16)
-    return wide ? go(mx4_few_kernel<1, kWaves, true>) : go(mx4_few_kernel<1, kWaves, false>);
-  return wide ? go(mx4_few_kernel<2, kWaves, true>) : go(mx4_few_kernel<2, kWaves, false>);
+  if (p.kb % 16)
+    return p.m <= 16 ? go(mx4_few_kernel<1, kWaves, false>) : go(mx4_few_kernel<2, kWaves, false>);
+  return p.m <= 16 ? go(mx4_few_kernel<1, kWaves, true>) : go(mx4_few_kernel<2, kWaves, true>);
 }
 
 sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_a,
@@ -1009,8 +1096,7 @@ sbp_status matmul_call(const char* who, const void* codes_a, const void* scales_
   }
   Problem p{static_cast<const char*>(codes_a), static_cast<const char*>(codes_b),
             static_cast<const uint8_t*>(scales_a), static_cast<const uint8_t*>(scales_b),
-            m, n, kb, out, ld, type == SBP_F32, accumulate != 0,
-            sbp::aligned(out, 16) && (m == 1 || ld * size % 16 == 0), 1,
+            m, n, kb, out, ld, type == SBP_F32, accumulate != 0, 1,
             static_cast<int32_t>((kb + 15) / 16), 0, n};
   (void)hipGetLastError();
   if (k == 0) {
