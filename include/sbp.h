@@ -606,12 +606,13 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
  *   255 and codes 0.  Values beyond the last column are zeros, with code 0.
  *   Results depend on the values, the seed and the offset alone.
  *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE (more than SBP_MAX_SHARD_NUMEL
- *   values, counted in whole blocks of rows and of columns; ld above 2^40),
- *   SBP_ENOMEM, SBP_EHIP.
+ *   values, counted in whole blocks of rows and, but for one row along itself, of
+ *   columns; ld above 2^40), SBP_ENOMEM, SBP_EHIP.
  *
  * sbp_mx_dequantize: out (rows x cols, SBP_BF16 or SBP_F32, rows ld elements
  *   apart) = the values; exact in both types (in SBP_BF16 and SBP_F32 alike,
- *   scales above 252 may overflow to infinity).  Errors as above.
+ *   scales above 252 may overflow to infinity).  Errors as above (values counted
+ *   in whole blocks of rows).
  *
  * sbp_mx_reduce_shard: out[i] = fl( (acc[i] + S[i]) * scale ), without acc
  *   fl( S[i] * scale ): S[i] the R peers' values summed in ascending peer order,

@@ -433,8 +433,10 @@ constexpr int64_t kMaxLd = int64_t{1} << 40;  // elements from row to row
 
 int type_bytes(int32_t type) { return type == SBP_F32 ? 4 : 2; }
 
-// Sizes of a matrix and its row distance.
-sbp_status check_matrix(const Text& w, int64_t rows, int64_t cols, int64_t ld, int32_t type) {
+// Sizes of a matrix and its row distance; down: its columns are cut into blocks too, or
+// its tiles of 128 x 128 are counted.
+sbp_status check_matrix(const Text& w, int64_t rows, int64_t cols, int64_t ld, int32_t type,
+                        bool down) {
   if (type != SBP_BF16 && type != SBP_F32)
     return sbp::fail(SBP_EINVAL, w + ": the type must be SBP_BF16 or SBP_F32");
   if (rows < 0 || cols < 0) return sbp::fail(SBP_EINVAL, w + ": rows or cols < 0");
@@ -443,7 +445,7 @@ sbp_status check_matrix(const Text& w, int64_t rows, int64_t cols, int64_t ld, i
   if (rows > 1 && ld > kMaxLd) return sbp::fail(SBP_ERANGE, w + ": a row distance above 2^40");
   const int64_t most = SBP_MAX_SHARD_NUMEL;
   if (rows > most || cols > most || sbp::mx4_blocks(cols) * 32 > most / rows ||
-      sbp::mx4_blocks(rows) * 32 > most / cols)
+      (down && sbp::mx4_blocks(rows) * 32 > most / cols))
     return sbp::fail(SBP_ERANGE, w + ": more than SBP_MAX_SHARD_NUMEL values in whole blocks");
   return SBP_OK;
 }
@@ -505,7 +507,7 @@ sbp_status quantize_call(const char* who, const void* x, int32_t type, int64_t r
                          int64_t ld, void* codes, void* scales, void* codes_t, void* scales_t,
                          const sbp_mx_random* random, hipStream_t stream) {
   const Text w(who);
-  sbp_status st = check_matrix(w, rows, cols, ld, type);
+  sbp_status st = check_matrix(w, rows, cols, ld, type, rows > 1 || codes_t != nullptr);
   if (st != SBP_OK) return st;
   if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
     return sbp::fail(SBP_EINVAL, w + ": codes without scales, or scales without codes");
@@ -557,7 +559,7 @@ sbp_status dequantize(const char* who, const void* codes, const void* scales, in
 sbp_status dequantize_call(const char* who, const void* codes, const void* scales, int64_t rows,
                            int64_t cols, void* out, int32_t type, int64_t ld, hipStream_t stream) {
   const Text w(who);
-  sbp_status st = check_matrix(w, rows, cols, ld, type);
+  sbp_status st = check_matrix(w, rows, cols, ld, type, false);
   if (st != SBP_OK) return st;
   if (rows == 0 || cols == 0) return sbp::ok();  // nothing is read or written
   if (codes == nullptr || scales == nullptr || out == nullptr)
