@@ -99,6 +99,14 @@ struct RowScales {
   }
 };
 
+// Of the 8 scales that a lane has of a row's 16, the lower half of the lanes the first
+// and the upper half the others: to each half its own, the even or the odd ones, of both.
+__device__ __forceinline__ u32x2 every_other(u32x2 w) {
+  const uint32_t even = __builtin_amdgcn_perm(w.y, w.x, 0x06040200u);
+  const uint32_t odd = __builtin_amdgcn_perm(w.y, w.x, 0x07050301u);
+  const auto r = __builtin_amdgcn_permlane32_swap(even, odd, false, false);
+  return u32x2{r[0], r[1]};
+}
 // Four neighbours of a row of C, from column c on.
 __device__ __forceinline__ void store4(const Problem& p, int64_t row, int64_t c, f32x4 v) {
   const int64_t at = row * p.ld + c;
@@ -264,21 +272,22 @@ __global__ void __launch_bounds__(256)
 mx4_pack_kernel(Pack a, Pack b, int64_t kb, unsigned blocks_a) {
   const bool second = blockIdx.x >= blocks_a;
   const Pack p = second ? b : a;
-  const int64_t w = static_cast<int64_t>(second ? blockIdx.x - blocks_a : blockIdx.x) * 2 +
-                    (threadIdx.x >> 7);
-  const int lane = threadIdx.x & 63, word = (threadIdx.x >> 6) & 1, h = lane >> 5;
-  const int64_t chunks = (kb + 15) / 16;
-  if (w >= chunks * p.tiles) return;
-  const int64_t c = w / p.tiles, t = w - c * p.tiles;
+  const unsigned w = second ? blockIdx.x - blocks_a : blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t tiles = p.tiles, t = w % p.tiles, c0 = static_cast<int64_t>(w / p.tiles) * 8;
   const int64_t row = t * 32 + (p.pairs ? row_of<true>(lane & 31) : lane & 31);
-  uint32_t out = 0;
+  const RowScales<false, 2> from(p.scales, row < p.rows ? row : p.rows - 1, p.rows, kb,
+                                 lane >> 5 << 3);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t block = c * 16 + (word * 4 + s) * 2 + h;
-    if (row < p.rows && block < kb)
-      out |= static_cast<uint32_t>(p.scales[row * kb + block]) << (8 * s);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t c = c0 + wave + i * 4;
+    if (c * 16 >= kb) break;
+    u32x2 v = every_other(from.fix(from.load(c * 16), c * 16, kb));
+    if (row >= p.rows) v = u32x2{0, 0};
+    uint32_t* to = p.packed + (c * tiles + t) * 128 + lane;
+    to[0] = v.x;
+    to[64] = v.y;
   }
-  p.packed[w * 128 + (threadIdx.x & 127)] = out;
 }
 
 // `bytes` from p on as a buffer; loads from beyond them give zeros.  Whole offsets
@@ -354,14 +363,6 @@ template <typename TL>
 struct Scales {  // of a chunk: byte s % 4 of word s / 4 for its steps s of 64 values
   u32x2 a[TL::kSub], b[TL::kSub];
 };
-// The same of the 8 scales that a lane has of a row's 16, the lower half of the lanes the
-// first and the upper half the others: each half takes its own, even or odd, of both.
-__device__ __forceinline__ u32x2 every_other(u32x2 w) {
-  const uint32_t even = __builtin_amdgcn_perm(w.y, w.x, 0x06040200u);
-  const uint32_t odd = __builtin_amdgcn_perm(w.y, w.x, 0x07050301u);
-  const auto r = __builtin_amdgcn_permlane32_swap(even, odd, false, false);
-  return u32x2{r[0], r[1]};
-}
 template <typename TL>
 using Acc = f32x16[TL::kSub][TL::kSub];
 
@@ -987,8 +988,8 @@ sbp_status run_large(const char* who, const Problem& p, const Form& f, char* ws,
   const int32_t tiles_b = static_cast<int32_t>(f.step_b / 512);
   const Pack a{p.sa, reinterpret_cast<uint32_t*>(ws), p.m, tiles_a, 0};
   const Pack b{p.sb, reinterpret_cast<uint32_t*>(ws + chunks * f.step_a), p.n, tiles_b, !p.f32};
-  const unsigned blocks_a = static_cast<unsigned>((chunks * tiles_a + 1) / 2);
-  const unsigned blocks_b = static_cast<unsigned>((chunks * tiles_b + 1) / 2);
+  const unsigned blocks_a = static_cast<unsigned>((chunks + 7) / 8 * tiles_a);
+  const unsigned blocks_b = static_cast<unsigned>((chunks + 7) / 8 * tiles_b);
   hipLaunchKernelGGL(mx4_pack_kernel, dim3(blocks_a + blocks_b), dim3(256), 0, stream, a, b, p.kb,
                      blocks_a);
   sbp_status st = launched(who);
