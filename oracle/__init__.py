@@ -29,9 +29,9 @@ Modules:
   mx4    microscaled 4-bit floats: quantization (nearest, and at random from a
          counter-based generator), values, the ascending-rank reduce of them
 
-Every function is pinned by tests/test_oracle_*.py and tests/test_mx4_host.py against closed forms,
-invariants, special cases, library routines or brute force; none is
-"parity unpinned".
+Every function is pinned by tests/test_oracle_*.py and tests/test_mx4_host.py
+against closed forms, invariants, special cases, library routines or brute
+force; none is "parity unpinned".
 """
 
 from . import mx4, plan, step  # noqa: F401

@@ -1,10 +1,22 @@
 // C = A B' of two microscaled 4-bit operands (mx4.h) on CDNA4's scaled matrix
 // instructions.  Exact semantics are in include/sbp.h.
 //
+//   C[i][j] = sum over blocks b of 2^(sa[i][b] - 127) * 2^(sb[j][b] - 127)
+//             * sum over the block's 32 values of a * b
+//
 // v_mfma_scale_f32_16x16x128 takes 16 rows of each operand and 128 contracted
 // values: lane l holds row l % 16's block l / 16 of 32 values (16 bytes) and its
-// scale byte.  B's rows go in as the first operand, A's as the second, so that a
-// lane's four results are neighbours in a row of C.
+// scale byte; 32x32x64 takes 32 rows and two blocks of each.  Both apply the scales
+// and sum in binary32.  B's rows go in as the first operand, A's as the second, so
+// that a lane's results are neighbours in a row of C.
+//
+// What bounds it.  A few rows: B's codes and scales, once from memory (16 x 28672 x
+// 4096, 62 MB, 12.6 us: 5.0 TB/s), and below some 10 MB the launch and one
+// memory latency after another (1 x 4096 x 4096 4 us).  Many rows: the matrix units, of
+// which large tiles keep 62% busy at 1.66 GHz, where the card's power holds them:
+// the large tile's loop sustains 4.65 PFLOP/s on random data and 7.2 on zeros, and other
+// orders of its loads, reads and products change nothing.  8192 x 14336 x 4096 takes
+// 224 us (4.3 PFLOP/s), 4096 x 4096 x 8192 into fp32 sums 78 (3.5).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -501,7 +513,7 @@ mx4_tile_kernel(Problem p, Packed packed, unsigned total) {
   struct Place {
     unsigned ti, tj;
   };
-  // Strips of 4 tile rows, column by column (4096 x 4096 x 4096 40.2 us, of 8 41.1; at
+  // Strips of 4 tile rows, column by column (4096 x 4096 x 4096 40.2 us, then, of 8 41.1; at
   // larger sizes within 0.5%, of 16 up to 2% behind).
   auto place_of = [&](unsigned i) {
     constexpr unsigned kStrip = 4;
@@ -903,37 +915,40 @@ Form form_of(int64_t m, int64_t n, int64_t kb) {
   Form f{};
   f.part_chunks = static_cast<int>(chunks);
   f.parts = 1;
-  // Few rows: 16 x 8192 x 4096 5.4 to 6.2 us, with small tiles 6.7; 32 x 4096 x 4096
-  // 5.3 and 7.0; but 32 x 8192 x 4096 8.6 and 7.0, 16 x 16384 x 4096 10.9 and 8.8, since
-  // each 16 columns read all of A.
+  // Few rows: 16 x 8192 x 4096 6.3 us, with small tiles 6.8; 32 x 4096 x 4096 5.4 and
+  // 7.0; but 32 x 8192 x 4096 8.6 and 7.0, 16 x 16384 x 4096 10.8 and 8.5, since each 16
+  // columns read all of A.
   if (m == 1 || (m <= 32 && n <= 4096) || (m <= 16 && n <= 8192) || std::min(m, n) * kb < 16)
     return f;
-  // Microseconds as measured (bf16 results), by the chunks c and the tiles; 512 of the
-  // small and the middle ones run at once, 256 of the large.
-  //   small   64 tiles c = 8 6.7, 28 18.3; 256 tiles 7.9, 21.3; 512 c = 8 11.5; 1024 21.0;
-  //           8192 c = 1 54, c = 4 86
-  //   middle  128 tiles c = 8 13.8; 256 c = 4 9.0, 8 15.3, 16 27.4; 512 c = 8 28.4;
-  //           1088 66; 2048 c = 1 23 to 34, c = 4 54
-  //   large   64 tiles c = 8 25; 128 30; 256 42, c = 16 72; 272 c = 8 61; 512 c = 1 22,
-  //           c = 2 30, c = 4 46, c = 8 77; 1792 c = 8 230
+  // Microseconds as measured (bf16 results), by the chunks c; 512 of the small and the
+  // middle tiles run at once, 256 of the large.
+  //                            small   middle   large
+  //   1024 x 1024, c = 8 / 28    7 / 19  13 / 42  25 / 69
+  //   1024 x 2048, c = 8           12      13       25
+  //   2048 x 2048, c = 4 / 8     12 / 23  10 / 16  17 / 26
+  //   4096 x 2048, c = 8           42      28       29
+  //   4224 x 4224, c = 8           91      62       57
+  //   4096 x 4096, c = 8 / 16    82 / 147 54 / 104 41 / 69
+  //   4096 x 8192, c = 1 / 2     59 / 58  24 / 34  30 / 41
+  //                c = 4 / 8     88 / 161 55 / 107 47 / 71
+  //   8192 x 8192, c = 1           113      44       54 (taken: the fit is off here)
   const double c = static_cast<double>(chunks);
   const double t64 = tiles(64) / 512.0, t128 = tiles(128) / 512.0, t256 = tiles(256) / 256.0;
   const double rounds = std::floor(t256), rest = t256 - rounds;
   double cost64 = t64 < 1 ? 3 + c * std::max(0.6, 1.15 * t64) : t64 * (2.5 + 0.95 * c);
-  double cost128 = t128 < 1 ? 3 + c * std::max(1.3, 3.1 * t128) : t128 * (5 + 3.1 * c);
-  const double cost256 =
-      12 + rounds * (3 + 3.4 * c) + (rest > 0 ? 3 + c * (2.1 + 1.3 * rest) : 0);
+  double cost128 = t128 < 1 ? 3 + c * std::max(1.3, 3.1 * t128) : t128 * (3 + 3.1 * c);
+  const double cost256 = 8 + rounds * (7 + 3 * c) + (rest > 0 ? c * (2.05 + 0.8 * rest) : 0);
   if (kb % 16) {
     // The small tile's scales at odd addresses and its cut last chunk: 64 x 4096 x 11008
     // 11.5, x 11264 11.0; 1440 x 1440 x 2304 13.9, x 2560 11.8; 2880 x 2880 x 2080 37.7,
     // with large tiles 23.9.  The middle tile has no registers for them: with spills 44.
-    cost64 *= 1.3;
+    cost64 *= 1.2;
     cost128 = HUGE_VAL;
   }
   f.T = cost64 <= std::min(cost128, cost256) ? 64 : cost128 <= cost256 ? 128 : 256;
   // Few tiles and long sums: parts of at least four chunks, up to a tile a compute
-  // unit.  16 tiles c = 28 16.1, in 7 parts 9.6; 64 tiles 20.2, in 4 parts 12.7; but
-  // c = 8 7.5, in 2 parts 8.3: the joining takes 3 to 4.
+  // unit.  256 x 256 x 14336 17.0, in 7 parts 9.6; 512 x 512 17.0, in 4 parts 11.9; but
+  // 16 tiles c = 8 7.5, in 2 parts 8.3: the joining takes 3 to 4.
   int64_t parts = 1;
   if (f.T == 64 && chunks >= 12)
     parts = std::max<int64_t>(1, std::min(256 / tiles(64), chunks / 4));
