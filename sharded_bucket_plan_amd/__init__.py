@@ -140,6 +140,9 @@ def lib():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() "
                            "(there is no fallback path)")
+    # torch brings a HIP runtime of its own: loaded first, it serves this library too;
+    # loaded second there are two in the process, and this one finds no device
+    _t()
     L = ctypes.CDLL(LIB_PATH)
     st = ctypes.c_int32
     sig = {

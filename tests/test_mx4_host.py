@@ -3,6 +3,9 @@ generator and values against closed forms, and every refusal of the calls (the
 fake addresses are never dereferenced)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -280,3 +283,13 @@ def test_calls_refuse_host_tensors_and_shapes():
         with pytest.raises(ValueError):
             call()
 
+
+def test_one_hip_runtime_whatever_is_loaded_first():
+    """The library loaded before the caller imports torch: torch's HIP runtime serves
+    both (with a second one the library's calls find no device)."""
+    code = ("import sharded_bucket_plan_amd as sbp; sbp.lib(); import torch; "
+            "torch.cuda.is_available(); "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "1", r.stdout + r.stderr
