@@ -141,8 +141,13 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is not built: run __graft_entry__.build() "
                            "(there is no fallback path)")
     # torch brings a HIP runtime of its own: loaded first, it serves this library too;
-    # loaded second there are two in the process, and this one finds no device
-    _t()
+    # loaded second there are two in the process, and this one finds no device.  Where
+    # torch is not installed the host-only calls work by themselves
+    try:
+        _t()
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
     L = ctypes.CDLL(LIB_PATH)
     st = ctypes.c_int32
     sig = {

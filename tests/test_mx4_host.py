@@ -293,3 +293,31 @@ def test_one_hip_runtime_whatever_is_loaded_first():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "1", r.stdout + r.stderr
+
+
+def test_planner_works_where_torch_is_not_installed():
+    """Host-only use (plans, queries, sizes, factors) needs no torch."""
+    code = ("import sys; sys.modules['torch'] = None; import sharded_bucket_plan_amd as sbp; "
+            "plan = sbp.bucket_plan([100, 30], 1 << 20, world_n=2); "
+            "print(plan.shard_numel, plan.bucket(0)['padded'], sbp.mean_scale(4), "
+            "sbp.mx_matmul_workspace(8192, 8192, 512))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    # 30 values, 2 to the next multiple of 8, 100 more: padded to a multiple of 2 * 8
+    assert r.stdout.split() == ["72", "144", "0.25", str(2 * 8192 * 16)]
+
+
+def test_a_torch_that_does_not_load_is_not_passed_over():
+    """A torch that is installed but broken raises its own error: going on without it
+    would put a second HIP runtime beside it later."""
+    code = ("import sys, importlib.abc\n"
+            "class Broken(importlib.abc.MetaPathFinder):\n"
+            "    def find_spec(self, name, path, target=None):\n"
+            "        if name == 'torch': raise ImportError('torch is broken', name='torch._C')\n"
+            "sys.meta_path.insert(0, Broken())\n"
+            "import sharded_bucket_plan_amd as sbp\n"
+            "sbp.lib()\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode != 0 and "torch is broken" in r.stderr
