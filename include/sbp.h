@@ -607,7 +607,7 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
  *   Results depend on the values, the seed and the offset alone.
  *   Errors: SBP_EINVAL, SBP_EALIGN, SBP_ERANGE (more than SBP_MAX_SHARD_NUMEL
  *   values, counted in whole blocks of rows and, but for one row along itself, of
- *   columns; ld above 2^40), SBP_ENOMEM, SBP_EHIP.
+ *   columns; ld above 2^40, rows * ld above 2^60), SBP_ENOMEM, SBP_EHIP.
  *
  * sbp_mx_dequantize: out (rows x cols, SBP_BF16 or SBP_F32, rows ld elements
  *   apart) = the values; exact in both types (in SBP_BF16 and SBP_F32 alike,

@@ -429,7 +429,8 @@ sbp_status launched(const char* who) {
   return sbp::ok();
 }
 
-constexpr int64_t kMaxLd = int64_t{1} << 40;  // elements from row to row
+constexpr int64_t kMaxLd = int64_t{1} << 40;    // elements from row to row
+constexpr int64_t kMaxSpan = int64_t{1} << 60;  // rows * ld: the bytes of a span fit 63 bits
 
 int type_bytes(int32_t type) { return type == SBP_F32 ? 4 : 2; }
 
@@ -447,6 +448,8 @@ sbp_status check_matrix(const Text& w, int64_t rows, int64_t cols, int64_t ld, i
   if (rows > most || cols > most || sbp::mx4_blocks(cols) * 32 > most / rows ||
       (down && sbp::mx4_blocks(rows) * 32 > most / cols))
     return sbp::fail(SBP_ERANGE, w + ": more than SBP_MAX_SHARD_NUMEL values in whole blocks");
+  if (rows > 1 && ld > kMaxSpan / rows)
+    return sbp::fail(SBP_ERANGE, w + ": rows * ld above 2^60");
   return SBP_OK;
 }
 

@@ -321,3 +321,28 @@ def test_a_torch_that_does_not_load_is_not_passed_over():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode != 0 and "torch is broken" in r.stderr
+
+
+# rows * ld past what 64 bits hold in bytes: the overlap checks would be made with a wrapped length
+FAR = [(1 << 27, 1 << 40), (1 << 29, 1 << 34), ((1 << 20) + 1, 1 << 40), ((1 << 30) - 64, 1 << 40)]
+
+
+@pytest.mark.parametrize("rows,ld", FAR)
+@pytest.mark.parametrize("type_", [sbp.SBP_BF16, sbp.SBP_F32])
+def test_arrays_longer_than_an_address_are_refused(rows, ld, type_):
+    # 0x2000000 lies behind the first row's end and inside the array
+    far = dict(rows=rows, cols=32, ld=ld, type=type_)
+    assert _dequantize(out=V(0x1000000), **far) == ERANGE
+    assert "sbp_mx_dequantize" in sbp.lib().sbp_last_error().decode()
+    assert _quantize(codes_t=None, scales_t=None, scales=V(1 << 50), **far) == ERANGE
+    assert "sbp_mx_quantize" in sbp.lib().sbp_last_error().decode()
+
+
+@pytest.mark.parametrize("rows,ld", [(1 << 20, 1 << 40), (1 << 27, 1 << 33)])
+def test_overlaps_of_the_longest_arrays_are_seen(rows, ld):
+    last = 0x1000000 + (rows - 1) * ld * 4  # where the last row begins
+    far = dict(rows=rows, cols=32, ld=ld, type=sbp.SBP_F32, codes=V((1 << 62) + (1 << 40)))
+    assert _dequantize(out=V(0x1000000), scales=V(last), **far) == EINVAL
+    assert "overlaps" in sbp.lib().sbp_last_error().decode()
+    assert _quantize(codes_t=None, scales_t=None, scales=V(last), **far) == EINVAL
+    assert "overlap" in sbp.lib().sbp_last_error().decode()
