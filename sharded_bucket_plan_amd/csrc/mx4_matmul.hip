@@ -28,6 +28,7 @@
 #include "bf16.h"
 #include "internal.h"
 #include "mx4.h"
+#include "mx4_index.h"
 
 #pragma clang fp contract(off)
 
@@ -314,11 +315,12 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // comes from the lanes' global addresses.
 template <typename TL, bool PAIRS>
 struct Operand {
-  static constexpr int kOut = 0x7FFFFFF0;  // an offset beyond every buffer
-  const char* from;                        // next slice to load
-  int bytes, round_bytes, all, voff, piece;  // voff: `all`, or kOut past the rows' end
-  int at[TL::kSteps];                      // LDS offsets of this lane's first fragments
-  static constexpr int kLanes = TL::kRow / 16;  // that load a row
+  using Loads = sbp::Mx4Loads<TL::kRow>;
+  static constexpr int kLanes = Loads::kLanes;  // that load a row
+  const char* from;                             // next slice to load
+  int bytes, piece;
+  sbp::Mx4Offset round_bytes, all, voff;  // voff: `all`, or kMx4Past past the rows' end
+  int at[TL::kSteps];                     // LDS offsets of this lane's first fragments
 
   static __device__ __forceinline__ int turn(int i) {  // of row i of an MFMA tile
     if constexpr (kLanes == 8) return (i >> 1) & 7;
@@ -326,10 +328,10 @@ struct Operand {
   }
   // wrow: the wave's first row in the tile
   __device__ __forceinline__ void init(int kb, int wave, int lane, int wrow) {
-    const int row = wave * (64 / kLanes) + lane / kLanes;
+    const int row = Loads::row(wave, lane);
     piece = lane % kLanes ^ turn(row_of<PAIRS>(row & 31));  // row_of undoes itself
-    all = row * kb * 16 + piece * 16;
-    round_bytes = (256 / kLanes) * kb * 16;
+    all = Loads::first(row, kb, piece);
+    round_bytes = Loads::round_bytes(kb);
     const int i = lane & 31, h = lane >> 5;
 #pragma unroll
     for (int k = 0; k < TL::kSteps; ++k)
@@ -350,7 +352,8 @@ struct Operand {
     // a length below 0 would count as a huge one
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(from, bytes > 0 ? bytes : 0),
                                              (lds_ptr)(buf + (r * 4 + wave) * 1024), 16,
-                                             voff + r * round_bytes, 0, 0, 0);
+                                             static_cast<int>(Loads::at(voff, round_bytes, r)), 0,
+                                             0, 0);
   }
   // To the next slice; `bytes` may go below 0.
   __device__ __forceinline__ void advance() {
@@ -359,7 +362,7 @@ struct Operand {
   }
   // `left` blocks of the rows remain for the next slice: the rest reads as zeros.
   __device__ __forceinline__ void cut(int left) {
-    if (left < kLanes) voff = piece < left ? voff : kOut;
+    if (left < kLanes) voff = piece < left ? voff : sbp::kMx4Past;
   }
   // Step k of a slice, MFMA tile i.
   __device__ __forceinline__ u32x4 read(const char* buf, int k, int i) const {

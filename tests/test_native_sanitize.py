@@ -44,3 +44,9 @@ def test_planner_under_asan_ubsan(tmp_path):
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 def test_layout_segments_under_asan_ubsan(tmp_path):
     _build_and_run(tmp_path, "layout_fuzz", ["layout_host.cpp", "plan.cpp"], 12000, "ok")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_product_offsets_under_asan_ubsan(tmp_path):
+    """tests/native/mx4_offsets.cpp: the offsets of the 4-bit product's loads."""
+    _build_and_run(tmp_path, "mx4_offsets", [], 1, "offsets ok")
