@@ -570,9 +570,13 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
  *               all-to-all of codes and scales -> sbp_mx_reduce_shard ->
  *               sbp_adamw_shard(R = 0, acc)
  *   parameters  sbp_mx_quantize of the fp32 master shard -> all-gather ->
- *               sbp_mx_dequantize, or straight into sbp_mx_matmul: a tensor
- *               of whole rows per rank (sbp_bucket_plan_per_tensor) with a
- *               multiple of 32 columns is, after the all-gather, the operand
+ *               sbp_mx_dequantize, or straight into sbp_mx_matmul: under
+ *               sbp_bucket_plan_per_tensor with align_elems a multiple of 32
+ *               (below that a tensor's rows may begin inside a block of the
+ *               shard) the ranks' chunks of a tensor with a multiple of 32
+ *               columns, one behind the other, are the operand: blocks
+ *               shard_offset / 32 to (shard_offset + chunk) / 32 of each rank's
+ *               shard, rows of padding at the end
  *   a layer     y = x W' of quantized x and W; its gradients dy W and dy' x are
  *               the same call on the operands quantized along their columns,
  *               the latter added to the fp32 accumulator of the gradients

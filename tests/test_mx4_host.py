@@ -346,3 +346,49 @@ def test_overlaps_of_the_longest_arrays_are_seen(rows, ld):
     assert "overlaps" in sbp.lib().sbp_last_error().decode()
     assert _quantize(codes_t=None, scales_t=None, scales=V(last), **far) == EINVAL
     assert "overlap" in sbp.lib().sbp_last_error().decode()
+
+
+# ---- from a plan to an operand --------------------------------------------------------
+
+def _shards(plan, tensors, N):
+    """Each rank's fp32 master shard: its chunk of every tensor, at the plan's places."""
+    shards = [np.zeros(plan.shard_numel, F32) for _ in range(N)]
+    for t, x in enumerate(tensors):
+        b = plan.bucket(plan.tensor(t)[0])
+        padded = np.zeros(b["padded"], F32)
+        padded[:x.size] = x.reshape(-1)
+        for r in range(N):
+            shards[r][b["shard_offset"]:b["shard_offset"] + b["chunk"]] = \
+                padded[r * b["chunk"]:(r + 1) * b["chunk"]]
+    return shards
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 8])
+def test_gathered_chunks_of_a_plan_are_operands(N):
+    """Shards quantized as flat buffers; a tensor's blocks of every rank's, one behind the
+    other, are the tensor quantized as a matrix, and then rows of zeros."""
+    rng = np.random.default_rng(N)
+    shapes = [(50, 96), (13,), (7, 32), (1, 64), (129, 160)]
+    tensors = [rng.standard_normal(s).astype(F32) for s in shapes]
+    plan = sbp.bucket_plan_per_tensor([x.size for x in tensors], N,
+                                      [s[-1] if len(s) == 2 else 1 for s in shapes], align=32)
+    shards = [OM.quantize(s[None]) for s in _shards(plan, tensors, N)]
+    for t, x in enumerate(tensors):
+        if x.ndim == 1:
+            continue
+        b = plan.bucket(plan.tensor(t)[0])
+        assert b["shard_offset"] % 32 == 0 and b["chunk"] % x.shape[1] == 0
+        blocks = slice(b["shard_offset"] // 32, (b["shard_offset"] + b["chunk"]) // 32)
+        code = np.concatenate([c[0, blocks] for c, _ in shards])
+        scale = np.concatenate([s[0, blocks] for _, s in shards])
+        kb = x.shape[1] // 32
+        want_code, want_scale = OM.quantize(x)
+        assert np.array_equal(code.reshape(-1, kb, 32)[:len(x)], want_code)
+        assert np.array_equal(scale.reshape(-1, kb)[:len(x)], want_scale)
+        assert not code.reshape(-1, kb, 32)[len(x):].any()
+
+
+def test_plans_of_finer_alignment_may_begin_rows_inside_a_block():
+    """Why the alignment has to be a multiple of 32."""
+    plan = sbp.bucket_plan_per_tensor([13, 50 * 96], 1, [1, 96], align=8, order="forward")
+    assert plan.bucket(plan.tensor(1)[0])["shard_offset"] == 16
