@@ -87,3 +87,27 @@ def test_tiles_of_128_nan_and_scales_anywhere(m, n, k):
     got = sbp.mx_matmul(a, b, dtype=torch.float32)
     assert torch.equal(got.isnan(), want.isnan())
     assert torch.equal(got.nan_to_num(0), want.nan_to_num(0))
+
+
+# a size of each form: few rows, tiles of 64, parts, tiles of 128 and of 256
+SIZES = [(20, 20, 160), (1, 300, 2048), (65, 130, 1024), (70, 61, 6144), (300, 700, 128),
+         (1700, 1750, 1024), (2900, 2952, 160)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("sa,sb", [(252, 120), (10, 100), (0, 0), (254, 254), (0, 254), (254, 0),
+                                   (0, 105), (0, 127), (1, 127), (240, 128), (250, 126), (130, 0)])
+def test_scales_at_both_ends(m, n, k, sa, sb):
+    """All ones: sums of k equal powers of two, exact down to the least subnormal, and
+    infinity from 2^128 on; in bf16 the same rounded once, subnormals too."""
+    import torch
+    q = [sbp.Mx4(torch.full((rows, k // 2), 0x22, dtype=torch.uint8, device=H.dev()),
+                 torch.full((rows, k // 32), s, dtype=torch.uint8, device=H.dev()), (rows, k))
+         for rows, s in ((m, sa), (n, sb))]
+    with np.errstate(over="ignore"):
+        want = float(np.float32(np.float64(k) * 2.0 ** (sa - 127.0) * 2.0 ** (sb - 127.0)))
+    got = sbp.mx_matmul(*q, dtype=torch.float32)
+    assert bool((got == want).all()), (got.min(), got.max(), want)
+    half = float(torch.tensor(want).bfloat16())
+    got = sbp.mx_matmul(*q)
+    assert bool((got == half).all()), (got.min(), got.max(), half)
