@@ -111,3 +111,19 @@ def test_scales_at_both_ends(m, n, k, sa, sb):
     half = float(torch.tensor(want).bfloat16())
     got = sbp.mx_matmul(*q)
     assert bool((got == half).all()), (got.min(), got.max(), half)
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_order_of_a_sum_depends_on_the_sizes_alone(m, n, k):
+    """The same bits every time, and with the rows of both operands in another order: on
+    values whose sums round."""
+    import torch
+    from tests.test_gpu_mx4 import _operand
+    a, b = _operand(m, k, 5)[0], _operand(n, k, 6)[0]
+    first = sbp.mx_matmul(a, b, dtype=torch.float32)
+    for _ in range(3):
+        assert torch.equal(sbp.mx_matmul(a, b, dtype=torch.float32), first)
+    pa, pb = (torch.randperm(r, generator=torch.Generator().manual_seed(r)).to(H.dev())
+              for r in (m, n))
+    moved = [sbp.Mx4(q.codes[p], q.scales[p], q.shape) for q, p in ((a, pa), (b, pb))]
+    assert torch.equal(sbp.mx_matmul(*moved, dtype=torch.float32), first[pa][:, pb])
