@@ -9,6 +9,7 @@ import sharded_bucket_plan_amd as sbp
 from oracle import mx4 as OM
 from tests import helpers as H
 from tests.test_gpu_mx4 import _check_product, _data, _device, _operand
+from tests.test_gpu_mx4_forms import exact_operand
 from tests.test_mx4_host import _shards
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,65 @@ def test_from_a_plan_to_a_product(N):
         code, scale = OM.quantize(tensors[t])
         _check_product(sbp.mx_matmul(x, w).float().cpu().numpy(), xv,
                        OM.values(OM.pack(code), scale, cols), True, what=f"tensor {t}")
+
+
+# two kernels each: parts of a long sum and their joining, packed scales and large tiles
+WITH_WORKSPACE = [(300, 280, 7200), (300, 280, 6113), (2900, 2952, 300), (2900, 2950, 1600)]
+
+
+@pytest.mark.parametrize("m,n,k", WITH_WORKSPACE)
+@pytest.mark.parametrize("own", [False, True])
+def test_workspaces_of_two_streams(m, n, k, own):
+    """Products of two pairs of operands by turns on two streams, with the calls' workspaces
+    (own: the caller's, one a stream, filled with NaN scales and values)."""
+    import torch
+    size = sbp.mx_matmul_workspace(m, n, k)
+    assert size > 0
+    pairs = [[exact_operand(r, k, seed + i) for i, r in enumerate((m, n))] for seed in (1, 11)]
+    wants = [(a[1] @ b[1].T).float() for a, b in pairs]
+    spaces = [torch.full((size,), 255, dtype=torch.uint8, device=H.dev()) if own else None
+              for _ in pairs]
+    streams = [torch.cuda.Stream() for _ in pairs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, ((a, _), (b, _)) in enumerate(pairs):
+            got[i].append(sbp.mx_matmul(a, b, dtype=torch.float32, workspace=spaces[i],
+                                        stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, wants[i]) for g in got[i])
+
+
+@pytest.mark.parametrize("m,n,k", WITH_WORKSPACE)
+@pytest.mark.parametrize("shared", [False, True])
+def test_workspaces_of_two_graphs(m, n, k, shared):
+    """Two captured graphs, their workspaces the calls' or one that they share, replayed by
+    turns with eager calls in between."""
+    import torch
+    size = sbp.mx_matmul_workspace(m, n, k)
+    assert size > 0
+    pairs = [[exact_operand(r, k, seed + i) for i, r in enumerate((m, n))] for seed in (2, 12)]
+    wants = [(a[1] @ b[1].T).float() for a, b in pairs]
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=H.dev()) if shared else None
+    outs = [torch.empty(m, n, device=H.dev()) for _ in pairs]
+    for ((a, _), (b, _)), out in zip(pairs, outs):  # before the capture: loads the kernels
+        sbp.mx_matmul(a, b, out, workspace=ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for ((a, _), (b, _)), out in zip(pairs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sbp.mx_matmul(a, b, out, workspace=ws)
+        graphs.append(g)
+    for rep in range(4):
+        eager = sbp.mx_matmul(pairs[rep % 2][0][0], pairs[rep % 2][1][0], dtype=torch.float32)
+        for out in outs:
+            out.fill_(float("nan"))
+        if shared:
+            ws.fill_(255)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, wants[rep % 2]), rep
+        assert all(torch.equal(o, w) for o, w in zip(outs, wants)), rep
