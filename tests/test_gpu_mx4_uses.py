@@ -109,3 +109,42 @@ def test_workspaces_of_two_graphs(m, n, k, shared):
         torch.cuda.synchronize()
         assert torch.equal(eager, wants[rep % 2]), rep
         assert all(torch.equal(o, w) for o, w in zip(outs, wants)), rep
+
+
+def _grid(rows, cols, seed):
+    """Values of the format's grid, a 4 or a 6 in every block of 32 along rows and columns:
+    quantized either way each is itself, with scale 1."""
+    g = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+    rng = np.random.default_rng(seed)
+    x = g[rng.integers(0, 6, (rows, cols))] * rng.choice([-1.0, 1.0], (rows, cols))
+    x[(np.arange(rows)[:, None] + np.arange(cols)) % 16 == 3] = 6
+    return x.astype(np.float32)
+
+
+def test_layer_gradients_are_differences():
+    """The device's gradients against differences of the device's outputs: with values that
+    quantization keeps, every product and sum is exact, and L = <dy, x W'> is linear in each
+    entry of x and of W."""
+    import torch
+    t, d_in, d_out = 96, 160, 224
+    x, w, dy = _grid(t, d_in, 80), _grid(d_out, d_in, 81), _grid(t, d_out, 82)
+
+    def q(v, along="rows"):
+        return sbp.mx_quantize(torch.from_numpy(v).to(H.dev()), along)
+
+    def loss(x_, w_):
+        y = sbp.mx_matmul(q(x_), q(w_), dtype=torch.float32)
+        return float((y.double() * torch.from_numpy(dy).to(H.dev()).double()).sum())
+
+    assert bool((sbp.mx_dequantize(q(w)).float().cpu() == torch.from_numpy(w)).all())
+    gq, gt = q(dy, "both")
+    dx = sbp.mx_matmul(gq, q(w, "cols"), dtype=torch.float32).cpu().numpy()
+    dw = torch.zeros(d_out, d_in, device=H.dev())
+    sbp.mx_matmul(gt, q(x, "cols"), dw, accumulate=True)
+    dw = dw.cpu().numpy()
+    before = loss(x, w)
+    for r, c in ((0, 0), (5, 31), (40, 77), (t - 1, d_in - 1), (33, 64)):
+        for v, grad, of in ((x, dx, lambda u: loss(u, w)), (w, dw, lambda u: loss(x, u))):
+            moved = v.copy()
+            moved[r, c] = 2.0 if v[r, c] != 2.0 else -1.5
+            assert of(moved) - before == float(grad[r, c]) * float(moved[r, c] - v[r, c]), (r, c)
