@@ -8,7 +8,7 @@ import pytest
 import sharded_bucket_plan_amd as sbp
 from oracle import mx4 as OM
 from tests import helpers as H
-from tests.test_gpu_mx4 import _check_product, _data, _device, _operand
+from tests.test_gpu_mx4 import _check_product, _data, _device, _operand, _same_codes
 from tests.test_gpu_mx4_forms import exact_operand
 from tests.test_mx4_host import _shards
 
@@ -148,3 +148,35 @@ def test_layer_gradients_are_differences():
             moved = v.copy()
             moved[r, c] = 2.0 if v[r, c] != 2.0 else -1.5
             assert of(moved) - before == float(grad[r, c]) * float(moved[r, c] - v[r, c]), (r, c)
+
+
+def _packed(x, seed):
+    code, scale = OM.quantize(x, seed)
+    return OM.pack(code), scale
+
+
+# a block of lanes ends after 2048 values, a quad of lanes after 32, an octet after 8
+@pytest.mark.parametrize("n", [7, 9, 2040, 2047, 2048, 2049, 2056, 2080, 3 * 2048 - 25, 5 * 2048])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seed", [None, 3])
+def test_flat_ends(n, dtype, seed):
+    x = _data(1, n, n)
+    q = sbp.mx_quantize(_device(x, dtype)[0], seed=seed)
+    _same_codes(q, OM.quantize(x, seed), f"n={n}")
+    assert np.array_equal(sbp.mx_dequantize(q).float().cpu().numpy(),
+                          OM.values(*_packed(x, seed), n).astype(np.float32))
+
+
+# tiles of 128 x 128 in strips of four: one to 21 of them, strips of every width, counts
+# that eight do not divide
+@pytest.mark.parametrize("tiles", [(1, 1), (1, 3), (9, 1), (3, 3), (2, 4), (3, 5), (2, 6), (3, 7),
+                                   (1, 9)])
+@pytest.mark.parametrize("seed", [None, 3])
+def test_matrix_tiles(tiles, seed):
+    rows, cols = (128 * n - d for n, d in zip(tiles, (37, 30)))
+    x = _data(rows, cols, rows)
+    a, t = sbp.mx_quantize(_device(x, "bf16"), "both", seed=seed)
+    _same_codes(a, OM.quantize(x, seed), "rows")
+    _same_codes(t, OM.quantize(x.T, seed, 0, True), "cols")
+    _same_codes(sbp.mx_quantize(_device(x, "f32"), "cols", seed=seed),
+                OM.quantize(x.T, seed, 0, True), "cols alone")
