@@ -1107,8 +1107,9 @@ def mx_matmul_workspace(m, n, k):
     """Bytes of workspace sbp_mx_matmul needs for m x k times (n x k)'."""
     need = lib().sbp_mx_matmul_workspace(m, n, k)
     if need < 0:
-        raise SbpError(SBP_EINVAL if min(m, n, k) < 0 else SBP_ERANGE,
-                       lib().sbp_last_error().decode())
+        why = lib().sbp_last_error().decode()
+        raise SbpError(SBP_ENOMEM if "out of host memory" in why else
+                       SBP_EINVAL if min(m, n, k) < 0 else SBP_ERANGE, why)
     return need
 
 

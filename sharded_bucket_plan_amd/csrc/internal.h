@@ -12,6 +12,16 @@ namespace sbp {
 
 // Records `msg` as this thread's last error and returns `code`.
 sbp_status fail(sbp_status code, const std::string& msg);
+// The same for text that outlives the thread's use of it, a literal: it is kept as it is,
+// so that nothing is thrown where there is no memory for a copy.
+sbp_status fail_literal(sbp_status code, const char* msg) noexcept;
+template <size_t N>
+sbp_status fail(sbp_status code, const char (&msg)[N]) noexcept {
+  return fail_literal(code, msg);
+}
+// SBP_ENOMEM with "<who>: out of host memory", or the latter part alone where there is no
+// memory for both: for handlers, which must not throw.
+sbp_status no_memory(const char* who) noexcept;
 // Clears this thread's last error and returns SBP_OK.
 sbp_status ok();
 

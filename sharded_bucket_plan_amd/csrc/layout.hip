@@ -460,7 +460,7 @@ sbp_status launch_fans(const char* who, const sbp_plan* plan, const void* const*
       return launch_segments(who, segs, stream);
     }
   } catch (...) {
-    return sbp::fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+    return sbp::no_memory(who);
   }
   (void)hipGetLastError();
   FanList L;

@@ -1142,6 +1142,7 @@ int64_t sbp_mx_matmul_workspace(int64_t m, int64_t n, int64_t k) {
     (void)sbp::ok();
     return workspace_of(m, n, k);
   } catch (...) {
+    (void)sbp::fail(SBP_ENOMEM, "sbp_mx_matmul_workspace: out of host memory");
     return -1;
   }
 }

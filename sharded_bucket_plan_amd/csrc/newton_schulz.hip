@@ -1980,7 +1980,7 @@ int64_t sbp_newton_schulz_workspace(const sbp_matrices* groups, int32_t n_groups
     (void)sbp::ok();
     return most;
   } catch (...) {
-    (void)sbp::fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+    (void)sbp::no_memory(who);
     return -1;
   }
 }
@@ -1993,7 +1993,7 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
   try {
     return newton_schulz(who, groups, n_groups, hp, workspace, workspace_bytes, stream);
   } catch (...) {
-    return sbp::fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+    return sbp::no_memory(who);
   }
 }
 

@@ -21,15 +21,31 @@ namespace sbp {
 
 namespace {
 thread_local std::string g_last_error;
+thread_local const char* g_literal = nullptr;  // the last error, where it is a literal
 }
 
 sbp_status fail(sbp_status code, const std::string& msg) {
   g_last_error = msg;
+  g_literal = nullptr;
   return code;
+}
+
+sbp_status fail_literal(sbp_status code, const char* msg) noexcept {
+  g_literal = msg;
+  return code;
+}
+
+sbp_status no_memory(const char* who) noexcept {
+  try {
+    return fail(SBP_ENOMEM, std::string(who) + ": out of host memory");
+  } catch (...) {
+    return fail(SBP_ENOMEM, "out of host memory");
+  }
 }
 
 sbp_status ok() {
   g_last_error.clear();
+  g_literal = nullptr;
   return SBP_OK;
 }
 
@@ -140,7 +156,9 @@ using sbp::ok;
 
 extern "C" {
 
-const char* sbp_last_error(void) { return sbp::g_last_error.c_str(); }
+const char* sbp_last_error(void) {
+  return sbp::g_literal ? sbp::g_literal : sbp::g_last_error.c_str();
+}
 
 const char* sbp_version(void) { return "sbp 0.1.0 (gfx950)"; }
 

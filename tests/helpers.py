@@ -198,3 +198,24 @@ def build_c_client(out_dir):
     r = subprocess.run(cmd, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-3000:]
     return exe
+
+
+def run_native(name, out_dir):
+    """Compile tests/native/<name>, a C++ client of include/sbp.h, with g++, link it against
+    the built library, and run it."""
+    import os
+    import subprocess
+
+    import sharded_bucket_plan_amd as sbp
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    pkg = os.path.dirname(sbp.LIB_PATH)
+    exe = os.path.join(str(out_dir), name + ".exe")
+    cmd = ["g++", "-std=c++17", "-O1", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-I", os.path.join(root, "include"), "-I", "/opt/rocm/include",
+           os.path.join(root, "tests", "native", name), "-o", exe, "-L", pkg, "-lsbp",
+           "-L", "/opt/rocm/lib", "-lamdhip64",
+           "-Wl,-rpath," + pkg, "-Wl,-rpath,/opt/rocm/lib"]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    return subprocess.run([exe], capture_output=True, text=True, timeout=120)

@@ -392,3 +392,12 @@ def test_plans_of_finer_alignment_may_begin_rows_inside_a_block():
     """Why the alignment has to be a multiple of 32."""
     plan = sbp.bucket_plan_per_tensor([13, 50 * 96], 1, [1, 96], align=8, order="forward")
     assert plan.bucket(plan.tensor(1)[0])["shard_offset"] == 16
+
+
+# ---- no memory on the host ---------------------------------------------------------------
+
+def test_no_exception_leaves_a_call(tmp_path):
+    """tests/native/no_memory.cpp: operator new fails at each place where the calls use it."""
+    from tests import helpers as H
+    r = H.run_native("no_memory.cpp", tmp_path)
+    assert r.returncode == 0 and "no exception left a call" in r.stdout, r.stdout + r.stderr
