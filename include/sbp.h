@@ -591,10 +591,9 @@ sbp_status sbp_newton_schulz(const sbp_matrices* groups, int32_t n_groups,
  * A flat buffer is a matrix of one row.
  *
  * sbp_mx_quantize: x (rows x cols, device SBP_BF16 or SBP_F32, aligned to its
- *   type, rows ld elements apart; 16-byte rows take the vector path) into
- *   codes and scales, and / or x' (cols x rows: blocks down x's columns) into
- *   codes_t and scales_t; either pair may be null.  With a the largest
- *   magnitude of a block and E its biased exponent:
+ *   type, rows ld elements apart) into codes and scales, and / or x' (cols x
+ *   rows: blocks down x's columns) into codes_t and scales_t; either pair may be
+ *   null.  With a the largest magnitude of a block and E its biased exponent:
  *     random null    nearest: s = max(E - 2, 0); |x| * 2^(127 - s) to the nearest
  *                    code, ties to the even one, above 6 to 6
  *     random given   s is one more where a > 6 * 2^(s - 127); a magnitude between

@@ -15,8 +15,10 @@
 // memory latency after another (1 x 4096 x 4096 4 us).  Many rows: the matrix units, of
 // which large tiles keep 62% busy at 1.66 GHz, where the card's power holds them:
 // the large tile's loop sustains 4.65 PFLOP/s on random data and 7.2 on zeros, and other
-// orders of its loads, reads and products change nothing.  8192 x 14336 x 4096 takes
-// 224 us (4.3 PFLOP/s), 4096 x 4096 x 8192 into fp32 sums 78 (3.5).
+// orders of its loads, reads and products change nothing.  On two sets of operands in
+// turn 8192 x 14336 x 4096 takes 243 us a call (4.0 PFLOP/s; 224 to 227 repeated on one
+// set), 4096 x 4096 x 8192 added to fp32 sums 87 (3.1; 78 repeated); 5 of them are the
+// packing of the scales.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -920,11 +922,12 @@ Form form_of(int64_t m, int64_t n, int64_t kb) {
   f.parts = 1;
   // Few rows: 16 x 8192 x 4096 6.3 us, with small tiles 6.8; 32 x 4096 x 4096 5.4 and
   // 7.0; but 32 x 8192 x 4096 8.6 and 7.0, 16 x 16384 x 4096 10.8 and 8.5, since each 16
-  // columns read all of A.
+  // columns read all of A.  (All at k = 4096; k is not looked at.)
   if (m == 1 || (m <= 32 && n <= 4096) || (m <= 16 && n <= 8192) || std::min(m, n) * kb < 16)
     return f;
   // Microseconds as measured (bf16 results), by the chunks c; 512 of the small and the
-  // middle tiles run at once, 256 of the large.
+  // middle tiles run at once, 256 of the large.  fp32 and added results go by the same
+  // costs, which do not know of their larger C.
   //                            small   middle   large
   //   1024 x 1024, c = 8 / 28    7 / 19  13 / 42  25 / 69
   //   1024 x 2048, c = 8           12      13       25
