@@ -16,9 +16,9 @@
 // which large tiles keep 62% busy at 1.66 GHz, where the card's power holds them:
 // the large tile's loop sustains 4.65 PFLOP/s on random data and 7.2 on zeros, and other
 // orders of its loads, reads and products change nothing.  On two sets of operands in
-// turn 8192 x 14336 x 4096 takes 243 us a call (4.0 PFLOP/s; 224 to 227 repeated on one
-// set), 4096 x 4096 x 8192 added to fp32 sums 87 (3.1; 78 repeated); 5 of them are the
-// packing of the scales.
+// turn 8192 x 14336 x 4096 takes 237 to 249 us a call (3.9 to 4.1 PFLOP/s; 224 to 227
+// repeated on one set), 4096 x 4096 x 8192 added to fp32 sums 85 to 87 (3.2; 78 repeated);
+// 5 of them are the packing of the scales.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
